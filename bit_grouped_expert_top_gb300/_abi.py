@@ -60,6 +60,15 @@ class lily_gdn_shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "H_k", "H_v", "d_k", "d_v")]
 
 
+class lily_kvq_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H_q", "H_kv", "D", "block_size", "max_blocks", "bits")]
+
+
+class lily_kvq_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_q", "k_sb", "v_q", "v_sb")] + [
+        (n, ctypes.c_int64) for n in ("n_blocks", "code_bytes")]
+
+
 class lily_moe_decode_trace(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "topk_idx", "topk_w")]
 
@@ -91,6 +100,15 @@ def _configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lily_attn_decode.restype = I32
     L.lily_gdn_scan.argtypes = [ctypes.POINTER(lily_gdn_shape), P, P, P, P, P, P, ctypes.c_float, P, P, P]
     L.lily_gdn_scan.restype = I32
+    PQ, PC = ctypes.POINTER(lily_kvq_shape), ctypes.POINTER(lily_kvq_cache)
+    L.lily_kvq_workspace_bytes.restype = S
+    L.lily_kvq_workspace_bytes.argtypes = [PQ, ctypes.c_int32]
+    for n in ("lily_kvq_append", "lily_kvq_read"):
+        getattr(L, n).argtypes = [PQ, PC, P, I64, P, I64, ctypes.c_int32, P, P, P, P, S, P]
+    L.lily_kvq_attn_decode.argtypes = [PQ, PC, P, I64, P, P, ctypes.c_float, P, P, S, P]
+    L.lily_kvq_attn_prefill.argtypes = [PQ, PC, P, I64, ctypes.c_int32, P, P, P, ctypes.c_float, P, P, S, P]
+    for n in ("lily_kvq_append", "lily_kvq_read", "lily_kvq_attn_decode", "lily_kvq_attn_prefill"):
+        getattr(L, n).restype = I32
     L.lily_moe_device_status.argtypes = [P, P]
     L.lily_moe_clear_status.argtypes = [P, P]
     for n in ("lily_moe_check_shape", "lily_moe_route", "lily_moe_grouped_gemm", "lily_moe_forward",
@@ -324,6 +342,138 @@ def lily_attn_decode(shape: lily_attn_shape, q, k_cache, v_cache, block_table, s
                                  _ptr(block_table), _ptr(seq_lens), float(scale), _ptr(out), _ptr(ws),
                                  ws.numel() if isinstance(ws, torch.Tensor) else 0, _stream(stream))
     return _check("lily_attn_decode", rc) if check else rc
+
+
+# ------------------------------------------------------------------ quantised KV cache
+def make_kvq_shape(B: int, H_q: int, H_kv: int, D: int, block_size: int, max_blocks: int, bits: int = 4) -> lily_kvq_shape:
+    return lily_kvq_shape(B, H_q, H_kv, D, block_size, max_blocks, bits)
+
+
+def alloc_kvq_cache(shape: lily_kvq_shape, n_blocks: int, device="cuda") -> Dict[str, torch.Tensor]:
+    """The four arrays of a cache of n_blocks blocks (codes uint8 and parameters
+    bf16 of K and V, zeroed); hand them to make_kvq_cache."""
+    if lily_kvq_workspace_bytes(shape) == 0:
+        raise ValueError("unsupported quantised-cache shape")
+    lead = (n_blocks, shape.H_kv, shape.D // 64, shape.block_size)
+    out = {}
+    for n in ("k", "v"):
+        out[n + "_q"] = torch.zeros(lead + (8 * shape.bits,), dtype=torch.uint8, device=device)
+        out[n + "_sb"] = torch.zeros(lead + (2,), dtype=torch.bfloat16, device=device)
+    return out
+
+
+def make_kvq_cache(tensors: Dict[str, torch.Tensor]) -> lily_kvq_cache:
+    """Cache struct of the four arrays of alloc_kvq_cache (codes [n_blocks][H_kv]
+    [D/64][block_size][8 bits], parameters [...][2]).  The caller keeps the
+    tensors alive."""
+    k_q = tensors["k_q"]
+    for n in ("k", "v"):
+        q, sb = tensors[n + "_q"], tensors[n + "_sb"]
+        if q.dtype != torch.uint8 or sb.dtype != torch.bfloat16:
+            raise ValueError(f"{n}_q must be uint8 and {n}_sb bfloat16, got {q.dtype} and {sb.dtype}")
+        if q.dim() != 5 or q.shape != k_q.shape or sb.shape != q.shape[:-1] + (2,):
+            raise ValueError(f"cache arrays of unlike shapes: {n}_q {tuple(q.shape)}, {n}_sb {tuple(sb.shape)}")
+        if q.device != k_q.device or sb.device != k_q.device:
+            raise ValueError("cache arrays on different devices")
+    return lily_kvq_cache(_ptr(k_q), _ptr(tensors["k_sb"]), _ptr(tensors["v_q"]), _ptr(tensors["v_sb"]),
+                          k_q.shape[0], k_q.numel())
+
+
+def lily_kvq_workspace_bytes(shape: lily_kvq_shape, n_query: int = 0) -> int:
+    return load().lily_kvq_workspace_bytes(ctypes.byref(shape), int(n_query))
+
+
+def alloc_kvq_workspace(shape: lily_kvq_shape, n_query: int = 0, device="cuda") -> torch.Tensor:
+    """Workspace of the lily_kvq_* calls; n_query: the most query tokens of a
+    lily_kvq_attn_prefill call (0: none)."""
+    n = lily_kvq_workspace_bytes(shape, n_query)
+    if n == 0:
+        raise ValueError("unsupported quantised-cache shape")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _on_current_device(name: str, t) -> None:
+    """The library launches on the current device: a tensor elsewhere is refused."""
+    if not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _dense(name: str, t, dtype, shape: tuple) -> int:
+    """Address of a dense CUDA tensor of this dtype and at least this shape's size."""
+    if t.dtype != dtype or t.numel() < math.prod(shape):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    _on_current_device(name, t)
+    return _ptr(t)
+
+
+def _tokens(name: str, t, heads: int, D: int):
+    """Address and token stride of a bf16 [n][heads][D] CUDA tensor whose tokens are dense."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name}: expected bfloat16 [n][{heads}][{D}], got {t.dtype} {list(t.shape)}")
+    _on_current_device(name, t)
+    s0, s1, s2 = t.stride()
+    if (heads > 1 and s1 != D) or s2 != 1:
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * D)
+
+
+def _kvq_copy(fn: str, shape, cache, k, v, cu, starts, block_table, ws, stream, check: bool) -> int:
+    N, i32 = k.shape[0], torch.int32
+    if v.shape[0] != N:
+        raise ValueError(f"k has {N} tokens, v {v.shape[0]}")
+    pk, sk = _tokens("k", k, shape.H_kv, shape.D)
+    pv, sv = _tokens("v", v, shape.H_kv, shape.D)
+    rc = getattr(load(), fn)(ctypes.byref(shape), ctypes.byref(cache), pk, sk, pv, sv, N,
+                             _dense("cu", cu, i32, (shape.B + 1,)), _dense("starts", starts, i32, (shape.B,)),
+                             _dense("block_table", block_table, i32, (shape.B, shape.max_blocks)),
+                             _ptr(ws), ws.numel(), _stream(stream))
+    return _check(fn, rc) if check else rc
+
+
+def lily_kvq_append(shape: lily_kvq_shape, cache: lily_kvq_cache, k, v, cu_new, starts, block_table, ws, stream=None,
+                    *, check: bool = True) -> int:
+    """Quantises k and v (bf16 [N][H_kv][D], any token stride) into the cache
+    (see include/lily_moe.h)."""
+    return _kvq_copy("lily_kvq_append", shape, cache, k, v, cu_new, starts, block_table, ws, stream, check)
+
+
+def lily_kvq_read(shape: lily_kvq_shape, cache: lily_kvq_cache, k, v, cu, starts, block_table, ws, stream=None,
+                  *, check: bool = True) -> int:
+    """Reads cached tokens back into k and v (bf16 [N][H_kv][D], any token stride)."""
+    return _kvq_copy("lily_kvq_read", shape, cache, k, v, cu, starts, block_table, ws, stream, check)
+
+
+def lily_kvq_attn_decode(shape: lily_kvq_shape, cache: lily_kvq_cache, q, block_table, seq_lens, out, ws,
+                         scale: Optional[float] = None, stream=None, *, check: bool = True) -> int:
+    """Decode attention over the quantised cache (see include/lily_moe.h): q and
+    out bf16 [B][H_q][D].  scale defaults to 1/sqrt(D)."""
+    B, H, D, i32 = shape.B, shape.H_q, shape.D, torch.int32
+    pq, sq = _tokens("q", q, H, D)
+    if q.shape[0] != B:
+        raise ValueError(f"q: expected {B} sequences, got {q.shape[0]}")
+    rc = load().lily_kvq_attn_decode(ctypes.byref(shape), ctypes.byref(cache), pq, sq,
+                                     _dense("block_table", block_table, i32, (B, shape.max_blocks)),
+                                     _dense("seq_lens", seq_lens, i32, (B,)), D ** -0.5 if scale is None else scale,
+                                     _dense("out", out, torch.bfloat16, (B, H, D)), _ptr(ws), ws.numel(), _stream(stream))
+    return _check("lily_kvq_attn_decode", rc) if check else rc
+
+
+def lily_kvq_attn_prefill(shape: lily_kvq_shape, cache: lily_kvq_cache, q, cu_q, block_table, seq_lens, out, ws,
+                          scale: Optional[float] = None, stream=None, *, check: bool = True) -> int:
+    """Causal attention of a chunk of query tokens per sequence (q, out bf16
+    [N][H_q][D], rows by cu_q) over the quantised cache that already holds the
+    chunk's keys.  scale defaults to 1/sqrt(D)."""
+    B, H, D, N, i32 = shape.B, shape.H_q, shape.D, q.shape[0], torch.int32
+    pq, sq = _tokens("q", q, H, D)
+    rc = load().lily_kvq_attn_prefill(ctypes.byref(shape), ctypes.byref(cache), pq, sq, N,
+                                      _dense("cu_q", cu_q, i32, (B + 1,)),
+                                      _dense("block_table", block_table, i32, (B, shape.max_blocks)),
+                                      _dense("seq_lens", seq_lens, i32, (B,)), D ** -0.5 if scale is None else scale,
+                                      _dense("out", out, torch.bfloat16, (N, H, D)), _ptr(ws), ws.numel(),
+                                      _stream(stream))
+    return _check("lily_kvq_attn_prefill", rc) if check else rc
 
 
 # ------------------------------------------------------------------ Gated DeltaNet scan

@@ -227,6 +227,62 @@ AttnLayout attn_layout(const lily_attn_shape &s)
     return L;
 }
 
+// ------------------------------------------------------------------ quantised KV cache
+int kvq_check_shape(const lily_kvq_shape *s)
+{
+    if (!s) return LILY_ERR_INVALID;
+    if (s->B < 1 || s->H_q < 1 || s->H_kv < 1 || s->max_blocks < 1 || s->H_q % s->H_kv != 0) return LILY_ERR_INVALID;
+    if (s->bits != 4 && s->bits != 8) return LILY_ERR_UNSUPPORTED;
+    if (s->D != 64 && s->D != 128 && s->D != 256) return LILY_ERR_UNSUPPORTED;
+    if (s->block_size != 32 && s->block_size != 64 && s->block_size != 128) return LILY_ERR_UNSUPPORTED;
+    if (s->H_q / s->H_kv > kKvqMaxGroup || s->B > 65535 || s->H_kv > 4096) return LILY_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(s->max_blocks) * s->block_size >= (int64_t(1) << 31)) return LILY_ERR_UNSUPPORTED;
+    return LILY_OK;
+}
+
+struct KvqLayout {
+    size_t ctrl, total;
+};
+
+KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
+{
+    (void)s;
+    (void)n_query;
+    KvqLayout L{};
+    L.ctrl = 0;
+    L.total = align_up(sizeof(Ctrl));
+    return L;
+}
+
+int check_ptr(const void *p);
+
+int kvq_check_cache(const lily_kvq_shape &s, const lily_kvq_cache *c)
+{
+    if (!c || c->n_blocks < 1) return LILY_ERR_INVALID;
+    int rc;
+    if ((rc = check_ptr(c->k_q)) || (rc = check_ptr(c->k_sb)) || (rc = check_ptr(c->v_q)) || (rc = check_ptr(c->v_sb)))
+        return rc;
+    const int64_t per_block = static_cast<int64_t>(s.H_kv) * s.D * s.block_size * s.bits / 8;
+    if (c->n_blocks > (int64_t(1) << 40) / per_block) return LILY_ERR_UNSUPPORTED;
+    return c->code_bytes == c->n_blocks * per_block ? LILY_OK : LILY_ERR_INVALID;
+}
+
+// Token stride of a [N][heads][D] array: at least dense, every token 16-byte aligned.
+int kvq_check_stride(int64_t stride, int heads, int D)
+{
+    if (stride < static_cast<int64_t>(heads) * D || stride > (int64_t(1) << 31)) return LILY_ERR_INVALID;
+    return stride % 8 == 0 ? LILY_OK : LILY_ERR_MISALIGNED;
+}
+
+KvqCache kvq_device_cache(const lily_kvq_shape &s, const lily_kvq_cache &c)
+{
+    KvqCache d{};
+    d.k_q = c.k_q; d.v_q = c.v_q; d.k_sb = c.k_sb; d.v_sb = c.v_sb;
+    d.n_blocks = c.n_blocks;
+    d.H_kv = s.H_kv; d.groups = s.D / 64; d.bs = s.block_size; d.bits = s.bits;
+    return d;
+}
+
 template <typename P>
 P *at(void *ws, size_t off)
 {
@@ -819,6 +875,102 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
     a.out = out;
     a.ctrl = at<Ctrl>(ws, L.ctrl);
     return to_status(launch_attn_decode(a, tmK, tmV, stream), "attention launch");
+}
+
+size_t lily_kvq_workspace_bytes(const lily_kvq_shape *shape, int32_t n_query)
+{
+    if (kvq_check_shape(shape) != LILY_OK || n_query < 0) return 0;
+    return kvq_layout(*shape, n_query).total;
+}
+
+namespace {
+
+// Shared by append (write) and read: the argument checks and the launch.
+int kvq_copy(bool append, const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *k, int64_t k_stride,
+             const uint16_t *v, int64_t v_stride, int32_t N, const int32_t *cu, const int32_t *starts,
+             const int32_t *block_table, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    int rc;
+    if ((rc = kvq_check_shape(shape)) || (rc = kvq_check_cache(*shape, cache))) return rc;
+    const lily_kvq_shape s = *shape;
+    if (N < 0) return LILY_ERR_INVALID;
+    if ((rc = check_ws(ws, ws_bytes, kvq_layout(s, 0).total))) return rc;
+    if (N == 0) return LILY_OK;
+    for (const void *p : {static_cast<const void *>(k), static_cast<const void *>(v), static_cast<const void *>(cu),
+                          static_cast<const void *>(starts), static_cast<const void *>(block_table)})
+        if ((rc = check_ptr(p))) return rc;
+    if ((rc = kvq_check_stride(k_stride, s.H_kv, s.D)) || (rc = kvq_check_stride(v_stride, s.H_kv, s.D))) return rc;
+    KvqCopyArgs a{};
+    a.c = kvq_device_cache(s, *cache);
+    a.B = s.B; a.max_blocks = s.max_blocks; a.N = N;
+    a.k = const_cast<uint16_t *>(k); a.v = const_cast<uint16_t *>(v);
+    a.k_stride = k_stride; a.v_stride = v_stride;
+    a.cu = cu; a.starts = starts; a.block_table = block_table;
+    a.ctrl = at<Ctrl>(ws, 0);
+    return append ? to_status(launch_kvq_append(a, stream), "cache append launch")
+                  : to_status(launch_kvq_read(a, stream), "cache read launch");
+}
+
+// Shared by the two attention calls (cu_q is NULL for decode).
+int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
+                  bool ragged, int32_t N, const int32_t *cu_q, const int32_t *block_table, const int32_t *seq_lens,
+                  float scale, uint16_t *out, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    int rc;
+    if ((rc = kvq_check_shape(shape)) || (rc = kvq_check_cache(*shape, cache))) return rc;
+    const lily_kvq_shape s = *shape;
+    if (N < 0 || !std::isfinite(scale)) return LILY_ERR_INVALID;
+    const KvqLayout L = kvq_layout(s, ragged ? N : 0);
+    if ((rc = check_ws(ws, ws_bytes, L.total))) return rc;
+    if (N == 0) return LILY_OK;
+    for (const void *p : {static_cast<const void *>(q), static_cast<const void *>(block_table),
+                          static_cast<const void *>(seq_lens), static_cast<const void *>(out)})
+        if ((rc = check_ptr(p))) return rc;
+    if (ragged && (rc = check_ptr(cu_q))) return rc;
+    if ((rc = kvq_check_stride(q_stride, s.H_q, s.D))) return rc;
+    KvqAttnArgs a{};
+    a.c = kvq_device_cache(s, *cache);
+    a.B = s.B; a.H_q = s.H_q; a.D = s.D; a.group = s.H_q / s.H_kv; a.max_blocks = s.max_blocks; a.N = N;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.q = q; a.q_stride = q_stride;
+    a.cu_q = ragged ? cu_q : nullptr;
+    a.block_table = block_table; a.seq_lens = seq_lens;
+    a.out = out;
+    a.ctrl = at<Ctrl>(ws, L.ctrl);
+    return to_status(launch_kvq_attn(a, stream), "quantised-cache attention launch");
+}
+
+}  // namespace
+
+int lily_kvq_append(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, int32_t N, const int32_t *cu_new, const int32_t *starts,
+                    const int32_t *block_table, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    return kvq_copy(true, shape, cache, k, k_stride, v, v_stride, N, cu_new, starts, block_table, ws, ws_bytes, stream);
+}
+
+int lily_kvq_read(const lily_kvq_shape *shape, const lily_kvq_cache *cache, uint16_t *k, int64_t k_stride, uint16_t *v,
+                  int64_t v_stride, int32_t N, const int32_t *cu, const int32_t *starts, const int32_t *block_table,
+                  void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    return kvq_copy(false, shape, cache, k, k_stride, v, v_stride, N, cu, starts, block_table, ws, ws_bytes, stream);
+}
+
+int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
+                         const int32_t *block_table, const int32_t *seq_lens, float scale, uint16_t *out, void *ws,
+                         size_t ws_bytes, cudaStream_t stream)
+{
+    return kvq_attention(shape, cache, q, q_stride, false, shape ? shape->B : 0, nullptr, block_table, seq_lens, scale,
+                         out, ws, ws_bytes, stream);
+}
+
+int lily_kvq_attn_prefill(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q,
+                          int64_t q_stride, int32_t N, const int32_t *cu_q, const int32_t *block_table,
+                          const int32_t *seq_lens, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+                          cudaStream_t stream)
+{
+    return kvq_attention(shape, cache, q, q_stride, true, N, cu_q, block_table, seq_lens, scale, out, ws, ws_bytes,
+                         stream);
 }
 
 int lily_gdn_scan(const lily_gdn_shape *shape, const uint16_t *q, const uint16_t *k, const uint16_t *v,

@@ -185,6 +185,42 @@ size_t attn_smem_bytes(int D, int bs);
 // tmK / tmV: the caches as 2-D bf16 [n_blocks * H_kv * bs][D], box 64 x bs, 128-byte swizzle.
 cudaError_t launch_attn_decode(const AttnArgs &a, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t stream);
 
+// Quantised KV cache (kvq.cu): append (quantise and write) and read back.
+struct KvqCache {
+    uint8_t *k_q, *v_q;     // codes [n_blocks][H_kv][D/64][bs][64 bits / 8]
+    uint16_t *k_sb, *v_sb;  // scale, bias bf16 [n_blocks][H_kv][D/64][bs][2]
+    long long n_blocks;
+    int H_kv, groups, bs, bits;  // groups = D / 64
+};
+struct KvqCopyArgs {
+    KvqCache c;
+    int B, max_blocks, N;
+    uint16_t *k, *v;              // bf16 [N][H_kv][D], token strides below (read only by the append)
+    long long k_stride, v_stride;
+    const int *cu, *starts;       // [B+1], [B]
+    const int *block_table;       // [B][max_blocks]
+    Ctrl *ctrl;
+};
+cudaError_t launch_kvq_append(const KvqCopyArgs &a, cudaStream_t stream);
+cudaError_t launch_kvq_read(const KvqCopyArgs &a, cudaStream_t stream);
+
+// Attention over the quantised cache (kvq_attn.cu).
+struct KvqAttnArgs {
+    KvqCache c;
+    int B, H_q, D, group, max_blocks;
+    int N;                        // query tokens (decode: B, one per sequence)
+    float scale_log2;             // scale * log2(e)
+    const uint16_t *q;            // bf16 [N][H_q][D], token stride q_stride
+    long long q_stride;
+    const int *cu_q;              // [B+1], or NULL (decode)
+    const int *block_table;       // [B][max_blocks]
+    const int *seq_lens;          // [B]
+    uint16_t *out;                // bf16 [N][H_q][D]
+    Ctrl *ctrl;
+};
+constexpr int kKvqMaxGroup = 8;   // query heads per KV head
+cudaError_t launch_kvq_attn(const KvqAttnArgs &a, cudaStream_t stream);
+
 // Gated DeltaNet scan (gdn.cu): CTA (16-row slice of the state, value head).
 struct GdnArgs {
     int T, H_k, H_v, d_k, d_v;

@@ -307,6 +307,119 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
                      cudaStream_t stream);
 
 /*
+ * Quantised KV cache: the fixed-block cache of the full-attention layers held
+ * in 4- or 8-bit codes, the calls that write it and read it back, and the
+ * attention over it.
+ *
+ * Method: the page "Perplexity libera o Lily" (noticiai.com.br), section "O
+ * modelo em tres formatos de carga" (grouped-query attention, a growing KV
+ * cache) and section "Prefill e decode: onde estao os ganhos" (4-bit
+ * group-of-64 affine values rebuilt inside the kernel, a fixed-block cache
+ * layout, packed query heads).  The page keeps its cache in bf16; this is the
+ * weights' affine format applied to the cache.
+ *
+ * Format.  The 64 channels [64 c, 64 c + 64) of one token and one KV head are a
+ * group.  With lo and hi the smallest and largest of the group's bf16 values x
+ * and L = 2^bits - 1:
+ *   scale = bf16((hi - lo) / L), 0 if that is below 2^-126;   bias = lo
+ *   code  = min(rint((x - lo) / scale), L)   (0 where scale is 0)
+ *   value = code * scale + bias
+ * with fp32 arithmetic, round-to-nearest-even.  |value - x| is at most about
+ * scale / 2; a group of equal values is kept exactly.
+ *
+ * Layout of K and of V (device, row-major, every array 16-byte aligned):
+ *   codes      uint8 [n_blocks][H_kv][D/64][block_size][64 * bits / 8]; 4 bits:
+ *              byte j holds channel 2j in its LOW nibble, 2j + 1 in its HIGH one
+ *   parameters bf16  [n_blocks][H_kv][D/64][block_size][2]: scale, bias
+ * (36 bytes per 64 values at 4 bits, 68 at 8, against 128 in bf16.)
+ * A sequence's token t is row t % block_size of block block_table[b][t / block_size].
+ *
+ * Supported: bits in {4, 8}; D in {64, 128, 256}; block_size in {32, 64, 128};
+ * H_q % H_kv == 0 and H_q / H_kv <= 8; 1 <= B <= 65535; H_kv <= 4096;
+ * max_blocks * block_size < 2^31.  Byte offsets are 64-bit.
+ * Device-detected (read with lily_moe_device_status on the workspace that the
+ * call was given): a used table entry outside [0, n_blocks) or a position or
+ * length outside [0, max_blocks * block_size] records LILY_ERR_DEVICE_INDEX.
+ * lily_kvq_append and lily_kvq_read then leave that token's row alone; the
+ * attention reads block 0 / clamps the length instead.
+ * Every call is bit-reproducible from run to run.
+ */
+typedef struct lily_kvq_shape {
+    int32_t B;           /* sequences */
+    int32_t H_q, H_kv;   /* query heads, KV heads */
+    int32_t D;           /* head dimension */
+    int32_t block_size;  /* tokens per cache block */
+    int32_t max_blocks;  /* columns of block_table */
+    int32_t bits;        /* bits per code: 4 or 8 */
+} lily_kvq_shape;
+
+typedef struct lily_kvq_cache {
+    uint8_t *k_q;        /* codes of K */
+    uint16_t *k_sb;      /* scale and bias of K */
+    uint8_t *v_q;
+    uint16_t *v_sb;
+    int64_t n_blocks;    /* blocks in each of the four arrays */
+    int64_t code_bytes;  /* bytes of k_q, and of v_q: n_blocks * H_kv * D * block_size * bits / 8 */
+} lily_kvq_cache;
+
+/*
+ * Workspace bytes of the lily_kvq_* calls for this shape (0: unsupported), with
+ * n_query the most query tokens of a lily_kvq_attn_prefill call (0: none).
+ */
+size_t lily_kvq_workspace_bytes(const lily_kvq_shape *shape, int32_t n_query);
+
+/*
+ * Quantises new keys and values as they are written into the cache.
+ *   k, v        bf16 [N][H_kv][D] device; token n starts n * k_stride (v_stride)
+ *               elements after the first: at least H_kv * D, a multiple of 8
+ *               (so k and v may be slices of a fused projection's output)
+ *   cu_new      int32 [B+1] device, ascending from 0: the tokens of sequence b
+ *               are rows [cu_new[b], cu_new[b+1]); rows from cu_new[B] on are
+ *               padding, neither read nor written
+ *   starts      int32 [B] device: position of each sequence's first new token
+ * No two tokens of a call may go to the same cache row.  N = 0 enqueues nothing.
+ */
+int lily_kvq_append(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, int32_t N, const int32_t *cu_new, const int32_t *starts,
+                    const int32_t *block_table, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Reads tokens back: positions [starts[b], starts[b] + cu[b+1] - cu[b]) of each
+ * sequence into rows [cu[b], cu[b+1]) of k and v, bf16 [N][H_kv][D] with the
+ * strides of lily_kvq_append; each value is rounded to bf16 once.  Rows from
+ * cu[B] on are left as they were.
+ */
+int lily_kvq_read(const lily_kvq_shape *shape, const lily_kvq_cache *cache, uint16_t *k, int64_t k_stride, uint16_t *v,
+                  int64_t v_stride, int32_t N, const int32_t *cu, const int32_t *starts, const int32_t *block_table,
+                  void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Decode attention over the quantised cache: lily_attn_decode's operation, one
+ * query token per sequence, on the values that the codes stand for:
+ *   out[b][h] = sum_{t < seq_lens[b]} softmax_t(scale * q[b][h] . K_g[t]) V_g[t].
+ *   q     bf16 [B][H_q][D], sequence b q_stride elements after the first (at
+ *         least H_q * D, a multiple of 8)
+ *   out   bf16 [B][H_q][D] dense; a sequence with no tokens gets zeros
+ * Cache rows at or past seq_lens[b] are not used, whatever they hold.
+ */
+int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
+                         const int32_t *block_table, const int32_t *seq_lens, float scale, uint16_t *out, void *ws,
+                         size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * The same for a chunk of query tokens per sequence (a prompt, a piece of one,
+ * draft tokens), causal: seq_lens[b] counts the chunk's own tokens, which are
+ * already in the cache, and query i of the m = cu_q[b+1] - cu_q[b] of sequence b
+ * attends to the positions <= seq_lens[b] - m + i.  A query with none gets zeros.
+ *   q     bf16 [N][H_q][D] (q_stride as above), rows by cu_q int32 [B+1]
+ *   out   bf16 [N][H_q][D] dense; rows from cu_q[B] on are left as they were
+ */
+int lily_kvq_attn_prefill(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q,
+                          int64_t q_stride, int32_t N, const int32_t *cu_q, const int32_t *block_table,
+                          const int32_t *seq_lens, float scale, uint16_t *out, void *ws, size_t ws_bytes,
+                          cudaStream_t stream);
+
+/*
  * Gated DeltaNet scan: the fixed-size recurrence of the model's linear-attention
  * layers over T tokens of one sequence, the state kept in registers.
  *
