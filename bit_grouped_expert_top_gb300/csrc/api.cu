@@ -240,17 +240,27 @@ int kvq_check_shape(const lily_kvq_shape *s)
     return LILY_OK;
 }
 
+// Workspace: control block, then the decode kernel's partial results.
 struct KvqLayout {
-    size_t ctrl, total;
+    size_t ctrl, meta, ends_here, part_ml, part_acc, total;
 };
 
 KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
 {
-    (void)s;
     (void)n_query;
     KvqLayout L{};
-    L.ctrl = 0;
-    L.total = align_up(sizeof(Ctrl));
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes);
+        return at;
+    };
+    L.ctrl = take(sizeof(Ctrl));
+    L.meta = take(kKvqDecodeCtas * sizeof(int4));
+    L.ends_here = take(kKvqDecodeCtas * sizeof(int));
+    L.part_ml = take(2 * kKvqDecodeCtas * kKvqMaxGroup * 2 * sizeof(float));
+    L.part_acc = take(2 * kKvqDecodeCtas * kKvqMaxGroup * static_cast<size_t>(s.D) * sizeof(float));
+    L.total = off;
     return L;
 }
 
@@ -937,7 +947,12 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     a.block_table = block_table; a.seq_lens = seq_lens;
     a.out = out;
     a.ctrl = at<Ctrl>(ws, L.ctrl);
-    return to_status(launch_kvq_attn(a, stream), "quantised-cache attention launch");
+    a.meta = at<int4>(ws, L.meta);
+    a.ends_here = at<int>(ws, L.ends_here);
+    a.part_ml = at<float>(ws, L.part_ml);
+    a.part_acc = at<float>(ws, L.part_acc);
+    return to_status(ragged ? launch_kvq_prefill(a, stream) : launch_kvq_decode(a, stream),
+                     "quantised-cache attention launch");
 }
 
 }  // namespace

@@ -1,0 +1,732 @@
+// Decode attention over the quantised KV cache (one query token per sequence),
+// for sm_103a: with g = h / (H_q / H_kv),
+//   o_h = sum_{t < L} softmax_t(scale q_h . k_{g,t}) v_{g,t},
+//   k_{t,d} = ck_{t,d} sk_{t,c} + bk_{t,c},  v likewise,  c = d / 64.
+//
+// Mathematics.  The codes themselves are the matrix operands, the affine part
+// stays in fp32:
+//   q . k_t  = sum_c ( sk_{t,c} sum_{d in c} q_d ck_{t,d}  +  bk_{t,c} sum_{d in c} q_d )
+//   o_d      = sum_t (p_t sv_{t,c}) cv_{t,d}  +  sum_t p_t bv_{t,c}
+// so no value is ever rebuilt, and nothing of K or V is rounded.  A code needs
+// no conversion either: its bits at the bottom of a 16-bit word are the fp16
+// subnormal c 2^-24 (at bits 4..7: c 2^-20), which the tensor cores multiply
+// exactly; eight codes of 4 bits become four operand registers with one shift and
+// four ANDs.  The factors 2^-24 / 2^-20 are undone in fp32.
+// q is scaled per head by a power of two into fp16 (2^14..2^15 at its largest
+// value, so a value keeps its 8 bits down to 2^-24 of that).  The weights
+// p_t sv_{t,c} are rounded to fp16 (2^-11 relative) after a power of two f that
+// keeps the largest scale seen at 16..128: f follows the data as the running
+// maximum of the softmax does, so the cache's values have no range limit.  p is
+// taken against a running maximum that moves only when a score passes it by 8 (in
+// powers of two), which one vote per 32 tokens finds; sums are fp32.
+//
+// Bound: the cache's bytes (36 per 64 values at 4 bits).  Work split: the cache
+// blocks of all (sequence, KV head) segments form one list that the CTAs (one per
+// SM) share evenly, so a batch of unlike lengths leaves no SM idle; a segment cut
+// between CTAs leaves partials that a second kernel joins.  With no more than
+// kWholeTokens tokens a sequence can hold, each segment is one CTA and there is one
+// launch.
+// Inside a CTA:
+//   warp 8      producer: one bulk copy per block for each of the K and V codes
+//               and parameters (contiguous in the cache's layout) into a ring of
+//               shared-memory stages;
+//   warps 0..7  consumers, 32 tokens at a time each on its own, with their own
+//               running maximum, sum and output: no barrier until the segment
+//               ends, where the warps' results are joined through shared memory.
+//               S^T = K q^T and O^T += V^T P on mma.sync m16n8k16 (fp16 in, fp32
+//               out), the query heads of the KV head on the N = 8 side.  The order
+//               of channels inside a matrix step is free, so each lane takes the
+//               16 channels that one load gives it; P moves from the accumulator
+//               layout to the operand layout by movmatrix.
+// Every mbarrier wait is bounded; a wait that gives up records
+// LILY_ERR_DEVICE_TIMEOUT, and the producer waits for its copies before it exits.
+#include <cmath>
+#include <cstdint>
+
+#include "lily_device.cuh"
+#include "lily_internal.h"
+
+namespace lily {
+namespace {
+
+constexpr int kNW = 8;                        // consumer warps
+constexpr int kThreads = (kNW + 1) * 32;      // + the producer
+constexpr int kMaxStages = 16;
+constexpr int kUnit = 32;                     // tokens a warp takes at a time
+constexpr int kSmemLimit = 208 * 1024;        // leaves room for the join kernel's early CTAs
+constexpr int kBarConsumers = 1;
+constexpr float kNoMax = -1.7e38f;            // running maximum before any token (finite: -inf - kNoMax = -inf)
+
+struct Fixed {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int abort, b0;
+    long long pre, sum[kThreads / 32];
+    float ml[kNW][8][2];
+};
+constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
+
+__host__ __device__ constexpr int merge_bytes(int D) { return kNW * 8 * (D + 8) * 4; }
+constexpr int stage_bytes(int D, int bs, int bits) { return 2 * (bs * D * bits / 8 + bs * (D / 64) * 4); }
+int stages_for(int D, int bs, int bits)
+{
+    const int n = (kSmemLimit - 128 - kFixed - merge_bytes(D)) / stage_bytes(D, bs, bits);
+    return n < kMaxStages ? n : kMaxStages;
+}
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+// d += a b: m16n8k16, fp16 inputs, fp32 accumulators
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Channel, within the 16 that lane t of a group holds, of slot r (low and high half
+// of the first, of the second operand register) of K step j.
+template <int BITS>
+__device__ __forceinline__ constexpr int k_channel(int j, int r)
+{
+    return BITS == 4 ? 8 * (j >> 1) + (j & 1) + (r == 0 ? 0 : r == 1 ? 4 : r == 2 ? 2 : 6)
+                     : 4 * j + (r == 0 ? 0 : r == 1 ? 2 : r == 2 ? 1 : 3);
+}
+// A token of the cache row that operand row / column k (0..7) of an 8-token half
+// stands for: lanes t = 0..3 of one V load then read four consecutive rows.
+__device__ __forceinline__ int token_of(int k) { return (k >> 1) | ((k & 1) << 2); }
+
+__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int b)
+{
+    int L = a.seq_lens[b];
+    const int cap = a.max_blocks * a.c.bs;
+    if (L < 0 || L > cap) {
+        record_error(&a.ctrl->status, kErrDeviceIndex);
+        L = L < 0 ? 0 : cap;
+    }
+    return L;
+}
+// Cache blocks of a sequence in the work list (an empty one still has its zeros to write).
+__device__ __forceinline__ int blocks_of(int L, int bs) { return L > 0 ? (L + bs - 1) / bs : 1; }
+
+// This CTA's share of the work list: segments from (b, g, block j0) on, `left` blocks in all.
+struct Walk {
+    int b, g, j0, L, next_L;
+    long long left;
+};
+
+__device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
+{
+    Walk w{};
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    if (a.whole) {
+        w.b = c / a.c.H_kv;
+        w.g = c % a.c.H_kv;
+        w.L = length_of(a, w.b);
+        w.left = blocks_of(w.L, a.c.bs);
+        return w;
+    }
+    auto chunk = [&](int b) { return b < a.B ? static_cast<long long>(blocks_of(length_of(a, b), a.c.bs)) : 0LL; };
+    long long v = 0;
+    for (int b = tid; b < a.B; b += kThreads) v += chunk(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) F.sum[warp] = v;
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < kThreads / 32; ++i) total += F.sum[i];
+    total *= a.c.H_kv;
+    // no more CTAs than blocks: every CTA between a segment's first and last has a part of it
+    const long long used = min(total, static_cast<long long>(gridDim.x));
+    if (c >= used) return w;
+    const long long begin = total * c / used, end = total * (c + 1) / used;
+    w.left = end - begin;
+    // the sequence that `begin` falls into: a scan over the lengths, kThreads at a time
+    long long pre = 0;
+    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+        const long long n = chunk(s0 + tid) * a.c.H_kv;
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) F.sum[warp] = inc;
+        __syncthreads();
+        long long before = pre, all = pre;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += F.sum[i];
+            all += F.sum[i];
+        }
+        const long long lo = before + inc - n;
+        if (begin >= lo && begin < lo + n) {
+            F.b0 = s0 + tid;
+            F.pre = lo;
+        }
+        pre = all;
+        if (begin < all) break;
+    }
+    __syncthreads();
+    w.b = F.b0;
+    w.L = length_of(a, w.b);
+    const int nblk = blocks_of(w.L, a.c.bs);
+    w.g = static_cast<int>((begin - F.pre) / nblk);
+    w.j0 = static_cast<int>((begin - F.pre) % nblk);
+    return w;
+}
+
+// The next segment (after `done` blocks of this one).
+__device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done)
+{
+    w.left -= done;
+    w.j0 = 0;
+    if (++w.g == a.c.H_kv) {
+        w.g = 0;
+        ++w.b;
+        if (w.left > 0) w.L = length_of(a, w.b);
+    }
+}
+
+template <int BITS, int GR>
+__global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
+{
+    constexpr int D = GR * 64, GB = 8 * BITS;  // bytes of a group's codes in one row
+    extern __shared__ uint8_t dsm_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~uintptr_t(127));
+    Fixed &F = *reinterpret_cast<Fixed *>(base);
+    float *merge = reinterpret_cast<float *>(base + kFixed);  // [warp][head][D + 8]
+    uint8_t *ring = base + kFixed + merge_bytes(D);
+    const int bs = a.c.bs, NS = a.stages, G = a.group;
+    const int CB = GR * bs * GB, PB = GR * bs * 4, SB = 2 * (CB + PB);  // codes, parameters, stage
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, t = lane & 3;
+    int *status = &a.ctrl->status;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&F.full[i], 1);
+            mbar_init(&F.empty[i], bs / kUnit);
+        }
+        F.abort = 0;
+        fence_mbar_init();
+    }
+    pdl_trigger();
+    pdl_wait();
+    __syncthreads();
+    Walk w = first_segment(a, F);
+
+    if (warp == kNW) {
+        // ------------------------------------------------ producer
+        int issued = 0;
+        bool ok = true;
+        while (w.left > 0 && ok) {
+            const int nblk = blocks_of(w.L, bs), n = static_cast<int>(min(static_cast<long long>(nblk - w.j0), w.left));
+            for (int i0 = 0; i0 < n && ok; i0 += 32) {
+                int pb = 0;
+                if (i0 + lane < n && w.L > 0) {
+                    pb = a.block_table[static_cast<size_t>(w.b) * a.max_blocks + w.j0 + i0 + lane];
+                    if (pb < 0 || pb >= a.c.n_blocks) {
+                        record_error(status, kErrDeviceIndex);
+                        pb = 0;
+                    }
+                }
+                for (int i = i0; i < min(n, i0 + 32); ++i) {
+                    const int slot = issued % NS;
+                    if (issued >= NS && !mbar_wait(&F.empty[slot], ((issued / NS) - 1) & 1, &F.abort, status)) ok = false;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const long long blk = __shfl_sync(0xffffffffu, pb, i - i0);
+                    const long long row0 = (blk * a.c.H_kv + w.g) * GR * bs;
+                    uint8_t *dst = ring + static_cast<size_t>(slot) * SB;
+                    if (lane == 0) mbar_arrive_expect_tx(&F.full[slot], static_cast<uint32_t>(SB));
+                    __syncwarp();
+                    if (lane == 0) bulk_load(dst, a.c.k_q + row0 * GB, CB, &F.full[slot]);
+                    if (lane == 1) bulk_load(dst + CB, a.c.k_sb + row0 * 2, PB, &F.full[slot]);
+                    if (lane == 2) bulk_load(dst + CB + PB, a.c.v_q + row0 * GB, CB, &F.full[slot]);
+                    if (lane == 3) bulk_load(dst + 2 * CB + PB, a.c.v_sb + row0 * 2, PB, &F.full[slot]);
+                    ++issued;
+                }
+            }
+            advance(a, w, n);
+        }
+        // no copy into this CTA's shared memory may still be in flight at exit
+        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) {
+            const uint32_t addr = smem_u32(&F.full[i % NS]);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(addr, (i / NS) & 1))
+                if (global_timer_ns() - t0 > LILY_DRAIN_LIMIT_NS) {
+                    record_error(status, kErrDeviceTimeout);
+                    break;
+                }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    if (!a.whole && threadIdx.x == 0 && !a.key_by_segment) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    const int ups = bs / kUnit;  // units per stage
+    int unit = 0, stage0 = 0;    // units and stages of the segments before this one
+    bool ok = true;
+    while (w.left > 0) {
+        const int nblk = blocks_of(w.L, bs), n = static_cast<int>(min(static_cast<long long>(nblk - w.j0), w.left));
+        const int tok0 = w.j0 * bs;
+
+        // ---- q: per head a power of two into fp16, the operand registers of the K steps, sums per group
+        uint32_t qb[GR * 4][2];
+        float qsum[GR][2], mul[2];
+        {
+            const uint16_t *qh = a.q + w.b * a.q_stride + static_cast<long long>(w.g * G + (gi < G ? gi : 0)) * D;
+            float qv[GR][16], big = 0.0f;
+#pragma unroll
+            for (int c = 0; c < GR; ++c) {
+                uint4 x[2];
+                x[0] = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16);
+                x[1] = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16 + 8);
+                const uint32_t xs[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    qv[c][2 * i] = gi < G ? lo_bf16(xs[i]) : 0.0f;
+                    qv[c][2 * i + 1] = gi < G ? hi_bf16(xs[i]) : 0.0f;
+                    big = fmaxf(big, fmaxf(fabsf(qv[c][2 * i]), fabsf(qv[c][2 * i + 1])));
+                }
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            const int e = big > 0.0f ? 14 - ilogbf(big) : 0;
+#pragma unroll
+            for (int c = 0; c < GR; ++c) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    qv[c][i] = scalbnf(qv[c][i], e);
+                    s += qv[c][i];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float odd = BITS == 4 && (j & 1) ? 0.0625f : 1.0f;  // those codes carry 2^-20
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        qb[c * 4 + j][r] = pack_f16(qv[c][k_channel<BITS>(j, 2 * r)] * odd, qv[c][k_channel<BITS>(j, 2 * r + 1)] * odd);
+                }
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                qsum[c][0] = __shfl_sync(0xffffffffu, s, 8 * t) * 0x1p-24f;      // heads 2t and 2t + 1
+                qsum[c][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4) * 0x1p-24f;
+            }
+            const float m = scalbnf(a.scale_log2 * 0x1p24f, -e);
+            mul[0] = __shfl_sync(0xffffffffu, m, 8 * t);
+            mul[1] = __shfl_sync(0xffffffffu, m, 8 * t + 4);
+        }
+        float acc[GR][4][4], bsum[GR][2], m_run[2] = {kNoMax, kNoMax}, l_run[2] = {0.0f, 0.0f}, f = 0x1p127f;
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+            bsum[c][0] = bsum[c][1] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[c][m][x] = 0.0f;
+        }
+
+        const int units = n * ups;
+        for (int u = (warp - unit % kNW + kNW) % kNW; u < units; u += kNW) {
+            const int st = stage0 + u / ups, slot = st % NS, r0 = (u % ups) * kUnit;
+            ok = ok && mbar_wait(&F.full[slot], (st / NS) & 1, &F.abort, status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint8_t *kq = ring + static_cast<size_t>(slot) * SB, *kp = kq + CB, *vq = kp + PB, *vp = vq + CB;
+            const int left = w.L - (tok0 + u * kUnit);  // tokens of this unit that exist (may be <= 0, or more than 32)
+            const int row = r0 + token_of(gi);          // + 16 i + 8 h: this lane's token rows of S^T
+
+            // ---- scores: sc[i][2h + x], tokens row + 16 i + 8 h, heads 2t + x
+            float sc[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < GR; ++c) {
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t k0[BITS / 2], k1[BITS / 2];
+                    const uint8_t *p0 = kq + (c * bs + row + 16 * i) * GB + t * (GB / 4), *p1 = p0 + 8 * GB;
+                    if (BITS == 4) {
+                        const uint2 x0 = *reinterpret_cast<const uint2 *>(p0), x1 = *reinterpret_cast<const uint2 *>(p1);
+                        k0[0] = x0.x; k0[1] = x0.y; k1[0] = x1.x; k1[1] = x1.y;
+                    } else {
+                        const uint4 x0 = *reinterpret_cast<const uint4 *>(p0), x1 = *reinterpret_cast<const uint4 *>(p1);
+                        k0[0] = x0.x; k0[1] = x0.y; k0[2 % (BITS / 2)] = x0.z; k0[3 % (BITS / 2)] = x0.w;
+                        k1[0] = x1.x; k1[1] = x1.y; k1[2 % (BITS / 2)] = x1.z; k1[3 % (BITS / 2)] = x1.w;
+                    }
+#pragma unroll
+                    for (int x = 0; x < BITS / 2; ++x) {
+                        const uint32_t h0 = k0[x] >> 8, h1 = k1[x] >> 8;
+                        if (BITS == 4) {
+                            mma_f16(d, k0[x] & 0x000F000Fu, k1[x] & 0x000F000Fu, h0 & 0x000F000Fu, h1 & 0x000F000Fu,
+                                    qb[c * 4 + 2 * (x & 1)][0], qb[c * 4 + 2 * (x & 1)][1]);
+                            mma_f16(d, k0[x] & 0x00F000F0u, k1[x] & 0x00F000F0u, h0 & 0x00F000F0u, h1 & 0x00F000F0u,
+                                    qb[c * 4 + 2 * (x & 1) + 1][0], qb[c * 4 + 2 * (x & 1) + 1][1]);
+                        } else {
+                            mma_f16(d, k0[x] & 0x00FF00FFu, k1[x] & 0x00FF00FFu, h0 & 0x00FF00FFu, h1 & 0x00FF00FFu,
+                                    qb[c * 4 + x][0], qb[c * 4 + x][1]);
+                        }
+                    }
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i) * 4);
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i + 8) * 4);
+                    const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
+                    sc[i][0] = fmaf(b0, qsum[c][0], fmaf(s0, d[0], sc[i][0]));
+                    sc[i][1] = fmaf(b0, qsum[c][1], fmaf(s0, d[1], sc[i][1]));
+                    sc[i][2] = fmaf(b1, qsum[c][0], fmaf(s1, d[2], sc[i][2]));
+                    sc[i][3] = fmaf(b1, qsum[c][1], fmaf(s1, d[3], sc[i][3]));
+                }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sc[i][x] *= mul[x & 1];
+            }
+            uint32_t vw[2][GR][2];  // scale, bias of V: tokens row + 16 i + 8 h
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < GR; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        vw[i][c][h] = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
+            if (left < kUnit) {
+                // rows behind the sequence: no weight, whatever they hold
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (token_of(gi) + 16 * i + 8 * h >= left) {
+                            sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < GR; ++c) vw[i][c][h] = 0u;
+                        }
+            }
+
+            // ---- running maximum, and the power of two of the value scales: both move rarely
+            const float top0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+            const float top1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
+            float smax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(vw[i][c][0])), fabsf(lo_bf16(vw[i][c][1]))));
+            const bool grew = top0 > m_run[0] + 8.0f || top1 > m_run[1] + 8.0f;
+            if (__any_sync(0xffffffffu, grew || smax * f > 128.0f)) {
+                float mn0 = top0, mn1 = top1;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    mn0 = fmaxf(mn0, __shfl_xor_sync(0xffffffffu, mn0, o));
+                    mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
+                }
+                mn0 = fmaxf(mn0, m_run[0]);
+                mn1 = fmaxf(mn1, m_run[1]);
+                const float al0 = ex2(m_run[0] - mn0), al1 = ex2(m_run[1] - mn1);
+                m_run[0] = mn0;
+                m_run[1] = mn1;
+                l_run[0] *= al0;
+                l_run[1] *= al1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+                float r1 = 1.0f, r2 = 1.0f;
+                if (smax * f > 128.0f) {  // f smax back into [16, 32)
+                    const int ex = min(max(258 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 254);
+                    r2 = 1.0f / f;
+                    f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+                    r1 = f;
+                }
+#pragma unroll
+                for (int c = 0; c < GR; ++c) {
+                    bsum[c][0] *= al0;
+                    bsum[c][1] *= al1;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        acc[c][m][0] = acc[c][m][0] * al0 * r2 * r1;
+                        acc[c][m][1] = acc[c][m][1] * al1 * r2 * r1;
+                        acc[c][m][2] = acc[c][m][2] * al0 * r2 * r1;
+                        acc[c][m][3] = acc[c][m][3] * al1 * r2 * r1;
+                    }
+                }
+            }
+
+            // ---- O^T += V^T P: weights p s f in fp16, tokens on K
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float p[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) p[x] = ex2(sc[i][x] - m_run[x & 1]);
+                l_run[0] += p[0] + p[2];
+                l_run[1] += p[1] + p[3];
+                const float pf[4] = {p[0] * f, p[1] * f, p[2] * f, p[3] * f};
+#pragma unroll
+                for (int c = 0; c < GR; ++c) {
+                    const float s0 = lo_bf16(vw[i][c][0]), b0 = hi_bf16(vw[i][c][0]);
+                    const float s1 = lo_bf16(vw[i][c][1]), b1 = hi_bf16(vw[i][c][1]);
+                    bsum[c][0] = fmaf(p[0], b0, fmaf(p[2], b1, bsum[c][0]));
+                    bsum[c][1] = fmaf(p[1], b0, fmaf(p[3], b1, bsum[c][1]));
+                    const uint32_t y0 = transpose8x8(pack_f16(pf[0] * s0, pf[1] * s0));
+                    const uint32_t y1 = transpose8x8(pack_f16(pf[2] * s1, pf[3] * s1));
+                    // lane: channels 8 gi .. 8 gi + 7 of the group, tokens t, t + 4, t + 8, t + 12
+                    const uint8_t *pv = vq + (c * bs + r0 + 16 * i + t) * GB + gi * BITS;
+                    uint32_t v[4][2];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (BITS == 4) {
+                            v[r][0] = *reinterpret_cast<const uint32_t *>(pv + 4 * r * GB);
+                        } else {
+                            const uint2 x2 = *reinterpret_cast<const uint2 *>(pv + 4 * r * GB);
+                            v[r][0] = x2.x;
+                            v[r][1] = x2.y;
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < BITS / 4; ++x) {
+                        const uint32_t za = __byte_perm(v[0][x], v[1][x], 0x5410), zb = __byte_perm(v[2][x], v[3][x], 0x5410);
+                        const uint32_t ya = __byte_perm(v[0][x], v[1][x], 0x7632), yb = __byte_perm(v[2][x], v[3][x], 0x7632);
+                        const uint32_t za8 = za >> 8, zb8 = zb >> 8, ya8 = ya >> 8, yb8 = yb >> 8;
+                        if (BITS == 4) {  // channels (0, 2), (1, 3), (4, 6), (5, 7)
+                            mma_f16(acc[c][0], za & 0x000F000Fu, za8 & 0x000F000Fu, zb & 0x000F000Fu, zb8 & 0x000F000Fu, y0, y1);
+                            mma_f16(acc[c][1], za & 0x00F000F0u, za8 & 0x00F000F0u, zb & 0x00F000F0u, zb8 & 0x00F000F0u, y0, y1);
+                            mma_f16(acc[c][2], ya & 0x000F000Fu, ya8 & 0x000F000Fu, yb & 0x000F000Fu, yb8 & 0x000F000Fu, y0, y1);
+                            mma_f16(acc[c][3], ya & 0x00F000F0u, ya8 & 0x00F000F0u, yb & 0x00F000F0u, yb8 & 0x00F000F0u, y0, y1);
+                        } else {          // channels (4x, 4x + 2), (4x + 1, 4x + 3)
+                            mma_f16(acc[c][2 * x], za & 0x00FF00FFu, ya & 0x00FF00FFu, zb & 0x00FF00FFu, yb & 0x00FF00FFu, y0, y1);
+                            mma_f16(acc[c][2 * x + 1], za8 & 0x00FF00FFu, ya8 & 0x00FF00FFu, zb8 & 0x00FF00FFu, yb8 & 0x00FF00FFu, y0, y1);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&F.empty[slot]);
+        }
+
+        // ---- the segment's end: this warp's sums over its lanes, then the warps through shared memory
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                l_run[x] += __shfl_xor_sync(0xffffffffu, l_run[x], o);
+#pragma unroll
+                for (int c = 0; c < GR; ++c) bsum[c][x] += __shfl_xor_sync(0xffffffffu, bsum[c][x], o);
+            }
+        }
+        const float rf = 1.0f / f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float *dst = merge + (warp * 8 + 2 * t + x) * (D + 8) + gi * 8;
+#pragma unroll
+            for (int c = 0; c < GR; ++c) {
+                auto out = [&](int m, int h) {
+                    const float unit_scale = BITS == 4 && (m & 1) ? 0x1p20f : 0x1p24f;
+                    return fmaf(acc[c][m][2 * h + x] * unit_scale, rf, bsum[c][x]);
+                };
+                *reinterpret_cast<float4 *>(dst + c * 64) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
+                *reinterpret_cast<float4 *>(dst + c * 64 + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));
+            }
+            if (gi == 0) {
+                F.ml[warp][2 * t + x][0] = m_run[x];
+                F.ml[warp][2 * t + x][1] = l_run[x];
+            }
+        }
+        named_barrier_sync(kBarConsumers, kNW * 32);
+        const bool starts = w.j0 == 0, ends = w.j0 + n == nblk;
+        const int part = 2 * blockIdx.x + (starts ? 1 : 0), active = min(units, kNW);
+        for (int i = threadIdx.x; i < 8 * (D / 4); i += kNW * 32) {
+            const int h = i / (D / 4), d4 = i % (D / 4);
+            float M = kNoMax;
+            for (int j = 0; j < active; ++j) M = fmaxf(M, F.ml[(unit + j) % kNW][h][0]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float den = 0.0f;
+            for (int j = 0; j < active; ++j) {
+                const int wj = (unit + j) % kNW;
+                const float e = ex2(F.ml[wj][h][0] - M);
+                const float4 x = *reinterpret_cast<const float4 *>(merge + (wj * 8 + h) * (D + 8) + d4 * 4);
+                den = fmaf(e, F.ml[wj][h][1], den);
+                o.x = fmaf(e, x.x, o.x);
+                o.y = fmaf(e, x.y, o.y);
+                o.z = fmaf(e, x.z, o.z);
+                o.w = fmaf(e, x.w, o.w);
+            }
+            if (starts && ends) {
+                if (h < G) {
+                    const float r = den > 0.0f ? 1.0f / den : 0.0f;
+                    uint2 y;
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
+                    y.x = *reinterpret_cast<const uint32_t *>(&lo);
+                    y.y = *reinterpret_cast<const uint32_t *>(&hi);
+                    reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(w.b) * a.H_q + w.g * G + h) * D)[d4] = y;
+                }
+            } else {
+                reinterpret_cast<float4 *>(a.part_acc + (static_cast<size_t>(part) * 8 + h) * D)[d4] = o;
+                if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * 8 + h) * 2) = make_float2(M, den);
+            }
+        }
+        if (!a.whole && threadIdx.x == 0 && starts && (!ends || a.key_by_segment)) {
+            // who joins the parts: the last CTA is the one that holds the segment's last block
+            const int bg = w.b * a.c.H_kv + w.g;
+            a.meta[a.key_by_segment ? bg : blockIdx.x] = make_int4(ends ? -1 : bg, blockIdx.x, nblk, 0);
+        }
+        if (!a.whole && threadIdx.x == 0 && !starts) a.ends_here[blockIdx.x] = ends ? 1 : 0;
+        unit += units;
+        stage0 += n;
+        advance(a, w, n);
+        named_barrier_sync(kBarConsumers, kNW * 32);
+    }
+}
+
+// Joins the parts of a segment that was cut: CTA (segment key x head, 64-wide slice
+// of D), 256 threads: thread (e, sg) takes float4 column e and parts sg, sg + 16, ..
+// with a running maximum of its own, then the 16 groups agree on the common one and
+// are added in a fixed order.  Parts of CTA c0 (the one the segment starts in) are in
+// slot 2 c0 + 1, those of the following CTAs c in slot 2 c, up to the CTA it ends in.
+__global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant__ KvqAttnArgs a, int n_ctas)
+{
+    constexpr int kCols = 16, kGroups = 16, kBatch = 8;
+    __shared__ float4 part[kGroups][kCols];
+    __shared__ float red_max[8], red_den[8];
+    __shared__ int s_end;
+    const int key = blockIdx.x / a.group, h = blockIdx.x % a.group;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int e = tid % kCols, sg = tid / kCols;
+    pdl_trigger();
+    pdl_wait();
+    const int4 meta = a.meta[key];
+    if (meta.x < 0) return;
+    const int c0 = meta.y;
+    // the first CTA after c0 whose first segment ends in it
+    if (warp == 0) {
+        for (int c = c0 + 1; ; c += 32) {
+            const bool end = c + lane >= n_ctas || a.ends_here[c + lane] == 1;
+            const uint32_t any = __ballot_sync(0xffffffffu, end);
+            if (any) {
+                if (lane == 0) s_end = min(c + __ffs(any) - 1, n_ctas - 1);
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    const int S = s_end - c0 + 1, q = blockIdx.y * kCols + e;
+    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)); };
+    float mt = kNoMax, dt = 0.0f;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = sg; s0 < S; s0 += kBatch * kGroups) {
+        float4 v[kBatch];
+        float2 ml[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int s = s0 + k * kGroups;
+            const size_t at = s < S ? slot(s) * 8 + h : 0;
+            ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + at * 2) : make_float2(kNoMax, 0.0f);
+            v[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + at * a.D)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float bm = mt;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
+        const float c = ex2(mt - bm);
+        num.x *= c;
+        num.y *= c;
+        num.z *= c;
+        num.w *= c;
+        dt *= c;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = ex2(ml[k].x - bm);
+            num.x = fmaf(w, v[k].x, num.x);
+            num.y = fmaf(w, v[k].y, num.y);
+            num.z = fmaf(w, v[k].z, num.z);
+            num.w = fmaf(w, v[k].w, num.w);
+            dt = fmaf(w, ml[k].y, dt);
+        }
+        mt = bm;
+    }
+    float mx = mt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) red_max[warp] = mx;
+    __syncthreads();
+    mx = red_max[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) mx = fmaxf(mx, red_max[w]);
+    const float f = ex2(mt - mx);
+    part[sg][e] = make_float4(num.x * f, num.y * f, num.z * f, num.w * f);
+    float den = e == 0 ? dt * f : 0.0f;  // the threads of column 0 hold every part once
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane == 0) red_den[warp] = den;
+    __syncthreads();
+    if (tid < kCols) {
+        float4 t = part[0][tid];
+#pragma unroll
+        for (int g2 = 1; g2 < kGroups; ++g2) {
+            t.x += part[g2][tid].x;
+            t.y += part[g2][tid].y;
+            t.z += part[g2][tid].z;
+            t.w += part[g2][tid].w;
+        }
+        float dsum = red_den[0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) dsum += red_den[w];
+        const float r = dsum > 0.0f ? 1.0f / dsum : 0.0f;
+        uint2 y;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(t.x * r, t.y * r), hi = __floats2bfloat162_rn(t.z * r, t.w * r);
+        y.x = *reinterpret_cast<const uint32_t *>(&lo);
+        y.y = *reinterpret_cast<const uint32_t *>(&hi);
+        const int b = meta.x / a.c.H_kv, g = meta.x % a.c.H_kv;
+        reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(b) * a.H_q + g * a.group + h) * a.D)[q] = y;
+    }
+}
+
+template <int BITS, int GR>
+cudaError_t launch(const KvqAttnArgs &a, int ctas, size_t smem, cudaStream_t stream)
+{
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR>), static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_decode_kernel<BITS, GR>, dim3(ctas), dim3(kThreads), smem, stream, a);
+}
+
+}  // namespace
+
+// With at most this many tokens per sequence each segment is one CTA.
+constexpr long long kWholeTokens = 1024;
+
+cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
+{
+    KvqAttnArgs a = args;
+    const long long segments = static_cast<long long>(a.B) * a.c.H_kv;
+    a.whole = static_cast<long long>(a.max_blocks) * a.c.bs <= kWholeTokens;
+    a.key_by_segment = segments <= kKvqDecodeCtas;
+    a.stages = stages_for(a.D, a.c.bs, a.c.bits);
+    const size_t smem = 128 + kFixed + merge_bytes(a.D) + static_cast<size_t>(a.stages) * stage_bytes(a.D, a.c.bs, a.c.bits);
+    const int ctas = a.whole ? static_cast<int>(segments) : kKvqDecodeCtas;
+    cudaError_t e;
+    if (a.c.bits == 4)
+        e = a.D == 64 ? launch<4, 1>(a, ctas, smem, stream) : a.D == 128 ? launch<4, 2>(a, ctas, smem, stream) : launch<4, 4>(a, ctas, smem, stream);
+    else
+        e = a.D == 64 ? launch<8, 1>(a, ctas, smem, stream) : a.D == 128 ? launch<8, 2>(a, ctas, smem, stream) : launch<8, 4>(a, ctas, smem, stream);
+    if (e != cudaSuccess || a.whole) return e;
+    const int keys = a.key_by_segment ? static_cast<int>(segments) : ctas;
+    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 64), dim3(256), 0, stream, a, ctas);
+}
+
+}  // namespace lily

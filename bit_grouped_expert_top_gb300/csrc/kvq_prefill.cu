@@ -18,7 +18,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTile = 32;  // tokens per tile
 
-__global__ void __launch_bounds__(kThreads) kvq_attn_kernel(const KvqAttnArgs a)
+__global__ void __launch_bounds__(kThreads) kvq_prefill_kernel(const KvqAttnArgs a)
 {
     extern __shared__ float sm[];
     const int D = a.D, G = a.group, n = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
@@ -120,12 +120,12 @@ __global__ void __launch_bounds__(kThreads) kvq_attn_kernel(const KvqAttnArgs a)
 
 }  // namespace
 
-cudaError_t launch_kvq_attn(const KvqAttnArgs &a, cudaStream_t stream)
+cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, cudaStream_t stream)
 {
     const size_t smem = sizeof(float) * (kKvqMaxGroup * a.D + kTile * (a.D + 1) + kKvqMaxGroup * kTile + kKvqMaxGroup);
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_attn_kernel), static_cast<int>(smem));
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_attn_kernel, dim3(a.N, a.c.H_kv), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kvq_prefill_kernel, dim3(a.N, a.c.H_kv), dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace lily

@@ -204,7 +204,7 @@ struct KvqCopyArgs {
 cudaError_t launch_kvq_append(const KvqCopyArgs &a, cudaStream_t stream);
 cudaError_t launch_kvq_read(const KvqCopyArgs &a, cudaStream_t stream);
 
-// Attention over the quantised cache (kvq_attn.cu).
+// Attention over the quantised cache (kvq_decode.cu, kvq_prefill.cu).
 struct KvqAttnArgs {
     KvqCache c;
     int B, H_q, D, group, max_blocks;
@@ -217,9 +217,19 @@ struct KvqAttnArgs {
     const int *seq_lens;          // [B]
     uint16_t *out;                // bf16 [N][H_q][D]
     Ctrl *ctrl;
+    // decode: partial results of segments cut between CTAs (workspace)
+    int4 *meta;                   // [CTAs]: segment (or -1), its first CTA
+    int *ends_here;               // [CTAs]: the CTA's first segment, begun earlier, ends in it
+    float *part_ml;               // [2 CTAs][8][2]: max (log2 units), sum of weights
+    float *part_acc;              // [2 CTAs][8][D]
+    int whole, key_by_segment, stages;  // set by launch_kvq_decode
 };
-constexpr int kKvqMaxGroup = 8;   // query heads per KV head
-cudaError_t launch_kvq_attn(const KvqAttnArgs &a, cudaStream_t stream);
+constexpr int kKvqMaxGroup = 8;      // query heads per KV head
+// CTAs of the decode kernel, one per SM of a GB300: a constant, so that the work
+// split and the workspace are functions of the shape alone.
+constexpr int kKvqDecodeCtas = 152;
+cudaError_t launch_kvq_decode(const KvqAttnArgs &a, cudaStream_t stream);
+cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, cudaStream_t stream);
 
 // Gated DeltaNet scan (gdn.cu): CTA (16-row slice of the state, value head).
 struct GdnArgs {
