@@ -242,7 +242,7 @@ int kvq_check_shape(const lily_kvq_shape *s)
 
 // Workspace: control block, then the decode kernel's partial results.
 struct KvqLayout {
-    size_t ctrl, meta, ends_here, part_ml, part_acc, total;
+    size_t ctrl, meta, part_ml, part_acc, total;
 };
 
 KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
@@ -257,7 +257,6 @@ KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
     };
     L.ctrl = take(sizeof(Ctrl));
     L.meta = take(kKvqDecodeCtas * sizeof(int4));
-    L.ends_here = take(kKvqDecodeCtas * sizeof(int));
     L.part_ml = take(2 * kKvqDecodeCtas * kKvqMaxGroup * 2 * sizeof(float));
     L.part_acc = take(2 * kKvqDecodeCtas * kKvqMaxGroup * static_cast<size_t>(s.D) * sizeof(float));
     L.total = off;
@@ -948,7 +947,6 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     a.out = out;
     a.ctrl = at<Ctrl>(ws, L.ctrl);
     a.meta = at<int4>(ws, L.meta);
-    a.ends_here = at<int>(ws, L.ends_here);
     a.part_ml = at<float>(ws, L.part_ml);
     a.part_acc = at<float>(ws, L.part_acc);
     return to_status(ragged ? launch_kvq_prefill(a, stream) : launch_kvq_decode(a, stream),

@@ -18,7 +18,7 @@
 // keeps the largest scale seen at 16..128: f follows the data as the running
 // maximum of the softmax does, so the cache's values have no range limit.  p is
 // taken against a running maximum that moves only when a score passes it by 8 (in
-// powers of two), which one vote per 32 tokens finds; sums are fp32.
+// powers of two), which one vote per step finds; sums are fp32.
 //
 // Bound: the cache's bytes (36 per 64 values at 4 bits).  Work split: the cache
 // blocks of all (sequence, KV head) segments form one list that the CTAs (one per
@@ -27,10 +27,10 @@
 // kWholeTokens tokens a sequence can hold, each segment is one CTA and there is one
 // launch.
 // Inside a CTA:
-//   warp 8      producer: one bulk copy per block for each of the K and V codes
-//               and parameters (contiguous in the cache's layout) into a ring of
-//               shared-memory stages;
-//   warps 0..7  consumers, 32 tokens at a time each on its own, with their own
+//   last warps  producers of K and of V: one bulk copy per block for the codes and
+//               one for the parameters (contiguous in the cache's layout) into a
+//               ring of shared-memory stages;
+//   the others  consumers, 16 or 32 tokens at a time each on its own, with their own
 //               running maximum, sum and output: no barrier until the segment
 //               ends, where the warps' results are joined through shared memory.
 //               S^T = K q^T and O^T += V^T P on mma.sync m16n8k16 (fp16 in, fp32
@@ -39,7 +39,7 @@
 //               16 channels that one load gives it; P moves from the accumulator
 //               layout to the operand layout by movmatrix.
 // Every mbarrier wait is bounded; a wait that gives up records
-// LILY_ERR_DEVICE_TIMEOUT, and the producer waits for its copies before it exits.
+// LILY_ERR_DEVICE_TIMEOUT, and the producers wait for their copies before they exit.
 #include <cmath>
 #include <cstdint>
 
@@ -49,27 +49,30 @@
 namespace lily {
 namespace {
 
-constexpr int kNW = 8;                        // consumer warps
-constexpr int kThreads = (kNW + 1) * 32;      // + the producer
+#ifndef KVQ_NW
+#define KVQ_NW 10
+#endif
+constexpr int kNW = KVQ_NW;                   // consumer warps
+constexpr int kThreads = (kNW + 2) * 32;      // + the producers of K and of V
 constexpr int kMaxStages = 16;
-constexpr int kUnit = 32;                     // tokens a warp takes at a time
 constexpr int kSmemLimit = 208 * 1024;        // leaves room for the join kernel's early CTAs
 constexpr int kBarConsumers = 1;
 constexpr float kNoMax = -1.7e38f;            // running maximum before any token (finite: -inf - kNoMax = -inf)
 
 struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    int abort, b0;
-    long long pre, sum[kThreads / 32];
+    int abort, b0, len0;
+    long long pre, begin, total, used, sum[kThreads / 32];
     float ml[kNW][8][2];
 };
 constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
 
-__host__ __device__ constexpr int merge_bytes(int D) { return kNW * 8 * (D + 8) * 4; }
+constexpr int kMergeRow = 64 + 8;             // floats of a head's row in the join buffer, padded
+constexpr int kMergeBytes = 2 * kNW * 8 * kMergeRow * 4;
 constexpr int stage_bytes(int D, int bs, int bits) { return 2 * (bs * D * bits / 8 + bs * (D / 64) * 4); }
 int stages_for(int D, int bs, int bits)
 {
-    const int n = (kSmemLimit - 128 - kFixed - merge_bytes(D)) / stage_bytes(D, bs, bits);
+    const int n = (kSmemLimit - kFixed - kMergeBytes) / stage_bytes(D, bs, bits);
     return n < kMaxStages ? n : kMaxStages;
 }
 
@@ -94,14 +97,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
 {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
 // d += a b: m16n8k16, fp16 inputs, fp32 accumulators
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -135,7 +138,7 @@ __device__ __forceinline__ int blocks_of(int L, int bs) { return L > 0 ? (L + bs
 
 // This CTA's share of the work list: segments from (b, g, block j0) on, `left` blocks in all.
 struct Walk {
-    int b, g, j0, L, next_L;
+    int b, g, j0, L;
     long long left;
 };
 
@@ -150,25 +153,14 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
         w.left = blocks_of(w.L, a.c.bs);
         return w;
     }
-    auto chunk = [&](int b) { return b < a.B ? static_cast<long long>(blocks_of(length_of(a, b), a.c.bs)) : 0LL; };
-    long long v = 0;
-    for (int b = tid; b < a.B; b += kThreads) v += chunk(b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) F.sum[warp] = v;
-    __syncthreads();
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) total += F.sum[i];
-    total *= a.c.H_kv;
-    // no more CTAs than blocks: every CTA between a segment's first and last has a part of it
-    const long long used = min(total, static_cast<long long>(gridDim.x));
-    if (c >= used) return w;
-    const long long begin = total * c / used, end = total * (c + 1) / used;
-    w.left = end - begin;
-    // the sequence that `begin` falls into: a scan over the lengths, kThreads at a time
-    long long pre = 0;
-    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        const long long n = chunk(s0 + tid) * a.c.H_kv;
+    // blocks of sequence s0 + tid, their inclusive scan over the threads before this one (in .y)
+    int len = 0;
+    auto scan = [&](int s0) {
+        long long n = 0;
+        if (s0 + tid < a.B) {
+            len = length_of(a, s0 + tid);
+            n = static_cast<long long>(blocks_of(len, a.c.bs)) * a.c.H_kv;
+        }
         long long inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -178,22 +170,46 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
         __syncthreads();
         if (lane == 31) F.sum[warp] = inc;
         __syncthreads();
-        long long before = pre, all = pre;
+        long long before = inc - n, all = 0;
+#pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += F.sum[i];
             all += F.sum[i];
         }
-        const long long lo = before + inc - n;
+        return make_longlong2(before, all);
+    };
+    longlong2 sc{};
+    long long total = 0;
+    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+        sc = scan(s0);
+        total += sc.y;
+    }
+    // no more CTAs than blocks: every CTA between a segment's first and last has a part of it
+    const long long used = min(total, static_cast<long long>(gridDim.x));
+    if (c >= used) return w;
+    const long long begin = total * c / used;
+    w.left = total * (c + 1) / used - begin;
+    if (tid == 0) {
+        F.begin = begin;
+        F.total = total;
+        F.used = used;
+    }
+    // the sequence that `begin` falls into (with no more sequences than threads, the scan above has it)
+    long long pre = 0;
+    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+        if (a.B > kThreads) sc = scan(s0);
+        const long long lo = pre + sc.x, n = s0 + tid < a.B ? static_cast<long long>(blocks_of(len, a.c.bs)) * a.c.H_kv : 0;
         if (begin >= lo && begin < lo + n) {
             F.b0 = s0 + tid;
+            F.len0 = len;
             F.pre = lo;
         }
-        pre = all;
-        if (begin < all) break;
+        pre += sc.y;
+        if (begin < pre) break;
     }
     __syncthreads();
     w.b = F.b0;
-    w.L = length_of(a, w.b);
+    w.L = F.len0;
     const int nblk = blocks_of(w.L, a.c.bs);
     w.g = static_cast<int>((begin - F.pre) / nblk);
     w.j0 = static_cast<int>((begin - F.pre) % nblk);
@@ -212,23 +228,23 @@ __device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done)
     }
 }
 
-template <int BITS, int GR>
+template <int BITS, int GR, int bs>
 __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
 {
     constexpr int D = GR * 64, GB = 8 * BITS;  // bytes of a group's codes in one row
-    extern __shared__ uint8_t dsm_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dsm_raw) + 127) & ~uintptr_t(127));
+    extern __shared__ __align__(128) uint8_t base[];
     Fixed &F = *reinterpret_cast<Fixed *>(base);
-    float *merge = reinterpret_cast<float *>(base + kFixed);  // [warp][head][D + 8]
-    uint8_t *ring = base + kFixed + merge_bytes(D);
-    const int bs = a.c.bs, NS = a.stages, G = a.group;
-    const int CB = GR * bs * GB, PB = GR * bs * 4, SB = 2 * (CB + PB);  // codes, parameters, stage
+    float *merge = reinterpret_cast<float *>(base + kFixed);  // [2][warp][head][kMergeRow]
+    uint8_t *ring = base + kFixed + kMergeBytes;
+    constexpr int CB = GR * bs * GB, PB = GR * bs * 4, SB = 2 * (CB + PB);  // codes, parameters, stage
+    constexpr int IH = GR == 4 ? 1 : 2, kUnit = 16 * IH;  // a warp takes one or two halves of 16 tokens at a time
+    const int NS = a.stages, G = a.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, t = lane & 3;
     int *status = &a.ctrl->status;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&F.full[i], 1);
+            mbar_init(&F.full[i], 2);
             mbar_init(&F.empty[i], bs / kUnit);
         }
         F.abort = 0;
@@ -239,8 +255,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     __syncthreads();
     Walk w = first_segment(a, F);
 
-    if (warp == kNW) {
-        // ------------------------------------------------ producer
+    if (warp >= kNW) {
+        // ------------------------------------------------ producers: K, V (two, as issuing a copy takes ~130 cycles)
+        const bool isv = warp > kNW;
+        const uint8_t *codes = isv ? a.c.v_q : a.c.k_q;
+        const uint16_t *params = isv ? a.c.v_sb : a.c.k_sb;
+        uint8_t *dst0 = ring + (isv ? CB + PB : 0);
         int issued = 0;
         bool ok = true;
         while (w.left > 0 && ok) {
@@ -259,15 +279,14 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                     if (issued >= NS && !mbar_wait(&F.empty[slot], ((issued / NS) - 1) & 1, &F.abort, status)) ok = false;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    const long long blk = __shfl_sync(0xffffffffu, pb, i - i0);
-                    const long long row0 = (blk * a.c.H_kv + w.g) * GR * bs;
-                    uint8_t *dst = ring + static_cast<size_t>(slot) * SB;
-                    if (lane == 0) mbar_arrive_expect_tx(&F.full[slot], static_cast<uint32_t>(SB));
+                    const long long row0 = (static_cast<long long>(__shfl_sync(0xffffffffu, pb, i - i0)) * a.c.H_kv + w.g) * (GR * bs);
+                    if (lane == 0) {
+                        uint8_t *dst = dst0 + slot * SB;
+                        mbar_arrive_expect_tx(&F.full[slot], static_cast<uint32_t>(CB + PB));
+                        bulk_load(dst, codes + row0 * GB, CB, &F.full[slot]);
+                        bulk_load(dst + CB, params + row0 * 2, PB, &F.full[slot]);
+                    }
                     __syncwarp();
-                    if (lane == 0) bulk_load(dst, a.c.k_q + row0 * GB, CB, &F.full[slot]);
-                    if (lane == 1) bulk_load(dst + CB, a.c.k_sb + row0 * 2, PB, &F.full[slot]);
-                    if (lane == 2) bulk_load(dst + CB + PB, a.c.v_q + row0 * GB, CB, &F.full[slot]);
-                    if (lane == 3) bulk_load(dst + 2 * CB + PB, a.c.v_sb + row0 * 2, PB, &F.full[slot]);
                     ++issued;
                 }
             }
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
 
     // ---------------------------------------------------- consumers
     if (!a.whole && threadIdx.x == 0 && !a.key_by_segment) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    const int ups = bs / kUnit;  // units per stage
+    constexpr int ups = bs / kUnit;  // units per stage
     int unit = 0, stage0 = 0;    // units and stages of the segments before this one
     bool ok = true;
     while (w.left > 0) {
@@ -300,37 +319,39 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
         float qsum[GR][2], mul[2];
         {
             const uint16_t *qh = a.q + w.b * a.q_stride + static_cast<long long>(w.g * G + (gi < G ? gi : 0)) * D;
-            float qv[GR][16], big = 0.0f;
+            uint32_t xs[GR][8];
+            float big = 0.0f;
 #pragma unroll
             for (int c = 0; c < GR; ++c) {
-                uint4 x[2];
-                x[0] = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16);
-                x[1] = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16 + 8);
-                const uint32_t xs[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+                const uint4 x0 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16);
+                const uint4 x1 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16 + 8);
+                xs[c][0] = x0.x; xs[c][1] = x0.y; xs[c][2] = x0.z; xs[c][3] = x0.w;
+                xs[c][4] = x1.x; xs[c][5] = x1.y; xs[c][6] = x1.z; xs[c][7] = x1.w;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    qv[c][2 * i] = gi < G ? lo_bf16(xs[i]) : 0.0f;
-                    qv[c][2 * i + 1] = gi < G ? hi_bf16(xs[i]) : 0.0f;
-                    big = fmaxf(big, fmaxf(fabsf(qv[c][2 * i]), fabsf(qv[c][2 * i + 1])));
+                    if (gi >= G) xs[c][i] = 0u;
+                    big = fmaxf(big, fmaxf(fabsf(lo_bf16(xs[c][i])), fabsf(hi_bf16(xs[c][i]))));
                 }
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             const int e = big > 0.0f ? 14 - ilogbf(big) : 0;
+            const float e1 = scalbnf(1.0f, e / 2), e2 = scalbnf(1.0f, e - e / 2);  // 2^e may pass the fp32 range, its halves do not
 #pragma unroll
             for (int c = 0; c < GR; ++c) {
-                float s = 0.0f;
+                float qv[16], s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    qv[c][i] = scalbnf(qv[c][i], e);
-                    s += qv[c][i];
+                for (int i = 0; i < 8; ++i) {
+                    qv[2 * i] = lo_bf16(xs[c][i]) * e1 * e2;
+                    qv[2 * i + 1] = hi_bf16(xs[c][i]) * e1 * e2;
+                    s += qv[2 * i] + qv[2 * i + 1];
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float odd = BITS == 4 && (j & 1) ? 0.0625f : 1.0f;  // those codes carry 2^-20
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
-                        qb[c * 4 + j][r] = pack_f16(qv[c][k_channel<BITS>(j, 2 * r)] * odd, qv[c][k_channel<BITS>(j, 2 * r + 1)] * odd);
+                        qb[c * 4 + j][r] = pack_f16(qv[k_channel<BITS>(j, 2 * r)] * odd, qv[k_channel<BITS>(j, 2 * r + 1)] * odd);
                 }
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
@@ -361,77 +382,84 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
             const int left = w.L - (tok0 + u * kUnit);  // tokens of this unit that exist (may be <= 0, or more than 32)
             const int row = r0 + token_of(gi);          // + 16 i + 8 h: this lane's token rows of S^T
 
-            // ---- scores: sc[i][2h + x], tokens row + 16 i + 8 h, heads 2t + x
-            float sc[2][4];
+            // ---- scores: sc[i][2h + x], tokens row + 16 i + 8 h, heads 2t + x.  One accumulator per
+            // (token half, group), four of them between dependent matrix steps
+            constexpr int KW = BITS / 2;
+            float sc[IH][4];
+            {
+                uint32_t k0[IH][GR][KW], k1[IH][GR][KW];
+                float d[IH][GR][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
+                for (int i = 0; i < IH; ++i)
 #pragma unroll
-                for (int c = 0; c < GR; ++c) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t k0[BITS / 2], k1[BITS / 2];
-                    const uint8_t *p0 = kq + (c * bs + row + 16 * i) * GB + t * (GB / 4), *p1 = p0 + 8 * GB;
-                    if (BITS == 4) {
-                        const uint2 x0 = *reinterpret_cast<const uint2 *>(p0), x1 = *reinterpret_cast<const uint2 *>(p1);
-                        k0[0] = x0.x; k0[1] = x0.y; k1[0] = x1.x; k1[1] = x1.y;
-                    } else {
-                        const uint4 x0 = *reinterpret_cast<const uint4 *>(p0), x1 = *reinterpret_cast<const uint4 *>(p1);
-                        k0[0] = x0.x; k0[1] = x0.y; k0[2 % (BITS / 2)] = x0.z; k0[3 % (BITS / 2)] = x0.w;
-                        k1[0] = x1.x; k1[1] = x1.y; k1[2 % (BITS / 2)] = x1.z; k1[3 % (BITS / 2)] = x1.w;
-                    }
-#pragma unroll
-                    for (int x = 0; x < BITS / 2; ++x) {
-                        const uint32_t h0 = k0[x] >> 8, h1 = k1[x] >> 8;
-                        if (BITS == 4) {
-                            mma_f16(d, k0[x] & 0x000F000Fu, k1[x] & 0x000F000Fu, h0 & 0x000F000Fu, h1 & 0x000F000Fu,
-                                    qb[c * 4 + 2 * (x & 1)][0], qb[c * 4 + 2 * (x & 1)][1]);
-                            mma_f16(d, k0[x] & 0x00F000F0u, k1[x] & 0x00F000F0u, h0 & 0x00F000F0u, h1 & 0x00F000F0u,
-                                    qb[c * 4 + 2 * (x & 1) + 1][0], qb[c * 4 + 2 * (x & 1) + 1][1]);
+                    for (int c = 0; c < GR; ++c) {
+                        const uint8_t *p0 = kq + (c * bs + row + 16 * i) * GB + t * (GB / 4), *p1 = p0 + 8 * GB;
+                        if constexpr (BITS == 4) {
+                            const uint2 x0 = *reinterpret_cast<const uint2 *>(p0), x1 = *reinterpret_cast<const uint2 *>(p1);
+                            k0[i][c][0] = x0.x; k0[i][c][1] = x0.y;
+                            k1[i][c][0] = x1.x; k1[i][c][1] = x1.y;
                         } else {
-                            mma_f16(d, k0[x] & 0x00FF00FFu, k1[x] & 0x00FF00FFu, h0 & 0x00FF00FFu, h1 & 0x00FF00FFu,
-                                    qb[c * 4 + x][0], qb[c * 4 + x][1]);
+                            const uint4 x0 = *reinterpret_cast<const uint4 *>(p0), x1 = *reinterpret_cast<const uint4 *>(p1);
+                            k0[i][c][0] = x0.x; k0[i][c][1] = x0.y; k0[i][c][2] = x0.z; k0[i][c][3] = x0.w;
+                            k1[i][c][0] = x1.x; k1[i][c][1] = x1.y; k1[i][c][2] = x1.z; k1[i][c][3] = x1.w;
                         }
+                        d[i][c][0] = d[i][c][1] = d[i][c][2] = d[i][c][3] = 0.0f;
                     }
-                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i) * 4);
-                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i + 8) * 4);
-                    const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
-                    sc[i][0] = fmaf(b0, qsum[c][0], fmaf(s0, d[0], sc[i][0]));
-                    sc[i][1] = fmaf(b0, qsum[c][1], fmaf(s0, d[1], sc[i][1]));
-                    sc[i][2] = fmaf(b1, qsum[c][0], fmaf(s1, d[2], sc[i][2]));
-                    sc[i][3] = fmaf(b1, qsum[c][1], fmaf(s1, d[3], sc[i][3]));
+#pragma unroll
+                for (int x = 0; x < KW; ++x) {
+#pragma unroll
+                    for (int odd = 0; odd < (BITS == 4 ? 2 : 1); ++odd) {
+                        const uint32_t M = BITS == 8 ? 0x00FF00FFu : odd ? 0x00F000F0u : 0x000F000Fu;
+                        const int j = BITS == 4 ? 2 * x + odd : x;
+#pragma unroll
+                        for (int i = 0; i < IH; ++i)
+#pragma unroll
+                            for (int c = 0; c < GR; ++c)
+                                mma_f16(d[i][c], k0[i][c][x] & M, k1[i][c][x] & M, (k0[i][c][x] >> 8) & M, (k1[i][c][x] >> 8) & M,
+                                        qb[c * 4 + j][0], qb[c * 4 + j][1]);
+                    }
                 }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[i][x] *= mul[x & 1];
+                for (int i = 0; i < IH; ++i) {
+                    float *s4 = sc[i];
+                    s4[0] = s4[1] = s4[2] = s4[3] = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < GR; ++c) {
+                        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i) * 4);
+                        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i + 8) * 4);
+                        const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
+                        s4[0] = fmaf(b0, qsum[c][0], fmaf(s0, d[i][c][0], s4[0]));
+                        s4[1] = fmaf(b0, qsum[c][1], fmaf(s0, d[i][c][1], s4[1]));
+                        s4[2] = fmaf(b1, qsum[c][0], fmaf(s1, d[i][c][2], s4[2]));
+                        s4[3] = fmaf(b1, qsum[c][1], fmaf(s1, d[i][c][3], s4[3]));
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s4[x] *= mul[x & 1];
+                }
             }
-            uint32_t vw[2][GR][2];  // scale, bias of V: tokens row + 16 i + 8 h
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < GR; ++c)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vw[i][c][h] = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
+            // scale and bias of V, tokens row + 16 i + 8 h; nothing for rows behind the sequence, whatever they hold
+            auto v_param = [&](int i, int c, int h) {
+                const uint32_t x = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
+                return token_of(gi) + 16 * i + 8 * h < left ? x : 0u;
+            };
             if (left < kUnit) {
-                // rows behind the sequence: no weight, whatever they hold
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < IH; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        if (token_of(gi) + 16 * i + 8 * h >= left) {
-                            sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
-#pragma unroll
-                            for (int c = 0; c < GR; ++c) vw[i][c][h] = 0u;
-                        }
+                        if (token_of(gi) + 16 * i + 8 * h >= left) sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
             }
 
             // ---- running maximum, and the power of two of the value scales: both move rarely
-            const float top0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
-            const float top1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
-            float smax = 0.0f;
+            float top0 = fmaxf(sc[0][0], sc[0][2]), top1 = fmaxf(sc[0][1], sc[0][3]), smax = 0.0f;
+            if constexpr (IH == 2) {
+                top0 = fmaxf(top0, fmaxf(sc[IH - 1][0], sc[IH - 1][2]));
+                top1 = fmaxf(top1, fmaxf(sc[IH - 1][1], sc[IH - 1][3]));
+            }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < IH; ++i)
 #pragma unroll
-                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(vw[i][c][0])), fabsf(lo_bf16(vw[i][c][1]))));
+                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(v_param(i, c, 0))), fabsf(lo_bf16(v_param(i, c, 1)))));
             const bool grew = top0 > m_run[0] + 8.0f || top1 > m_run[1] + 8.0f;
             if (__any_sync(0xffffffffu, grew || smax * f > 128.0f)) {
                 float mn0 = top0, mn1 = top1;
@@ -470,9 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                 }
             }
 
+            asm volatile("" ::: "memory");  // the parameters are loaded again: 16 registers fewer
             // ---- O^T += V^T P: weights p s f in fp16, tokens on K
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < IH; ++i) {
                 float p[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) p[x] = ex2(sc[i][x] - m_run[x & 1]);
@@ -481,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                 const float pf[4] = {p[0] * f, p[1] * f, p[2] * f, p[3] * f};
 #pragma unroll
                 for (int c = 0; c < GR; ++c) {
-                    const float s0 = lo_bf16(vw[i][c][0]), b0 = hi_bf16(vw[i][c][0]);
-                    const float s1 = lo_bf16(vw[i][c][1]), b1 = hi_bf16(vw[i][c][1]);
+                    const uint32_t w0 = v_param(i, c, 0), w1 = v_param(i, c, 1);
+                    const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
                     bsum[c][0] = fmaf(p[0], b0, fmaf(p[2], b1, bsum[c][0]));
                     bsum[c][1] = fmaf(p[1], b0, fmaf(p[3], b1, bsum[c][1]));
                     const uint32_t y0 = transpose8x8(pack_f16(pf[0] * s0, pf[1] * s0));
@@ -532,62 +561,64 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
             }
         }
         const float rf = 1.0f / f;
+        const bool starts = w.j0 == 0, ends = w.j0 + n == nblk;
+        const int part = 2 * blockIdx.x + (starts ? 1 : 0), active = min(units, kNW);
+        if (gi == 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float *dst = merge + (warp * 8 + 2 * t + x) * (D + 8) + gi * 8;
-#pragma unroll
-            for (int c = 0; c < GR; ++c) {
-                auto out = [&](int m, int h) {
-                    const float unit_scale = BITS == 4 && (m & 1) ? 0x1p20f : 0x1p24f;
-                    return fmaf(acc[c][m][2 * h + x] * unit_scale, rf, bsum[c][x]);
-                };
-                *reinterpret_cast<float4 *>(dst + c * 64) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
-                *reinterpret_cast<float4 *>(dst + c * 64 + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));
-            }
-            if (gi == 0) {
+            for (int x = 0; x < 2; ++x) {
                 F.ml[warp][2 * t + x][0] = m_run[x];
                 F.ml[warp][2 * t + x][1] = l_run[x];
             }
         }
-        named_barrier_sync(kBarConsumers, kNW * 32);
-        const bool starts = w.j0 == 0, ends = w.j0 + n == nblk;
-        const int part = 2 * blockIdx.x + (starts ? 1 : 0), active = min(units, kNW);
-        for (int i = threadIdx.x; i < 8 * (D / 4); i += kNW * 32) {
-            const int h = i / (D / 4), d4 = i % (D / 4);
-            float M = kNoMax;
-            for (int j = 0; j < active; ++j) M = fmaxf(M, F.ml[(unit + j) % kNW][h][0]);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float den = 0.0f;
-            for (int j = 0; j < active; ++j) {
-                const int wj = (unit + j) % kNW;
-                const float e = ex2(F.ml[wj][h][0] - M);
-                const float4 x = *reinterpret_cast<const float4 *>(merge + (wj * 8 + h) * (D + 8) + d4 * 4);
-                den = fmaf(e, F.ml[wj][h][1], den);
-                o.x = fmaf(e, x.x, o.x);
-                o.y = fmaf(e, x.y, o.y);
-                o.z = fmaf(e, x.z, o.z);
-                o.w = fmaf(e, x.w, o.w);
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {  // 64 channels at a time, the two halves of the buffer in turn
+            float *buf = merge + (c & 1) * kNW * 8 * kMergeRow;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float *dst = buf + (warp * 8 + 2 * t + x) * kMergeRow + gi * 8;
+                auto out = [&](int m, int h) {
+                    const float unit_scale = BITS == 4 && (m & 1) ? 0x1p20f : 0x1p24f;
+                    return fmaf(acc[c][m][2 * h + x] * unit_scale, rf, bsum[c][x]);
+                };
+                *reinterpret_cast<float4 *>(dst) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
+                *reinterpret_cast<float4 *>(dst + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));
             }
-            if (starts && ends) {
-                if (h < G) {
+            named_barrier_sync(kBarConsumers, kNW * 32);
+            const int h = threadIdx.x / 16, d4 = threadIdx.x % 16;
+            if (h < G) {
+                float M = kNoMax, den = 0.0f;
+                for (int j = 0; j < active; ++j) M = fmaxf(M, F.ml[(unit + j) % kNW][h][0]);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j = 0; j < active; ++j) {
+                    const int wj = (unit + j) % kNW;
+                    const float e = ex2(F.ml[wj][h][0] - M);
+                    const float4 x = *reinterpret_cast<const float4 *>(buf + (wj * 8 + h) * kMergeRow + d4 * 4);
+                    den = fmaf(e, F.ml[wj][h][1], den);
+                    o.x = fmaf(e, x.x, o.x);
+                    o.y = fmaf(e, x.y, o.y);
+                    o.z = fmaf(e, x.z, o.z);
+                    o.w = fmaf(e, x.w, o.w);
+                }
+                if (starts && ends) {
                     const float r = den > 0.0f ? 1.0f / den : 0.0f;
                     uint2 y;
                     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
                     y.x = *reinterpret_cast<const uint32_t *>(&lo);
                     y.y = *reinterpret_cast<const uint32_t *>(&hi);
-                    reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(w.b) * a.H_q + w.g * G + h) * D)[d4] = y;
+                    reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(w.b) * a.H_q + w.g * G + h) * D)[c * 16 + d4] = y;
+                } else {
+                    reinterpret_cast<float4 *>(a.part_acc + (static_cast<size_t>(part) * 8 + h) * D)[c * 16 + d4] = o;
+                    if (c == 0 && d4 == 0)
+                        *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * 8 + h) * 2) = make_float2(M, den);
                 }
-            } else {
-                reinterpret_cast<float4 *>(a.part_acc + (static_cast<size_t>(part) * 8 + h) * D)[d4] = o;
-                if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * 8 + h) * 2) = make_float2(M, den);
             }
         }
         if (!a.whole && threadIdx.x == 0 && starts && (!ends || a.key_by_segment)) {
-            // who joins the parts: the last CTA is the one that holds the segment's last block
+            // who joins the parts: the CTAs from this one to the one that has the segment's last block
             const int bg = w.b * a.c.H_kv + w.g;
-            a.meta[a.key_by_segment ? bg : blockIdx.x] = make_int4(ends ? -1 : bg, blockIdx.x, nblk, 0);
+            const int last = static_cast<int>(((F.begin + stage0 + nblk) * F.used - 1) / F.total);
+            a.meta[a.key_by_segment ? bg : blockIdx.x] = make_int4(ends ? -1 : bg, blockIdx.x, last, 0);
         }
-        if (!a.whole && threadIdx.x == 0 && !starts) a.ends_here[blockIdx.x] = ends ? 1 : 0;
         unit += units;
         stage0 += n;
         advance(a, w, n);
@@ -600,12 +631,11 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
 // with a running maximum of its own, then the 16 groups agree on the common one and
 // are added in a fixed order.  Parts of CTA c0 (the one the segment starts in) are in
 // slot 2 c0 + 1, those of the following CTAs c in slot 2 c, up to the CTA it ends in.
-__global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant__ KvqAttnArgs a, int n_ctas)
+__global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant__ KvqAttnArgs a)
 {
     constexpr int kCols = 16, kGroups = 16, kBatch = 8;
     __shared__ float4 part[kGroups][kCols];
     __shared__ float red_max[8], red_den[8];
-    __shared__ int s_end;
     const int key = blockIdx.x / a.group, h = blockIdx.x % a.group;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int e = tid % kCols, sg = tid / kCols;
@@ -613,20 +643,7 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
     pdl_wait();
     const int4 meta = a.meta[key];
     if (meta.x < 0) return;
-    const int c0 = meta.y;
-    // the first CTA after c0 whose first segment ends in it
-    if (warp == 0) {
-        for (int c = c0 + 1; ; c += 32) {
-            const bool end = c + lane >= n_ctas || a.ends_here[c + lane] == 1;
-            const uint32_t any = __ballot_sync(0xffffffffu, end);
-            if (any) {
-                if (lane == 0) s_end = min(c + __ffs(any) - 1, n_ctas - 1);
-                break;
-            }
-        }
-    }
-    __syncthreads();
-    const int S = s_end - c0 + 1, q = blockIdx.y * kCols + e;
+    const int c0 = meta.y, S = meta.z - c0 + 1, q = blockIdx.y * kCols + e;
     auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)); };
     float mt = kNoMax, dt = 0.0f;
     float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -697,12 +714,23 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
     }
 }
 
-template <int BITS, int GR>
-cudaError_t launch(const KvqAttnArgs &a, int ctas, size_t smem, cudaStream_t stream)
+template <int BITS, int GR, int bs>
+cudaError_t launch(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 {
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR>), static_cast<int>(smem));
+    const size_t smem = kFixed + kMergeBytes + static_cast<size_t>(a.stages) * stage_bytes(64 * GR, bs, BITS);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR, bs>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_decode_kernel<BITS, GR>, dim3(ctas), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kvq_decode_kernel<BITS, GR, bs>, dim3(ctas), dim3(kThreads), smem, stream, a);
+}
+template <int BITS, int GR>
+cudaError_t launch_bs(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
+{
+    return a.c.bs == 32 ? launch<BITS, GR, 32>(a, ctas, stream) : a.c.bs == 64 ? launch<BITS, GR, 64>(a, ctas, stream) : launch<BITS, GR, 128>(a, ctas, stream);
+}
+template <int BITS>
+cudaError_t launch_d(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
+{
+    return a.D == 64 ? launch_bs<BITS, 1>(a, ctas, stream) : a.D == 128 ? launch_bs<BITS, 2>(a, ctas, stream) : launch_bs<BITS, 4>(a, ctas, stream);
 }
 
 }  // namespace
@@ -717,16 +745,11 @@ cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
     a.whole = static_cast<long long>(a.max_blocks) * a.c.bs <= kWholeTokens;
     a.key_by_segment = segments <= kKvqDecodeCtas;
     a.stages = stages_for(a.D, a.c.bs, a.c.bits);
-    const size_t smem = 128 + kFixed + merge_bytes(a.D) + static_cast<size_t>(a.stages) * stage_bytes(a.D, a.c.bs, a.c.bits);
     const int ctas = a.whole ? static_cast<int>(segments) : kKvqDecodeCtas;
-    cudaError_t e;
-    if (a.c.bits == 4)
-        e = a.D == 64 ? launch<4, 1>(a, ctas, smem, stream) : a.D == 128 ? launch<4, 2>(a, ctas, smem, stream) : launch<4, 4>(a, ctas, smem, stream);
-    else
-        e = a.D == 64 ? launch<8, 1>(a, ctas, smem, stream) : a.D == 128 ? launch<8, 2>(a, ctas, smem, stream) : launch<8, 4>(a, ctas, smem, stream);
+    const cudaError_t e = a.c.bits == 4 ? launch_d<4>(a, ctas, stream) : launch_d<8>(a, ctas, stream);
     if (e != cudaSuccess || a.whole) return e;
     const int keys = a.key_by_segment ? static_cast<int>(segments) : ctas;
-    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 64), dim3(256), 0, stream, a, ctas);
+    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 64), dim3(256), 0, stream, a);
 }
 
 }  // namespace lily

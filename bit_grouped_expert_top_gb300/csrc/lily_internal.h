@@ -218,8 +218,7 @@ struct KvqAttnArgs {
     uint16_t *out;                // bf16 [N][H_q][D]
     Ctrl *ctrl;
     // decode: partial results of segments cut between CTAs (workspace)
-    int4 *meta;                   // [CTAs]: segment (or -1), its first CTA
-    int *ends_here;               // [CTAs]: the CTA's first segment, begun earlier, ends in it
+    int4 *meta;                   // [CTAs]: segment (or -1), its first and last CTA
     float *part_ml;               // [2 CTAs][8][2]: max (log2 units), sum of weights
     float *part_acc;              // [2 CTAs][8][D]
     int whole, key_by_segment, stages;  // set by launch_kvq_decode
