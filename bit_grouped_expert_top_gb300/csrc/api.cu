@@ -237,6 +237,7 @@ int kvq_check_shape(const lily_kvq_shape *s)
     if (s->block_size != 32 && s->block_size != 64 && s->block_size != 128) return LILY_ERR_UNSUPPORTED;
     if (s->H_q / s->H_kv > kKvqMaxGroup || s->B > 65535 || s->H_kv > 4096) return LILY_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(s->max_blocks) * s->block_size >= (int64_t(1) << 31)) return LILY_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(s->max_blocks) * s->B * s->H_kv >= (int64_t(1) << 31)) return LILY_ERR_UNSUPPORTED;
     return LILY_OK;
 }
 

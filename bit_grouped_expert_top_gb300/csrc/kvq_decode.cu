@@ -54,25 +54,24 @@ namespace {
 #endif
 constexpr int kNW = KVQ_NW;                   // consumer warps
 constexpr int kThreads = (kNW + 2) * 32;      // + the producers of K and of V
-constexpr int kMaxStages = 16;
-constexpr int kSmemLimit = 208 * 1024;        // leaves room for the join kernel's early CTAs
-constexpr int kBarConsumers = 1;
+constexpr int kMaxStages = 14;                // segments in flight <= stages < named barriers
+constexpr int kSmemLimit = 227 * 1024;
+constexpr int kBarriers = 15;                 // named barriers 1..15, by segment
 constexpr float kNoMax = -1.7e38f;            // running maximum before any token (finite: -inf - kNoMax = -inf)
 
 struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    int abort, b0, len0;
-    long long pre, begin, total, used, sum[kThreads / 32];
-    float ml[kNW][8][2];
+    int abort, b0, len0, pre, begin, total, used, sum[kThreads / 32];
+    alignas(8) float ml[kNW][8][2];
 };
 constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
 
-constexpr int kMergeRow = 64 + 8;             // floats of a head's row in the join buffer, padded
-constexpr int kMergeBytes = 2 * kNW * 8 * kMergeRow * 4;
+__host__ __device__ constexpr int merge_row(int D) { return D + 8; }  // floats of a head's row in the join buffer, padded
+__host__ __device__ constexpr int merge_bytes(int D) { return kNW * 8 * merge_row(D) * 4; }
 constexpr int stage_bytes(int D, int bs, int bits) { return 2 * (bs * D * bits / 8 + bs * (D / 64) * 4); }
 int stages_for(int D, int bs, int bits)
 {
-    const int n = (kSmemLimit - kFixed - kMergeBytes) / stage_bytes(D, bs, bits);
+    const int n = (kSmemLimit - kFixed - merge_bytes(D)) / stage_bytes(D, bs, bits);
     return n < kMaxStages ? n : kMaxStages;
 }
 
@@ -123,9 +122,8 @@ __device__ __forceinline__ constexpr int k_channel(int j, int r)
 // stands for: lanes t = 0..3 of one V load then read four consecutive rows.
 __device__ __forceinline__ int token_of(int k) { return (k >> 1) | ((k & 1) << 2); }
 
-__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int b)
+__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int L)
 {
-    int L = a.seq_lens[b];
     const int cap = a.max_blocks * a.c.bs;
     if (L < 0 || L > cap) {
         record_error(&a.ctrl->status, kErrDeviceIndex);
@@ -138,8 +136,7 @@ __device__ __forceinline__ int blocks_of(int L, int bs) { return L > 0 ? (L + bs
 
 // This CTA's share of the work list: segments from (b, g, block j0) on, `left` blocks in all.
 struct Walk {
-    int b, g, j0, L;
-    long long left;
+    int b, g, j0, L, next, left;  // next: the length of sequence b + 1 as stored (loaded one sequence ahead)
 };
 
 __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
@@ -149,70 +146,69 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
     if (a.whole) {
         w.b = c / a.c.H_kv;
         w.g = c % a.c.H_kv;
-        w.L = length_of(a, w.b);
+        w.L = length_of(a, a.seq_lens[w.b]);
         w.left = blocks_of(w.L, a.c.bs);
         return w;
     }
-    // blocks of sequence s0 + tid, their inclusive scan over the threads before this one (in .y)
-    int len = 0;
+    // blocks of sequence s0 + tid: those of the threads before this one, and of all (fewer than 2^31 by the host's check)
+    int len = 0, before, all;
     auto scan = [&](int s0) {
-        long long n = 0;
+        int n = 0;
         if (s0 + tid < a.B) {
-            len = length_of(a, s0 + tid);
-            n = static_cast<long long>(blocks_of(len, a.c.bs)) * a.c.H_kv;
+            len = length_of(a, a.seq_lens[s0 + tid]);
+            n = blocks_of(len, a.c.bs) * a.c.H_kv;
         }
-        long long inc = n;
+        int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            const int up = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += up;
         }
         __syncthreads();
         if (lane == 31) F.sum[warp] = inc;
         __syncthreads();
-        long long before = inc - n, all = 0;
+        before = inc - n;
+        all = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += F.sum[i];
             all += F.sum[i];
         }
-        return make_longlong2(before, all);
     };
-    longlong2 sc{};
-    long long total = 0;
+    int total = 0;
     for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        sc = scan(s0);
-        total += sc.y;
+        scan(s0);
+        total += all;
     }
     // no more CTAs than blocks: every CTA between a segment's first and last has a part of it
-    const long long used = min(total, static_cast<long long>(gridDim.x));
+    const int used = min(total, static_cast<int>(gridDim.x));
     if (c >= used) return w;
-    const long long begin = total * c / used;
-    w.left = total * (c + 1) / used - begin;
-    if (tid == 0) {
-        F.begin = begin;
-        F.total = total;
-        F.used = used;
-    }
+    const int per = total / used, rest = total % used;
+    const int begin = per * c + rest * c / used;
+    w.left = per * (c + 1) + rest * (c + 1) / used - begin;
     // the sequence that `begin` falls into (with no more sequences than threads, the scan above has it)
-    long long pre = 0;
+    int pre = 0;
     for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        if (a.B > kThreads) sc = scan(s0);
-        const long long lo = pre + sc.x, n = s0 + tid < a.B ? static_cast<long long>(blocks_of(len, a.c.bs)) * a.c.H_kv : 0;
-        if (begin >= lo && begin < lo + n) {
+        if (a.B > kThreads) scan(s0);
+        const int lo = pre + before, n = s0 + tid < a.B ? blocks_of(len, a.c.bs) * a.c.H_kv : 0;
+        if (begin >= lo && begin - lo < n) {
             F.b0 = s0 + tid;
             F.len0 = len;
             F.pre = lo;
+            F.begin = begin;
+            F.total = total;
+            F.used = used;
         }
-        pre += sc.y;
+        pre += all;
         if (begin < pre) break;
     }
     __syncthreads();
     w.b = F.b0;
     w.L = F.len0;
+    w.next = w.b + 1 < a.B ? a.seq_lens[w.b + 1] : 0;
     const int nblk = blocks_of(w.L, a.c.bs);
-    w.g = static_cast<int>((begin - F.pre) / nblk);
-    w.j0 = static_cast<int>((begin - F.pre) % nblk);
+    w.g = (begin - F.pre) / nblk;
+    w.j0 = (begin - F.pre) % nblk;
     return w;
 }
 
@@ -224,7 +220,50 @@ __device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done)
     if (++w.g == a.c.H_kv) {
         w.g = 0;
         ++w.b;
-        if (w.left > 0) w.L = length_of(a, w.b);
+        if (w.left > 0) {
+            w.L = length_of(a, w.next);
+            w.next = w.b + 1 < a.B ? a.seq_lens[w.b + 1] : 0;
+        }
+    }
+}
+
+// Four channels of head h of a segment: the warps' results on their common maximum,
+// to the output (part < 0: the segment is whole) or to a part's slot.
+template <int D>
+__device__ __forceinline__ void join_column(const KvqAttnArgs &a, const Fixed &F, const float *merge, const Walk &w, int unit,
+                                            int active, int part, int h, int d4)
+{
+    float M = kNoMax, den = 0.0f;
+    float2 ml[kNW];
+    const int w0 = unit % kNW;
+    auto warp_of = [&](int j) { return w0 + j < kNW ? w0 + j : w0 + j - kNW; };
+#pragma unroll
+    for (int j = 0; j < kNW; ++j) {
+        ml[j] = j < active ? *reinterpret_cast<const float2 *>(F.ml[warp_of(j)][h]) : make_float2(kNoMax, 0.0f);
+        M = fmaxf(M, ml[j].x);
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kNW; ++j) {
+        const float4 x = j < active ? *reinterpret_cast<const float4 *>(merge + (warp_of(j) * 8 + h) * merge_row(D) + d4 * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float e = ex2(ml[j].x - M);
+        den = fmaf(e, ml[j].y, den);
+        o.x = fmaf(e, x.x, o.x);
+        o.y = fmaf(e, x.y, o.y);
+        o.z = fmaf(e, x.z, o.z);
+        o.w = fmaf(e, x.w, o.w);
+    }
+    if (part < 0) {
+        const float r = den > 0.0f ? 1.0f / den : 0.0f;
+        uint2 y;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
+        y.x = *reinterpret_cast<const uint32_t *>(&lo);
+        y.y = *reinterpret_cast<const uint32_t *>(&hi);
+        reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(w.b) * a.H_q + w.g * a.group + h) * D)[d4] = y;
+    } else {
+        reinterpret_cast<float4 *>(a.part_acc + (static_cast<size_t>(part) * 8 + h) * D)[d4] = o;
+        if (d4 == 0) *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * 8 + h) * 2) = make_float2(M, den);
     }
 }
 
@@ -234,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     constexpr int D = GR * 64, GB = 8 * BITS;  // bytes of a group's codes in one row
     extern __shared__ __align__(128) uint8_t base[];
     Fixed &F = *reinterpret_cast<Fixed *>(base);
-    float *merge = reinterpret_cast<float *>(base + kFixed);  // [2][warp][head][kMergeRow]
-    uint8_t *ring = base + kFixed + kMergeBytes;
+    float *merge = reinterpret_cast<float *>(base + kFixed);  // [warp][head][merge_row]
+    uint8_t *ring = base + kFixed + merge_bytes(D);
     constexpr int CB = GR * bs * GB, PB = GR * bs * 4, SB = 2 * (CB + PB);  // codes, parameters, stage
     constexpr int IH = GR == 4 ? 1 : 2, kUnit = 16 * IH;  // a warp takes one or two halves of 16 tokens at a time
     const int NS = a.stages, G = a.group;
@@ -264,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
         int issued = 0;
         bool ok = true;
         while (w.left > 0 && ok) {
-            const int nblk = blocks_of(w.L, bs), n = static_cast<int>(min(static_cast<long long>(nblk - w.j0), w.left));
+            const int nblk = blocks_of(w.L, bs), n = min(nblk - w.j0, w.left);
             for (int i0 = 0; i0 < n && ok; i0 += 32) {
                 int pb = 0;
                 if (i0 + lane < n && w.L > 0) {
@@ -306,13 +345,23 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     }
 
     // ---------------------------------------------------- consumers
-    if (!a.whole && threadIdx.x == 0 && !a.key_by_segment) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (!a.whole && threadIdx.x == 0 && !a.key_by_segment && w.left == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     constexpr int ups = bs / kUnit;  // units per stage
-    int unit = 0, stage0 = 0;    // units and stages of the segments before this one
+    int unit = 0, stage0 = 0, bar = 0;  // units and stages of the segments before this one; named barrier
     bool ok = true;
     while (w.left > 0) {
-        const int nblk = blocks_of(w.L, bs), n = static_cast<int>(min(static_cast<long long>(nblk - w.j0), w.left));
-        const int tok0 = w.j0 * bs;
+        const int nblk = blocks_of(w.L, bs), n = min(nblk - w.j0, w.left);
+        const int tok0 = w.j0 * bs, units = n * ups;
+        // the units are dealt to the warps in turn; a warp that gets none of this segment goes on to the next one,
+        // so short segments are worked on side by side
+        const int first = (warp - unit % kNW + kNW) % kNW, active = min(units, kNW);
+        if (first >= units) {
+            unit += units;
+            stage0 += n;
+            bar = (bar + 1) % kBarriers;
+            advance(a, w, n);
+            continue;
+        }
 
         // ---- q: per head a power of two into fp16, the operand registers of the K steps, sums per group
         uint32_t qb[GR * 4][2];
@@ -335,30 +384,29 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
             }
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            const int e = big > 0.0f ? 14 - ilogbf(big) : 0;
-            const float e1 = scalbnf(1.0f, e / 2), e2 = scalbnf(1.0f, e - e / 2);  // 2^e may pass the fp32 range, its halves do not
+            // 2^(14 - floor(log2 big)): its exponent field, within the normal numbers
+            const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
+            const float up = __uint_as_float(static_cast<uint32_t>(ef) << 23);
 #pragma unroll
             for (int c = 0; c < GR; ++c) {
-                float qv[16], s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    qv[2 * i] = lo_bf16(xs[c][i]) * e1 * e2;
-                    qv[2 * i + 1] = hi_bf16(xs[c][i]) * e1 * e2;
-                    s += qv[2 * i] + qv[2 * i + 1];
-                }
+                float ones[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float odd = BITS == 4 && (j & 1) ? 0.0625f : 1.0f;  // those codes carry 2^-20
+                    const float u = BITS == 4 && (j & 1) ? up * 0.0625f : up;  // those codes carry 2^-20
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        qb[c * 4 + j][r] = pack_f16(qv[k_channel<BITS>(j, 2 * r)] * odd, qv[k_channel<BITS>(j, 2 * r + 1)] * odd);
+                    for (int r = 0; r < 2; ++r) {
+                        const int i0 = k_channel<BITS>(j, 2 * r), i1 = k_channel<BITS>(j, 2 * r + 1);
+                        qb[c * 4 + j][r] = pack_f16((i0 & 1 ? hi_bf16(xs[c][i0 / 2]) : lo_bf16(xs[c][i0 / 2])) * u,
+                                                    (i1 & 1 ? hi_bf16(xs[c][i1 / 2]) : lo_bf16(xs[c][i1 / 2])) * u);
+                    }
+                    // the sums over the group, heads 2t and 2t + 1, by a step against ones (16 where q has a sixteenth)
+                    const uint32_t one = BITS == 4 && (j & 1) ? 0x4C004C00u : 0x3C003C00u;
+                    mma_f16(ones, one, one, one, one, qb[c * 4 + j][0], qb[c * 4 + j][1]);
                 }
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
-                qsum[c][0] = __shfl_sync(0xffffffffu, s, 8 * t) * 0x1p-24f;      // heads 2t and 2t + 1
-                qsum[c][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4) * 0x1p-24f;
+                qsum[c][0] = ones[0] * 0x1p-24f;
+                qsum[c][1] = ones[1] * 0x1p-24f;
             }
-            const float m = scalbnf(a.scale_log2 * 0x1p24f, -e);
+            const float m = a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23);
             mul[0] = __shfl_sync(0xffffffffu, m, 8 * t);
             mul[1] = __shfl_sync(0xffffffffu, m, 8 * t + 4);
         }
@@ -372,10 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                 for (int x = 0; x < 4; ++x) acc[c][m][x] = 0.0f;
         }
 
-        const int units = n * ups;
-        for (int u = (warp - unit % kNW + kNW) % kNW; u < units; u += kNW) {
-            const int st = stage0 + u / ups, slot = st % NS, r0 = (u % ups) * kUnit;
-            ok = ok && mbar_wait(&F.full[slot], (st / NS) & 1, &F.abort, status);
+        for (int u = first; u < units; u += kNW) {
+            const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
+            ok = ok && mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t *kq = ring + static_cast<size_t>(slot) * SB, *kp = kq + CB, *vq = kp + PB, *vp = vq + CB;
@@ -437,17 +484,25 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                     for (int x = 0; x < 4; ++x) s4[x] *= mul[x & 1];
                 }
             }
-            // scale and bias of V, tokens row + 16 i + 8 h; nothing for rows behind the sequence, whatever they hold
-            auto v_param = [&](int i, int c, int h) {
-                const uint32_t x = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
-                return token_of(gi) + 16 * i + 8 * h < left ? x : 0u;
-            };
+            uint32_t vw[IH][GR][2];  // scale, bias of V: tokens row + 16 i + 8 h
+#pragma unroll
+            for (int i = 0; i < IH; ++i)
+#pragma unroll
+                for (int c = 0; c < GR; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        vw[i][c][h] = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
             if (left < kUnit) {
+                // rows behind the sequence: no weight, whatever they hold
 #pragma unroll
                 for (int i = 0; i < IH; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        if (token_of(gi) + 16 * i + 8 * h >= left) sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
+                        if (token_of(gi) + 16 * i + 8 * h >= left) {
+                            sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < GR; ++c) vw[i][c][h] = 0u;
+                        }
             }
 
             // ---- running maximum, and the power of two of the value scales: both move rarely
@@ -459,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < IH; ++i)
 #pragma unroll
-                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(v_param(i, c, 0))), fabsf(lo_bf16(v_param(i, c, 1)))));
+                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(vw[i][c][0])), fabsf(lo_bf16(vw[i][c][1]))));
             const bool grew = top0 > m_run[0] + 8.0f || top1 > m_run[1] + 8.0f;
             if (__any_sync(0xffffffffu, grew || smax * f > 128.0f)) {
                 float mn0 = top0, mn1 = top1;
@@ -498,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                 }
             }
 
-            asm volatile("" ::: "memory");  // the parameters are loaded again: 16 registers fewer
             // ---- O^T += V^T P: weights p s f in fp16, tokens on K
 #pragma unroll
             for (int i = 0; i < IH; ++i) {
@@ -510,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                 const float pf[4] = {p[0] * f, p[1] * f, p[2] * f, p[3] * f};
 #pragma unroll
                 for (int c = 0; c < GR; ++c) {
-                    const uint32_t w0 = v_param(i, c, 0), w1 = v_param(i, c, 1);
+                    const uint32_t w0 = vw[i][c][0], w1 = vw[i][c][1];
                     const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
                     bsum[c][0] = fmaf(p[0], b0, fmaf(p[2], b1, bsum[c][0]));
                     bsum[c][1] = fmaf(p[1], b0, fmaf(p[3], b1, bsum[c][1]));
@@ -546,8 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                     }
                 }
             }
+            // the last one is given back after the join: no segment then meets another that has its named barrier
             __syncwarp();
-            if (lane == 0) mbar_arrive(&F.empty[slot]);
+            if (lane == 0 && u + kNW < units) mbar_arrive(&F.empty[slot]);
         }
 
         // ---- the segment's end: this warp's sums over its lanes, then the warps through shared memory
@@ -562,7 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
         }
         const float rf = 1.0f / f;
         const bool starts = w.j0 == 0, ends = w.j0 + n == nblk;
-        const int part = 2 * blockIdx.x + (starts ? 1 : 0), active = min(units, kNW);
+        const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+        auto join_sync = [&]() {
+            if (active > 1)
+                named_barrier_sync(1 + bar, active * 32);
+            else
+                __syncwarp();
+        };
         if (gi == 0) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -571,58 +632,33 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
             }
         }
 #pragma unroll
-        for (int c = 0; c < GR; ++c) {  // 64 channels at a time, the two halves of the buffer in turn
-            float *buf = merge + (c & 1) * kNW * 8 * kMergeRow;
+        for (int x = 0; x < 2; ++x) {
+            float *dst = merge + (warp * 8 + 2 * t + x) * merge_row(D) + gi * 8;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float *dst = buf + (warp * 8 + 2 * t + x) * kMergeRow + gi * 8;
+            for (int c = 0; c < GR; ++c) {
                 auto out = [&](int m, int h) {
                     const float unit_scale = BITS == 4 && (m & 1) ? 0x1p20f : 0x1p24f;
                     return fmaf(acc[c][m][2 * h + x] * unit_scale, rf, bsum[c][x]);
                 };
-                *reinterpret_cast<float4 *>(dst) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
-                *reinterpret_cast<float4 *>(dst + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));
-            }
-            named_barrier_sync(kBarConsumers, kNW * 32);
-            const int h = threadIdx.x / 16, d4 = threadIdx.x % 16;
-            if (h < G) {
-                float M = kNoMax, den = 0.0f;
-                for (int j = 0; j < active; ++j) M = fmaxf(M, F.ml[(unit + j) % kNW][h][0]);
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int j = 0; j < active; ++j) {
-                    const int wj = (unit + j) % kNW;
-                    const float e = ex2(F.ml[wj][h][0] - M);
-                    const float4 x = *reinterpret_cast<const float4 *>(buf + (wj * 8 + h) * kMergeRow + d4 * 4);
-                    den = fmaf(e, F.ml[wj][h][1], den);
-                    o.x = fmaf(e, x.x, o.x);
-                    o.y = fmaf(e, x.y, o.y);
-                    o.z = fmaf(e, x.z, o.z);
-                    o.w = fmaf(e, x.w, o.w);
-                }
-                if (starts && ends) {
-                    const float r = den > 0.0f ? 1.0f / den : 0.0f;
-                    uint2 y;
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
-                    y.x = *reinterpret_cast<const uint32_t *>(&lo);
-                    y.y = *reinterpret_cast<const uint32_t *>(&hi);
-                    reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(w.b) * a.H_q + w.g * G + h) * D)[c * 16 + d4] = y;
-                } else {
-                    reinterpret_cast<float4 *>(a.part_acc + (static_cast<size_t>(part) * 8 + h) * D)[c * 16 + d4] = o;
-                    if (c == 0 && d4 == 0)
-                        *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * 8 + h) * 2) = make_float2(M, den);
-                }
+                *reinterpret_cast<float4 *>(dst + c * 64) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
+                *reinterpret_cast<float4 *>(dst + c * 64 + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));
             }
         }
-        if (!a.whole && threadIdx.x == 0 && starts && (!ends || a.key_by_segment)) {
+        join_sync();
+        for (int i = first * 32 + lane; i < G * (D / 4); i += active * 32)
+            join_column<D>(a, F, merge, w, unit, active, starts && ends ? -1 : part, i / (D / 4), i % (D / 4));
+        if (!a.whole && first == 0 && lane == 0 && (a.key_by_segment ? starts : w.left == n)) {
             // who joins the parts: the CTAs from this one to the one that has the segment's last block
             const int bg = w.b * a.c.H_kv + w.g;
-            const int last = static_cast<int>(((F.begin + stage0 + nblk) * F.used - 1) / F.total);
-            a.meta[a.key_by_segment ? bg : blockIdx.x] = make_int4(ends ? -1 : bg, blockIdx.x, last, 0);
+            const int last = static_cast<int>((static_cast<long long>(F.begin + stage0 - w.j0 + nblk) * F.used - 1) / F.total);
+            a.meta[a.key_by_segment ? bg : blockIdx.x] = make_int4(starts && !ends ? bg : -1, blockIdx.x, last, 0);
         }
         unit += units;
+        join_sync();
+        if (lane == 0 && ok) mbar_arrive(&F.empty[(stage0 + (units - 1 - (units - 1 - first) % kNW) / ups) % NS]);
         stage0 += n;
         advance(a, w, n);
-        named_barrier_sync(kBarConsumers, kNW * 32);
+        bar = (bar + 1) % kBarriers;
     }
 }
 
@@ -717,7 +753,7 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
 template <int BITS, int GR, int bs>
 cudaError_t launch(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 {
-    const size_t smem = kFixed + kMergeBytes + static_cast<size_t>(a.stages) * stage_bytes(64 * GR, bs, BITS);
+    const size_t smem = kFixed + merge_bytes(64 * GR) + static_cast<size_t>(a.stages) * stage_bytes(64 * GR, bs, BITS);
     const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR, bs>), static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     return launch_pdl(kvq_decode_kernel<BITS, GR, bs>, dim3(ctas), dim3(kThreads), smem, stream, a);
@@ -745,6 +781,7 @@ cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
     a.whole = static_cast<long long>(a.max_blocks) * a.c.bs <= kWholeTokens;
     a.key_by_segment = segments <= kKvqDecodeCtas;
     a.stages = stages_for(a.D, a.c.bs, a.c.bits);
+    a.stages_inv = 0xFFFFFFFFu / a.stages + 1;  // x / stages = the high word of x stages_inv for x < 2^32 / stages
     const int ctas = a.whole ? static_cast<int>(segments) : kKvqDecodeCtas;
     const cudaError_t e = a.c.bits == 4 ? launch_d<4>(a, ctas, stream) : launch_d<8>(a, ctas, stream);
     if (e != cudaSuccess || a.whole) return e;

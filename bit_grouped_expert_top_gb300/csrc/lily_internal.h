@@ -222,6 +222,7 @@ struct KvqAttnArgs {
     float *part_ml;               // [2 CTAs][8][2]: max (log2 units), sum of weights
     float *part_acc;              // [2 CTAs][8][D]
     int whole, key_by_segment, stages;  // set by launch_kvq_decode
+    unsigned int stages_inv;            // ceil(2^32 / stages)
 };
 constexpr int kKvqMaxGroup = 8;      // query heads per KV head
 // CTAs of the decode kernel, one per SM of a GB300: a constant, so that the work

@@ -336,7 +336,8 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
  *
  * Supported: bits in {4, 8}; D in {64, 128, 256}; block_size in {32, 64, 128};
  * H_q % H_kv == 0 and H_q / H_kv <= 8; 1 <= B <= 65535; H_kv <= 4096;
- * max_blocks * block_size < 2^31.  Byte offsets are 64-bit.
+ * max_blocks * block_size < 2^31; B * H_kv * max_blocks < 2^31.  Byte offsets are
+ * 64-bit.
  * Device-detected (read with lily_moe_device_status on the workspace that the
  * call was given): a used table entry outside [0, n_blocks) or a position or
  * length outside [0, max_blocks * block_size] records LILY_ERR_DEVICE_INDEX.
