@@ -67,6 +67,7 @@ class lily_kvq_shape(ctypes.Structure):
 class lily_kvq_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_q", "k_sb", "v_q", "v_sb")] + [
         (n, ctypes.c_int64) for n in ("n_blocks", "code_bytes")]
+    device = 0  # CUDA device of the arrays (not part of the C struct)
 
 
 class lily_moe_decode_trace(ctypes.Structure):
@@ -375,8 +376,10 @@ def make_kvq_cache(tensors: Dict[str, torch.Tensor]) -> lily_kvq_cache:
             raise ValueError(f"cache arrays of unlike shapes: {n}_q {tuple(q.shape)}, {n}_sb {tuple(sb.shape)}")
         if q.device != k_q.device or sb.device != k_q.device:
             raise ValueError("cache arrays on different devices")
-    return lily_kvq_cache(_ptr(k_q), _ptr(tensors["k_sb"]), _ptr(tensors["v_q"]), _ptr(tensors["v_sb"]),
-                          k_q.shape[0], k_q.numel())
+    cache = lily_kvq_cache(_ptr(k_q), _ptr(tensors["k_sb"]), _ptr(tensors["v_q"]), _ptr(tensors["v_sb"]),
+                           k_q.shape[0], k_q.numel())
+    cache.device = k_q.get_device()
+    return cache
 
 
 def lily_kvq_workspace_bytes(shape: lily_kvq_shape, n_query: int = 0) -> int:
@@ -392,43 +395,64 @@ def alloc_kvq_workspace(shape: lily_kvq_shape, n_query: int = 0, device="cuda") 
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _on_current_device(name: str, t) -> None:
-    """The library launches on the current device: a tensor elsewhere is refused."""
-    if not t.is_cuda:
+# The checks of a call's tensors are written flat: a decode step of short sequences
+# takes the GPU less time than a careless wrapper takes the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream without a Stream object
+
+
+def _device_of(name: str, t, cache) -> int:
+    """The device of the call's first tensor: the library launches on the current
+    device, so a tensor (or a cache) elsewhere is refused."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
-    if t.get_device() != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, {name} on cuda:{dev}")
+    return dev
 
 
-def _dense(name: str, t, dtype, shape: tuple) -> int:
-    """Address of a dense CUDA tensor of this dtype and at least this shape's size."""
-    if t.dtype != dtype or t.numel() < math.prod(shape):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    _on_current_device(name, t)
-    return _ptr(t)
+def _dense(name: str, t, dtype, n: int, dev: int) -> int:
+    """Address of a dense tensor of this dtype and device with at least n elements."""
+    if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} on cuda:{dev}, got {t.dtype} {list(t.shape)} with "
+                         f"strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
-def _tokens(name: str, t, heads: int, D: int):
-    """Address and token stride of a bf16 [n][heads][D] CUDA tensor whose tokens are dense."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name}: expected bfloat16 [n][{heads}][{D}], got {t.dtype} {list(t.shape)}")
-    _on_current_device(name, t)
-    s0, s1, s2 = t.stride()
-    if (heads > 1 and s1 != D) or s2 != 1:
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * D)
+def _tokens(name: str, t, heads: int, D: int, dev: int):
+    """Address and token stride of a bf16 [n][heads][D] tensor whose tokens are dense."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name}: expected bfloat16 [n][{heads}][{D}], got {t.dtype} {list(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a CUDA tensor on cuda:{dev}, got one on {t.device}")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != D and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {stride}")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * D)
+
+
+def _launch_stream(stream, dev: int):
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _kvq_copy(fn: str, shape, cache, k, v, cu, starts, block_table, ws, stream, check: bool) -> int:
-    N, i32 = k.shape[0], torch.int32
+    N, B, H, D, i32 = k.shape[0], shape.B, shape.H_kv, shape.D, torch.int32
+    if k.dtype is not torch.bfloat16:
+        raise ValueError(f"k: expected bfloat16, got {k.dtype}")
     if v.shape[0] != N:
         raise ValueError(f"k has {N} tokens, v {v.shape[0]}")
-    pk, sk = _tokens("k", k, shape.H_kv, shape.D)
-    pv, sv = _tokens("v", v, shape.H_kv, shape.D)
-    rc = getattr(load(), fn)(ctypes.byref(shape), ctypes.byref(cache), pk, sk, pv, sv, N,
-                             _dense("cu", cu, i32, (shape.B + 1,)), _dense("starts", starts, i32, (shape.B,)),
-                             _dense("block_table", block_table, i32, (shape.B, shape.max_blocks)),
-                             _ptr(ws), ws.numel(), _stream(stream))
+    dev = _device_of("k", k, cache)
+    pk, sk = _tokens("k", k, H, D, dev)
+    pv, sv = _tokens("v", v, H, D, dev)
+    rc = getattr(_lib or load(), fn)(
+        ctypes.byref(shape), ctypes.byref(cache), pk, sk, pv, sv, N, _dense("cu", cu, i32, B + 1, dev),
+        _dense("starts", starts, i32, B, dev), _dense("block_table", block_table, i32, B * shape.max_blocks, dev),
+        _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
     return _check(fn, rc) if check else rc
 
 
@@ -445,18 +469,28 @@ def lily_kvq_read(shape: lily_kvq_shape, cache: lily_kvq_cache, k, v, cu, starts
     return _kvq_copy("lily_kvq_read", shape, cache, k, v, cu, starts, block_table, ws, stream, check)
 
 
+def _kvq_query(q, H: int, D: int, cache) -> int:
+    if q.dtype is not torch.bfloat16:
+        raise ValueError(f"q: expected bfloat16 [n][{H}][{D}], got {q.dtype} {list(q.shape)}")
+    if q.dim() != 3 or q.shape[1] != H or q.shape[2] != D:
+        raise ValueError(f"q: expected bfloat16 [n][{H}][{D}], got {list(q.shape)}")
+    return _device_of("q", q, cache)
+
+
 def lily_kvq_attn_decode(shape: lily_kvq_shape, cache: lily_kvq_cache, q, block_table, seq_lens, out, ws,
                          scale: Optional[float] = None, stream=None, *, check: bool = True) -> int:
     """Decode attention over the quantised cache (see include/lily_moe.h): q and
     out bf16 [B][H_q][D].  scale defaults to 1/sqrt(D)."""
     B, H, D, i32 = shape.B, shape.H_q, shape.D, torch.int32
-    pq, sq = _tokens("q", q, H, D)
+    dev = _kvq_query(q, H, D, cache)
+    pq, sq = _tokens("q", q, H, D, dev)
     if q.shape[0] != B:
         raise ValueError(f"q: expected {B} sequences, got {q.shape[0]}")
-    rc = load().lily_kvq_attn_decode(ctypes.byref(shape), ctypes.byref(cache), pq, sq,
-                                     _dense("block_table", block_table, i32, (B, shape.max_blocks)),
-                                     _dense("seq_lens", seq_lens, i32, (B,)), D ** -0.5 if scale is None else scale,
-                                     _dense("out", out, torch.bfloat16, (B, H, D)), _ptr(ws), ws.numel(), _stream(stream))
+    rc = (_lib or load()).lily_kvq_attn_decode(
+        ctypes.byref(shape), ctypes.byref(cache), pq, sq, _dense("block_table", block_table, i32, B * shape.max_blocks, dev),
+        _dense("seq_lens", seq_lens, i32, B, dev), D ** -0.5 if scale is None else scale,
+        _dense("out", out, torch.bfloat16, B * H * D, dev), _dense("ws", ws, torch.uint8, 1, dev), ws.numel(),
+        _launch_stream(stream, dev))
     return _check("lily_kvq_attn_decode", rc) if check else rc
 
 
@@ -466,13 +500,13 @@ def lily_kvq_attn_prefill(shape: lily_kvq_shape, cache: lily_kvq_cache, q, cu_q,
     [N][H_q][D], rows by cu_q) over the quantised cache that already holds the
     chunk's keys.  scale defaults to 1/sqrt(D)."""
     B, H, D, N, i32 = shape.B, shape.H_q, shape.D, q.shape[0], torch.int32
-    pq, sq = _tokens("q", q, H, D)
-    rc = load().lily_kvq_attn_prefill(ctypes.byref(shape), ctypes.byref(cache), pq, sq, N,
-                                      _dense("cu_q", cu_q, i32, (B + 1,)),
-                                      _dense("block_table", block_table, i32, (B, shape.max_blocks)),
-                                      _dense("seq_lens", seq_lens, i32, (B,)), D ** -0.5 if scale is None else scale,
-                                      _dense("out", out, torch.bfloat16, (N, H, D)), _ptr(ws), ws.numel(),
-                                      _stream(stream))
+    dev = _kvq_query(q, H, D, cache)
+    pq, sq = _tokens("q", q, H, D, dev)
+    rc = (_lib or load()).lily_kvq_attn_prefill(
+        ctypes.byref(shape), ctypes.byref(cache), pq, sq, N, _dense("cu_q", cu_q, i32, B + 1, dev),
+        _dense("block_table", block_table, i32, B * shape.max_blocks, dev), _dense("seq_lens", seq_lens, i32, B, dev),
+        D ** -0.5 if scale is None else scale, _dense("out", out, torch.bfloat16, N * H * D, dev),
+        _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
     return _check("lily_kvq_attn_prefill", rc) if check else rc
 
 

@@ -9,8 +9,11 @@
 //   scale = bf16((hi - lo) / L),  code = min(rint((x - lo) / scale), L),
 //   value = code * scale + lo.
 //
-// Eight threads hold one group, eight channels each: the extremes are three
-// butterfly shuffles.
+// Bound: HBM (2 + 0.5625 bytes a value at 4 bits, 2 + 1.0625 at 8).  A warp takes
+// four consecutive tokens of one (K or V, head, group): eight threads a token, eight
+// channels each, so that it reads whole 128-byte lines of the bf16 side and touches
+// one 128-byte run of codes; four such steps are in flight per thread.  The extremes
+// are three butterfly shuffles of one packed register (lo, -hi).
 #include <cstdint>
 
 #include "lily_device.cuh"
@@ -56,124 +59,215 @@ __device__ __forceinline__ long long group_index(const KvqCache &c, int2 slot, i
     return ((static_cast<long long>(slot.x) * c.H_kv + head) * c.groups + group) * c.bs + slot.y;
 }
 
-// The codes of eight channels x (fp32) of a group, packed low to high.
+// Scale and bias of a group, and what its codes are computed with: code =
+// min(rint(q), L) with q = (x - lo) / scale, correctly rounded as in Markstein's
+// division: q0 = d r with r = 1 / h, then q = q0 + r (d - q0 h) with fused
+// multiply-adds, for d = (x - lo) m and h = scale m.  The factor m (a power of two)
+// keeps every term within the normal numbers: x - lo of any two finite bf16 values is
+// finite in halves, and below a scale of 2^-40 all of the group is below 2^-24, so 2^64
+// lifts the remainder out of the subnormals.
+struct GroupScale {
+    float m, h, r, mlo;
+    uint32_t sb;  // scale, bias as stored
+};
 template <int BITS>
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float lo, float scale)
+__device__ __forceinline__ GroupScale group_scale(float lo, float hi)
 {
     constexpr float L = BITS == 4 ? 15.0f : 255.0f;
+    GroupScale g;
+    float scale = __bfloat162float(__float2bfloat16_rn((0.5f * hi - 0.5f * lo) / (0.5f * L)));
+    if (!(scale >= 1.17549435e-38f)) scale = 0.0f;  // 2^-126
+    g.m = scale < 0x1p-40f ? 0x1p64f : 0.5f;
+    g.h = scale * g.m;
+    g.r = scale > 0.0f ? 1.0f / g.h : 0.0f;  // 0: every code is 0
+    g.mlo = -lo * g.m;
+    g.sb = (__float_as_uint(scale) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
+    return g;
+}
+
+// The codes of eight channels (bf16 pairs) packed low to high: n + 1.5 2^23 holds the
+// integer n in its low bits, so the codes add up by multiply-adds on the bit patterns.
+template <int BITS>
+__device__ __forceinline__ uint2 quantise8(const uint4 &w, const GroupScale &g)
+{
+    constexpr float L = BITS == 4 ? 15.0f : 255.0f;
+    constexpr uint32_t kMagic = 0x4B400000u, kStep = 1u << BITS;
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
     uint32_t c[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float t = scale > 0.0f ? fminf(rintf((0.5f * x[j] - 0.5f * lo) / (0.5f * scale)), L) : 0.0f;
-        c[j] = static_cast<uint32_t>(t);
+        const float x = j & 1 ? __uint_as_float(ws[j / 2] & 0xFFFF0000u) : __uint_as_float(ws[j / 2] << 16);
+        const float d = fmaf(x, g.m, g.mlo);
+        const float q0 = __fmul_rn(d, g.r);
+        const float q = fmaf(g.r, fmaf(-q0, g.h, d), q0);
+        c[j] = __float_as_uint(__fadd_rn(fminf(q, L), 12582912.0f));
     }
-    uint2 w = make_uint2(0u, 0u);
     if (BITS == 4) {
+        uint32_t p = c[7], k = kMagic;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w.x |= c[j] << (4 * j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w.x |= c[j] << (8 * j);
-            w.y |= c[j + 4] << (8 * j);
+        for (int j = 6; j >= 0; --j) {
+            p = p * kStep + c[j];
+            k = k * kStep + kMagic;
         }
+        return make_uint2(p - k, 0u);
     }
-    return w;
+    uint32_t p = c[3], q = c[7], k = kMagic;
+#pragma unroll
+    for (int j = 2; j >= 0; --j) {
+        p = p * kStep + c[j];
+        q = q * kStep + c[j + 4];
+        k = k * kStep + kMagic;
+    }
+    return make_uint2(p - k, q - k);
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads) kvq_append_kernel(const KvqCopyArgs a)
+__device__ __forceinline__ uint32_t bf16x2_min(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+constexpr int kBatch = 4;  // groups of a warp's tokens in flight
+
+// The CTA's 4 QUADS tokens from blockIdx.x 4 QUADS on: their cache rows, then
+// fn(token within the call, slot, which, head * groups + group) for every quad and
+// (K or V, head, group), in batches: `load` for all of a batch, then `use`.
+template <int QUADS, typename T, typename Load, typename Use>
+__device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &load, const Use &use)
+{
+    __shared__ int2 slots[4 * QUADS];
+    const int n0 = blockIdx.x * (4 * QUADS);
+    if (threadIdx.x < 4 * QUADS)
+        slots[threadIdx.x] = n0 + static_cast<int>(threadIdx.x) < a.N ? token_slot(a, n0 + threadIdx.x) : make_int2(-1, 0);
+    __syncthreads();
+    const int warp = threadIdx.x / 32, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8;
+    const int2 slot = slots[tok];
+    const long long n = n0 + tok;
+    const int per = a.c.H_kv * a.c.groups, units = 2 * per;
+    constexpr int kStride = kThreads / 32 / QUADS;
+    for (int u0 = warp / QUADS; u0 < units; u0 += kStride * kBatch) {
+        T v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * kStride;
+            if (slot.x >= 0 && u < units) v[i] = load(n, slot, u >= per, u >= per ? u - per : u);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * kStride;
+            if (u < units) use(n, slot, u >= per, u >= per ? u - per : u, v[i]);  // the whole warp
+        }
+    }
+}
+
+template <int BITS, int QUADS>
+__global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_constant__ KvqCopyArgs a)
 {
     pdl_trigger();
     pdl_wait();
-    const int n = blockIdx.x;
-    const int2 slot = token_slot(a, n);
-    if (slot.x < 0) return;
-    const int units = 2 * a.c.H_kv * a.c.groups;  // K, then V
-    for (int u0 = 0; u0 < units; u0 += kThreads / 8) {
-        const int u = u0 + threadIdx.x / 8, e = threadIdx.x % 8;
-        const bool act = u < units;
-        const int uu = act ? u : 0;
-        const int which = uu / (a.c.H_kv * a.c.groups), hg = uu % (a.c.H_kv * a.c.groups);
-        const uint16_t *src = which ? a.v + n * a.v_stride : a.k + n * a.k_stride;
-        const uint4 w = *reinterpret_cast<const uint4 *>(src + hg * 64 + e * 8);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float x[8];
+    const int e = threadIdx.x % 8;
+    for_tokens<QUADS, uint4>(
+        a,
+        [&](long long n, int2, bool isv, int hg) {
+            const uint16_t *src = isv ? a.v + n * a.v_stride : a.k + n * a.k_stride;
+            return *reinterpret_cast<const uint4 *>(src + hg * 64 + e * 8);
+        },
+        [&](long long, int2 slot, bool isv, int hg, const uint4 &w) {
+            const uint32_t lo2 = bf16x2_min(bf16x2_min(w.x, w.y), bf16x2_min(w.z, w.w));
+            const uint32_t hi2 = bf16x2_max(bf16x2_max(w.x, w.y), bf16x2_max(w.z, w.w)) ^ 0x80008000u;  // -hi
+            // (lo, -hi): the two halves of each, then the eight threads
+            uint32_t x = bf16x2_min(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(ws[j] << 16);
-            x[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-        }
-        float lo = x[0], hi = x[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) {
-            lo = fminf(lo, x[j]);
-            hi = fmaxf(hi, x[j]);
-        }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        // halves, so that the range of any two finite bf16 values is finite
-        constexpr float L = BITS == 4 ? 15.0f : 255.0f;
-        const __nv_bfloat16 sb = __float2bfloat16_rn((0.5f * hi - 0.5f * lo) / (0.5f * L));
-        float scale = __bfloat162float(sb);
-        if (!(scale >= 1.17549435e-38f)) scale = 0.0f;
-        const uint2 c = quantise8<BITS>(x, lo, scale);
-        if (!act) continue;
-        const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
-        uint8_t *dq = (which ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
-        if (BITS == 4)
-            *reinterpret_cast<uint32_t *>(dq) = c.x;
-        else
-            *reinterpret_cast<uint2 *>(dq) = c;
-        if (e == 0)
-            *reinterpret_cast<uint32_t *>((which ? a.c.v_sb : a.c.k_sb) + gi * 2) =
-                (__float_as_uint(scale) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
-    }
+            for (int o = 1; o < 8; o <<= 1) x = bf16x2_min(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (slot.x < 0) return;
+            const GroupScale g = group_scale<BITS>(__uint_as_float(x << 16), -__uint_as_float(x & 0xFFFF0000u));
+            const uint2 c = quantise8<BITS>(w, g);
+            const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
+            uint8_t *dq = (isv ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
+            if (BITS == 4)
+                *reinterpret_cast<uint32_t *>(dq) = c.x;
+            else
+                *reinterpret_cast<uint2 *>(dq) = c;
+            if (e == 0) *reinterpret_cast<uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2) = g.sb;
+        });
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads) kvq_read_kernel(const KvqCopyArgs a)
+template <int BITS, int QUADS>
+__global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constant__ KvqCopyArgs a)
 {
     pdl_trigger();
     pdl_wait();
-    const int n = blockIdx.x;
-    const int2 slot = token_slot(a, n);
-    if (slot.x < 0) return;
-    const int units = 2 * a.c.H_kv * a.c.groups;
-    for (int i = threadIdx.x; i < units * 8; i += kThreads) {
-        const int u = i / 8, e = i % 8;
-        const int which = u / (a.c.H_kv * a.c.groups), hg = u % (a.c.H_kv * a.c.groups);
-        const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
-        const uint8_t *sq = (which ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
-        const uint32_t sb = *reinterpret_cast<const uint32_t *>((which ? a.c.v_sb : a.c.k_sb) + gi * 2);
-        const float s = __uint_as_float(sb << 16), b = __uint_as_float(sb & 0xFFFF0000u);
-        uint32_t o[4];
+    const int e = threadIdx.x % 8;
+    struct Codes {
+        uint32_t q0, q1, sb;
+    };
+    for_tokens<QUADS, Codes>(
+        a,
+        [&](long long, int2 slot, bool isv, int hg) {
+            const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
+            const uint8_t *sq = (isv ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
+            Codes c;
+            c.q0 = reinterpret_cast<const uint32_t *>(sq)[0];
+            c.q1 = BITS == 8 ? reinterpret_cast<const uint32_t *>(sq)[BITS / 8] : 0u;
+            c.sb = *reinterpret_cast<const uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2);
+            return c;
+        },
+        [&](long long n, int2 slot, bool isv, int hg, const Codes &c) {
+            if (slot.x < 0) return;
+            const float s = __uint_as_float(c.sb << 16), b = __uint_as_float(c.sb & 0xFFFF0000u);
+            float x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t w = BITS == 4 ? *reinterpret_cast<const uint32_t *>(sq) >> (8 * j)
-                                         : static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(sq)[j]);
-            const float c0 = static_cast<float>(w & ((1u << BITS) - 1)), c1 = static_cast<float>((w >> BITS) & ((1u << BITS) - 1));
-            o[j] = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(fmaf(c0, s, b)))) |
-                   (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(fmaf(c1, s, b)))) << 16);
-        }
-        uint16_t *dst = (which ? a.v + n * a.v_stride : a.k + n * a.k_stride) + hg * 64 + e * 8;
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
+            for (int j = 0; j < 8; ++j) {
+                // 2^23 + code is the code in the low bits of the pattern of 2^23
+                const uint32_t w = BITS == 4 ? c.q0 >> (4 * j) : (j < 4 ? c.q0 : c.q1) >> (8 * (j & 3));
+                const float code = __uint_as_float((w & ((1u << BITS) - 1)) | 0x4B000000u) - 8388608.0f;
+                x[j] = fmaf(code, s, b);
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                o[j] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+            uint16_t *dst = (isv ? a.v + n * a.v_stride : a.k + n * a.k_stride) + hg * 64 + e * 8;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        });
+}
+
+// 16 tokens a CTA; four where those would leave SMs idle (fewer than 16 x 304 tokens).
+constexpr int kFewTokens = 16 * 304;
+int ctas(int N, int quads) { return (N + 4 * quads - 1) / (4 * quads); }
+
+template <int BITS>
+cudaError_t append(const KvqCopyArgs &a, cudaStream_t stream)
+{
+    return a.N < kFewTokens ? launch_pdl(kvq_append_kernel<BITS, 1>, dim3(ctas(a.N, 1)), dim3(kThreads), 0, stream, a)
+                            : launch_pdl(kvq_append_kernel<BITS, 4>, dim3(ctas(a.N, 4)), dim3(kThreads), 0, stream, a);
+}
+template <int BITS>
+cudaError_t read(const KvqCopyArgs &a, cudaStream_t stream)
+{
+    return a.N < kFewTokens ? launch_pdl(kvq_read_kernel<BITS, 1>, dim3(ctas(a.N, 1)), dim3(kThreads), 0, stream, a)
+                            : launch_pdl(kvq_read_kernel<BITS, 4>, dim3(ctas(a.N, 4)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kvq_append(const KvqCopyArgs &a, cudaStream_t stream)
 {
-    return launch_pdl(a.c.bits == 4 ? kvq_append_kernel<4> : kvq_append_kernel<8>, dim3(a.N), dim3(kThreads), 0, stream, a);
+    return a.c.bits == 4 ? append<4>(a, stream) : append<8>(a, stream);
 }
 
 cudaError_t launch_kvq_read(const KvqCopyArgs &a, cudaStream_t stream)
 {
-    return launch_pdl(a.c.bits == 4 ? kvq_read_kernel<4> : kvq_read_kernel<8>, dim3(a.N), dim3(kThreads), 0, stream, a);
+    return a.c.bits == 4 ? read<4>(a, stream) : read<8>(a, stream);
 }
 
 }  // namespace lily
