@@ -13,7 +13,11 @@
 // four consecutive tokens of one (K or V, head, group): eight threads a token, eight
 // channels each, so that it reads whole 128-byte lines of the bf16 side and touches
 // one 128-byte run of codes; four such steps are in flight per thread.  The extremes
-// are three butterfly shuffles of one packed register (lo, -hi).
+// are three butterfly shuffles of one packed register (lo, -hi).  Measured (2 KV heads
+// of 256): 65,536 tokens at 4 bits read in 31.9 us (5.4 TB/s, 0.80 of the measured copy
+// rate; writes are 78% of the bytes); with 4 heads of 128 at 8 bits, 63,251 tokens
+// written and read back in 81.2 us (4.9 TB/s).  The append is bound by issue (~19
+// instructions a value at first, 13 now), the read by HBM.
 #include <cstdint>
 
 #include "lily_device.cuh"
@@ -52,20 +56,14 @@ __device__ __forceinline__ int2 token_slot(const KvqCopyArgs &a, int n)
     return make_int2(pb, p % a.c.bs);
 }
 
-// Index of (physical block, head, group, row) in the parameter arrays (pairs)
-// and, times the bytes of a group's codes, in the code arrays.
-__device__ __forceinline__ long long group_index(const KvqCache &c, int2 slot, int head, int group)
-{
-    return ((static_cast<long long>(slot.x) * c.H_kv + head) * c.groups + group) * c.bs + slot.y;
-}
-
-// Scale and bias of a group, and what its codes are computed with: code =
-// min(rint(q), L) with q = (x - lo) / scale, correctly rounded as in Markstein's
-// division: q0 = d r with r = 1 / h, then q = q0 + r (d - q0 h) with fused
-// multiply-adds, for d = (x - lo) m and h = scale m.  The factor m (a power of two)
-// keeps every term within the normal numbers: x - lo of any two finite bf16 values is
-// finite in halves, and below a scale of 2^-40 all of the group is below 2^-24, so 2^64
-// lifts the remainder out of the subnormals.
+// Scale and bias of a group, and what its codes are computed with.  Both quotients,
+// (hi - lo) / L and q = (x - lo) / scale, are rounded correctly as in Markstein's
+// division: q0 = d r with r about 1 / h, then q = q0 + r (d - q0 h) with fused
+// multiply-adds; h has 8 bits, so no quotient of a 24-bit d comes nearer than 2^-33 to
+// a rounding border, and r may be the hardware's approximation.  All of it is computed
+// times m, a power of two that keeps every term within the normal numbers: the range of
+// two finite bf16 values is finite in halves, and where it is below 2^-32 all of the
+// group is below 2^-24 and takes 2^64.
 struct GroupScale {
     float m, h, r, mlo;
     uint32_t sb;  // scale, bias as stored
@@ -73,15 +71,19 @@ struct GroupScale {
 template <int BITS>
 __device__ __forceinline__ GroupScale group_scale(float lo, float hi)
 {
-    constexpr float L = BITS == 4 ? 15.0f : 255.0f;
+    constexpr float L = BITS == 4 ? 15.0f : 255.0f, rL = 1.0f / L;
     GroupScale g;
-    float scale = __bfloat162float(__float2bfloat16_rn((0.5f * hi - 0.5f * lo) / (0.5f * L)));
-    if (!(scale >= 1.17549435e-38f)) scale = 0.0f;  // 2^-126
-    g.m = scale < 0x1p-40f ? 0x1p64f : 0.5f;
-    g.h = scale * g.m;
-    g.r = scale > 0.0f ? 1.0f / g.h : 0.0f;  // 0: every code is 0
+    const float half = 0.5f * hi - 0.5f * lo;
+    const bool lift = half < 0x1p-33f;
+    g.m = lift ? 0x1p64f : 0.5f;
     g.mlo = -lo * g.m;
-    g.sb = (__float_as_uint(scale) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
+    const float range = fmaf(hi, g.m, g.mlo);
+    const float q0 = __fmul_rn(range, rL);
+    g.h = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q0, L, range), rL, q0)));
+    if (g.h < (lift ? 0x1p-62f : 0x1p-127f)) g.h = 0.0f;  // a scale below 2^-126
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.r) : "f"(g.h));
+    if (g.h == 0.0f) g.r = 0.0f;  // every code is 0
+    g.sb = (__float_as_uint(g.h * (lift ? 0x1p-64f : 2.0f)) >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
     return g;
 }
 
@@ -90,7 +92,7 @@ __device__ __forceinline__ GroupScale group_scale(float lo, float hi)
 template <int BITS>
 __device__ __forceinline__ uint2 quantise8(const uint4 &w, const GroupScale &g)
 {
-    constexpr float L = BITS == 4 ? 15.0f : 255.0f;
+    constexpr float L = 255.0f;
     constexpr uint32_t kMagic = 0x4B400000u, kStep = 1u << BITS;
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
     uint32_t c[8];
@@ -100,7 +102,8 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &w, const GroupScale &g)
         const float d = fmaf(x, g.m, g.mlo);
         const float q0 = __fmul_rn(d, g.r);
         const float q = fmaf(g.r, fmaf(-q0, g.h, d), q0);
-        c[j] = __float_as_uint(__fadd_rn(fminf(q, L), 12582912.0f));
+        // the scale is rounded by 2^-8 at most, so at 4 bits q stays below 15.06 and needs no limit
+        c[j] = __float_as_uint(__fadd_rn(BITS == 4 ? q : fminf(q, L), 12582912.0f));
     }
     if (BITS == 4) {
         uint32_t p = c[7], k = kMagic;
@@ -134,12 +137,20 @@ __device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b)
     return r;
 }
 
-constexpr int kBatch = 4;  // groups of a warp's tokens in flight
+// One thread's place in a call: its token's row on the bf16 side (+ 64 per group), and
+// in the codes and the parameters of K or of V (+ group_step bytes, + 2 bs elements).
+struct Place {
+    uint16_t *row;
+    uint8_t *codes;
+    uint16_t *params;
+    int bs, groups;  // groups of a token: H_kv D / 64
+    bool act;        // the token has a cache row
+};
 
-// The CTA's 4 QUADS tokens from blockIdx.x 4 QUADS on: their cache rows, then
-// fn(token within the call, slot, which, head * groups + group) for every quad and
-// (K or V, head, group), in batches: `load` for all of a batch, then `use`.
-template <int QUADS, typename T, typename Load, typename Use>
+// The CTA's 4 QUADS tokens from blockIdx.x 4 QUADS on.  Half of the warps take K,
+// half V; fn(place, group) runs for every group of the warp's four tokens, kBatch at a
+// time: `load` for all of a batch, then `use` (by the whole warp).
+template <int BITS, int QUADS, int kBatch, typename T, typename Load, typename Use>
 __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &load, const Use &use)
 {
     __shared__ int2 slots[4 * QUADS];
@@ -147,23 +158,27 @@ __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &loa
     if (threadIdx.x < 4 * QUADS)
         slots[threadIdx.x] = n0 + static_cast<int>(threadIdx.x) < a.N ? token_slot(a, n0 + threadIdx.x) : make_int2(-1, 0);
     __syncthreads();
-    const int warp = threadIdx.x / 32, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8;
+    const int warp = threadIdx.x / 32, e = threadIdx.x % 8, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8;
     const int2 slot = slots[tok];
     const long long n = n0 + tok;
-    const int per = a.c.H_kv * a.c.groups, units = 2 * per;
-    constexpr int kStride = kThreads / 32 / QUADS;
-    for (int u0 = warp / QUADS; u0 < units; u0 += kStride * kBatch) {
+    const bool isv = (warp / QUADS) & 1;
+    Place p;
+    p.act = slot.x >= 0;
+    p.bs = a.c.bs;
+    p.groups = a.c.H_kv * a.c.groups;
+    p.row = (isv ? a.v + n * a.v_stride : a.k + n * a.k_stride) + e * 8;
+    const long long at = p.act ? static_cast<long long>(slot.x) * p.groups * p.bs + slot.y : 0;
+    p.codes = (isv ? a.c.v_q : a.c.k_q) + at * (8 * BITS) + e * BITS;
+    p.params = (isv ? a.c.v_sb : a.c.k_sb) + at * 2;
+    constexpr int kStep = kThreads / 32 / QUADS / 2;
+    for (int g0 = warp / QUADS / 2; g0 < p.groups; g0 += kStep * kBatch) {
         T v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int u = u0 + i * kStride;
-            if (slot.x >= 0 && u < units) v[i] = load(n, slot, u >= per, u >= per ? u - per : u);
-        }
+        for (int i = 0; i < kBatch; ++i)
+            if (p.act && g0 + i * kStep < p.groups) v[i] = load(p, g0 + i * kStep);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int u = u0 + i * kStride;
-            if (u < units) use(n, slot, u >= per, u >= per ? u - per : u, v[i]);  // the whole warp
-        }
+        for (int i = 0; i < kBatch; ++i)
+            if (g0 + i * kStep < p.groups) use(p, g0 + i * kStep, v[i]);
     }
 }
 
@@ -172,30 +187,24 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
 {
     pdl_trigger();
     pdl_wait();
-    const int e = threadIdx.x % 8;
-    for_tokens<QUADS, uint4>(
-        a,
-        [&](long long n, int2, bool isv, int hg) {
-            const uint16_t *src = isv ? a.v + n * a.v_stride : a.k + n * a.k_stride;
-            return *reinterpret_cast<const uint4 *>(src + hg * 64 + e * 8);
-        },
-        [&](long long, int2 slot, bool isv, int hg, const uint4 &w) {
+    for_tokens<BITS, QUADS, 4, uint4>(
+        a, [](const Place &p, int g) { return *reinterpret_cast<const uint4 *>(p.row + g * 64); },
+        [](const Place &p, int g, const uint4 &w) {
             const uint32_t lo2 = bf16x2_min(bf16x2_min(w.x, w.y), bf16x2_min(w.z, w.w));
             const uint32_t hi2 = bf16x2_max(bf16x2_max(w.x, w.y), bf16x2_max(w.z, w.w)) ^ 0x80008000u;  // -hi
             // (lo, -hi): the two halves of each, then the eight threads
             uint32_t x = bf16x2_min(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) x = bf16x2_min(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (slot.x < 0) return;
-            const GroupScale g = group_scale<BITS>(__uint_as_float(x << 16), -__uint_as_float(x & 0xFFFF0000u));
-            const uint2 c = quantise8<BITS>(w, g);
-            const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
-            uint8_t *dq = (isv ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
+            if (!p.act) return;
+            const GroupScale s = group_scale<BITS>(__uint_as_float(x << 16), -__uint_as_float(x & 0xFFFF0000u));
+            const uint2 c = quantise8<BITS>(w, s);
+            uint8_t *dst = p.codes + g * p.bs * (8 * BITS);
             if (BITS == 4)
-                *reinterpret_cast<uint32_t *>(dq) = c.x;
+                *reinterpret_cast<uint32_t *>(dst) = c.x;
             else
-                *reinterpret_cast<uint2 *>(dq) = c;
-            if (e == 0) *reinterpret_cast<uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2) = g.sb;
+                *reinterpret_cast<uint2 *>(dst) = c;
+            if (threadIdx.x % 8 == 0) *reinterpret_cast<uint32_t *>(p.params + g * p.bs * 2) = s.sb;
         });
 }
 
@@ -204,45 +213,40 @@ __global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constan
 {
     pdl_trigger();
     pdl_wait();
-    const int e = threadIdx.x % 8;
     struct Codes {
-        uint32_t q0, q1, sb;
+        uint2 q;
+        uint32_t sb;
     };
-    for_tokens<QUADS, Codes>(
+    for_tokens<BITS, QUADS, 8, Codes>(
         a,
-        [&](long long, int2 slot, bool isv, int hg) {
-            const long long gi = group_index(a.c, slot, hg / a.c.groups, hg % a.c.groups);
-            const uint8_t *sq = (isv ? a.c.v_q : a.c.k_q) + gi * (8 * BITS) + e * BITS;
+        [](const Place &p, int g) {
+            const uint8_t *src = p.codes + g * p.bs * (8 * BITS);
             Codes c;
-            c.q0 = reinterpret_cast<const uint32_t *>(sq)[0];
-            c.q1 = BITS == 8 ? reinterpret_cast<const uint32_t *>(sq)[BITS / 8] : 0u;
-            c.sb = *reinterpret_cast<const uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2);
+            c.q = BITS == 8 ? *reinterpret_cast<const uint2 *>(src) : make_uint2(*reinterpret_cast<const uint32_t *>(src), 0u);
+            c.sb = *reinterpret_cast<const uint32_t *>(p.params + g * p.bs * 2);
             return c;
         },
-        [&](long long n, int2 slot, bool isv, int hg, const Codes &c) {
-            if (slot.x < 0) return;
+        [](const Place &p, int g, const Codes &c) {
+            if (!p.act) return;
             const float s = __uint_as_float(c.sb << 16), b = __uint_as_float(c.sb & 0xFFFF0000u);
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // 2^23 + code is the code in the low bits of the pattern of 2^23
-                const uint32_t w = BITS == 4 ? c.q0 >> (4 * j) : (j < 4 ? c.q0 : c.q1) >> (8 * (j & 3));
-                const float code = __uint_as_float((w & ((1u << BITS) - 1)) | 0x4B000000u) - 8388608.0f;
-                x[j] = fmaf(code, s, b);
-            }
             uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                // 2^23 + code is the code in the low bits of the pattern of 2^23
+                const uint32_t w = BITS == 4 ? c.q.x >> (8 * j) : (j < 2 ? c.q.x : c.q.y) >> (16 * (j & 1));
+                const float c0 = __uint_as_float((w & ((1u << BITS) - 1)) | 0x4B000000u) - 8388608.0f;
+                const float c1 = __uint_as_float(((w >> BITS) & ((1u << BITS) - 1)) | 0x4B000000u) - 8388608.0f;
+                const __nv_bfloat162 y = __floats2bfloat162_rn(fmaf(c0, s, b), fmaf(c1, s, b));
                 o[j] = *reinterpret_cast<const uint32_t *>(&y);
             }
-            uint16_t *dst = (isv ? a.v + n * a.v_stride : a.k + n * a.k_stride) + hg * 64 + e * 8;
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(p.row + g * 64) = make_uint4(o[0], o[1], o[2], o[3]);
         });
 }
 
-// 16 tokens a CTA; four where those would leave SMs idle (fewer than 16 x 304 tokens).
-constexpr int kFewTokens = 16 * 304;
+// 16 tokens a CTA; four where 16 would leave half of the SMs without one (a CTA's first
+// step waits for its tokens' rows, so more and smaller CTAs cost more otherwise: 4,385
+// tokens of 64 channels and 3 heads read in 5.7 us with four a CTA, 3.1 us with 16).
+constexpr int kFewTokens = 16 * 76;
 int ctas(int N, int quads) { return (N + 4 * quads - 1) / (4 * quads); }
 
 template <int BITS>
