@@ -241,15 +241,16 @@ int kvq_check_shape(const lily_kvq_shape *s)
     return LILY_OK;
 }
 
-// Workspace: control block, then the decode kernel's partial results.
+// Workspace: control block, then the partial results of the decode kernel or (n_query
+// > 0) of the prefill kernel, whichever are larger.
 struct KvqLayout {
     size_t ctrl, meta, part_ml, part_acc, total;
 };
 
 KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
 {
-    (void)n_query;
     KvqLayout L{};
+    const size_t parts = n_query > 0 ? 2 * kKvqPrefillCtas * kKvqPrefillRows : 2 * kKvqDecodeCtas * kKvqMaxGroup;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -257,9 +258,9 @@ KvqLayout kvq_layout(const lily_kvq_shape &s, int32_t n_query)
         return at;
     };
     L.ctrl = take(sizeof(Ctrl));
-    L.meta = take(kKvqDecodeCtas * sizeof(int4));
-    L.part_ml = take(2 * kKvqDecodeCtas * kKvqMaxGroup * 2 * sizeof(float));
-    L.part_acc = take(2 * kKvqDecodeCtas * kKvqMaxGroup * static_cast<size_t>(s.D) * sizeof(float));
+    L.meta = take(std::max(kKvqDecodeCtas, kKvqPrefillCtas) * sizeof(int4));
+    L.part_ml = take(parts * 2 * sizeof(float));
+    L.part_acc = take(parts * s.D * sizeof(float));
     L.total = off;
     return L;
 }

@@ -1,11 +1,29 @@
-// Attention over the quantised KV cache, for sm_103a: per query token n of
-// sequence b and query head h, with g = h / (H_q / H_kv),
-//   o = sum_{t < limit} softmax_t(scale q . k_t) v_t,
-// k_t and v_t the values code * scale + bias of row t of KV head g.
+// Prefill attention over the quantised KV cache (a chunk of query tokens per
+// sequence, causal), for sm_103a: query i of the m of sequence b, head h,
+//   o = sum_{t < L - m + i + 1} softmax_t(scale q . k_t) v_t,
+// k_t and v_t the values code * scale + bias of row t of KV head g = h / (H_q / H_kv).
 //
-// One CTA per (query token, KV head) walks the cache in tiles of 32 tokens, the
-// values rebuilt in fp32 in shared memory, with a running maximum and sum per
-// query head.
+// The tensor cores bound this one: 4 D operations per (query head, token) pair.  A
+// work item is a tile of 128 query rows: the G query heads of a KV head for TQ =
+// 128 / G tokens (one rebuilt K and V serves them all), against the cache in chunks
+// of 64 tokens.  The chunks of all items form one list that the CTAs, one per SM,
+// share evenly (a long prompt's later tiles have more of them); an item cut between
+// CTAs leaves partial results that a second kernel joins.
+// Per CTA, with every wait bounded:
+//   warps 0..3   one query row per thread: q into tensor memory as fp16 (times a
+//                power of two per row, so q has no range limit), then per chunk S
+//                from tensor memory, the softmax weights back into it as fp16 (the A
+//                operand of P V), at the end O out of it.  The running maximum moves
+//                only when a score passes it by 8 (in powers of two; the weights
+//                then stay below 2^8), so O in tensor memory is rescaled rarely.
+//   warps 4..11  rebuild K and V of a chunk in fp16 (rounded once) into swizzled
+//                shared memory, two buffers each: a thread takes one (token, group of
+//                64 channels); its codes are loaded one chunk ahead.  Rows behind the
+//                sequence become zeros.
+//   warp 12      one thread issues tcgen05.mma: S = Q K^T (A from tensor memory, B
+//                K-major) of chunk i + 1, then O += P V (B with the channels
+//                contiguous) of chunk i, so the softmax runs beside them.
+// K and V must stay within fp16: |value| >= 65520 records LILY_ERR_DEVICE_RANGE.
 #include <cmath>
 #include <cstdint>
 
@@ -15,117 +33,662 @@
 namespace lily {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 32;  // tokens per tile
+constexpr int kRows = 128;                 // query rows of a tile
+constexpr int kChunk = 64;                 // cache tokens per step
+constexpr int kSoftWarps = 4, kDeqWarps = 8, kMmaWarp = 12;
+constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
+constexpr uint32_t kTmemCols = 512;
+constexpr float kNoMax = -1.7e38f;
 
-__global__ void __launch_bounds__(kThreads) kvq_prefill_kernel(const KvqAttnArgs a)
+struct Fixed {
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
+    uint64_t pv_done[2], q_full, o_free, drain;
+    uint32_t tmem;
+    int abort, b0, m0, L0;
+    long long pre, per, begin, total, used, sum[kThreads / 32];
+};
+constexpr int kFixed = 1024;
+static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
+constexpr int smem_bytes(int D) { return 1024 + kFixed + 4 * (D / 64) * kBox; }
+
+// Tensor-memory columns: O [0, D), S / P two buffers of 64, Q D / 2.
+template <int GR>
+struct Cols {
+    static constexpr uint32_t O = 0, S = 64 * GR, Q = 64 * GR + 128;
+};
+
+// Channel, within eight, of position p in the order in which the codes unpack.
+template <int BITS>
+__device__ __forceinline__ constexpr int unpacked(int p)
 {
-    extern __shared__ float sm[];
-    const int D = a.D, G = a.group, n = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
-    float *qs = sm, *kv = qs + kKvqMaxGroup * D, *p = kv + kTile * (D + 1), *al = p + kKvqMaxGroup * kTile;
-    pdl_trigger();
-    pdl_wait();
-    int b = n, m = 1, i = 0;
-    if (a.cu_q) {
-        int lo = 0, hi = a.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu_q[mid] <= n)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        b = lo;
-        i = n - a.cu_q[b];
-        m = a.cu_q[b + 1] - a.cu_q[b];
-        if (i < 0 || i >= m) return;  // padding
-    }
-    const long long cap = static_cast<long long>(a.max_blocks) * a.c.bs;
-    long long L = a.seq_lens[b];
+    return BITS == 4 ? (p < 4 ? 2 * p : 2 * (p - 4) + 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Descriptor of an operand with its M/N side contiguous (128-byte swizzle): boxes of
+// 64 contiguous elements x rows of 128 bytes; `lead` bytes between boxes, 1024 bytes
+// between groups of eight rows.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr, uint32_t lead)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFF);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFF) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+// One lane waits for the warp.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    int go = 0;
+    if ((threadIdx.x & 31) == 0) go = mbar_wait(bar, parity, abort_flag, status);
+    return __shfl_sync(0xffffffffu, go, 0) != 0;
+}
+
+// ------------------------------------------------------------------ work list
+__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int b)
+{
+    int L = a.seq_lens[b];
+    const int cap = a.max_blocks * a.c.bs;
     if (L < 0 || L > cap) {
-        if (tid == 0) record_error(&a.ctrl->status, kErrDeviceIndex);
+        record_error(&a.ctrl->status, kErrDeviceIndex);
         L = L < 0 ? 0 : cap;
     }
-    const int limit = static_cast<int>(L - m + i + 1 > 0 ? L - m + i + 1 : 0);
-    for (int j = tid; j < G * D; j += kThreads)
-        qs[j] = __uint_as_float(static_cast<uint32_t>(a.q[n * a.q_stride + static_cast<long long>(g) * G * D + j]) << 16);
-    float acc[kKvqMaxGroup][2], mx = -INFINITY, sum = 0.0f;
-    for (int h = 0; h < kKvqMaxGroup; ++h) acc[h][0] = acc[h][1] = 0.0f;
-    const int bits = a.c.bits, bs = a.c.bs, gb = 8 * bits;
-    auto load = [&](const uint8_t *codes, const uint16_t *sb, int t0, int cnt) {
-        for (int j = tid; j < cnt * D; j += kThreads) {
-            const int t = j / D, d = j % D, pos = t0 + t;
-            int pb = a.block_table[static_cast<size_t>(b) * a.max_blocks + pos / bs];
-            if (pb < 0 || pb >= a.c.n_blocks) {
-                record_error(&a.ctrl->status, kErrDeviceIndex);
-                pb = 0;
-            }
-            const long long gi = ((static_cast<long long>(pb) * a.c.H_kv + g) * a.c.groups + d / 64) * bs + pos % bs;
-            const uint32_t w = codes[gi * gb + (bits == 4 ? (d % 64) / 2 : d % 64)];
-            const float c = static_cast<float>(bits == 4 ? (d % 2 ? w >> 4 : w & 15) : w);
-            const uint32_t q = *reinterpret_cast<const uint32_t *>(sb + gi * 2);
-            kv[t * (D + 1) + d] = fmaf(c, __uint_as_float(q << 16), __uint_as_float(q & 0xFFFF0000u));
+    return L;
+}
+// Query tokens of a sequence (rows outside the call's N are none).
+__device__ __forceinline__ int queries_of(const KvqAttnArgs &a, int b)
+{
+    const int q0 = a.cu_q[b], q1 = min(a.cu_q[b + 1], a.N);
+    return q0 < 0 || q1 <= q0 ? 0 : q1 - q0;
+}
+__device__ __forceinline__ int tile_chunks(int m, int L, int t, int TQ)
+{
+    const int limit = min(L, L - m + min(m, (t + 1) * TQ));
+    return limit > 0 ? (limit + kChunk - 1) / kChunk : 1;
+}
+// Chunks of the tiles [0, t) of a sequence.  All but the last tile have the limit
+// x + i TQ, x = L - m + TQ: the sum of ceil(. / 64) is the arithmetic series less the
+// residues, which repeat with period 64 / gcd(TQ, 64).
+__device__ __forceinline__ long long chunks_before(int m, int L, int t, int TQ)
+{
+    const int n = (m + TQ - 1) / TQ, k = min(t, n - 1);
+    if (k <= 0) return t >= n ? tile_chunks(m, L, n - 1, TQ) : 0;
+    int x = L - m + TQ, z = 0;
+    if (x <= 0) {  // tiles that see nothing count as one chunk
+        z = min(k, -x / TQ + 1);
+        x += z * TQ;
+    }
+    const long long cnt = k - z, y = x + kChunk - 1;
+    long long total = cnt * y + TQ * (cnt * (cnt - 1) / 2);
+    const int g = min(TQ & -TQ, kChunk), P = kChunk / g;
+    const int full = static_cast<int>(cnt / P), rest = static_cast<int>(cnt % P);
+    long long res = static_cast<long long>(full) * (P * (y % g) + g * (P * (P - 1) / 2));
+    int r = static_cast<int>(y % kChunk);
+    for (int i = 0; i < rest; ++i) {
+        res += r;
+        r = (r + TQ) % kChunk;
+    }
+    return z + (total - res) / kChunk + (t >= n ? tile_chunks(m, L, n - 1, TQ) : 0);
+}
+
+// A CTA's place in the list: item (b, g, t) from chunk j0 on, `left` chunks in all.
+struct Walk {
+    int b, g, t, m, L, j0;
+    long long left;
+};
+
+__device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int TQ)
+{
+    Walk w{};
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    int m = 0, L = 0;
+    long long per = 0, before = 0, all = 0;  // this thread's sequence: chunks per KV head
+    auto scan = [&](int s0) {
+        m = L = 0;
+        per = 0;
+        if (s0 + tid < a.B && (m = queries_of(a, s0 + tid)) > 0) {
+            L = length_of(a, s0 + tid);
+            per = chunks_before(m, L, (m + TQ - 1) / TQ, TQ);
+        }
+        const long long n = per * a.c.H_kv;
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) F.sum[warp] = inc;
+        __syncthreads();
+        before = inc - n;
+        all = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += F.sum[i];
+            all += F.sum[i];
         }
     };
-    for (int t0 = 0; t0 < limit; t0 += kTile) {
-        const int cnt = min(kTile, limit - t0);
-        __syncthreads();
-        load(a.c.k_q, a.c.k_sb, t0, cnt);
-        __syncthreads();
-        for (int j = tid; j < G * kTile; j += kThreads) {
-            const int h = j / kTile, t = j % kTile;
-            float s = -INFINITY;
-            if (t < cnt) {
-                s = 0.0f;
-                for (int d = 0; d < D; ++d) s = fmaf(qs[h * D + d], kv[t * (D + 1) + d], s);
-                s *= a.scale_log2;
-            }
-            p[j] = s;
+    long long total = 0;
+    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+        scan(s0);
+        total += all;
+    }
+    // no more CTAs than chunks: every CTA between an item's first and last has a part of it
+    const long long used = min(total, static_cast<long long>(gridDim.x));
+    if (c >= used) return w;
+    const long long begin = total * c / used;
+    w.left = total * (c + 1) / used - begin;
+    long long pre = 0;
+    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+        if (a.B > kThreads) scan(s0);
+        const long long lo = pre + before;
+        if (begin >= lo && begin < lo + per * a.c.H_kv) {
+            F.b0 = s0 + tid;
+            F.m0 = m;
+            F.L0 = L;
+            F.pre = lo;
+            F.per = per;
+            F.begin = begin;
+            F.total = total;
+            F.used = used;
         }
-        __syncthreads();
-        load(a.c.v_q, a.c.v_sb, t0, cnt);
-        if (tid < G) {  // thread h: the running maximum and sum of head h
-            float mn = mx;
-            for (int t = 0; t < cnt; ++t) mn = fmaxf(mn, p[tid * kTile + t]);
-            al[tid] = exp2f(mx - mn);
-            sum *= al[tid];
-            for (int t = 0; t < cnt; ++t) {
-                const float w = exp2f(p[tid * kTile + t] - mn);
-                p[tid * kTile + t] = w;
-                sum += w;
-            }
-            mx = mn;
-        }
-        __syncthreads();
-        for (int x = 0; x < 2; ++x) {
-            const int d = tid + x * kThreads;
-            if (d >= D) break;
-            for (int h = 0; h < G; ++h) {
-                float o = acc[h][x] * al[h];
-                for (int t = 0; t < cnt; ++t) o = fmaf(p[h * kTile + t], kv[t * (D + 1) + d], o);
-                acc[h][x] = o;
-            }
-        }
+        pre += all;
+        if (begin < pre) break;
     }
     __syncthreads();
-    if (tid < G) al[tid] = sum > 0.0f ? 1.0f / sum : 0.0f;
-    __syncthreads();
-    for (int x = 0; x < 2; ++x) {
-        const int d = tid + x * kThreads;
-        if (d >= D) break;
-        for (int h = 0; h < G; ++h)
-            a.out[(static_cast<size_t>(n) * a.H_q + g * G + h) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[h][x] * al[h]));
+    w.b = F.b0;
+    w.m = F.m0;
+    w.L = F.L0;
+    const long long off = begin - F.pre;
+    w.g = static_cast<int>(off / F.per);
+    const long long r = off % F.per;
+    // the tile that chunk r falls into: the last t with chunks_before(t) <= r, 32 candidates at a time
+    int t_lo = 0, t_hi = (w.m + TQ - 1) / TQ;  // chunks_before(t_lo) <= r < chunks_before(t_hi)
+    while (t_hi - t_lo > 1) {
+        const int step = (t_hi - t_lo + 31) / 32, t = min(t_lo + lane * step, t_hi);
+        const uint32_t ok = __ballot_sync(0xffffffffu, t < t_hi && chunks_before(w.m, w.L, t, TQ) <= r);
+        const int last = 31 - __clz(ok);
+        t_lo += last * step;
+        t_hi = min(t_lo + step, t_hi);
     }
+    w.t = t_lo;
+    w.j0 = static_cast<int>(r - chunks_before(w.m, w.L, t_lo, TQ));
+    return w;
+}
+
+__device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done, int TQ)
+{
+    w.left -= done;
+    w.j0 = 0;
+    if (w.left <= 0) return;
+    if (++w.t * TQ < w.m) return;
+    w.t = 0;
+    if (++w.g < a.c.H_kv) return;
+    w.g = 0;
+    do {
+        w.m = queries_of(a, ++w.b);
+    } while (w.m == 0 && w.b + 1 < a.B);  // `left` chunks are still to come, so there is one
+    w.L = length_of(a, w.b);
+}
+
+// ------------------------------------------------------------------ the kernel
+// Codes of one (token, group) in registers.
+template <int BITS>
+struct Raw {
+    uint4 q[BITS / 2];
+    uint32_t sb;
+};
+
+template <int BITS>
+__device__ __forceinline__ void rebuild(const Raw<BITS> &raw, uint32_t row_addr, int sw, int *status)
+{
+    const float s = lo_bf16(raw.sb), b = hi_bf16(raw.sb);
+    constexpr float L = BITS == 4 ? 15.0f : 255.0f, kUp = BITS == 4 ? 8.0f : 64.0f;
+    if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
+    const __half2 s2 = __float2half2_rn(s * kUp), b2 = __float2half2_rn(b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint4 v;
+        if constexpr (BITS == 4) {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(raw.q)[i];
+            v = dequant8_f16_e2m3(w, s2, b2);
+        } else {
+            // 16 + code / 64 is the code under the exponent of 16
+            const __half2 off = __half2half2(__ushort_as_half(0xCC00));  // -16
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t w = reinterpret_cast<const uint32_t *>(raw.q)[2 * i + j];
+                const uint32_t e = (w & 0x00FF00FFu) | 0x4C004C00u, d = ((w >> 8) & 0x00FF00FFu) | 0x4C004C00u;
+                __half2 he = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&e), off), s2, b2);
+                __half2 hd = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&d), off), s2, b2);
+                o[2 * j] = *reinterpret_cast<uint32_t *>(&he);
+                o[2 * j + 1] = *reinterpret_cast<uint32_t *>(&hd);
+            }
+            v = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        sts128(row_addr + ((i ^ sw) << 4), v);
+    }
+}
+
+template <int BITS, int GR>
+__global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a)
+{
+    constexpr int D = 64 * GR, GB = 8 * BITS;
+    extern __shared__ uint8_t dsm_raw[];
+    uint8_t *base = dsm_raw + ((1024 - (smem_u32(dsm_raw) & 1023)) & 1023);
+    Fixed &F = *reinterpret_cast<Fixed *>(base);
+    const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + 2 * GR * kBox;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group, TQ = kRows / G;
+    int *status = &a.ctrl->status;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&F.k_full[i], 2 * GR);
+            mbar_init(&F.v_full[i], 2 * GR);
+            mbar_init(&F.k_free[i], 1);
+            mbar_init(&F.v_free[i], 1);
+            mbar_init(&F.s_full[i], 1);
+            mbar_init(&F.p_full[i], kSoftWarps);
+            mbar_init(&F.pv_done[i], 1);
+        }
+        mbar_init(&F.q_full, kSoftWarps);
+        mbar_init(&F.o_free, kSoftWarps);
+        mbar_init(&F.drain, 1);
+        F.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&F.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_trigger();
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = F.tmem;
+    Walk w = first_item(a, F, TQ);
+    bool ok = true;
+
+    if (warp < kSoftWarps) {
+        // ------------------------------------------------ one query row per thread
+        const int row = threadIdx.x;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        int it = 0, items = 0;
+        if (w.left == 0 && threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        long long done = 0;
+        while (w.left > 0 && ok) {
+            const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+            const int tq = w.t * TQ + row / G, head = w.g * G + row % G;
+            const bool valid = row < TQ * G && tq < w.m;
+            const int limit = valid ? w.L - w.m + tq + 1 : 0;  // tokens this row sees (may be <= 0)
+            const long long qrow = a.cu_q[w.b] + tq;
+            const bool any_row = __any_sync(0xffffffffu, valid);
+            float mul = 0.0f;
+            if (any_row) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (valid ? qrow : a.cu_q[w.b]) * a.q_stride + static_cast<long long>(head) * D);
+                float big = 0.0f;
+#pragma unroll 8
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = src[i];
+                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(x.x)), fabsf(hi_bf16(x.x))), fmaxf(fabsf(lo_bf16(x.y)), fabsf(hi_bf16(x.y)))));
+                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(x.z)), fabsf(hi_bf16(x.z))), fmaxf(fabsf(lo_bf16(x.w)), fabsf(hi_bf16(x.w)))));
+                }
+                // times 2^(14 - floor(log2 big)), within the normal numbers, and the sign of the scale
+                const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
+                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(ef) << 23), a.scale_log2);
+                // never 0: a masked score is -inf, and stays it
+                mul = fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23), 1.17549435e-38f);
+#pragma unroll
+                for (int c = 0; c < GR; ++c) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 x = src[c * 8 + i];
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        float f[8];
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            const int ch = unpacked<BITS>(p);
+                            f[p] = (ch & 1 ? hi_bf16(xs[ch / 2]) : lo_bf16(xs[ch / 2])) * up;
+                        }
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) r[4 * i + p] = pack_f16(f[2 * p], f[2 * p + 1]);
+                    }
+                    tmem_st_32x32b_x32(lanes + Cols<GR>::Q + c * 32, r);
+                }
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&F.q_full);
+
+            float m_run = kNoMax, l_run = 0.0f;
+            for (int i = 0; i < n; ++i, ++it) {
+                const int sb = it & 1;
+                if (!(ok = warp_wait(&F.s_full[sb], (it >> 1) & 1, &F.abort, status))) break;
+                if (any_row) {
+                    tc_fence_after();
+                    const int vis = limit - (w.j0 + i) * kChunk;  // columns this row sees
+                    uint32_t s[2][32];
+                    tmem_ld_x32(lanes + Cols<GR>::S + sb * 64, s[0]);
+                    tmem_ld_x32(lanes + Cols<GR>::S + sb * 64 + 32, s[1]);
+                    tmem_ld_wait();
+                    if (__any_sync(0xffffffffu, vis < kChunk)) {
+#pragma unroll
+                        for (int x = 0; x < 64; ++x)
+                            if (x >= vis) s[x / 32][x % 32] = 0xFF800000u;  // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x / 32][x % 32]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float mn = top > -INFINITY ? top * mul : kNoMax;
+                    if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {
+                        const float to = fmaxf(m_run, mn), al = ex2(m_run - to);
+                        m_run = to;
+                        l_run *= al;
+                        if (i > 0) {
+                            // O of the chunks before this one, once their products are done
+                            if (!(ok = warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status))) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * al);
+                                tmem_st_32x32b_x32(lanes + Cols<GR>::O + c * 32, o);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    uint32_t p[32];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float p0 = ex2(fmaf(__uint_as_float(s[x / 16][(2 * x) % 32]), mul, -m_run));
+                        const float p1 = ex2(fmaf(__uint_as_float(s[x / 16][(2 * x) % 32 + 1]), mul, -m_run));
+                        sum[(2 * x) & 3] += p0;
+                        sum[(2 * x + 1) & 3] += p1;
+                        p[x] = pack_f16(p0, p1);
+                    }
+                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_32x32b_x32(lanes + Cols<GR>::S + sb * 64, p);
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&F.p_full[sb]);
+            }
+            // ---- the item's end: O out of tensor memory
+            if (ok) ok = warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
+            tc_fence_after();
+            const bool starts = w.j0 == 0, ends = w.j0 + n == nch;
+            const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+            if (ok && any_row) {
+                const bool seen = l_run > 0.0f;  // a row that saw nothing has zeros
+                const float r = seen ? 1.0f / l_run : 0.0f;
+                uint16_t *dst = a.out + (qrow * a.H_q + head) * D;
+                float *pdst = a.part_acc + (static_cast<size_t>(part) * kRows + row) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
+                    tmem_ld_wait();
+                    if (valid) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x[8];
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) x[unpacked<BITS>(p)] = seen ? __uint_as_float(o[8 * i + p]) : 0.0f;
+                        if (starts && ends) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * p] * r, x[2 * p + 1] * r);
+                                y[p] = *reinterpret_cast<const uint32_t *>(&t);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+                        } else {
+                            *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8) = make_float4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                        }
+                    }
+                    }
+                    __syncwarp();
+                }
+                if (valid && !(starts && ends))
+                    *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * kRows + row) * 2) = make_float2(m_run, l_run);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&F.o_free);
+            if (threadIdx.x == 0 && w.left == n) {
+                // who joins the parts of an item that starts here and goes on: up to the CTA with its last chunk
+                const long long last = ((F.begin + done - w.j0 + nch) * F.used - 1) / F.total;
+                a.meta[blockIdx.x] = make_int4(starts && !ends ? w.b : -1, w.g, w.t, static_cast<int>(last));
+            }
+            done += n;
+            ++items;
+            advance(a, w, n, TQ);
+        }
+    } else if (warp < kSoftWarps + kDeqWarps) {
+        // ------------------------------------------------ K and V of the chunks into shared memory
+        constexpr int kItems = GR == 4 ? 2 : 1;  // (K or V, group, 32 tokens) per warp and chunk
+        const int dw = warp - kSoftWarps;
+        const bool idle = dw >= 4 * GR;          // D = 64: four warps are enough
+        int it = 0;
+        while (w.left > 0 && ok && !idle) {
+            const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+            Raw<BITS> raw[kItems];
+            int pb = 0;
+            // the table entry of this warp's 32 tokens of chunk j (both items have the same half of the chunk)
+            const int half = dw & 1;
+            auto entry = [&](int j) {
+                const int t0 = j * kChunk + half * 32;
+                if (t0 >= w.L) return 0;
+                int e = a.block_table[static_cast<size_t>(w.b) * a.max_blocks + t0 / a.c.bs];
+                if (e < 0 || e >= a.c.n_blocks) {
+                    record_error(status, kErrDeviceIndex);
+                    e = 0;
+                }
+                return e;
+            };
+            auto fetch = [&](int j, int block) {
+                const int tok = j * kChunk + half * 32 + lane;
+#pragma unroll
+                for (int x = 0; x < kItems; ++x) {
+                    const int item = dw + x * kDeqWarps, group = (item % (2 * GR)) >> 1;
+                    const bool isv = item >= 2 * GR;
+                    const long long gi = ((static_cast<long long>(block) * a.c.H_kv + w.g) * GR + group) * a.c.bs + tok % a.c.bs;
+                    const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.c.v_q : a.c.k_q) + gi * GB);
+#pragma unroll
+                    for (int y = 0; y < BITS / 2; ++y) raw[x].q[y] = src[y];
+                    const uint32_t sb = *reinterpret_cast<const uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2);
+                    raw[x].sb = tok < w.L ? sb : 0u;  // rows behind the sequence, whatever they hold
+                }
+            };
+            pb = entry(w.j0);
+            fetch(w.j0, pb);
+            pb = n > 1 ? entry(w.j0 + 1) : 0;
+            for (int i = 0; i < n; ++i, ++it) {
+                Raw<BITS> cur[kItems];
+#pragma unroll
+                for (int x = 0; x < kItems; ++x) cur[x] = raw[x];
+                if (i + 1 < n) {
+                    fetch(w.j0 + i + 1, pb);
+                    pb = i + 2 < n ? entry(w.j0 + i + 2) : 0;
+                }
+                const int buf = it & 1;
+#pragma unroll
+                for (int x = 0; x < kItems; ++x) {
+                    const int item = dw + x * kDeqWarps, group = (item % (2 * GR)) >> 1;
+                    const bool isv = item >= 2 * GR;
+                    if (it >= 2 && !(ok = warp_wait(isv ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
+                    const int r = half * 32 + lane;
+                    rebuild<BITS>(cur[x], (isv ? v_smem : k_smem) + (buf * GR + group) * kBox + r * 128, r & 7, status);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(isv ? &F.v_full[buf] : &F.k_full[buf]);
+                }
+                if (!ok) break;
+            }
+            advance(a, w, n, TQ);
+        }
+    } else {
+        // ------------------------------------------------ MMA issuer (one thread)
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, kRows, kChunk);
+            constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, kRows, D) | (1u << 16);  // B: channels contiguous
+            int it = 0, items = 0;
+            while (w.left > 0 && ok) {
+                const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+                if (!(ok = mbar_wait(&F.q_full, items & 1, &F.abort, status))) break;
+                tc_fence_after();
+                for (int i = 0; i <= n && ok; ++i) {
+                    if (i < n) {
+                        const int x = it + i, buf = x & 1;
+                        if (!(ok = mbar_wait(&F.k_full[buf], (x >> 1) & 1, &F.abort, status))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < GR; ++c) {
+                            const uint64_t bd = sdesc_sw128(k_smem + (buf * GR + c) * kBox);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_ts(tmem + Cols<GR>::S + buf * 64, tmem + Cols<GR>::Q + c * 32 + kk * 8, bd + kk * 2, kIdescS, (c | kk) != 0);
+                        }
+                        umma_commit(&F.k_free[buf]);
+                        umma_commit(&F.s_full[buf]);
+                    }
+                    if (i > 0) {
+                        const int x = it + i - 1, buf = x & 1;
+                        if (i == 1 && items > 0 && !(ok = mbar_wait(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
+                        if (!(ok = mbar_wait(&F.v_full[buf], (x >> 1) & 1, &F.abort, status))) break;
+                        if (!(ok = mbar_wait(&F.p_full[buf], (x >> 1) & 1, &F.abort, status))) break;
+                        tc_fence_after();
+                        const uint64_t bd = sdesc_mn_sw128(v_smem + buf * GR * kBox, kBox);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_ts(tmem + Cols<GR>::O, tmem + Cols<GR>::S + buf * 64 + kk * 8, bd + kk * (2048 >> 4), kIdescO, i > 1 || kk > 0);
+                        umma_commit(&F.v_free[buf]);
+                        umma_commit(&F.pv_done[buf]);
+                    }
+                }
+                it += n;
+                ++items;
+                advance(a, w, n, TQ);
+            }
+            // all tensor-core work of this CTA must finish before tensor memory is freed
+            umma_commit(&F.drain);
+            const uint32_t addr = smem_u32(&F.drain);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(addr, 0))
+                if (global_timer_ns() - t0 > LILY_DRAIN_LIMIT_NS) {
+                    record_error(status, kErrDeviceTimeout);
+                    break;
+                }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the parts of an item that was cut: CTA (first CTA of the item, four rows),
+// 64 threads a row.  The part of the first CTA c0 is in slot 2 c0 + 1, those of the
+// following ones in slot 2 c.
+__global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int4 meta = a.meta[blockIdx.x];
+    if (meta.x < 0) return;
+    const int G = a.group, TQ = kRows / G, row = blockIdx.y * 4 + threadIdx.x / 64, d4 = threadIdx.x % 64;
+    const int m = queries_of(a, meta.x), tq = meta.z * TQ + row / G;
+    if (row >= TQ * G || tq >= m || d4 * 4 >= a.D) return;
+    const int c0 = blockIdx.x, S = meta.w - c0 + 1;
+    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kRows + row; };
+    float M = kNoMax, den = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < S; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2);
+        const float4 x = reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4];
+        const float to = fmaxf(M, ml.x), c = ex2(M - to), e = ex2(ml.x - to);
+        M = to;
+        den = fmaf(den, c, e * ml.y);
+        o.x = fmaf(o.x, c, e * x.x);
+        o.y = fmaf(o.y, c, e * x.y);
+        o.z = fmaf(o.z, c, e * x.z);
+        o.w = fmaf(o.w, c, e * x.w);
+    }
+    const float r = den > 0.0f ? 1.0f / den : 0.0f;
+    uint2 y;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
+    y.x = *reinterpret_cast<const uint32_t *>(&lo);
+    y.y = *reinterpret_cast<const uint32_t *>(&hi);
+    const long long n = a.cu_q[meta.x] + tq;
+    reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + row % G) * a.D)[d4] = y;
+}
+
+template <int BITS, int GR>
+cudaError_t launch(const KvqAttnArgs &a, cudaStream_t stream)
+{
+    const int smem = smem_bytes(64 * GR);
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR>), smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kvq_prefill_kernel<BITS, GR>, dim3(kKvqPrefillCtas), dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, cudaStream_t stream)
 {
-    const size_t smem = sizeof(float) * (kKvqMaxGroup * a.D + kTile * (a.D + 1) + kKvqMaxGroup * kTile + kKvqMaxGroup);
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel), static_cast<int>(smem));
+    cudaError_t e;
+    if (a.c.bits == 4)
+        e = a.D == 64 ? launch<4, 1>(a, stream) : a.D == 128 ? launch<4, 2>(a, stream) : launch<4, 4>(a, stream);
+    else
+        e = a.D == 64 ? launch<8, 1>(a, stream) : a.D == 128 ? launch<8, 2>(a, stream) : launch<8, 4>(a, stream);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_kernel, dim3(a.N, a.c.H_kv), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas, kRows / 4), dim3(256), 0, stream, a);
 }
 
 }  // namespace lily

@@ -217,17 +217,19 @@ struct KvqAttnArgs {
     const int *seq_lens;          // [B]
     uint16_t *out;                // bf16 [N][H_q][D]
     Ctrl *ctrl;
-    // decode: partial results of segments cut between CTAs (workspace)
-    int4 *meta;                   // [CTAs]: segment (or -1), its first and last CTA
-    float *part_ml;               // [2 CTAs][8][2]: max (log2 units), sum of weights
-    float *part_acc;              // [2 CTAs][8][D]
+    // partial results of work items cut between CTAs (workspace)
+    int4 *meta;                   // [CTAs]: decode: segment (or -1), its first and last CTA;
+                                  // prefill: sequence (or -1), KV head, tile, last CTA
+    float *part_ml;               // [2 CTAs][rows][2]: max (log2 units), sum of weights
+    float *part_acc;              // [2 CTAs][rows][D]; rows: 8 (decode), 128 (prefill)
     int whole, key_by_segment, stages;  // set by launch_kvq_decode
     unsigned int stages_inv;            // ceil(2^32 / stages)
 };
 constexpr int kKvqMaxGroup = 8;      // query heads per KV head
-// CTAs of the decode kernel, one per SM of a GB300: a constant, so that the work
+// CTAs of the attention kernels, one per SM of a GB300: a constant, so that the work
 // split and the workspace are functions of the shape alone.
-constexpr int kKvqDecodeCtas = 152;
+constexpr int kKvqDecodeCtas = 152, kKvqPrefillCtas = 152;
+constexpr int kKvqPrefillRows = 128;
 cudaError_t launch_kvq_decode(const KvqAttnArgs &a, cudaStream_t stream);
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, cudaStream_t stream);
 

@@ -505,3 +505,65 @@ def test_two_streams_with_their_own_workspaces():
             lm.lily_kvq_attn_decode(c.shape, c.handle, c.d["q"], c.d["block_table"], c.d["seq_lens"], o, c.ws, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
+
+
+def _scaled(cfg, k_gain, v_gain):
+    """A cache whose K and V are the workload's times a gain, the bf16 values quantised as usual."""
+    c = Cache(cfg, n_query=cfg.N)
+    first = c.a["cu_all"].numpy()
+    for n, g in (("k", k_gain), ("v", v_gain)):
+        x = raw((c.a[n + "_all"].float() * g).to(torch.bfloat16))
+        for b, L in enumerate(cfg.lens):
+            code, sb = kvq.quantise(x[first[b]:first[b] + L], cfg.bits)
+            kvq.write_rows(c.h[n + "_q"], c.table[b], 0, kvq.pack(code, cfg.bits))
+            kvq.write_rows(c.h[n + "_sb"], c.table[b], 0, sb)
+    return c.to_gpu()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_prefill_values_beyond_fp16_are_reported(bits):
+    # K and V are rebuilt in fp16: a value of 65520 or more would become infinite and is reported; decode has no limit
+    cfg = KvqConfig("range", lens=(200,), new=(30,), D=128, bits=bits, seed=70)
+    for k_gain, v_gain in ((1.0, 1e6), (1e6, 1.0)):
+        c = _scaled(cfg, k_gain, v_gain)
+        _prefill(c, scale=1e-8)
+        assert c.status() == -9   # LILY_ERR_DEVICE_RANGE
+    # large but within the range: exact to the usual bound
+    c = _scaled(cfg, 1000.0, 1000.0)
+    out = _prefill(c, scale=1e-4)
+    assert c.status() == 0
+    kk, vv, km, vm = c.sequence(0)
+    ref, mags = kvq.attend_and_bound(rounded(c.a["q"]), kk, vv, 171 + np.arange(30), 1e-4, km, vm)
+    check(rounded(out), ref, mags)
+
+
+def test_prefill_queries_of_any_size():
+    # q is scaled per row by a power of two before it becomes fp16
+    cfg = KvqConfig("qsize", lens=(200,), new=(30,), D=128, seed=71)
+    for gain in (1e-30, 1e30):
+        c = Cache(cfg, n_query=cfg.N)
+        c.a["q"] = (c.a["q"].float() * gain).to(torch.bfloat16)
+        c.to_gpu()
+        out = _prefill(c, scale=0.1 / gain)
+        assert c.status() == 0
+        kk, vv, km, vm = c.sequence(0)
+        ref, mags = kvq.attend_and_bound(rounded(c.a["q"]), kk, vv, 171 + np.arange(30), 0.1 / gain, km, vm)
+        check(rounded(out), ref, mags)
+
+
+def test_prefill_sharp_softmax():
+    # scores that grow along the sequence: the running maximum moves many times, O is rescaled each time
+    cfg = KvqConfig("sharp", lens=(1500,), new=(64,), D=256, seed=72)
+    c = Cache(cfg, n_query=cfg.N)
+    ramp = torch.linspace(0.0, 8.0, 1500).view(-1, 1, 1)
+    x = raw((c.a["k_all"].float() + ramp * torch.sign(c.a["q"][0].float().view(2, 8, 256).mean(1, keepdim=True)).view(1, 2, 256)).to(torch.bfloat16))
+    code, sb = kvq.quantise(x, cfg.bits)
+    kvq.write_rows(c.h["k_q"], c.table[0], 0, kvq.pack(code, cfg.bits))
+    kvq.write_rows(c.h["k_sb"], c.table[0], 0, sb)
+    c.to_gpu()
+    for scale in (None, 0.5):
+        out = _prefill(c, scale=scale)
+        assert c.status() == 0
+        kk, vv, km, vm = c.sequence(0)
+        ref, mags = kvq.attend_and_bound(rounded(c.a["q"]), kk, vv, 1437 + np.arange(64), scale, km, vm)
+        check(rounded(out), ref, mags)
