@@ -401,6 +401,21 @@ bool make_tmap(CUtensorMap *m, const void *ptr, CUtensorMapDataType dt, int elem
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q of the prefill attention: [N][H_q][D] with a token stride, box of 64 channels x
+// `heads` x `tokens`.
+bool tmap_query(CUtensorMap *m, const uint16_t *q, int64_t N, int H_q, int D, int64_t stride, int heads, int tokens)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tmap_bf16_sw128(CUtensorMap *m, const void *ptr, uint64_t inner, uint64_t rows)
 {
     return make_tmap(m, ptr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, rows, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -951,8 +966,11 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     a.meta = at<int4>(ws, L.meta);
     a.part_ml = at<float>(ws, L.part_ml);
     a.part_acc = at<float>(ws, L.part_acc);
-    return to_status(ragged ? launch_kvq_prefill(a, stream) : launch_kvq_decode(a, stream),
-                     "quantised-cache attention launch");
+    if (!ragged) return to_status(launch_kvq_decode(a, stream), "quantised-cache attention launch");
+    CUtensorMap tmQ;
+    if (!tmap_query(&tmQ, q, N, s.H_q, s.D, q_stride, a.group, kKvqPrefillRows / a.group))
+        return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (queries)");
+    return to_status(launch_kvq_prefill(a, tmQ, stream), "quantised-cache attention launch");
 }
 
 }  // namespace

@@ -10,19 +10,22 @@
 // share evenly (a long prompt's later tiles have more of them); an item cut between
 // CTAs leaves partial results that a second kernel joins.
 // Per CTA, with every wait bounded:
-//   warps 0..3   one query row per thread: q into tensor memory as fp16 (times a
-//                power of two per row, so q has no range limit), then per chunk S
-//                from tensor memory, the softmax weights back into it as fp16 (the A
-//                operand of P V), at the end O out of it.  The running maximum moves
-//                only when a score passes it by 8 (in powers of two; the weights
-//                then stay below 2^8), so O in tensor memory is rescaled rarely.
-//   warps 4..11  rebuild K and V of a chunk in fp16 (rounded once) into swizzled
+//   warps 0..7   two threads per query row (32 of a chunk's 64 tokens each): q into
+//                tensor memory as fp16 (times a power of two per row, so q has no range
+//                limit), then per chunk S from tensor memory, the softmax weights back
+//                into it as fp16 (the A operand of P V), at the end O out of it.  The
+//                running maximum moves only when a score passes it by 8 (in powers of
+//                two; the weights then stay below 2^8), so O in tensor memory is
+//                rescaled rarely.  The next item's q is converted before O is read, so
+//                its first scores are computed meanwhile.
+//   warps 8..15  rebuild K and V of a chunk in fp16 (rounded once) into swizzled
 //                shared memory, two buffers each: a thread takes one (token, group of
 //                64 channels); its codes are loaded one chunk ahead.  Rows behind the
 //                sequence become zeros.
-//   warp 12      one thread issues tcgen05.mma: S = Q K^T (A from tensor memory, B
+//   warp 16      one thread issues tcgen05.mma: S = Q K^T (A from tensor memory, B
 //                K-major) of chunk i + 1, then O += P V (B with the channels
 //                contiguous) of chunk i, so the softmax runs beside them.
+//   warp 17      one thread copies the next item's q into shared memory (TMA).
 // K and V must stay within fp16: |value| >= 65520 records LILY_ERR_DEVICE_RANGE.
 #include <cmath>
 #include <cstdint>
@@ -35,22 +38,26 @@ namespace {
 
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kChunk = 64;                 // cache tokens per step
-constexpr int kSoftWarps = 4, kDeqWarps = 8, kMmaWarp = 12;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kItemCost = 2;               // of taking up an item, in chunks, in the work list's shares
+constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
+constexpr int kThreads = (kLoadWarp + 1) * 32;
+constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
 constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
 constexpr uint32_t kTmemCols = 512;
 constexpr float kNoMax = -1.7e38f;
 
 struct Fixed {
     uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
-    uint64_t pv_done[2], q_full, o_free, drain;
+    uint64_t pv_done[2], q_full, q_loaded, q_free, o_free, drain;
     uint32_t tmem;
     int abort, b0, m0, L0;
     long long pre, per, begin, total, used, sum[kThreads / 32];
+    float xch[2][2][kRows];  // [chunk parity][half of the columns][row]
 };
-constexpr int kFixed = 1024;
+constexpr int kFixed = 4096;
 static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
-constexpr int smem_bytes(int D) { return 1024 + kFixed + 4 * (D / 64) * kBox; }
+constexpr int kQBox = kRows * 128;         // [128 rows][64 channels] bf16, 128-byte swizzle
+constexpr int smem_bytes(int D) { return 1024 + kFixed + (D / 64) * (4 * kBox + kQBox); }
 
 // Tensor-memory columns: O [0, D), S / P two buffers of 64, Q D / 2.
 template <int GR>
@@ -84,17 +91,21 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 32 lanes x 32 columns, complete on return: the load and its wait are one statement, as
+// nothing (not even a register copy) may touch the result between them.
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
+        : "r"(taddr)
+        : "memory");
 }
 // Descriptor of an operand with its M/N side contiguous (128-byte swizzle): boxes of
 // 64 contiguous elements x rows of 128 bytes; `lead` bytes between boxes, 1024 bytes
@@ -110,12 +121,35 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr, uint32_t 
     return d;
 }
 
-// One lane waits for the warp.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A whole warp waits.  Every lane does: what the barrier guards is read by every lane,
+// and a shuffle of one lane's result orders no memory access.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
 {
-    int go = 0;
-    if ((threadIdx.x & 31) == 0) go = mbar_wait(bar, parity, abort_flag, status);
-    return __shfl_sync(0xffffffffu, go, 0) != 0;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // ------------------------------------------------------------------ work list
@@ -140,7 +174,7 @@ __device__ __forceinline__ int tile_chunks(int m, int L, int t, int TQ)
     const int limit = min(L, L - m + min(m, (t + 1) * TQ));
     return limit > 0 ? (limit + kChunk - 1) / kChunk : 1;
 }
-// Chunks of the tiles [0, t) of a sequence.  All but the last tile have the limit
+// Chunks of the tiles [0, t) of a sequence, without the items' own cost.  All but the last tile have the limit
 // x + i TQ, x = L - m + TQ: the sum of ceil(. / 64) is the arithmetic series less the
 // residues, which repeat with period 64 / gcd(TQ, 64).
 __device__ __forceinline__ long long chunks_before(int m, int L, int t, int TQ)
@@ -165,24 +199,44 @@ __device__ __forceinline__ long long chunks_before(int m, int L, int t, int TQ)
     return z + (total - res) / kChunk + (t >= n ? tile_chunks(m, L, n - 1, TQ) : 0);
 }
 
-// A CTA's place in the list: item (b, g, t) from chunk j0 on, `left` chunks in all.
+// The same in places of the work list: an item of n chunks has kItemCost + n, the first
+// ones for taking it up.
+__device__ __forceinline__ long long places_before(int m, int L, int t, int TQ)
+{
+    return chunks_before(m, L, t, TQ) + static_cast<long long>(kItemCost) * t;
+}
+
+// A CTA's place in the list: item (b, g, t) from place s0 on, `left` places in all.
 struct Walk {
-    int b, g, t, m, L, j0;
+    int b, g, t, m, L, s0;
     long long left;
 };
+// Its share of the item: chunks [j0, j0 + n) of nch, `take` places.
+struct Share {
+    int j0, n, nch, take;
+};
+__device__ __forceinline__ Share share_of(const Walk &w, int TQ)
+{
+    Share h;
+    h.nch = tile_chunks(w.m, w.L, w.t, TQ);
+    h.take = static_cast<int>(min(static_cast<long long>(h.nch + kItemCost - w.s0), w.left));
+    h.j0 = max(w.s0 - kItemCost, 0);
+    h.n = max(w.s0 + h.take - kItemCost, 0) - h.j0;
+    return h;
+}
 
 __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int TQ)
 {
     Walk w{};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
     int m = 0, L = 0;
-    long long per = 0, before = 0, all = 0;  // this thread's sequence: chunks per KV head
+    long long per = 0, before = 0, all = 0;  // this thread's sequence: places per KV head
     auto scan = [&](int s0) {
         m = L = 0;
         per = 0;
         if (s0 + tid < a.B && (m = queries_of(a, s0 + tid)) > 0) {
             L = length_of(a, s0 + tid);
-            per = chunks_before(m, L, (m + TQ - 1) / TQ, TQ);
+            per = places_before(m, L, (m + TQ - 1) / TQ, TQ);
         }
         const long long n = per * a.c.H_kv;
         long long inc = n;
@@ -206,7 +260,7 @@ __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int T
         scan(s0);
         total += all;
     }
-    // no more CTAs than chunks: every CTA between an item's first and last has a part of it
+    // no more CTAs than places: every CTA between an item's first and last has a part of it
     const long long used = min(total, static_cast<long long>(gridDim.x));
     if (c >= used) return w;
     const long long begin = total * c / used;
@@ -235,24 +289,25 @@ __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int T
     const long long off = begin - F.pre;
     w.g = static_cast<int>(off / F.per);
     const long long r = off % F.per;
-    // the tile that chunk r falls into: the last t with chunks_before(t) <= r, 32 candidates at a time
-    int t_lo = 0, t_hi = (w.m + TQ - 1) / TQ;  // chunks_before(t_lo) <= r < chunks_before(t_hi)
+    // the tile that place r falls into: the last t with places_before(t) <= r, 32 candidates at a time
+    int t_lo = 0, t_hi = (w.m + TQ - 1) / TQ;  // places_before(t_lo) <= r < places_before(t_hi)
     while (t_hi - t_lo > 1) {
         const int step = (t_hi - t_lo + 31) / 32, t = min(t_lo + lane * step, t_hi);
-        const uint32_t ok = __ballot_sync(0xffffffffu, t < t_hi && chunks_before(w.m, w.L, t, TQ) <= r);
+        const uint32_t ok = __ballot_sync(0xffffffffu, t < t_hi && places_before(w.m, w.L, t, TQ) <= r);
         const int last = 31 - __clz(ok);
         t_lo += last * step;
         t_hi = min(t_lo + step, t_hi);
     }
     w.t = t_lo;
-    w.j0 = static_cast<int>(r - chunks_before(w.m, w.L, t_lo, TQ));
+    w.s0 = static_cast<int>(r - places_before(w.m, w.L, t_lo, TQ));
     return w;
 }
 
-__device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done, int TQ)
+// The next item after `take` places of this one.
+__device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int take, int TQ)
 {
-    w.left -= done;
-    w.j0 = 0;
+    w.left -= take;
+    w.s0 = 0;
     if (w.left <= 0) return;
     if (++w.t * TQ < w.m) return;
     w.t = 0;
@@ -260,8 +315,15 @@ __device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int done,
     w.g = 0;
     do {
         w.m = queries_of(a, ++w.b);
-    } while (w.m == 0 && w.b + 1 < a.B);  // `left` chunks are still to come, so there is one
+    } while (w.m == 0 && w.b + 1 < a.B);  // places are still to come, so there is one
     w.L = length_of(a, w.b);
+}
+// From here to an item with chunks for this CTA (only its last item may have none).
+__device__ __forceinline__ bool next_share(const KvqAttnArgs &a, const Walk &w, Share &h, int TQ)
+{
+    if (w.left <= 0) return false;
+    h = share_of(w, TQ);
+    return h.n > 0;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -305,13 +367,13 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, uint32_t row_addr,
 }
 
 template <int BITS, int GR>
-__global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a)
+__global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a, const __grid_constant__ CUtensorMap tmQ)
 {
     constexpr int D = 64 * GR, GB = 8 * BITS;
     extern __shared__ uint8_t dsm_raw[];
     uint8_t *base = dsm_raw + ((1024 - (smem_u32(dsm_raw) & 1023)) & 1023);
     Fixed &F = *reinterpret_cast<Fixed *>(base);
-    const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + 2 * GR * kBox;
+    const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + 2 * GR * kBox, q_smem = v_smem + 2 * GR * kBox;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.group, TQ = kRows / G;
     int *status = &a.ctrl->status;
@@ -327,6 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             mbar_init(&F.pv_done[i], 1);
         }
         mbar_init(&F.q_full, kSoftWarps);
+        mbar_init(&F.q_loaded, 1);
+        mbar_init(&F.q_free, kSoftWarps);
         mbar_init(&F.o_free, kSoftWarps);
         mbar_init(&F.drain, 1);
         F.abort = 0;
@@ -346,92 +410,107 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     bool ok = true;
 
     if (warp < kSoftWarps) {
-        // ------------------------------------------------ one query row per thread
-        const int row = threadIdx.x;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        int it = 0, items = 0;
-        if (w.left == 0 && threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        // ------------------------------------------------ two threads per query row
+        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        Share h, h2;
+        bool more = next_share(a, w, h, TQ);
+        int it = 0, items = 0, mine = 1;  // mine: this CTA's meta entry is still to be written
         long long done = 0;
-        while (w.left > 0 && ok) {
-            const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+        float mul = 0.0f;
+
+        // item x's q from shared memory to tensor memory: this thread's row, every second group of 64 channels
+        auto take_q = [&](int x) {
+            ok = ok && warp_wait(&F.q_loaded, x & 1, &F.abort, status);
+            const uint32_t src = q_smem + row * 128;
+            const int sw = row & 7;
+            float big = 0.0f;
+#pragma unroll
+            for (int c = half; c < GR; c += 2)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 y = lds128(src + c * kQBox + ((i ^ sw) << 4));
+                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(y.x)), fabsf(hi_bf16(y.x))), fmaxf(fabsf(lo_bf16(y.y)), fabsf(hi_bf16(y.y)))));
+                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(y.z)), fabsf(hi_bf16(y.z))), fmaxf(fabsf(lo_bf16(y.w)), fabsf(hi_bf16(y.w)))));
+                }
+            named_barrier_sync(kBarPair + quarter, 64);  // the other half is done with xch
+            F.xch[0][half][row] = big;
+            named_barrier_sync(kBarPair + quarter, 64);
+            big = fmaxf(big, F.xch[0][half ^ 1][row]);
+            named_barrier_sync(kBarPair + quarter, 64);
+            // times 2^(14 - floor(log2 big)), within the normal numbers, and the sign of the scale
+            const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
+            const float up = copysignf(__uint_as_float(static_cast<uint32_t>(ef) << 23), a.scale_log2);
+            // never 0: a masked score is -inf, and stays it
+            mul = fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23), 1.17549435e-38f);
+#pragma unroll
+            for (int c = half; c < GR; c += 2) {
+                uint32_t r[32];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 y = lds128(src + c * kQBox + ((i ^ sw) << 4));
+                    const uint32_t xs[4] = {y.x, y.y, y.z, y.w};
+                    float f[8];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int ch = unpacked<BITS>(p);
+                        f[p] = (ch & 1 ? hi_bf16(xs[ch / 2]) : lo_bf16(xs[ch / 2])) * up;
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) r[4 * i + p] = pack_f16(f[2 * p], f[2 * p + 1]);
+                }
+                if (ok) tmem_st_32x32b_x32(lanes + Cols<GR>::Q + c * 32, r);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&F.q_full);
+                mbar_arrive(&F.q_free);
+            }
+        };
+        // A warp whose wait gave up goes on through the named barriers (its partner may be in one), without the work.
+        if (more) take_q(0);
+        while (more) {
             const int tq = w.t * TQ + row / G, head = w.g * G + row % G;
             const bool valid = row < TQ * G && tq < w.m;
             const int limit = valid ? w.L - w.m + tq + 1 : 0;  // tokens this row sees (may be <= 0)
-            const long long qrow = a.cu_q[w.b] + tq;
             const bool any_row = __any_sync(0xffffffffu, valid);
-            float mul = 0.0f;
-            if (any_row) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (valid ? qrow : a.cu_q[w.b]) * a.q_stride + static_cast<long long>(head) * D);
-                float big = 0.0f;
-#pragma unroll 8
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = src[i];
-                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(x.x)), fabsf(hi_bf16(x.x))), fmaxf(fabsf(lo_bf16(x.y)), fabsf(hi_bf16(x.y)))));
-                    big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(x.z)), fabsf(hi_bf16(x.z))), fmaxf(fabsf(lo_bf16(x.w)), fabsf(hi_bf16(x.w)))));
-                }
-                // times 2^(14 - floor(log2 big)), within the normal numbers, and the sign of the scale
-                const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
-                const float up = copysignf(__uint_as_float(static_cast<uint32_t>(ef) << 23), a.scale_log2);
-                // never 0: a masked score is -inf, and stays it
-                mul = fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23), 1.17549435e-38f);
-#pragma unroll
-                for (int c = 0; c < GR; ++c) {
-                    uint32_t r[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 x = src[c * 8 + i];
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                        float f[8];
-#pragma unroll
-                        for (int p = 0; p < 8; ++p) {
-                            const int ch = unpacked<BITS>(p);
-                            f[p] = (ch & 1 ? hi_bf16(xs[ch / 2]) : lo_bf16(xs[ch / 2])) * up;
-                        }
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) r[4 * i + p] = pack_f16(f[2 * p], f[2 * p + 1]);
-                    }
-                    tmem_st_32x32b_x32(lanes + Cols<GR>::Q + c * 32, r);
-                }
-                tmem_st_wait();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&F.q_full);
-
             float m_run = kNoMax, l_run = 0.0f;
-            for (int i = 0; i < n; ++i, ++it) {
+            const float item_mul = mul;
+            for (int i = 0; i < h.n; ++i, ++it) {
                 const int sb = it & 1;
-                if (!(ok = warp_wait(&F.s_full[sb], (it >> 1) & 1, &F.abort, status))) break;
+                ok = ok && warp_wait(&F.s_full[sb], (it >> 1) & 1, &F.abort, status);
                 if (any_row) {
                     tc_fence_after();
-                    const int vis = limit - (w.j0 + i) * kChunk;  // columns this row sees
-                    uint32_t s[2][32];
-                    tmem_ld_x32(lanes + Cols<GR>::S + sb * 64, s[0]);
-                    tmem_ld_x32(lanes + Cols<GR>::S + sb * 64 + 32, s[1]);
-                    tmem_ld_wait();
-                    if (__any_sync(0xffffffffu, vis < kChunk)) {
+                    const int vis = limit - (h.j0 + i) * kChunk - half * 32;  // of this thread's 32 columns, those the row sees
+                    uint32_t s[32] = {};
+                    if (ok) tmem_ld_x32(lanes + Cols<GR>::S + sb * 64 + half * 32, s);
+                    if (__any_sync(0xffffffffu, vis < 32)) {
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (x >= vis) s[x / 32][x % 32] = 0xFF800000u;  // -inf
+                        for (int x = 0; x < 32; ++x)
+                            if (x >= vis) s[x] = 0xFF800000u;  // -inf
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x / 32][x % 32]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const float mn = top > -INFINITY ? top * mul : kNoMax;
-                    if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {
+                    for (int x = 0; x < 32; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    F.xch[sb][half][row] = top;
+                    named_barrier_sync(kBarPair + quarter, 64);  // also: both halves have S in registers, so P may overwrite it
+                    top = fmaxf(top, F.xch[sb][half ^ 1][row]);
+                    const float mn = top > -INFINITY ? top * item_mul : kNoMax;
+                    if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {  // the same in both halves
                         const float to = fmaxf(m_run, mn), al = ex2(m_run - to);
                         m_run = to;
                         l_run *= al;
                         if (i > 0) {
                             // O of the chunks before this one, once their products are done
-                            if (!(ok = warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status))) break;
+                            ok = ok && warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
+                            for (int c = half; c < D / 32 && ok; c += 2) {
                                 uint32_t o[32];
                                 tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
-                                tmem_ld_wait();
 #pragma unroll
                                 for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * al);
                                 tmem_st_32x32b_x32(lanes + Cols<GR>::O + c * 32, o);
@@ -439,84 +518,98 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                             tmem_st_wait();
                         }
                     }
-                    uint32_t p[32];
+                    uint32_t p[16];
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[x / 16][(2 * x) % 32]), mul, -m_run));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[x / 16][(2 * x) % 32 + 1]), mul, -m_run));
+                    for (int x = 0; x < 16; ++x) {
+                        const float p0 = ex2(fmaf(__uint_as_float(s[2 * x]), item_mul, -m_run));
+                        const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + 1]), item_mul, -m_run));
                         sum[(2 * x) & 3] += p0;
                         sum[(2 * x + 1) & 3] += p1;
                         p[x] = pack_f16(p0, p1);
                     }
                     l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tmem_st_32x32b_x32(lanes + Cols<GR>::S + sb * 64, p);
+                    if (ok) tmem_st_x16(lanes + Cols<GR>::S + sb * 64 + half * 16, p);
                     tmem_st_wait();
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&F.p_full[sb]);
             }
-            // ---- the item's end: O out of tensor memory
-            if (ok) ok = warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
+            // ---- the item's end.  The next item's q first: the last scores of this one are in (S is full), so Q is free
+            Walk w2 = w;
+            advance(a, w2, h.take, TQ);
+            const bool more2 = next_share(a, w2, h2, TQ);
+            if (more2) take_q(items + 1);
+            ok = ok && warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
             tc_fence_after();
-            const bool starts = w.j0 == 0, ends = w.j0 + n == nch;
+            const bool starts = h.j0 == 0, ends = h.j0 + h.n == h.nch;
             const int part = 2 * blockIdx.x + (starts ? 1 : 0);
-            if (ok && any_row) {
+            if (any_row) {
+                named_barrier_sync(kBarPair + quarter, 64);
+                F.xch[0][half][row] = l_run;
+                named_barrier_sync(kBarPair + quarter, 64);
+                l_run += F.xch[0][half ^ 1][row];
+                named_barrier_sync(kBarPair + quarter, 64);
                 const bool seen = l_run > 0.0f;  // a row that saw nothing has zeros
                 const float r = seen ? 1.0f / l_run : 0.0f;
-                uint16_t *dst = a.out + (qrow * a.H_q + head) * D;
+                const long long n = a.cu_q[w.b] + tq;
+                uint16_t *dst = a.out + (n * a.H_q + head) * D;
                 float *pdst = a.part_acc + (static_cast<size_t>(part) * kRows + row) * D;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                for (int c = half; c < D / 32 && ok; c += 2) {
                     uint32_t o[32];
                     tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
-                    tmem_ld_wait();
                     if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x[8];
+                        for (int i = 0; i < 4; ++i) {
+                            float x[8];
 #pragma unroll
-                        for (int p = 0; p < 8; ++p) x[unpacked<BITS>(p)] = seen ? __uint_as_float(o[8 * i + p]) : 0.0f;
-                        if (starts && ends) {
-                            uint32_t y[4];
+                            for (int p = 0; p < 8; ++p) x[unpacked<BITS>(p)] = seen ? __uint_as_float(o[8 * i + p]) : 0.0f;
+                            if (starts && ends) {
+                                uint32_t y[4];
 #pragma unroll
-                            for (int p = 0; p < 4; ++p) {
-                                const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * p] * r, x[2 * p + 1] * r);
-                                y[p] = *reinterpret_cast<const uint32_t *>(&t);
+                                for (int p = 0; p < 4; ++p) {
+                                    const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * p] * r, x[2 * p + 1] * r);
+                                    y[p] = *reinterpret_cast<const uint32_t *>(&t);
+                                }
+                                *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
+                            } else {
+                                *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8) = make_float4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
                             }
-                            *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(y[0], y[1], y[2], y[3]);
-                        } else {
-                            *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8) = make_float4(x[0], x[1], x[2], x[3]);
-                            *reinterpret_cast<float4 *>(pdst + c * 32 + i * 8 + 4) = make_float4(x[4], x[5], x[6], x[7]);
                         }
-                    }
                     }
                     __syncwarp();
                 }
-                if (valid && !(starts && ends))
+                if (valid && half == 0 && !(starts && ends))
                     *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * kRows + row) * 2) = make_float2(m_run, l_run);
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&F.o_free);
-            if (threadIdx.x == 0 && w.left == n) {
-                // who joins the parts of an item that starts here and goes on: up to the CTA with its last chunk
-                const long long last = ((F.begin + done - w.j0 + nch) * F.used - 1) / F.total;
-                a.meta[blockIdx.x] = make_int4(starts && !ends ? w.b : -1, w.g, w.t, static_cast<int>(last));
+            if (threadIdx.x == 0 && starts && !ends) {
+                // who joins the parts of an item that starts here and goes on: up to the CTA with its last place
+                const long long last = ((F.begin + done - w.s0 + h.nch + kItemCost) * F.used - 1) / F.total;
+                a.meta[blockIdx.x] = make_int4(w.b, w.g, w.t, static_cast<int>(last));
+                mine = 0;
             }
-            done += n;
+            done += h.take;
             ++items;
-            advance(a, w, n, TQ);
+            w = w2;
+            h = h2;
+            more = more2;
         }
+        if (threadIdx.x == 0 && mine) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     } else if (warp < kSoftWarps + kDeqWarps) {
         // ------------------------------------------------ K and V of the chunks into shared memory
         constexpr int kItems = GR == 4 ? 2 : 1;  // (K or V, group, 32 tokens) per warp and chunk
         const int dw = warp - kSoftWarps;
         const bool idle = dw >= 4 * GR;          // D = 64: four warps are enough
         int it = 0;
-        while (w.left > 0 && ok && !idle) {
-            const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+        Share h;
+        while (ok && !idle && next_share(a, w, h, TQ)) {
+            const int n = h.n;
             Raw<BITS> raw[kItems];
             int pb = 0;
             // the table entry of this warp's 32 tokens of chunk j (both items have the same half of the chunk)
@@ -545,16 +638,16 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                     raw[x].sb = tok < w.L ? sb : 0u;  // rows behind the sequence, whatever they hold
                 }
             };
-            pb = entry(w.j0);
-            fetch(w.j0, pb);
-            pb = n > 1 ? entry(w.j0 + 1) : 0;
+            pb = entry(h.j0);
+            fetch(h.j0, pb);
+            pb = n > 1 ? entry(h.j0 + 1) : 0;
             for (int i = 0; i < n; ++i, ++it) {
                 Raw<BITS> cur[kItems];
 #pragma unroll
                 for (int x = 0; x < kItems; ++x) cur[x] = raw[x];
                 if (i + 1 < n) {
-                    fetch(w.j0 + i + 1, pb);
-                    pb = i + 2 < n ? entry(w.j0 + i + 2) : 0;
+                    fetch(h.j0 + i + 1, pb);
+                    pb = i + 2 < n ? entry(h.j0 + i + 2) : 0;
                 }
                 const int buf = it & 1;
 #pragma unroll
@@ -570,16 +663,44 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 }
                 if (!ok) break;
             }
-            advance(a, w, n, TQ);
+            advance(a, w, h.take, TQ);
         }
+    } else if (warp == kLoadWarp) {
+        // ------------------------------------------------ q of the items, one ahead
+        if (lane == 0) {
+            prefetch_tmap(&tmQ);
+            Share h;
+            int items = 0;
+            while (next_share(a, w, h, TQ)) {
+                if (items > 0 && !mbar_wait(&F.q_free, (items - 1) & 1, &F.abort, status)) break;
+                mbar_arrive_expect_tx(&F.q_loaded, static_cast<uint32_t>(GR * TQ * G * 128));
+#pragma unroll
+                for (int c = 0; c < GR; ++c)
+                    tma_load_3d(base + kFixed + 4 * GR * kBox + c * kQBox, &tmQ, &F.q_loaded, c * 64, w.g * G, a.cu_q[w.b] + w.t * TQ);
+                ++items;
+                advance(a, w, h.take, TQ);
+            }
+            // no copy into this CTA's shared memory may still be in flight at exit
+            if (items > 0) {
+                const uint32_t addr = smem_u32(&F.q_loaded);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(addr, (items - 1) & 1))
+                    if (global_timer_ns() - t0 > LILY_DRAIN_LIMIT_NS) {
+                        record_error(status, kErrDeviceTimeout);
+                        break;
+                    }
+            }
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------ MMA issuer (one thread)
         if (lane == 0) {
             constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, kRows, kChunk);
             constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, kRows, D) | (1u << 16);  // B: channels contiguous
             int it = 0, items = 0;
-            while (w.left > 0 && ok) {
-                const int nch = tile_chunks(w.m, w.L, w.t, TQ), n = static_cast<int>(min(static_cast<long long>(nch - w.j0), w.left));
+            Share h;
+            while (ok && next_share(a, w, h, TQ)) {
+                const int n = h.n;
                 if (!(ok = mbar_wait(&F.q_full, items & 1, &F.abort, status))) break;
                 tc_fence_after();
                 for (int i = 0; i <= n && ok; ++i) {
@@ -613,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 }
                 it += n;
                 ++items;
-                advance(a, w, n, TQ);
+                advance(a, w, h.take, TQ);
             }
             // all tensor-core work of this CTA must finish before tensor memory is freed
             umma_commit(&F.drain);
@@ -670,23 +791,23 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
 }
 
 template <int BITS, int GR>
-cudaError_t launch(const KvqAttnArgs &a, cudaStream_t stream)
+cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
     const int smem = smem_bytes(64 * GR);
     const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR>), smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_kernel<BITS, GR>, dim3(kKvqPrefillCtas), dim3(kThreads), smem, stream, a);
+    return launch_pdl(kvq_prefill_kernel<BITS, GR>, dim3(kKvqPrefillCtas), dim3(kThreads), smem, stream, a, tmQ);
 }
 
 }  // namespace
 
-cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, cudaStream_t stream)
+cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
     cudaError_t e;
     if (a.c.bits == 4)
-        e = a.D == 64 ? launch<4, 1>(a, stream) : a.D == 128 ? launch<4, 2>(a, stream) : launch<4, 4>(a, stream);
+        e = a.D == 64 ? launch<4, 1>(a, tmQ, stream) : a.D == 128 ? launch<4, 2>(a, tmQ, stream) : launch<4, 4>(a, tmQ, stream);
     else
-        e = a.D == 64 ? launch<8, 1>(a, stream) : a.D == 128 ? launch<8, 2>(a, stream) : launch<8, 4>(a, stream);
+        e = a.D == 64 ? launch<8, 1>(a, tmQ, stream) : a.D == 128 ? launch<8, 2>(a, tmQ, stream) : launch<8, 4>(a, tmQ, stream);
     if (e != cudaSuccess) return e;
     return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas, kRows / 4), dim3(256), 0, stream, a);
 }

@@ -567,3 +567,18 @@ def test_prefill_sharp_softmax():
         kk, vv, km, vm = c.sequence(0)
         ref, mags = kvq.attend_and_bound(rounded(c.a["q"]), kk, vv, 1437 + np.arange(64), scale, km, vm)
         check(rounded(out), ref, mags)
+
+
+@pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 4), (256, 8)])
+def test_cold_caches_change_nothing(D, bits):
+    # with the inputs out of L2 the warps of a CTA meet in another order: the results are the same bits
+    cfg = KvqConfig("cold", lens=(1, 33, 300, 500), new=(1, 33, 40, 3), D=D, block_size=32, bits=bits, seed=73)
+    c, want = _check_prefill(cfg, poison=True)
+    one = Cache(cfg.with_(new=(1, 1, 1, 1))).to_gpu()
+    want_one = _decode(one)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(8):
+        flush.fill_(i)
+        assert torch.equal(want, _prefill(c)), i
+        flush.fill_(i)
+        assert torch.equal(want_one, _decode(one)), i
