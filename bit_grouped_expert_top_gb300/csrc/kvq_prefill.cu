@@ -69,7 +69,7 @@ struct Cols {
 template <int BITS>
 __device__ __forceinline__ constexpr int unpacked(int p)
 {
-    return BITS == 4 ? (p < 4 ? 2 * p : 2 * (p - 4) + 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
+    return BITS == 4 ? (p >> 1) + 4 * (p & 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -82,6 +82,29 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two fp32 values in one register pair
+__device__ __forceinline__ unsigned long long pair(float x, float y)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long v, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigned long long y, unsigned long long z)
+{
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigned long long y)
+{
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
     return r;
 }
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -143,6 +166,20 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ uint64_t join64(uint32_t lo, uint32_t hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
 
 // A whole warp waits.  Every lane does: what the barrier guards is read by every lane,
@@ -334,35 +371,40 @@ struct Raw {
     uint32_t sb;
 };
 
+// Values code * scale + bias in fp16, each rounded once: the code under the exponent
+// of a power of two P is P + code / 8, so P is taken off exactly and the multiply-add
+// gets 8 scale (8 scale is a normal fp16 number down to scales of 2^-17).
 template <int BITS>
-__device__ __forceinline__ void rebuild(const Raw<BITS> &raw, uint32_t row_addr, int sw, int *status)
+__device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint32_t row_addr, int *status)
 {
-    const float s = lo_bf16(raw.sb), b = hi_bf16(raw.sb);
-    constexpr float L = BITS == 4 ? 15.0f : 255.0f, kUp = BITS == 4 ? 8.0f : 64.0f;
+    const uint32_t sb = exists ? raw.sb : 0u;  // rows behind the sequence, whatever they hold
+    const float s = lo_bf16(sb), b = hi_bf16(sb);
+    constexpr float L = BITS == 4 ? 15.0f : 255.0f;
     if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
-    const __half2 s2 = __float2half2_rn(s * kUp), b2 = __float2half2_rn(b);
+    const __half2 s2 = __float2half2_rn(s * 8.0f), b2 = __float2half2_rn(b);
+    // codes under `mask` to fp16: `bits` the pattern of -P less the sign
+    auto value = [&](uint32_t w, uint32_t mask, uint32_t bits) {
+        const uint32_t x = (w & mask) | bits, off = bits | 0x80008000u;
+        const __half2 v = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&off)), s2, b2);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(raw.q);
         uint4 v;
-        if constexpr (BITS == 4) {
-            const uint32_t w = reinterpret_cast<const uint32_t *>(raw.q)[i];
-            v = dequant8_f16_e2m3(w, s2, b2);
-        } else {
-            // 16 + code / 64 is the code under the exponent of 16
-            const __half2 off = __half2half2(__ushort_as_half(0xCC00));  // -16
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t w = reinterpret_cast<const uint32_t *>(raw.q)[2 * i + j];
-                const uint32_t e = (w & 0x00FF00FFu) | 0x4C004C00u, d = ((w >> 8) & 0x00FF00FFu) | 0x4C004C00u;
-                __half2 he = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&e), off), s2, b2);
-                __half2 hd = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&d), off), s2, b2);
-                o[2 * j] = *reinterpret_cast<uint32_t *>(&he);
-                o[2 * j + 1] = *reinterpret_cast<uint32_t *>(&hd);
-            }
-            v = make_uint4(o[0], o[1], o[2], o[3]);
+        if constexpr (BITS == 4) {  // channels (0, 4), (1, 5), (2, 6), (3, 7)
+            const uint32_t w = q[i], w8 = w >> 8;
+            v.x = value(w, 0x000F000Fu, 0x58005800u);   // 128 + code / 8
+            v.y = value(w, 0x00F000F0u, 0x48004800u);   // 8 + 16 code / 128
+            v.z = value(w8, 0x000F000Fu, 0x58005800u);
+            v.w = value(w8, 0x00F000F0u, 0x48004800u);
+        } else {                    // channels (0, 2), (1, 3), (4, 6), (5, 7)
+            v.x = value(q[2 * i], 0x00FF00FFu, 0x58005800u);
+            v.y = value(q[2 * i] >> 8, 0x00FF00FFu, 0x58005800u);
+            v.z = value(q[2 * i + 1], 0x00FF00FFu, 0x58005800u);
+            v.w = value(q[2 * i + 1] >> 8, 0x00FF00FFu, 0x58005800u);
         }
-        sts128(row_addr + ((i ^ sw) << 4), v);
+        sts128(row_addr ^ (i << 4), v);
     }
 }
 
@@ -493,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) mx[x & 3] = fmaxf(mx[x & 3], __uint_as_float(s[x]));
+                    for (int x = 0; x < 32; x += 2)  // three operands a step
+                        mx[(x >> 1) & 3] = fmaxf(fmaxf(mx[(x >> 1) & 3], __uint_as_float(s[x])), __uint_as_float(s[x + 1]));
                     float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     F.xch[sb][half][row] = top;
                     named_barrier_sync(kBarPair + quarter, 64);  // also: both halves have S in registers, so P may overwrite it
@@ -519,16 +562,22 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                         }
                     }
                     uint32_t p[16];
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    unsigned long long sum[2] = {0ull, 0ull};
+                    const unsigned long long mul2 = pair(item_mul, item_mul), neg2 = pair(-m_run, -m_run);
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[2 * x]), item_mul, -m_run));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[2 * x + 1]), item_mul, -m_run));
-                        sum[(2 * x) & 3] += p0;
-                        sum[(2 * x + 1) & 3] += p1;
-                        p[x] = pack_f16(p0, p1);
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), mul2, neg2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        sum[x & 1] = add2(sum[x & 1], pair(e0, e1));
+                        p[x] = pack_f16(e0, e1);
                     }
-                    l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    {
+                        float a0, a1;
+                        unpair(add2(sum[0], sum[1]), a0, a1);
+                        l_run += a0 + a1;
+                    }
                     if (ok) tmem_st_x16(lanes + Cols<GR>::S + sb * 64 + half * 16, p);
                     tmem_st_wait();
                     tc_fence_before();
@@ -604,62 +653,54 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     } else if (warp < kSoftWarps + kDeqWarps) {
         // ------------------------------------------------ K and V of the chunks into shared memory
         constexpr int kItems = GR == 4 ? 2 : 1;  // (K or V, group, 32 tokens) per warp and chunk
-        const int dw = warp - kSoftWarps;
+        const int dw = warp - kSoftWarps, half = dw & 1;
         const bool idle = dw >= 4 * GR;          // D = 64: four warps are enough
+        auto is_v = [&](int x) { return dw + x * kDeqWarps >= 2 * GR; };
+        auto group_of = [&](int x) { return ((dw + x * kDeqWarps) % (2 * GR)) >> 1; };
+        const int bs_log = 31 - __clz(a.c.bs), row = half * 32 + lane;
+        const uint32_t row_addr = k_smem + row * 128 + ((row & 7) << 4);
+        const int block_rows = a.c.H_kv * GR * a.c.bs;
         int it = 0;
         Share h;
         while (ok && !idle && next_share(a, w, h, TQ)) {
-            const int n = h.n;
-            Raw<BITS> raw[kItems];
-            int pb = 0;
-            // the table entry of this warp's 32 tokens of chunk j (both items have the same half of the chunk)
-            const int half = dw & 1;
+            // the table entry of this warp's 32 tokens of chunk j (both items have the same half of the chunk), as
+            // stored: it is looked at one chunk later, as any use of a load's result waits for it
+            const int *table = a.block_table + static_cast<size_t>(w.b) * a.max_blocks;
             auto entry = [&](int j) {
                 const int t0 = j * kChunk + half * 32;
-                if (t0 >= w.L) return 0;
-                int e = a.block_table[static_cast<size_t>(w.b) * a.max_blocks + t0 / a.c.bs];
-                if (e < 0 || e >= a.c.n_blocks) {
-                    record_error(status, kErrDeviceIndex);
-                    e = 0;
-                }
-                return e;
+                return j < h.j0 + h.n && t0 < w.L ? table[t0 >> bs_log] : 0;
             };
-            auto fetch = [&](int j, int block) {
+            auto checked = [&](int e) {
+                if (e >= 0 && e < a.c.n_blocks) return e;
+                record_error(status, kErrDeviceIndex);
+                return 0;
+            };
+            Raw<BITS> raw[kItems];
+            auto fetch = [&](Raw<BITS> &r, int x, int j, int block) {
                 const int tok = j * kChunk + half * 32 + lane;
+                const uint32_t group0 = (static_cast<uint32_t>(w.g) * GR + group_of(x)) << bs_log;  // rows before the group's in a block
+                const long long gi = static_cast<long long>(block) * block_rows + (group0 + (tok & (a.c.bs - 1)));
+                const uint4 *src = reinterpret_cast<const uint4 *>((is_v(x) ? a.c.v_q : a.c.k_q) + gi * GB);
 #pragma unroll
-                for (int x = 0; x < kItems; ++x) {
-                    const int item = dw + x * kDeqWarps, group = (item % (2 * GR)) >> 1;
-                    const bool isv = item >= 2 * GR;
-                    const long long gi = ((static_cast<long long>(block) * a.c.H_kv + w.g) * GR + group) * a.c.bs + tok % a.c.bs;
-                    const uint4 *src = reinterpret_cast<const uint4 *>((isv ? a.c.v_q : a.c.k_q) + gi * GB);
-#pragma unroll
-                    for (int y = 0; y < BITS / 2; ++y) raw[x].q[y] = src[y];
-                    const uint32_t sb = *reinterpret_cast<const uint32_t *>((isv ? a.c.v_sb : a.c.k_sb) + gi * 2);
-                    raw[x].sb = tok < w.L ? sb : 0u;  // rows behind the sequence, whatever they hold
-                }
+                for (int y = 0; y < BITS / 2; ++y) r.q[y] = src[y];
+                r.sb = reinterpret_cast<const uint32_t *>(is_v(x) ? a.c.v_sb : a.c.k_sb)[gi];
             };
-            pb = entry(h.j0);
-            fetch(h.j0, pb);
-            pb = n > 1 ? entry(h.j0 + 1) : 0;
-            for (int i = 0; i < n; ++i, ++it) {
-                Raw<BITS> cur[kItems];
+            int pb = entry(h.j0), pb1 = entry(h.j0 + 1);
+            pb = checked(pb);
 #pragma unroll
-                for (int x = 0; x < kItems; ++x) cur[x] = raw[x];
-                if (i + 1 < n) {
-                    fetch(h.j0 + i + 1, pb);
-                    pb = i + 2 < n ? entry(h.j0 + i + 2) : 0;
-                }
-                const int buf = it & 1;
+            for (int x = 0; x < kItems; ++x) fetch(raw[x], x, h.j0, pb);
+            for (int i = 0; i < h.n; ++i, ++it) {
+                const int buf = it & 1, next = checked(pb1);
+                pb1 = entry(h.j0 + i + 2);
+                const bool exists = (h.j0 + i) * kChunk + row < w.L;
 #pragma unroll
                 for (int x = 0; x < kItems; ++x) {
-                    const int item = dw + x * kDeqWarps, group = (item % (2 * GR)) >> 1;
-                    const bool isv = item >= 2 * GR;
-                    if (it >= 2 && !(ok = warp_wait(isv ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
-                    const int r = half * 32 + lane;
-                    rebuild<BITS>(cur[x], (isv ? v_smem : k_smem) + (buf * GR + group) * kBox + r * 128, r & 7, status);
+                    if (it >= 2 && !(ok = warp_wait(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
+                    rebuild<BITS>(raw[x], exists, row_addr + ((is_v(x) ? 2 * GR : 0) + buf * GR + group_of(x)) * kBox, status);
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(isv ? &F.v_full[buf] : &F.k_full[buf]);
+                    if (lane == 0) mbar_arrive(is_v(x) ? &F.v_full[buf] : &F.k_full[buf]);
+                    if (i + 1 < h.n) fetch(raw[x], x, h.j0 + i + 1, next);
                 }
                 if (!ok) break;
             }
@@ -693,49 +734,60 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ MMA issuer (one thread)
-        if (lane == 0) {
-            constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, kRows, kChunk);
-            constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, kRows, D) | (1u << 16);  // B: channels contiguous
-            int it = 0, items = 0;
-            Share h;
-            while (ok && next_share(a, w, h, TQ)) {
-                const int n = h.n;
-                if (!(ok = mbar_wait(&F.q_full, items & 1, &F.abort, status))) break;
-                tc_fence_after();
-                for (int i = 0; i <= n && ok; ++i) {
-                    if (i < n) {
-                        const int x = it + i, buf = x & 1;
-                        if (!(ok = mbar_wait(&F.k_full[buf], (x >> 1) & 1, &F.abort, status))) break;
-                        tc_fence_after();
+        // ------------------------------------------------ MMA issuer
+        // The whole warp walks the list, so that every operand of an MMA is warp-uniform, and one elected
+        // lane issues: issuing from inside `if (lane == 0)` took ~87 cycles an MMA, more than it runs.
+        constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, kRows, kChunk);
+        constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, kRows, D) | (1u << 16);  // B: channels contiguous
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t kd = sdesc_sw128(k_smem), vd = sdesc_mn_sw128(v_smem, kBox);
+        int it = 0, items = 0;
+        Share h;
+        while (ok && next_share(a, w, h, TQ)) {
+            const int n = __shfl_sync(0xffffffffu, h.n, 0);
+            if (!(ok = warp_wait(&F.q_full, items & 1, &F.abort, status))) break;
+            tc_fence_after();
+            for (int i = 0; i <= n && ok; ++i) {
+                if (i < n) {
+                    const int x = it + i, buf = x & 1;
+                    if (!(ok = warp_wait(&F.k_full[buf], (x >> 1) & 1, &F.abort, status))) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t lo = static_cast<uint32_t>(kd) + buf * (GR * kBox >> 4), hi = static_cast<uint32_t>(kd >> 32);
 #pragma unroll
-                        for (int c = 0; c < GR; ++c) {
-                            const uint64_t bd = sdesc_sw128(k_smem + (buf * GR + c) * kBox);
+                        for (int c = 0; c < GR; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ts(tmem + Cols<GR>::S + buf * 64, tmem + Cols<GR>::Q + c * 32 + kk * 8, bd + kk * 2, kIdescS, (c | kk) != 0);
-                        }
+                                umma_ts(tm + Cols<GR>::S + buf * 64, tm + Cols<GR>::Q + c * 32 + kk * 8,
+                                        join64(lo + c * (kBox >> 4) + kk * 2, hi), kIdescS, (c | kk) != 0);
                         umma_commit(&F.k_free[buf]);
                         umma_commit(&F.s_full[buf]);
                     }
-                    if (i > 0) {
-                        const int x = it + i - 1, buf = x & 1;
-                        if (i == 1 && items > 0 && !(ok = mbar_wait(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
-                        if (!(ok = mbar_wait(&F.v_full[buf], (x >> 1) & 1, &F.abort, status))) break;
-                        if (!(ok = mbar_wait(&F.p_full[buf], (x >> 1) & 1, &F.abort, status))) break;
-                        tc_fence_after();
-                        const uint64_t bd = sdesc_mn_sw128(v_smem + buf * GR * kBox, kBox);
+                    __syncwarp();
+                }
+                if (i > 0) {
+                    const int x = it + i - 1, buf = x & 1;
+                    if (i == 1 && items > 0 && !(ok = warp_wait(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
+                    ok = __all_sync(0xffffffffu, mbar_wait2(&F.v_full[buf], (x >> 1) & 1, &F.p_full[buf], (x >> 1) & 1, &F.abort, status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t lo = static_cast<uint32_t>(vd) + buf * (GR * kBox >> 4), hi = static_cast<uint32_t>(vd >> 32);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_ts(tmem + Cols<GR>::O, tmem + Cols<GR>::S + buf * 64 + kk * 8, bd + kk * (2048 >> 4), kIdescO, i > 1 || kk > 0);
+                            umma_ts(tm + Cols<GR>::O, tm + Cols<GR>::S + buf * 64 + kk * 8, join64(lo + kk * (2048 >> 4), hi), kIdescO,
+                                    i > 1 || kk > 0);
                         umma_commit(&F.v_free[buf]);
                         umma_commit(&F.pv_done[buf]);
                     }
+                    __syncwarp();
                 }
-                it += n;
-                ++items;
-                advance(a, w, h.take, TQ);
             }
+            it += n;
+            ++items;
+            advance(a, w, h.take, TQ);
+        }
+        if (elect_one()) {
             // all tensor-core work of this CTA must finish before tensor memory is freed
             umma_commit(&F.drain);
             const uint32_t addr = smem_u32(&F.drain);
