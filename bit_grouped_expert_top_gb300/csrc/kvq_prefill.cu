@@ -182,6 +182,20 @@ __device__ __forceinline__ uint64_t join64(uint32_t lo, uint32_t hi)
     return r;
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ uint32_t phase_done(uint64_t *bar, uint32_t parity)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return r;
+}
+
 // A whole warp waits.  Every lane does: what the barrier guards is read by every lane,
 // and a shuffle of one lane's result orders no memory access.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
@@ -663,17 +677,19 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         int it = 0;
         Share h;
         while (ok && !idle && next_share(a, w, h, TQ)) {
-            // the table entry of this warp's 32 tokens of chunk j (both items have the same half of the chunk), as
-            // stored: it is looked at one chunk later, as any use of a load's result waits for it
+            // the table entries of this warp's 32 tokens of 32 chunks, one chunk per lane
             const int *table = a.block_table + static_cast<size_t>(w.b) * a.max_blocks;
-            auto entry = [&](int j) {
-                const int t0 = j * kChunk + half * 32;
-                return j < h.j0 + h.n && t0 < w.L ? table[t0 >> bs_log] : 0;
-            };
-            auto checked = [&](int e) {
-                if (e >= 0 && e < a.c.n_blocks) return e;
-                record_error(status, kErrDeviceIndex);
-                return 0;
+            auto entries = [&](int c0) {
+                const int j = c0 + lane, tok = j * kChunk + half * 32;
+                int e = 0;
+                if (j < h.j0 + h.n && tok < w.L) {
+                    e = table[tok >> bs_log];
+                    if (e < 0 || e >= a.c.n_blocks) {
+                        record_error(status, kErrDeviceIndex);
+                        e = 0;
+                    }
+                }
+                return e;
             };
             Raw<BITS> raw[kItems];
             auto fetch = [&](Raw<BITS> &r, int x, int j, int block) {
@@ -685,17 +701,22 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 for (int y = 0; y < BITS / 2; ++y) r.q[y] = src[y];
                 r.sb = reinterpret_cast<const uint32_t *>(is_v(x) ? a.c.v_sb : a.c.k_sb)[gi];
             };
-            int pb = entry(h.j0), pb1 = entry(h.j0 + 1);
-            pb = checked(pb);
+            int tab = entries(h.j0);
+            const int pb = __shfl_sync(0xffffffffu, tab, 0);
 #pragma unroll
             for (int x = 0; x < kItems; ++x) fetch(raw[x], x, h.j0, pb);
             for (int i = 0; i < h.n; ++i, ++it) {
-                const int buf = it & 1, next = checked(pb1);
-                pb1 = entry(h.j0 + i + 2);
+                const int buf = it & 1;
+                if (((i + 1) & 31) == 0) tab = entries(h.j0 + i + 1);
+                const int next = __shfl_sync(0xffffffffu, tab, (i + 1) & 31);
                 const bool exists = (h.j0 + i) * kChunk + row < w.L;
+                uint32_t is_free[kItems];
+#pragma unroll
+                for (int x = 0; x < kItems; ++x)
+                    is_free[x] = it >= 2 ? phase_done(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1) : 1u;
 #pragma unroll
                 for (int x = 0; x < kItems; ++x) {
-                    if (it >= 2 && !(ok = warp_wait(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
+                    if (!__all_sync(0xffffffffu, is_free[x]) && !(ok = warp_wait(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
                     rebuild<BITS>(raw[x], exists, row_addr + ((is_v(x) ? 2 * GR : 0) + buf * GR + group_of(x)) * kBox, status);
                     fence_async_shared();
                     __syncwarp();
