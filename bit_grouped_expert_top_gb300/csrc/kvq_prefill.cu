@@ -38,7 +38,10 @@ namespace {
 
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kChunk = 64;                 // cache tokens per step
-constexpr int kItemCost = 2;               // of taking up an item, in chunks, in the work list's shares
+// Taking up an item (its q, the first scores, its output) costs about six chunks, which
+// the shares of the work list count: an 8K prompt 627 us with 2, 531 with 4, 482 with
+// 6, 489 with 8.
+constexpr int kItemCost = 6;
 constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
@@ -69,7 +72,7 @@ struct Cols {
 template <int BITS>
 __device__ __forceinline__ constexpr int unpacked(int p)
 {
-    return BITS == 4 ? (p >> 1) + 4 * (p & 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
+    return BITS == 4 ? (p < 4 ? 2 * p : 2 * (p - 4) + 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -385,9 +388,10 @@ struct Raw {
     uint32_t sb;
 };
 
-// Values code * scale + bias in fp16, each rounded once: the code under the exponent
-// of a power of two P is P + code / 8, so P is taken off exactly and the multiply-add
-// gets 8 scale (8 scale is a normal fp16 number down to scales of 2^-17).
+// Values code * scale + bias in fp16, each rounded once.  4 bits: the nibbles are e2m3
+// bit patterns of code / 8, which converts exactly, and the multiply-add gets 8 scale (a
+// normal fp16 number down to scales of 2^-17).  8 bits: the code under the exponent of
+// 128 is 128 + code / 8, so 128 is taken off exactly first.
 template <int BITS>
 __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint32_t row_addr, int *status)
 {
@@ -396,9 +400,8 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
     constexpr float L = BITS == 4 ? 15.0f : 255.0f;
     if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
     const __half2 s2 = __float2half2_rn(s * 8.0f), b2 = __float2half2_rn(b);
-    // codes under `mask` to fp16: `bits` the pattern of -P less the sign
-    auto value = [&](uint32_t w, uint32_t mask, uint32_t bits) {
-        const uint32_t x = (w & mask) | bits, off = bits | 0x80008000u;
+    auto value = [&](uint32_t w) {
+        const uint32_t x = (w & 0x00FF00FFu) | 0x58005800u, off = 0xD800D800u;
         const __half2 v = __hfma2(__hadd2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&off)), s2, b2);
         return *reinterpret_cast<const uint32_t *>(&v);
     };
@@ -406,18 +409,10 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
     for (int i = 0; i < 8; ++i) {
         const uint32_t *q = reinterpret_cast<const uint32_t *>(raw.q);
         uint4 v;
-        if constexpr (BITS == 4) {  // channels (0, 4), (1, 5), (2, 6), (3, 7)
-            const uint32_t w = q[i], w8 = w >> 8;
-            v.x = value(w, 0x000F000Fu, 0x58005800u);   // 128 + code / 8
-            v.y = value(w, 0x00F000F0u, 0x48004800u);   // 8 + 16 code / 128
-            v.z = value(w8, 0x000F000Fu, 0x58005800u);
-            v.w = value(w8, 0x00F000F0u, 0x48004800u);
-        } else {                    // channels (0, 2), (1, 3), (4, 6), (5, 7)
-            v.x = value(q[2 * i], 0x00FF00FFu, 0x58005800u);
-            v.y = value(q[2 * i] >> 8, 0x00FF00FFu, 0x58005800u);
-            v.z = value(q[2 * i + 1], 0x00FF00FFu, 0x58005800u);
-            v.w = value(q[2 * i + 1] >> 8, 0x00FF00FFu, 0x58005800u);
-        }
+        if constexpr (BITS == 4)  // channels (0, 2), (4, 6), (1, 3), (5, 7)
+            v = dequant8_f16_e2m3(q[i], s2, b2);
+        else                      // channels (0, 2), (1, 3), (4, 6), (5, 7)
+            v = make_uint4(value(q[2 * i]), value(q[2 * i] >> 8), value(q[2 * i + 1]), value(q[2 * i + 1] >> 8));
         sts128(row_addr ^ (i << 4), v);
     }
 }
@@ -827,11 +822,13 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the parts of an item that was cut: CTA (first CTA of the item, four rows),
-// 64 threads a row.  The part of the first CTA c0 is in slot 2 c0 + 1, those of the
-// following ones in slot 2 c.
+// Joins the parts of an item that was cut: CTA (first CTA of the item, four rows), 64
+// threads a row, a float4 column each, eight parts in flight on a running maximum (a
+// grid of one row per CTA took 20 us to launch).  The part of the first CTA c0 is in
+// slot 2 c0 + 1, those of the following CTAs c in slot 2 c.
 __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a)
 {
+    constexpr int kBatch = 8;
     pdl_trigger();
     pdl_wait();
     const int4 meta = a.meta[blockIdx.x];
@@ -843,16 +840,34 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
     auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kRows + row; };
     float M = kNoMax, den = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < S; ++s) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2);
-        const float4 x = reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4];
-        const float to = fmaxf(M, ml.x), c = ex2(M - to), e = ex2(ml.x - to);
+    for (int s0 = 0; s0 < S; s0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch];
+        float to = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int s = s0 + k;
+            ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2) : make_float2(kNoMax, 0.0f);
+            x[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k].x);
+        const float c = ex2(M - to);
         M = to;
-        den = fmaf(den, c, e * ml.y);
-        o.x = fmaf(o.x, c, e * x.x);
-        o.y = fmaf(o.y, c, e * x.y);
-        o.z = fmaf(o.z, c, e * x.z);
-        o.w = fmaf(o.w, c, e * x.w);
+        den *= c;
+        o.x *= c;
+        o.y *= c;
+        o.z *= c;
+        o.w *= c;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float e = ex2(ml[k].x - to);
+            den = fmaf(e, ml[k].y, den);
+            o.x = fmaf(e, x[k].x, o.x);
+            o.y = fmaf(e, x[k].y, o.y);
+            o.z = fmaf(e, x[k].z, o.z);
+            o.w = fmaf(e, x[k].w, o.w);
+        }
     }
     const float r = den > 0.0f ? 1.0f / den : 0.0f;
     uint2 y;
