@@ -150,6 +150,35 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
         w.left = blocks_of(w.L, a.c.bs);
         return w;
     }
+    if (a.B <= 32) {
+        // every warp for itself, a sequence per lane: one load and no barrier
+        const int stored = lane < a.B ? a.seq_lens[lane] : 0;
+        const int len = lane < a.B ? length_of(a, stored) : 0, n = lane < a.B ? blocks_of(len, a.c.bs) * a.c.H_kv : 0;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31), used = min(total, static_cast<int>(gridDim.x));
+        if (c >= used) return w;
+        const int per = total / used, rest = total % used;
+        const int begin = per * c + rest * c / used;
+        w.left = per * (c + 1) + rest * (c + 1) / used - begin;
+        w.b = __ffs(__ballot_sync(0xffffffffu, begin < inc)) - 1;
+        w.L = __shfl_sync(0xffffffffu, len, w.b);
+        w.next = __shfl_sync(0xffffffffu, stored, min(w.b + 1, 31));
+        const int nblk = blocks_of(w.L, a.c.bs), off = begin - __shfl_sync(0xffffffffu, inc - n, w.b);
+        w.g = off / nblk;
+        w.j0 = off % nblk;
+        if (lane == 0) {  // the same values from every warp; each reads its own
+            F.begin = begin;
+            F.total = total;
+            F.used = used;
+        }
+        __syncwarp();
+        return w;
+    }
     // blocks of sequence s0 + tid: those of the threads before this one, and of all (fewer than 2^31 by the host's check)
     int len = 0, before, all;
     auto scan = [&](int s0) {
@@ -662,16 +691,17 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     }
 }
 
-// Joins the parts of a segment that was cut: CTA (segment key x head, 64-wide slice
-// of D), 256 threads: thread (e, sg) takes float4 column e and parts sg, sg + 16, ..
-// with a running maximum of its own, then the 16 groups agree on the common one and
-// are added in a fixed order.  Parts of CTA c0 (the one the segment starts in) are in
-// slot 2 c0 + 1, those of the following CTAs c in slot 2 c, up to the CTA it ends in.
+// Joins the parts of a segment that was cut: CTA (segment key x head, 32-wide slice
+// of D), 256 threads: thread (e, sg) takes float4 column e and parts sg, sg + 32, ..
+// on a running maximum of its own; the four part groups of a warp are joined by shuffles,
+// the eight warps through shared memory, in a fixed order.  Parts of CTA c0 (the one the
+// segment starts in) are in slot 2 c0 + 1, those of the following CTAs c in slot 2 c, up
+// to the CTA it ends in.
 __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant__ KvqAttnArgs a)
 {
-    constexpr int kCols = 16, kGroups = 16, kBatch = 8;
-    __shared__ float4 part[kGroups][kCols];
-    __shared__ float red_max[8], red_den[8];
+    constexpr int kCols = 8, kGroups = 32, kBatch = 4;
+    __shared__ float4 part[8][kCols];
+    __shared__ float part_m[8], part_den[8];
     const int key = blockIdx.x / a.group, h = blockIdx.x % a.group;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int e = tid % kCols, sg = tid / kCols;
@@ -680,28 +710,29 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
     const int4 meta = a.meta[key];
     if (meta.x < 0) return;
     const int c0 = meta.y, S = meta.z - c0 + 1, q = blockIdx.y * kCols + e;
-    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)); };
-    float mt = kNoMax, dt = 0.0f;
+    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * 8 + h; };
+    float mt = kNoMax, den = 0.0f;
     float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto scale_by = [&](float c) {
+        num.x *= c;
+        num.y *= c;
+        num.z *= c;
+        num.w *= c;
+        den *= c;
+    };
     for (int s0 = sg; s0 < S; s0 += kBatch * kGroups) {
         float4 v[kBatch];
         float2 ml[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const int s = s0 + k * kGroups;
-            const size_t at = s < S ? slot(s) * 8 + h : 0;
-            ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + at * 2) : make_float2(kNoMax, 0.0f);
-            v[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + at * a.D)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
+            ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2) : make_float2(kNoMax, 0.0f);
+            v[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float bm = mt;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) bm = fmaxf(bm, ml[k].x);
-        const float c = ex2(mt - bm);
-        num.x *= c;
-        num.y *= c;
-        num.z *= c;
-        num.w *= c;
-        dt *= c;
+        scale_by(ex2(mt - bm));
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
             const float w = ex2(ml[k].x - bm);
@@ -709,37 +740,43 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
             num.y = fmaf(w, v[k].y, num.y);
             num.z = fmaf(w, v[k].z, num.z);
             num.w = fmaf(w, v[k].w, num.w);
-            dt = fmaf(w, ml[k].y, dt);
+            den = fmaf(w, ml[k].y, den);
         }
         mt = bm;
     }
-    float mx = mt;
+    float mw = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
+    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+    scale_by(ex2(mt - mw));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) red_max[warp] = mx;
-    __syncthreads();
-    mx = red_max[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) mx = fmaxf(mx, red_max[w]);
-    const float f = ex2(mt - mx);
-    part[sg][e] = make_float4(num.x * f, num.y * f, num.z * f, num.w * f);
-    float den = e == 0 ? dt * f : 0.0f;  // the threads of column 0 hold every part once
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane == 0) red_den[warp] = den;
+    for (int o = 8; o < 32; o <<= 1) {
+        num.x += __shfl_xor_sync(0xffffffffu, num.x, o);
+        num.y += __shfl_xor_sync(0xffffffffu, num.y, o);
+        num.z += __shfl_xor_sync(0xffffffffu, num.z, o);
+        num.w += __shfl_xor_sync(0xffffffffu, num.w, o);
+        den += __shfl_xor_sync(0xffffffffu, den, o);
+    }
+    if (lane < kCols) part[warp][lane] = num;
+    if (lane == 0) {
+        part_m[warp] = mw;
+        part_den[warp] = den;
+    }
     __syncthreads();
     if (tid < kCols) {
-        float4 t = part[0][tid];
+        float mx = part_m[0];
 #pragma unroll
-        for (int g2 = 1; g2 < kGroups; ++g2) {
-            t.x += part[g2][tid].x;
-            t.y += part[g2][tid].y;
-            t.z += part[g2][tid].z;
-            t.w += part[g2][tid].w;
+        for (int w = 1; w < 8; ++w) mx = fmaxf(mx, part_m[w]);
+        float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float dsum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const float f = ex2(part_m[w] - mx);
+            const float4 x = part[w][tid];
+            t.x = fmaf(f, x.x, t.x);
+            t.y = fmaf(f, x.y, t.y);
+            t.z = fmaf(f, x.z, t.z);
+            t.w = fmaf(f, x.w, t.w);
+            dsum = fmaf(f, part_den[w], dsum);
         }
-        float dsum = red_den[0];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) dsum += red_den[w];
         const float r = dsum > 0.0f ? 1.0f / dsum : 0.0f;
         uint2 y;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(t.x * r, t.y * r), hi = __floats2bfloat162_rn(t.z * r, t.w * r);
@@ -786,7 +823,7 @@ cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
     const cudaError_t e = a.c.bits == 4 ? launch_d<4>(a, ctas, stream) : launch_d<8>(a, ctas, stream);
     if (e != cudaSuccess || a.whole) return e;
     const int keys = a.key_by_segment ? static_cast<int>(segments) : ctas;
-    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 64), dim3(256), 0, stream, a);
+    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 32), dim3(256), 0, stream, a);
 }
 
 }  // namespace lily
