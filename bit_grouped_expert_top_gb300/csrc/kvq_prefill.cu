@@ -46,11 +46,12 @@ constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
 constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
+constexpr int kBufs = 4;                   // buffers of K and of V
 constexpr uint32_t kTmemCols = 512;
 constexpr float kNoMax = -1.7e38f;
 
 struct Fixed {
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2];
+    uint64_t k_full[kBufs], k_free[kBufs], v_full[kBufs], v_free[kBufs], s_full[2], p_full[2];
     uint64_t pv_done[2], q_full, q_loaded, q_free, o_free, drain;
     uint32_t tmem;
     int abort, b0, m0, L0;
@@ -60,7 +61,18 @@ struct Fixed {
 constexpr int kFixed = 4096;
 static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
 constexpr int kQBox = kRows * 128;         // [128 rows][64 channels] bf16, 128-byte swizzle
-constexpr int smem_bytes(int D) { return 1024 + kFixed + (D / 64) * (4 * kBox + kQBox); }
+// CTAs that share an item's K and V: with D = 64 one; else a pair, whose MMAs read half
+// of K's tokens (of V's channels) from each CTA's shared memory, so each rebuilds half.
+__host__ __device__ constexpr int pair_of(int GR) { return GR == 1 ? 1 : 2; }
+__host__ __device__ constexpr int buf_bytes(int GR) { return GR * kBox / pair_of(GR); }
+// More than half of an SM's, so that no two CTAs that allocate tensor memory meet on
+// one SM: two pairs that each hold one of two SMs would wait for each other.
+constexpr int kSmemLeast = 120 * 1024;
+constexpr int smem_bytes(int D)
+{
+    const int n = 1024 + kFixed + 2 * kBufs * buf_bytes(D / 64) + (D / 64) * kQBox;
+    return n > kSmemLeast ? n : kSmemLeast;
+}
 
 // Tensor-memory columns: O [0, D), S / P two buffers of 64, Q D / 2.
 template <int GR>
@@ -171,6 +183,83 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// ---- a pair of CTAs
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+template <int CG>
+__device__ __forceinline__ void pair_sync()  // every thread of the CTA, or of both
+{
+    __syncwarp();
+    if constexpr (CG == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrives on a barrier of the first CTA of the pair.  What it announces has been made
+// visible by its own fences (shared memory: the async proxy's; tensor memory: wait::st and
+// before_thread_sync); a release at cluster scope on top waited for every access in
+// flight, ~1000 cycles a chunk.
+template <int CG>
+__device__ __forceinline__ void arrive_first(uint64_t *bar)
+{
+    if constexpr (CG == 1)
+        mbar_arrive(bar);
+    else
+        asm volatile(
+            "{\n\t.reg .b32 r;\n\t"
+            "mapa.shared::cluster.u32 r, %0, 0;\n\t"
+            "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void alloc_tmem(uint32_t *dst)
+{
+    if constexpr (CG == 1) {
+        tmem_alloc(dst, kTmemCols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+                     "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)), "r"(kTmemCols)
+                     : "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void free_tmem(uint32_t taddr)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, kTmemCols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(kTmemCols) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (CG == 1)
+        umma_ts(d, a, b, idesc, accumulate);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrives on this barrier of every CTA of the pair when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if constexpr (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                     "h"(static_cast<uint16_t>(3))
+                     : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -279,10 +368,11 @@ __device__ __forceinline__ Share share_of(const Walk &w, int TQ)
     return h;
 }
 
-__device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int TQ)
+// c of `shares`: which share of the list; TQ: query tokens of an item.
+__device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int TQ, int c, int shares)
 {
     Walk w{};
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int m = 0, L = 0;
     long long per = 0, before = 0, all = 0;  // this thread's sequence: places per KV head
     auto scan = [&](int s0) {
@@ -315,7 +405,7 @@ __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int T
         total += all;
     }
     // no more CTAs than places: every CTA between an item's first and last has a part of it
-    const long long used = min(total, static_cast<long long>(gridDim.x));
+    const long long used = min(total, static_cast<long long>(shares));
     if (c >= used) return w;
     const long long begin = total * c / used;
     w.left = total * (c + 1) / used - begin;
@@ -417,47 +507,49 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
     }
 }
 
-template <int BITS, int GR>
+template <int BITS, int GR, int CG>
 __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a, const __grid_constant__ CUtensorMap tmQ)
 {
     constexpr int D = 64 * GR, GB = 8 * BITS;
     extern __shared__ uint8_t dsm_raw[];
     uint8_t *base = dsm_raw + ((1024 - (smem_u32(dsm_raw) & 1023)) & 1023);
     Fixed &F = *reinterpret_cast<Fixed *>(base);
-    const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + 2 * GR * kBox, q_smem = v_smem + 2 * GR * kBox;
+    constexpr int BB = buf_bytes(GR), kKBox = kBox / CG;  // bytes of a K or V buffer; of one of its K boxes
+    constexpr int VG = GR / CG, NK = 2 * GR / CG;         // groups of V in this CTA; warps for K of a chunk, and for V
+    const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + kBufs * BB, q_smem = v_smem + kBufs * BB;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.group, TQ = kRows / G;
+    const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank()), share = blockIdx.x / CG;
+    const int G = a.group, TQ = kRows / G, TI = CG * TQ;  // query tokens of this CTA's 128 rows, of an item
     int *status = &a.ctrl->status;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&F.k_full[i], 2 * GR);
-            mbar_init(&F.v_full[i], 2 * GR);
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(&F.k_full[i], CG * NK);
+            mbar_init(&F.v_full[i], CG * NK);
             mbar_init(&F.k_free[i], 1);
             mbar_init(&F.v_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&F.s_full[i], 1);
-            mbar_init(&F.p_full[i], kSoftWarps);
+            mbar_init(&F.p_full[i], CG * kSoftWarps);
             mbar_init(&F.pv_done[i], 1);
         }
-        mbar_init(&F.q_full, kSoftWarps);
+        mbar_init(&F.q_full, CG * kSoftWarps);
         mbar_init(&F.q_loaded, 1);
         mbar_init(&F.q_free, kSoftWarps);
-        mbar_init(&F.o_free, kSoftWarps);
+        mbar_init(&F.o_free, CG * kSoftWarps);
         mbar_init(&F.drain, 1);
         F.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
-        tmem_alloc(&F.tmem, kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == kMmaWarp) alloc_tmem<CG>(&F.tmem);
     pdl_trigger();
     pdl_wait();
     tc_fence_before();
-    __syncthreads();
+    pair_sync<CG>();
     tc_fence_after();
     const uint32_t tmem = F.tmem;
-    Walk w = first_item(a, F, TQ);
+    Walk w = first_item(a, F, TI, share, kKvqPrefillCtas / CG);
     bool ok = true;
 
     if (warp < kSoftWarps) {
@@ -465,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         Share h, h2;
-        bool more = next_share(a, w, h, TQ);
+        bool more = next_share(a, w, h, TI);
         int it = 0, items = 0, mine = 1;  // mine: this CTA's meta entry is still to be written
         long long done = 0;
         float mul = 0.0f;
@@ -516,14 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&F.q_full);
+                arrive_first<CG>(&F.q_full);
                 mbar_arrive(&F.q_free);
             }
         };
         // A warp whose wait gave up goes on through the named barriers (its partner may be in one), without the work.
         if (more) take_q(0);
         while (more) {
-            const int tq = w.t * TQ + row / G, head = w.g * G + row % G;
+            const int tq = w.t * TI + rank * TQ + row / G, head = w.g * G + row % G;
             const bool valid = row < TQ * G && tq < w.m;
             const int limit = valid ? w.L - w.m + tq + 1 : 0;  // tokens this row sees (may be <= 0)
             const bool any_row = __any_sync(0xffffffffu, valid);
@@ -592,17 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&F.p_full[sb]);
+                if (lane == 0) arrive_first<CG>(&F.p_full[sb]);
             }
             // ---- the item's end.  The next item's q first: the last scores of this one are in (S is full), so Q is free
             Walk w2 = w;
-            advance(a, w2, h.take, TQ);
-            const bool more2 = next_share(a, w2, h2, TQ);
+            advance(a, w2, h.take, TI);
+            const bool more2 = next_share(a, w2, h2, TI);
             if (more2) take_q(items + 1);
             ok = ok && warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
             tc_fence_after();
             const bool starts = h.j0 == 0, ends = h.j0 + h.n == h.nch;
-            const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+            const size_t part_row = static_cast<size_t>(2 * share + (starts ? 1 : 0)) * (CG * kRows) + rank * kRows + row;
             if (any_row) {
                 named_barrier_sync(kBarPair + quarter, 64);
                 F.xch[0][half][row] = l_run;
@@ -613,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 const float r = seen ? 1.0f / l_run : 0.0f;
                 const long long n = a.cu_q[w.b] + tq;
                 uint16_t *dst = a.out + (n * a.H_q + head) * D;
-                float *pdst = a.part_acc + (static_cast<size_t>(part) * kRows + row) * D;
+                float *pdst = a.part_acc + part_row * D;
 #pragma unroll 1
                 for (int c = half; c < D / 32 && ok; c += 2) {
                     uint32_t o[32];
@@ -641,15 +733,15 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                     __syncwarp();
                 }
                 if (valid && half == 0 && !(starts && ends))
-                    *reinterpret_cast<float2 *>(a.part_ml + (static_cast<size_t>(part) * kRows + row) * 2) = make_float2(m_run, l_run);
+                    *reinterpret_cast<float2 *>(a.part_ml + part_row * 2) = make_float2(m_run, l_run);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&F.o_free);
-            if (threadIdx.x == 0 && starts && !ends) {
+            if (lane == 0) arrive_first<CG>(&F.o_free);
+            if (threadIdx.x == 0 && rank == 0 && starts && !ends) {
                 // who joins the parts of an item that starts here and goes on: up to the CTA with its last place
                 const long long last = ((F.begin + done - w.s0 + h.nch + kItemCost) * F.used - 1) / F.total;
-                a.meta[blockIdx.x] = make_int4(w.b, w.g, w.t, static_cast<int>(last));
+                a.meta[share] = make_int4(w.b, w.g, w.t, static_cast<int>(last));
                 mine = 0;
             }
             done += h.take;
@@ -658,26 +750,32 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             h = h2;
             more = more2;
         }
-        if (threadIdx.x == 0 && mine) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        if (threadIdx.x == 0 && rank == 0 && mine) a.meta[share] = make_int4(-1, 0, 0, 0);
     } else if (warp < kSoftWarps + kDeqWarps) {
         // ------------------------------------------------ K and V of the chunks into shared memory
-        constexpr int kItems = GR == 4 ? 2 : 1;  // (K or V, group, 32 tokens) per warp and chunk
-        const int dw = warp - kSoftWarps, half = dw & 1;
-        const bool idle = dw >= 4 * GR;          // D = 64: four warps are enough
-        auto is_v = [&](int x) { return dw + x * kDeqWarps >= 2 * GR; };
-        auto group_of = [&](int x) { return ((dw + x * kDeqWarps) % (2 * GR)) >> 1; };
-        const int bs_log = 31 - __clz(a.c.bs), row = half * 32 + lane;
-        const uint32_t row_addr = k_smem + row * 128 + ((row & 7) << 4);
-        const int block_rows = a.c.H_kv * GR * a.c.bs;
+        // A warp has one (K or V, group, 32 tokens); with fewer of them than warps, the warps take chunks in turn.
+        // Of a pair, this CTA has half of the chunk's tokens of K, and half of the groups of V.
+        constexpr int kTurns = kDeqWarps / (2 * NK);
+        const int dw = (warp - kSoftWarps) % (2 * NK), turn = (warp - kSoftWarps) / (2 * NK), idx = dw % NK;
+        const bool isv = dw >= NK;
+        const int half = !isv && CG == 2 ? rank : idx & 1, group_here = !isv && CG == 2 ? idx : idx >> 1;
+        const int group = isv && CG == 2 ? rank * VG + group_here : group_here, row = half * 32 + lane;
+        const int smem_row = !isv && CG == 2 ? lane : row;
+        const uint32_t row_addr = (isv ? v_smem + group_here * kBox : k_smem + group_here * kKBox) + smem_row * 128 + ((smem_row & 7) << 4);
+        const int bs_log = 31 - __clz(a.c.bs), block_rows = a.c.H_kv * GR * a.c.bs;
+        const uint8_t *codes = isv ? a.c.v_q : a.c.k_q;
+        const uint32_t *params = reinterpret_cast<const uint32_t *>(isv ? a.c.v_sb : a.c.k_sb);
+        uint64_t *full = isv ? F.v_full : F.k_full, *free_bar = isv ? F.v_free : F.k_free;
         int it = 0;
         Share h;
-        while (ok && !idle && next_share(a, w, h, TQ)) {
-            // the table entries of this warp's 32 tokens of 32 chunks, one chunk per lane
+        while (ok && next_share(a, w, h, TI)) {
+            const int end = h.j0 + h.n;
+            // the table entries of this warp's 32 tokens of its next 32 chunks, one chunk per lane
             const int *table = a.block_table + static_cast<size_t>(w.b) * a.max_blocks;
             auto entries = [&](int c0) {
-                const int j = c0 + lane, tok = j * kChunk + half * 32;
+                const int j = c0 + lane * kTurns, tok = j * kChunk + half * 32;
                 int e = 0;
-                if (j < h.j0 + h.n && tok < w.L) {
+                if (j < end && tok < w.L) {
                     e = table[tok >> bs_log];
                     if (e < 0 || e >= a.c.n_blocks) {
                         record_error(status, kErrDeviceIndex);
@@ -686,41 +784,31 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 }
                 return e;
             };
-            Raw<BITS> raw[kItems];
-            auto fetch = [&](Raw<BITS> &r, int x, int j, int block) {
-                const int tok = j * kChunk + half * 32 + lane;
-                const uint32_t group0 = (static_cast<uint32_t>(w.g) * GR + group_of(x)) << bs_log;  // rows before the group's in a block
-                const long long gi = static_cast<long long>(block) * block_rows + (group0 + (tok & (a.c.bs - 1)));
-                const uint4 *src = reinterpret_cast<const uint4 *>((is_v(x) ? a.c.v_q : a.c.k_q) + gi * GB);
+            const uint32_t group0 = (static_cast<uint32_t>(w.g) * GR + group) << bs_log;  // rows before the group's in a block
+            Raw<BITS> raw;
+            auto fetch = [&](int j, int block) {
+                const long long gi = static_cast<long long>(block) * block_rows + (group0 + ((j * kChunk + row) & (a.c.bs - 1)));
+                const uint4 *src = reinterpret_cast<const uint4 *>(codes + gi * GB);
 #pragma unroll
-                for (int y = 0; y < BITS / 2; ++y) r.q[y] = src[y];
-                r.sb = reinterpret_cast<const uint32_t *>(is_v(x) ? a.c.v_sb : a.c.k_sb)[gi];
+                for (int y = 0; y < BITS / 2; ++y) raw.q[y] = src[y];
+                raw.sb = params[gi];
             };
-            int tab = entries(h.j0);
-            const int pb = __shfl_sync(0xffffffffu, tab, 0);
-#pragma unroll
-            for (int x = 0; x < kItems; ++x) fetch(raw[x], x, h.j0, pb);
-            for (int i = 0; i < h.n; ++i, ++it) {
-                const int buf = it & 1;
-                if (((i + 1) & 31) == 0) tab = entries(h.j0 + i + 1);
-                const int next = __shfl_sync(0xffffffffu, tab, (i + 1) & 31);
-                const bool exists = (h.j0 + i) * kChunk + row < w.L;
-                uint32_t is_free[kItems];
-#pragma unroll
-                for (int x = 0; x < kItems; ++x)
-                    is_free[x] = it >= 2 ? phase_done(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1) : 1u;
-#pragma unroll
-                for (int x = 0; x < kItems; ++x) {
-                    if (!__all_sync(0xffffffffu, is_free[x]) && !(ok = warp_wait(is_v(x) ? &F.v_free[buf] : &F.k_free[buf], ((it >> 1) - 1) & 1, &F.abort, status))) break;
-                    rebuild<BITS>(raw[x], exists, row_addr + ((is_v(x) ? 2 * GR : 0) + buf * GR + group_of(x)) * kBox, status);
-                    fence_async_shared();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(is_v(x) ? &F.v_full[buf] : &F.k_full[buf]);
-                    if (i + 1 < h.n) fetch(raw[x], x, h.j0 + i + 1, next);
-                }
-                if (!ok) break;
+            int j = h.j0 + ((turn - it) & (kTurns - 1)), cnt = 0, tab = entries(j);
+            if (j < end) fetch(j, __shfl_sync(0xffffffffu, tab, 0));
+            for (; j < end; j += kTurns) {
+                const int x = it + j - h.j0, buf = x % kBufs, use = x / kBufs;
+                const uint32_t is_free = use > 0 ? phase_done(&free_bar[buf], (use - 1) & 1) : 1u;
+                if ((++cnt & 31) == 0) tab = entries(j + kTurns);
+                const int next = __shfl_sync(0xffffffffu, tab, cnt & 31);
+                if (!__all_sync(0xffffffffu, is_free) && !(ok = warp_wait(&free_bar[buf], (use - 1) & 1, &F.abort, status))) break;
+                rebuild<BITS>(raw, j * kChunk + row < w.L, row_addr + buf * BB, status);
+                fence_async_shared();
+                __syncwarp();
+                if (lane == 0) arrive_first<CG>(&full[buf]);
+                if (j + kTurns < end) fetch(j + kTurns, next);
             }
-            advance(a, w, h.take, TQ);
+            it += h.n;
+            advance(a, w, h.take, TI);
         }
     } else if (warp == kLoadWarp) {
         // ------------------------------------------------ q of the items, one ahead
@@ -728,14 +816,15 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             prefetch_tmap(&tmQ);
             Share h;
             int items = 0;
-            while (next_share(a, w, h, TQ)) {
+            while (next_share(a, w, h, TI)) {
                 if (items > 0 && !mbar_wait(&F.q_free, (items - 1) & 1, &F.abort, status)) break;
                 mbar_arrive_expect_tx(&F.q_loaded, static_cast<uint32_t>(GR * TQ * G * 128));
 #pragma unroll
                 for (int c = 0; c < GR; ++c)
-                    tma_load_3d(base + kFixed + 4 * GR * kBox + c * kQBox, &tmQ, &F.q_loaded, c * 64, w.g * G, a.cu_q[w.b] + w.t * TQ);
+                    tma_load_3d(base + kFixed + 2 * kBufs * BB + c * kQBox, &tmQ, &F.q_loaded, c * 64, w.g * G,
+                                a.cu_q[w.b] + w.t * TI + rank * TQ);
                 ++items;
-                advance(a, w, h.take, TQ);
+                advance(a, w, h.take, TI);
             }
             // no copy into this CTA's shared memory may still be in flight at exit
             if (items > 0) {
@@ -750,62 +839,62 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------ MMA issuer
+        // ------------------------------------------------ MMA issuer (of the pair's first CTA)
         // The whole warp walks the list, so that every operand of an MMA is warp-uniform, and one elected
         // lane issues: issuing from inside `if (lane == 0)` took ~87 cycles an MMA, more than it runs.
-        constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, kRows, kChunk);
-        constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, kRows, D) | (1u << 16);  // B: channels contiguous
+        constexpr uint32_t kIdescS = idesc_f32acc(kFmtF16, CG * kRows, kChunk);
+        constexpr uint32_t kIdescO = idesc_f32acc(kFmtF16, CG * kRows, D) | (1u << 16);  // B: channels contiguous
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t kd = sdesc_sw128(k_smem), vd = sdesc_mn_sw128(v_smem, kBox);
         int it = 0, items = 0;
         Share h;
-        while (ok && next_share(a, w, h, TQ)) {
+        while (rank == 0 && ok && next_share(a, w, h, TI)) {
             const int n = __shfl_sync(0xffffffffu, h.n, 0);
             if (!(ok = warp_wait(&F.q_full, items & 1, &F.abort, status))) break;
             tc_fence_after();
             for (int i = 0; i <= n && ok; ++i) {
                 if (i < n) {
-                    const int x = it + i, buf = x & 1;
-                    if (!(ok = warp_wait(&F.k_full[buf], (x >> 1) & 1, &F.abort, status))) break;
+                    const int x = it + i, buf = x % kBufs, sb = x & 1;
+                    if (!(ok = warp_wait(&F.k_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t lo = static_cast<uint32_t>(kd) + buf * (GR * kBox >> 4), hi = static_cast<uint32_t>(kd >> 32);
+                        const uint32_t lo = static_cast<uint32_t>(kd) + buf * (BB >> 4), hi = static_cast<uint32_t>(kd >> 32);
 #pragma unroll
                         for (int c = 0; c < GR; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_ts(tm + Cols<GR>::S + buf * 64, tm + Cols<GR>::Q + c * 32 + kk * 8,
-                                        join64(lo + c * (kBox >> 4) + kk * 2, hi), kIdescS, (c | kk) != 0);
-                        umma_commit(&F.k_free[buf]);
-                        umma_commit(&F.s_full[buf]);
+                                mma_ts<CG>(tm + Cols<GR>::S + sb * 64, tm + Cols<GR>::Q + c * 32 + kk * 8,
+                                           join64(lo + c * (kKBox >> 4) + kk * 2, hi), kIdescS, (c | kk) != 0);
+                        commit<CG>(&F.k_free[buf]);
+                        commit<CG>(&F.s_full[sb]);
                     }
                     __syncwarp();
                 }
                 if (i > 0) {
-                    const int x = it + i - 1, buf = x & 1;
+                    const int x = it + i - 1, buf = x % kBufs, sb = x & 1;
                     if (i == 1 && items > 0 && !(ok = warp_wait(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
-                    ok = __all_sync(0xffffffffu, mbar_wait2(&F.v_full[buf], (x >> 1) & 1, &F.p_full[buf], (x >> 1) & 1, &F.abort, status));
-                    if (!ok) break;
+                    if (!(ok = warp_wait(&F.v_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
+                    if (!(ok = warp_wait(&F.p_full[sb], (x >> 1) & 1, &F.abort, status))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t lo = static_cast<uint32_t>(vd) + buf * (GR * kBox >> 4), hi = static_cast<uint32_t>(vd >> 32);
+                        const uint32_t lo = static_cast<uint32_t>(vd) + buf * (BB >> 4), hi = static_cast<uint32_t>(vd >> 32);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_ts(tm + Cols<GR>::O, tm + Cols<GR>::S + buf * 64 + kk * 8, join64(lo + kk * (2048 >> 4), hi), kIdescO,
-                                    i > 1 || kk > 0);
-                        umma_commit(&F.v_free[buf]);
-                        umma_commit(&F.pv_done[buf]);
+                            mma_ts<CG>(tm + Cols<GR>::O, tm + Cols<GR>::S + sb * 64 + kk * 8, join64(lo + kk * (2048 >> 4), hi), kIdescO,
+                                       i > 1 || kk > 0);
+                        commit<CG>(&F.v_free[buf]);
+                        commit<CG>(&F.pv_done[sb]);
                     }
                     __syncwarp();
                 }
             }
             it += n;
             ++items;
-            advance(a, w, h.take, TQ);
+            advance(a, w, h.take, TI);
         }
-        if (elect_one()) {
-            // all tensor-core work of this CTA must finish before tensor memory is freed
-            umma_commit(&F.drain);
+        if (rank == 0 && elect_one()) {
+            // all tensor-core work must finish before tensor memory is freed (the pair's other CTA waits below)
+            commit<CG>(&F.drain);
             const uint32_t addr = smem_u32(&F.drain);
             const uint64_t t0 = global_timer_ns();
             while (!mbar_try_wait(addr, 0))
@@ -816,17 +905,19 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         }
         __syncwarp();
     }
+    // no CTA of a pair leaves while the other may still signal it or read its shared memory
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    pair_sync<CG>();
     tc_fence_after();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
 // Joins the parts of an item that was cut: CTA (first CTA of the item, four rows), 64
 // threads a row, a float4 column each, eight parts in flight on a running maximum (a
 // grid of one row per CTA took 20 us to launch).  The part of the first CTA c0 is in
 // slot 2 c0 + 1, those of the following CTAs c in slot 2 c.
-__global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a)
+__global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a, int pair)
 {
     constexpr int kBatch = 8;
     pdl_trigger();
@@ -834,10 +925,10 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
     const int4 meta = a.meta[blockIdx.x];
     if (meta.x < 0) return;
     const int G = a.group, TQ = kRows / G, row = blockIdx.y * 4 + threadIdx.x / 64, d4 = threadIdx.x % 64;
-    const int m = queries_of(a, meta.x), tq = meta.z * TQ + row / G;
-    if (row >= TQ * G || tq >= m || d4 * 4 >= a.D) return;
+    const int r = row % kRows, m = queries_of(a, meta.x), tq = (meta.z * pair + row / kRows) * TQ + r / G;
+    if (r >= TQ * G || tq >= m || d4 * 4 >= a.D) return;
     const int c0 = blockIdx.x, S = meta.w - c0 + 1;
-    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kRows + row; };
+    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (pair * kRows) + row; };
     float M = kNoMax, den = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < S; s0 += kBatch) {
@@ -869,35 +960,45 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
             o.w = fmaf(e, x[k].w, o.w);
         }
     }
-    const float r = den > 0.0f ? 1.0f / den : 0.0f;
+    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
     uint2 y;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * r, o.y * r), hi = __floats2bfloat162_rn(o.z * r, o.w * r);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     y.x = *reinterpret_cast<const uint32_t *>(&lo);
     y.y = *reinterpret_cast<const uint32_t *>(&hi);
     const long long n = a.cu_q[meta.x] + tq;
-    reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + row % G) * a.D)[d4] = y;
+    reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + r % G) * a.D)[d4] = y;
 }
 
 template <int BITS, int GR>
 cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    const int smem = smem_bytes(64 * GR);
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR>), smem);
+    constexpr int CG = pair_of(GR), smem = smem_bytes(64 * GR);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG>), smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_kernel<BITS, GR>, dim3(kKvqPrefillCtas), dim3(kThreads), smem, stream, a, tmQ);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kKvqPrefillCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG>, a, tmQ)) != cudaSuccess) return e;
+    return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas / CG, CG * kRows / 4), dim3(256), 0, stream, a, CG);
 }
 
 }  // namespace
 
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    cudaError_t e;
     if (a.c.bits == 4)
-        e = a.D == 64 ? launch<4, 1>(a, tmQ, stream) : a.D == 128 ? launch<4, 2>(a, tmQ, stream) : launch<4, 4>(a, tmQ, stream);
-    else
-        e = a.D == 64 ? launch<8, 1>(a, tmQ, stream) : a.D == 128 ? launch<8, 2>(a, tmQ, stream) : launch<8, 4>(a, tmQ, stream);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas, kRows / 4), dim3(256), 0, stream, a);
+        return a.D == 64 ? launch<4, 1>(a, tmQ, stream) : a.D == 128 ? launch<4, 2>(a, tmQ, stream) : launch<4, 4>(a, tmQ, stream);
+    return a.D == 64 ? launch<8, 1>(a, tmQ, stream) : a.D == 128 ? launch<8, 2>(a, tmQ, stream) : launch<8, 4>(a, tmQ, stream);
 }
 
 }  // namespace lily
