@@ -38,20 +38,20 @@ namespace {
 
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kChunk = 64;                 // cache tokens per step
-// Taking up an item (its q, the first scores, its output) costs about six chunks, which
-// the shares of the work list count: an 8K prompt 627 us with 2, 531 with 4, 482 with
-// 6, 489 with 8.
-constexpr int kItemCost = 6;
+// Taking up an item (its q, the first scores, its output) costs about eight chunks,
+// which the shares of the work list count: an 8K prompt 528 us with 2, 429 with 6, 410
+// with 8, 419 with 12.
+constexpr int kItemCost = 8;
 constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
 constexpr int kThreads = (kLoadWarp + 1) * 32;
 constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
 constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
-constexpr int kBufs = 4;                   // buffers of K and of V
+constexpr int kMaxBufs = 4;                // buffers of K and of V, at most
 constexpr uint32_t kTmemCols = 512;
 constexpr float kNoMax = -1.7e38f;
 
 struct Fixed {
-    uint64_t k_full[kBufs], k_free[kBufs], v_full[kBufs], v_free[kBufs], s_full[2], p_full[2];
+    uint64_t k_full[kMaxBufs], k_free[kMaxBufs], v_full[kMaxBufs], v_free[kMaxBufs], s_full[2], p_full[2];
     uint64_t pv_done[2], q_full, q_loaded, q_free, o_free, drain;
     uint32_t tmem;
     int abort, b0, m0, L0;
@@ -61,16 +61,16 @@ struct Fixed {
 constexpr int kFixed = 4096;
 static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
 constexpr int kQBox = kRows * 128;         // [128 rows][64 channels] bf16, 128-byte swizzle
-// CTAs that share an item's K and V: with D = 64 one; else a pair, whose MMAs read half
-// of K's tokens (of V's channels) from each CTA's shared memory, so each rebuilds half.
-__host__ __device__ constexpr int pair_of(int GR) { return GR == 1 ? 1 : 2; }
-__host__ __device__ constexpr int buf_bytes(int GR) { return GR * kBox / pair_of(GR); }
+// CG: the CTAs that share an item's K and V.  The MMAs of a pair read half of K's tokens
+// and of V's channels from each CTA's shared memory, so each rebuilds half.
+__host__ __device__ constexpr int buf_bytes(int GR, int CG) { return GR * kBox / CG; }
+__host__ __device__ constexpr int bufs_for(int GR, int CG) { return buf_bytes(GR, CG) > 16384 ? 2 : kMaxBufs; }
 // More than half of an SM's, so that no two CTAs that allocate tensor memory meet on
 // one SM: two pairs that each hold one of two SMs would wait for each other.
 constexpr int kSmemLeast = 120 * 1024;
-constexpr int smem_bytes(int D)
+constexpr int smem_bytes(int GR, int CG)
 {
-    const int n = 1024 + kFixed + 2 * kBufs * buf_bytes(D / 64) + (D / 64) * kQBox;
+    const int n = 1024 + kFixed + 2 * bufs_for(GR, CG) * buf_bytes(GR, CG) + GR * kQBox;
     return n > kSmemLeast ? n : kSmemLeast;
 }
 
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     extern __shared__ uint8_t dsm_raw[];
     uint8_t *base = dsm_raw + ((1024 - (smem_u32(dsm_raw) & 1023)) & 1023);
     Fixed &F = *reinterpret_cast<Fixed *>(base);
-    constexpr int BB = buf_bytes(GR), kKBox = kBox / CG;  // bytes of a K or V buffer; of one of its K boxes
+    constexpr int kBufs = bufs_for(GR, CG), BB = buf_bytes(GR, CG), kKBox = kBox / CG;  // BB: bytes of a K or V buffer, kKBox: of a K box
     constexpr int VG = GR / CG, NK = 2 * GR / CG;         // groups of V in this CTA; warps for K of a chunk, and for V
     const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + kBufs * BB, q_smem = v_smem + kBufs * BB;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -753,19 +753,31 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         if (threadIdx.x == 0 && rank == 0 && mine) a.meta[share] = make_int4(-1, 0, 0, 0);
     } else if (warp < kSoftWarps + kDeqWarps) {
         // ------------------------------------------------ K and V of the chunks into shared memory
-        // A warp has one (K or V, group, 32 tokens); with fewer of them than warps, the warps take chunks in turn.
-        // Of a pair, this CTA has half of the chunk's tokens of K, and half of the groups of V.
-        constexpr int kTurns = kDeqWarps / (2 * NK);
-        const int dw = (warp - kSoftWarps) % (2 * NK), turn = (warp - kSoftWarps) / (2 * NK), idx = dw % NK;
-        const bool isv = dw >= NK;
-        const int half = !isv && CG == 2 ? rank : idx & 1, group_here = !isv && CG == 2 ? idx : idx >> 1;
-        const int group = isv && CG == 2 ? rank * VG + group_here : group_here, row = half * 32 + lane;
-        const int smem_row = !isv && CG == 2 ? lane : row;
-        const uint32_t row_addr = (isv ? v_smem + group_here * kBox : k_smem + group_here * kKBox) + smem_row * 128 + ((smem_row & 7) << 4);
+        // The chunk's (K or V, group, 32 tokens) are dealt to the warps: one each (two for one CTA with D = 256);
+        // with fewer of them than warps, the warps take chunks in turn.  Of a pair, this CTA has half of the
+        // chunk's tokens of K, and half of the groups of V.
+        constexpr int kItems = 2 * NK > kDeqWarps ? 2 * NK / kDeqWarps : 1, kWarps = 2 * NK / kItems, kTurns = kDeqWarps / kWarps;
+        const int dw = (warp - kSoftWarps) % kWarps, turn = (warp - kSoftWarps) / kWarps;
+        struct Item {
+            uint32_t addr;  // this lane's row of the group in buffer 0
+            int row, group, half;
+            bool isv;
+        } item[kItems];
+#pragma unroll
+        for (int x = 0; x < kItems; ++x) {
+            Item &m = item[x];
+            const int n = dw + x * kWarps, idx = n % NK;
+            m.isv = n >= NK;
+            m.half = !m.isv && CG == 2 ? rank : idx & 1;
+            const int here = !m.isv && CG == 2 ? idx : idx >> 1;  // group within this CTA's
+            m.group = m.isv && CG == 2 ? rank * VG + here : here;
+            m.row = m.half * 32 + lane;
+            const int r = !m.isv && CG == 2 ? lane : m.row;
+            m.addr = (m.isv ? v_smem + here * kBox : k_smem + here * kKBox) + r * 128 + ((r & 7) << 4);
+        }
+        // every item of a warp has the same tokens (two items: K and V of the same group and half)
+        const int half = item[0].half, row = item[0].row;
         const int bs_log = 31 - __clz(a.c.bs), block_rows = a.c.H_kv * GR * a.c.bs;
-        const uint8_t *codes = isv ? a.c.v_q : a.c.k_q;
-        const uint32_t *params = reinterpret_cast<const uint32_t *>(isv ? a.c.v_sb : a.c.k_sb);
-        uint64_t *full = isv ? F.v_full : F.k_full, *free_bar = isv ? F.v_free : F.k_free;
         int it = 0;
         Share h;
         while (ok && next_share(a, w, h, TI)) {
@@ -784,28 +796,39 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 }
                 return e;
             };
-            const uint32_t group0 = (static_cast<uint32_t>(w.g) * GR + group) << bs_log;  // rows before the group's in a block
-            Raw<BITS> raw;
-            auto fetch = [&](int j, int block) {
+            Raw<BITS> raw[kItems];
+            auto fetch = [&](int x, int j, int block) {
+                const uint32_t group0 = (static_cast<uint32_t>(w.g) * GR + item[x].group) << bs_log;  // rows before the group's in a block
                 const long long gi = static_cast<long long>(block) * block_rows + (group0 + ((j * kChunk + row) & (a.c.bs - 1)));
-                const uint4 *src = reinterpret_cast<const uint4 *>(codes + gi * GB);
+                const uint4 *src = reinterpret_cast<const uint4 *>((item[x].isv ? a.c.v_q : a.c.k_q) + gi * GB);
 #pragma unroll
-                for (int y = 0; y < BITS / 2; ++y) raw.q[y] = src[y];
-                raw.sb = params[gi];
+                for (int y = 0; y < BITS / 2; ++y) raw[x].q[y] = src[y];
+                raw[x].sb = reinterpret_cast<const uint32_t *>(item[x].isv ? a.c.v_sb : a.c.k_sb)[gi];
             };
             int j = h.j0 + ((turn - it) & (kTurns - 1)), cnt = 0, tab = entries(j);
-            if (j < end) fetch(j, __shfl_sync(0xffffffffu, tab, 0));
-            for (; j < end; j += kTurns) {
+            const int block0 = __shfl_sync(0xffffffffu, tab, 0);
+#pragma unroll
+            for (int x = 0; x < kItems; ++x)
+                if (j < end) fetch(x, j, block0);
+            for (; j < end && ok; j += kTurns) {
                 const int x = it + j - h.j0, buf = x % kBufs, use = x / kBufs;
-                const uint32_t is_free = use > 0 ? phase_done(&free_bar[buf], (use - 1) & 1) : 1u;
+                uint32_t is_free[kItems];
+#pragma unroll
+                for (int y = 0; y < kItems; ++y)
+                    is_free[y] = use > 0 ? phase_done(item[y].isv ? &F.v_free[buf] : &F.k_free[buf], (use - 1) & 1) : 1u;
                 if ((++cnt & 31) == 0) tab = entries(j + kTurns);
                 const int next = __shfl_sync(0xffffffffu, tab, cnt & 31);
-                if (!__all_sync(0xffffffffu, is_free) && !(ok = warp_wait(&free_bar[buf], (use - 1) & 1, &F.abort, status))) break;
-                rebuild<BITS>(raw, j * kChunk + row < w.L, row_addr + buf * BB, status);
-                fence_async_shared();
-                __syncwarp();
-                if (lane == 0) arrive_first<CG>(&full[buf]);
-                if (j + kTurns < end) fetch(j + kTurns, next);
+#pragma unroll
+                for (int y = 0; y < kItems; ++y) {
+                    if (!__all_sync(0xffffffffu, is_free[y]) &&
+                        !(ok = ok && warp_wait(item[y].isv ? &F.v_free[buf] : &F.k_free[buf], (use - 1) & 1, &F.abort, status)))
+                        break;
+                    rebuild<BITS>(raw[y], j * kChunk + row < w.L, item[y].addr + buf * BB, status);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) arrive_first<CG>(item[y].isv ? &F.v_full[buf] : &F.k_full[buf]);
+                    if (j + kTurns < end) fetch(y, j + kTurns, next);
+                }
             }
             it += h.n;
             advance(a, w, h.take, TI);
@@ -969,10 +992,10 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
     reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + r % G) * a.D)[d4] = y;
 }
 
-template <int BITS, int GR>
+template <int BITS, int GR, int CG>
 cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    constexpr int CG = pair_of(GR), smem = smem_bytes(64 * GR);
+    constexpr int smem = smem_bytes(GR, CG);
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
@@ -992,13 +1015,24 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t st
     return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas / CG, CG * kRows / 4), dim3(256), 0, stream, a, CG);
 }
 
+// Pairs, but one CTA an item where D = 64 (its 64 channels of V are one swizzled box and
+// do not split) and where no sequence need have more query tokens than one CTA's 128
+// rows hold: a pair's second half would idle (eight drafts of four tokens: 28 us against
+// 34; prompts and chunks of 1,024 tokens and more are 1.15 to 1.25 times as fast with pairs).
+template <int BITS>
+cudaError_t launch_d(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
+{
+    if (a.D == 64) return launch<BITS, 1, 1>(a, tmQ, stream);
+    if (a.N <= static_cast<long long>(a.B) * (kRows / a.group))
+        return a.D == 128 ? launch<BITS, 2, 1>(a, tmQ, stream) : launch<BITS, 4, 1>(a, tmQ, stream);
+    return a.D == 128 ? launch<BITS, 2, 2>(a, tmQ, stream) : launch<BITS, 4, 2>(a, tmQ, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    if (a.c.bits == 4)
-        return a.D == 64 ? launch<4, 1>(a, tmQ, stream) : a.D == 128 ? launch<4, 2>(a, tmQ, stream) : launch<4, 4>(a, tmQ, stream);
-    return a.D == 64 ? launch<8, 1>(a, tmQ, stream) : a.D == 128 ? launch<8, 2>(a, tmQ, stream) : launch<8, 4>(a, tmQ, stream);
+    return a.c.bits == 4 ? launch_d<4>(a, tmQ, stream) : launch_d<8>(a, tmQ, stream);
 }
 
 }  // namespace lily
