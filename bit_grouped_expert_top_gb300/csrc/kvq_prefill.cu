@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             if (threadIdx.x == 0 && rank == 0 && starts && !ends) {
                 // who joins the parts of an item that starts here and goes on: up to the CTA with its last place
                 const long long last = ((F.begin + done - w.s0 + h.nch + kItemCost) * F.used - 1) / F.total;
-                a.meta[share] = make_int4(w.b, w.g, w.t, static_cast<int>(last));
+                a.meta[share] = make_int4(a.cu_q[w.b] + w.t * TI, w.g, w.m - w.t * TI, static_cast<int>(last));
                 mine = 0;
             }
             done += h.take;
@@ -936,22 +936,25 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
-// Joins the parts of an item that was cut: CTA (first CTA of the item, four rows), 64
-// threads a row, a float4 column each, eight parts in flight on a running maximum (a
-// grid of one row per CTA took 20 us to launch).  The part of the first CTA c0 is in
-// slot 2 c0 + 1, those of the following CTAs c in slot 2 c.
-__global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a, int pair)
+// Joins the parts of an item that was cut: CTA (first share of the item, four rows), 64
+// threads a row, a float4 column each, on a running maximum.  An item of pairs is cut
+// in two as a rule, one of few query tokens in up to 76: two parts in flight with many
+// CTAs on an SM (an 8K prompt's join 9 us), or eight (15 us there; 16 tokens on 32K
+// 6 us less).  One row per CTA took 20 us to launch.  The part of the first share c0 is
+// in slot 2 c0 + 1, those of the following ones c in slot 2 c.
+template <int CG>
+__global__ void __launch_bounds__(256, CG == 2 ? 8 : 2) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a)
 {
-    constexpr int kBatch = 8;
+    constexpr int kBatch = CG == 2 ? 2 : 8;
     pdl_trigger();
     pdl_wait();
     const int4 meta = a.meta[blockIdx.x];
     if (meta.x < 0) return;
     const int G = a.group, TQ = kRows / G, row = blockIdx.y * 4 + threadIdx.x / 64, d4 = threadIdx.x % 64;
-    const int r = row % kRows, m = queries_of(a, meta.x), tq = (meta.z * pair + row / kRows) * TQ + r / G;
-    if (r >= TQ * G || tq >= m || d4 * 4 >= a.D) return;
+    const int r = row % kRows, tq = row / kRows * TQ + r / G;  // query token within the item
+    if (r >= TQ * G || tq >= meta.z || d4 * 4 >= a.D) return;
     const int c0 = blockIdx.x, S = meta.w - c0 + 1;
-    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (pair * kRows) + row; };
+    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (CG * kRows) + row; };
     float M = kNoMax, den = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < S; s0 += kBatch) {
@@ -988,7 +991,7 @@ __global__ void __launch_bounds__(256) kvq_prefill_join_kernel(const __grid_cons
     const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     y.x = *reinterpret_cast<const uint32_t *>(&lo);
     y.y = *reinterpret_cast<const uint32_t *>(&hi);
-    const long long n = a.cu_q[meta.x] + tq;
+    const long long n = meta.x + tq;
     reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + r % G) * a.D)[d4] = y;
 }
 
@@ -1012,7 +1015,7 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t st
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG>, a, tmQ)) != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_join_kernel, dim3(kKvqPrefillCtas / CG, CG * kRows / 4), dim3(256), 0, stream, a, CG);
+    return launch_pdl(kvq_prefill_join_kernel<CG>, dim3(kKvqPrefillCtas / CG, CG * kRows / 4), dim3(256), 0, stream, a);
 }
 
 // Pairs, but one CTA an item where D = 64 (its 64 channels of V are one swizzled box and

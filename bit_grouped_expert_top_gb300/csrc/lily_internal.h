@@ -219,7 +219,7 @@ struct KvqAttnArgs {
     Ctrl *ctrl;
     // partial results of work items cut between CTAs (workspace)
     int4 *meta;                   // [CTAs]: decode: segment (or -1), its first and last CTA;
-                                  // prefill: sequence (or -1), KV head, tile, last CTA
+                                  // prefill: first query token (or -1), KV head, query tokens, last share
     float *part_ml;               // [2 CTAs][rows][2]: max (log2 units), sum of weights
     float *part_acc;              // [2 CTAs][rows][D]; rows: 8 (decode), 128 (prefill)
     int whole, key_by_segment, stages;  // set by launch_kvq_decode
