@@ -28,32 +28,36 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Cache row of the call's token n: physical block in .x, row in .y; .x < 0
-// where there is none (padding, or an index out of range, which is recorded).
-__device__ __forceinline__ int2 token_slot(const KvqCopyArgs &a, int n)
+constexpr int kMaxShared = kThreads - 1;  // sequences whose bounds a CTA takes into shared memory
+
+// Cache row of the call's token n: physical block in .x, row in .y; .x < 0 where there
+// is none (padding, or an index out of range, which is recorded).  cu, starts: the
+// call's, or their copies in shared memory (a search in global memory is a chain of
+// loads of ~0.6 us each).
+__device__ __forceinline__ int2 token_slot(const KvqCopyArgs &a, const int *cu, const int *starts, int n)
 {
     int lo = 0, hi = a.B;  // the last b with cu[b] <= n
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.cu[mid] <= n)
+        if (cu[mid] <= n)
             lo = mid;
         else
             hi = mid;
     }
-    const int i = n - a.cu[lo];
-    if (i < 0 || n >= a.cu[lo + 1]) return make_int2(-1, 0);
-    const long long pos = static_cast<long long>(a.starts[lo]) + i;
+    const int i = n - cu[lo];
+    if (i < 0 || n >= cu[lo + 1]) return make_int2(-1, 0);
+    const long long pos = static_cast<long long>(starts[lo]) + i;
     if (pos < 0 || pos >= static_cast<long long>(a.max_blocks) * a.c.bs) {
         record_error(&a.ctrl->status, kErrDeviceIndex);
         return make_int2(-1, 0);
     }
-    const int p = static_cast<int>(pos);
-    const int pb = a.block_table[static_cast<size_t>(lo) * a.max_blocks + p / a.c.bs];
+    const int p = static_cast<int>(pos), bs_log = 31 - __clz(a.c.bs);
+    const int pb = a.block_table[static_cast<size_t>(lo) * a.max_blocks + (p >> bs_log)];
     if (pb < 0 || pb >= a.c.n_blocks) {
         record_error(&a.ctrl->status, kErrDeviceIndex);
         return make_int2(-1, 0);
     }
-    return make_int2(pb, p % a.c.bs);
+    return make_int2(pb, p & (a.c.bs - 1));
 }
 
 // Scale and bias of a group, and what its codes are computed with.  Both quotients,
@@ -154,9 +158,16 @@ template <int BITS, int QUADS, int kBatch, typename T, typename Load, typename U
 __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &load, const Use &use)
 {
     __shared__ int2 slots[4 * QUADS];
-    const int n0 = blockIdx.x * (4 * QUADS);
-    if (threadIdx.x < 4 * QUADS)
-        slots[threadIdx.x] = n0 + static_cast<int>(threadIdx.x) < a.N ? token_slot(a, n0 + threadIdx.x) : make_int2(-1, 0);
+    __shared__ int cu_s[kThreads], starts_s[kThreads];
+    const int n0 = blockIdx.x * (4 * QUADS), t = threadIdx.x;
+    const bool shared = a.B <= kMaxShared;
+    if (shared) {
+        if (t <= a.B) cu_s[t] = a.cu[t];
+        if (t < a.B) starts_s[t] = a.starts[t];
+        __syncthreads();
+    }
+    if (t < 4 * QUADS)
+        slots[t] = n0 + t >= a.N ? make_int2(-1, 0) : shared ? token_slot(a, cu_s, starts_s, n0 + t) : token_slot(a, a.cu, a.starts, n0 + t);
     __syncthreads();
     const int warp = threadIdx.x / 32, e = threadIdx.x % 8, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8;
     const int2 slot = slots[tok];

@@ -582,3 +582,53 @@ def test_cold_caches_change_nothing(D, bits):
         assert torch.equal(want, _prefill(c)), i
         flush.fill_(i)
         assert torch.equal(want_one, _decode(one)), i
+
+
+@pytest.mark.parametrize("B", [255, 256, 700])
+def test_append_and_read_of_many_sequences(B):
+    # around the number of sequences whose bounds a CTA keeps at hand; every third one idle
+    lens = tuple((b * 7) % 23 + 1 for b in range(B))
+    new = tuple(0 if b % 3 == 0 else (b * 5) % L + 1 for b, L in enumerate(lens))
+    cfg = KvqConfig("many", lens=lens, new=new, H_q=2, H_kv=1, D=64, block_size=32, seed=74)
+    c = Cache(cfg).to_gpu()
+    first = c.a["cu_all"].numpy()
+    pick = np.concatenate([np.arange(first[b] + L - m, first[b] + L) for b, (L, m) in enumerate(zip(lens, new)) if m])
+    k, v = (c.d[n][torch.from_numpy(pick).cuda()] for n in ("k_all", "v_all"))
+    t, handle = _fresh(c)
+    lm.lily_kvq_append(c.shape, handle, k, v, c.d["cu"], c.d["starts"], c.d["block_table"], c.ws)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    lm.lily_kvq_read(c.shape, handle, ko, vo, c.d["cu"], c.d["starts"], c.d["block_table"], c.ws)
+    assert c.status() == 0
+    kk = np.concatenate([c.sequence(b)[0][L - m:] for b, (L, m) in enumerate(zip(lens, new)) if m])
+    np.testing.assert_array_equal(raw(ko), kvq.bf16_round(kk.astype(np.float32)))
+    out = torch.empty((B, cfg.H_q, cfg.D), dtype=torch.bfloat16, device="cuda")
+    q = torch.randn((B, cfg.H_q, cfg.D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    lm.lily_kvq_attn_decode(c.shape, c.handle, q.cuda(), c.d["block_table"], c.d["seq_lens"], out, c.ws)
+    ws = lm.alloc_kvq_workspace(c.shape, cfg.N)
+    chunk = torch.empty((cfg.N, cfg.H_q, cfg.D), dtype=torch.bfloat16, device="cuda")
+    lm.lily_kvq_attn_prefill(c.shape, c.handle, c.d["q"], c.d["cu"], c.d["block_table"], c.d["seq_lens"], chunk, ws)
+    assert c.status() == 0 and lm.lily_moe_device_status(ws) == 0
+    for b in list(range(0, B, 37)) + [B - 1]:
+        kk, vv, km, vm = c.sequence(b)
+        ref, mags = kvq.attend_and_bound(rounded(q[b:b + 1]), kk, vv, [lens[b]], None, km, vm)
+        check(rounded(out[b:b + 1]), ref, mags, operand=0.0)
+        m, n0 = new[b], int(c.a["cu"][b])
+        if m:
+            ref, mags = kvq.attend_and_bound(rounded(c.a["q"][n0:n0 + m]), kk, vv, lens[b] - m + 1 + np.arange(m), None, km, vm)
+            check(rounded(chunk[n0:n0 + m]), ref, mags)
+
+
+def test_prefill_on_two_streams():
+    # two calls at once, each with its own workspace: tensor memory and CTA pairs are taken by one after the other
+    cs = [Cache(KvqConfig("streams", lens=(900, 300), new=(400, 300), D=D, bits=bits, seed=75 + D), n_query=700).to_gpu()
+          for D, bits in ((256, 4), (128, 8))]
+    want = [_prefill(c).clone() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [torch.empty_like(w) for w in want]
+    for _ in range(6):
+        for c, st, o in zip(cs, streams, outs):
+            lm.lily_kvq_attn_prefill(c.shape, c.handle, c.d["q"], c.d["cu"], c.d["block_table"], c.d["seq_lens"], o, c.ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
+    assert all(c.status() == 0 for c in cs)
