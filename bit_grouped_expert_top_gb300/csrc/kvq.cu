@@ -194,7 +194,7 @@ __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &loa
 }
 
 template <int BITS, int QUADS>
-__global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_constant__ KvqCopyArgs a)
+__global__ void __launch_bounds__(kThreads, QUADS == 1 ? 4 : 5) kvq_append_kernel(const __grid_constant__ KvqCopyArgs a)
 {
     pdl_trigger();
     pdl_wait();
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) kvq_append_kernel(const __grid_const
 }
 
 template <int BITS, int QUADS>
-__global__ void __launch_bounds__(kThreads) kvq_read_kernel(const __grid_constant__ KvqCopyArgs a)
+__global__ void __launch_bounds__(kThreads, 4) kvq_read_kernel(const __grid_constant__ KvqCopyArgs a)
 {
     pdl_trigger();
     pdl_wait();
