@@ -543,11 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         fence_mbar_init();
     }
     if (warp == kMmaWarp) alloc_tmem<CG>(&F.tmem);
-    pdl_trigger();
-    pdl_wait();
     tc_fence_before();
     pair_sync<CG>();
     tc_fence_after();
+    // the next kernel may start only now: its CTAs must not take the tensor memory that these wait for
+    pdl_trigger();
+    pdl_wait();
     const uint32_t tmem = F.tmem;
     Walk w = first_item(a, F, TI, share, kKvqPrefillCtas / CG);
     bool ok = true;
