@@ -23,9 +23,8 @@
 // Bound: the cache's bytes (36 per 64 values at 4 bits).  Work split: the cache
 // blocks of all (sequence, KV head) segments form one list that the CTAs (one per
 // SM) share evenly, so a batch of unlike lengths leaves no SM idle; a segment cut
-// between CTAs leaves partials that a second kernel joins.  With no more than
-// kWholeTokens tokens a sequence can hold, each segment is one CTA and there is one
-// launch.
+// between CTAs leaves partials that a second kernel joins.  Short caches have a CTA for
+// each segment and one launch.
 // Inside a CTA:
 //   last warps  producers of K and of V: one bulk copy per block for the codes and
 //               one for the parameters (contiguous in the cache's layout) into a
@@ -49,10 +48,9 @@
 namespace lily {
 namespace {
 
-#ifndef KVQ_NW
-#define KVQ_NW 10
-#endif
-constexpr int kNW = KVQ_NW;                   // consumer warps
+// Consumer warps: 6, 8 or 10 take 25.6, 25.7 or 24.8 us for a sequence of 131,072 tokens
+// and 14.2, 14.8 or 14.8 for one of 32,768; 14 are slower (registers).
+constexpr int kNW = 10;
 constexpr int kThreads = (kNW + 2) * 32;      // + the producers of K and of V
 constexpr int kMaxStages = 14;                // segments in flight <= stages < named barriers
 constexpr int kSmemLimit = 227 * 1024;
@@ -691,20 +689,20 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     }
 }
 
-// Joins the parts of a segment that was cut: CTA (segment key x head, 32-wide slice
-// of D), 256 threads: thread (e, sg) takes float4 column e and parts sg, sg + 32, ..
-// on a running maximum of its own; the four part groups of a warp are joined by shuffles,
-// the eight warps through shared memory, in a fixed order.  Parts of CTA c0 (the one the
-// segment starts in) are in slot 2 c0 + 1, those of the following CTAs c in slot 2 c, up
-// to the CTA it ends in.
+// Joins the parts of a segment that was cut: CTA (segment key x head, slice of kCols
+// float4 columns of D), 256 threads: thread (e, sg) takes column e and parts sg,
+// sg + kGroups, .. on a running maximum of its own; the part groups are joined by
+// shuffles where a warp has several, then through shared memory, in a fixed order.  Parts
+// of CTA c0 (the one the segment starts in) are in slot 2 c0 + 1, those of the following
+// CTAs c in slot 2 c, up to the CTA it ends in.
+template <int kCols>
 __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant__ KvqAttnArgs a)
 {
-    constexpr int kCols = 8, kGroups = 32, kBatch = 4;
-    __shared__ float4 part[8][kCols];
-    __shared__ float part_m[8], part_den[8];
+    constexpr int kGroups = 256 / kCols, kBatch = 4, kRuns = kCols < 32 ? 8 : kGroups;  // kRuns: results in shared memory
+    __shared__ float4 part[kRuns][kCols];
+    __shared__ float part_m[kRuns], part_den[kRuns];
     const int key = blockIdx.x / a.group, h = blockIdx.x % a.group;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int e = tid % kCols, sg = tid / kCols;
+    const int tid = threadIdx.x, e = tid % kCols, sg = tid / kCols;
     pdl_trigger();
     pdl_wait();
     const int4 meta = a.meta[key];
@@ -744,31 +742,33 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
         }
         mt = bm;
     }
-    float mw = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+    float mw = mt;
+#pragma unroll
+    for (int o = kCols; o < 32; o <<= 1) mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
     scale_by(ex2(mt - mw));
 #pragma unroll
-    for (int o = 8; o < 32; o <<= 1) {
+    for (int o = kCols; o < 32; o <<= 1) {
         num.x += __shfl_xor_sync(0xffffffffu, num.x, o);
         num.y += __shfl_xor_sync(0xffffffffu, num.y, o);
         num.z += __shfl_xor_sync(0xffffffffu, num.z, o);
         num.w += __shfl_xor_sync(0xffffffffu, num.w, o);
         den += __shfl_xor_sync(0xffffffffu, den, o);
     }
-    if (lane < kCols) part[warp][lane] = num;
-    if (lane == 0) {
-        part_m[warp] = mw;
-        part_den[warp] = den;
+    const int run = kCols < 32 ? tid / 32 : sg;
+    if (kCols >= 32 || (tid & 31) < kCols) part[run][e] = num;
+    if (e == 0 && (kCols >= 32 || (tid & 31) == 0)) {
+        part_m[run] = mw;
+        part_den[run] = den;
     }
     __syncthreads();
     if (tid < kCols) {
         float mx = part_m[0];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) mx = fmaxf(mx, part_m[w]);
+        for (int w = 1; w < kRuns; ++w) mx = fmaxf(mx, part_m[w]);
         float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float dsum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
+        for (int w = 0; w < kRuns; ++w) {
             const float f = ex2(part_m[w] - mx);
             const float4 x = part[w][tid];
             t.x = fmaf(f, x.x, t.x);
@@ -808,14 +808,28 @@ cudaError_t launch_d(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 
 }  // namespace
 
-// With at most this many tokens per sequence each segment is one CTA.
-constexpr long long kWholeTokens = 1024;
+// A CTA for each segment, and no join, where no CTA then has much more than an even share
+// of a full cache: with n segments on 152 CTAs, where capacity (1 - n / 152) is at most 640
+// tokens, which cost what cutting and joining does.  Measured, one CTA each against cut (2
+// KV heads of 256): one sequence of 256 tokens 7.1 / 8.0 us, of 512 9.2 / 8.3, of 1,024
+// 12.8 / 8.5; 64 sequences of 1,024 14.5 / 22.3.  (4 heads of 128: 512 tokens 6.1 / 6.7,
+// 64 sequences of 256 7.7 / 11.3 with 128 segments.)  Above 1,024 tokens the lengths of a
+// batch can differ too much from its capacity.
+bool one_cta_each(long long segments, long long capacity)
+{
+    return segments <= kKvqDecodeCtas && capacity <= 1024 && capacity * (kKvqDecodeCtas - segments) <= 640LL * kKvqDecodeCtas;
+}
+// Segments from which the join takes all of D in a CTA.  Below, slices of 32 channels: a
+// segment then has up to 152 parts (two segments of 32,768 tokens, slices 14.1 us, all of
+// D 19.4); above, the slices are thousands of CTAs (128 segments of 1,024 tokens: 36 us,
+// 22).  At 8 segments slices are ahead by 0.7 us, at 16 all of D is by 0.7.
+constexpr int kJoinWhole = 16;
 
 cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
 {
     KvqAttnArgs a = args;
     const long long segments = static_cast<long long>(a.B) * a.c.H_kv;
-    a.whole = static_cast<long long>(a.max_blocks) * a.c.bs <= kWholeTokens;
+    a.whole = one_cta_each(segments, static_cast<long long>(a.max_blocks) * a.c.bs);
     a.key_by_segment = segments <= kKvqDecodeCtas;
     a.stages = stages_for(a.D, a.c.bs, a.c.bits);
     a.stages_inv = 0xFFFFFFFFu / a.stages + 1;  // x / stages = the high word of x stages_inv for x < 2^32 / stages
@@ -823,7 +837,9 @@ cudaError_t launch_kvq_decode(const KvqAttnArgs &args, cudaStream_t stream)
     const cudaError_t e = a.c.bits == 4 ? launch_d<4>(a, ctas, stream) : launch_d<8>(a, ctas, stream);
     if (e != cudaSuccess || a.whole) return e;
     const int keys = a.key_by_segment ? static_cast<int>(segments) : ctas;
-    return launch_pdl(kvq_combine_kernel, dim3(keys * a.group, a.D / 32), dim3(256), 0, stream, a);
+    if (keys < kJoinWhole || a.D == 64) return launch_pdl(kvq_combine_kernel<8>, dim3(keys * a.group, a.D / 32), dim3(256), 0, stream, a);
+    return a.D == 128 ? launch_pdl(kvq_combine_kernel<32>, dim3(keys * a.group), dim3(256), 0, stream, a)
+                      : launch_pdl(kvq_combine_kernel<64>, dim3(keys * a.group), dim3(256), 0, stream, a);
 }
 
 }  // namespace lily
