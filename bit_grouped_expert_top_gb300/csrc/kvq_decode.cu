@@ -327,8 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
         const uint8_t *codes = isv ? a.c.v_q : a.c.k_q;
         const uint16_t *params = isv ? a.c.v_sb : a.c.k_sb;
         uint8_t *dst0 = ring + (isv ? CB + PB : 0);
-        int issued = 0;
-        bool ok = true;
+        int issued = 0, slot = 0;
+        uint32_t turn = 0;  // of the ring, its parity
+        bool ok = true, is_free = true;
         while (w.left > 0 && ok) {
             const int nblk = blocks_of(w.L, bs), n = min(nblk - w.j0, w.left);
             for (int i0 = 0; i0 < n && ok; i0 += 32) {
@@ -340,20 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
                         pb = 0;
                     }
                 }
-                for (int i = i0; i < min(n, i0 + 32); ++i) {
-                    const int slot = issued % NS;
-                    if (issued >= NS && !mbar_wait(&F.empty[slot], ((issued / NS) - 1) & 1, &F.abort, status)) ok = false;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const long long row0 = (static_cast<long long>(__shfl_sync(0xffffffffu, pb, i - i0)) * a.c.H_kv + w.g) * (GR * bs);
-                    if (lane == 0) {
+                const long long row0 = (static_cast<long long>(pb) * a.c.H_kv + w.g) * (GR * bs);
+                const int cnt = min(n - i0, 32);
+                for (int i = 0; i < cnt; ++i) {
+                    if (!__all_sync(0xffffffffu, is_free) && !(ok = warp_wait(&F.empty[slot], turn ^ 1u, &F.abort, status))) break;
+                    const long long row = __shfl_sync(0xffffffffu, row0, i);
+                    if (elect_one()) {
                         uint8_t *dst = dst0 + slot * SB;
                         mbar_arrive_expect_tx(&F.full[slot], static_cast<uint32_t>(CB + PB));
-                        bulk_load(dst, codes + row0 * GB, CB, &F.full[slot]);
-                        bulk_load(dst + CB, params + row0 * 2, PB, &F.full[slot]);
+                        bulk_load(dst, codes + row * GB, CB, &F.full[slot]);
+                        bulk_load(dst + CB, params + row * 2, PB, &F.full[slot]);
                     }
                     __syncwarp();
                     ++issued;
+                    if (++slot == NS) {
+                        slot = 0;
+                        turn ^= 1u;
+                    }
+                    is_free = issued < NS || phase_done(&F.empty[slot], turn ^ 1u);  // looked at one stage ahead
                 }
             }
             advance(a, w, n);

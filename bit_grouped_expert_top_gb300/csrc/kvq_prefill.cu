@@ -260,39 +260,11 @@ __device__ __forceinline__ void commit(uint64_t *bar)
                      : "memory");
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 __device__ __forceinline__ uint64_t join64(uint32_t lo, uint32_t hi)
 {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
     return r;
-}
-
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ uint32_t phase_done(uint64_t *bar, uint32_t parity)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return r;
-}
-
-// A whole warp waits.  Every lane does: what the barrier guards is read by every lane,
-// and a shuffle of one lane's result orders no memory access.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // ------------------------------------------------------------------ work list
