@@ -48,7 +48,7 @@ namespace {
 
 using namespace lily;
 
-constexpr int kVersion = 10100;  // 1.1.0
+constexpr int kVersion = 10200;  // 1.2.0
 
 // Unique id of the CUDA context current on this thread (the runtime's primary
 // context of the current device), 0 if none is current yet.  Caches of
@@ -670,7 +670,7 @@ const char *lily_moe_status_string(int status)
     case LILY_ERR_DEVICE_TIMEOUT: return "device wait timed out";
     case LILY_ERR_DEVICE_INDEX: return "device index out of range";
     case LILY_ERR_SCRATCH_LIMIT: return "token count above the fixed scratch of lily_moe_route_noalloc";
-    case LILY_ERR_DEVICE_RANGE: return "a value of x or h beyond the fp16 range of the expert GEMMs";
+    case LILY_ERR_DEVICE_RANGE: return "a value beyond the fp16 range of a matrix operand (x, h, or the quantised cache's K and V in prefill)";
     default: return "unknown status";
     }
 }

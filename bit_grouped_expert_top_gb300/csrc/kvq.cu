@@ -14,10 +14,12 @@
 // channels each, so that it reads whole 128-byte lines of the bf16 side and touches
 // one 128-byte run of codes; four such steps are in flight per thread.  The extremes
 // are three butterfly shuffles of one packed register (lo, -hi).  Measured (2 KV heads
-// of 256): 65,536 tokens at 4 bits read in 31.9 us (5.4 TB/s, 0.80 of the measured copy
+// of 256): 65,536 tokens at 4 bits read in 31.7 us (5.4 TB/s, 0.80 of the measured copy
 // rate; writes are 78% of the bytes); with 4 heads of 128 at 8 bits, 63,251 tokens
-// written and read back in 81.2 us (4.9 TB/s).  The append is bound by issue (~19
-// instructions a value at first, 13 now), the read by HBM.
+// written and read back in 76.2 us (5.2 TB/s).  The append is bound by issue (~19
+// instructions a value at first, 13 now): with five CTAs an SM (48 registers, some spilled)
+// it takes 3 to 6% less than with four, the read 4% more and at 8 bits 26%; few tokens have
+// nothing to gain from either and keep four.
 #include <cstdint>
 
 #include "lily_device.cuh"

@@ -3,12 +3,14 @@
 //   o = sum_{t < L - m + i + 1} softmax_t(scale q . k_t) v_t,
 // k_t and v_t the values code * scale + bias of row t of KV head g = h / (H_q / H_kv).
 //
-// The tensor cores bound this one: 4 D operations per (query head, token) pair.  A
-// work item is a tile of 128 query rows: the G query heads of a KV head for TQ =
-// 128 / G tokens (one rebuilt K and V serves them all), against the cache in chunks
-// of 64 tokens.  The chunks of all items form one list that the CTAs, one per SM,
-// share evenly (a long prompt's later tiles have more of them); an item cut between
-// CTAs leaves partial results that a second kernel joins.
+// The tensor cores bound this one: 4 D operations per (query head, token) pair.  A CTA
+// takes 128 query rows, the G query heads of a KV head for TQ = 128 / G tokens (one
+// rebuilt K and V serves them all), against the cache in chunks of 64 tokens; a pair of
+// CTAs shares an item of 2 TQ tokens and each rebuilds half of K and V, since the rebuild
+// and not the MMAs bounds a CTA alone (2,048 queries on 32,768 tokens: 669 us with pairs,
+// 835 without).  The chunks of all items form one list that the pairs, one per two SMs,
+// share evenly (a long prompt's later tiles have more of them); an item cut between pairs
+// leaves partial results that a second kernel joins.
 // Per CTA, with every wait bounded:
 //   warps 0..7   two threads per query row (32 of a chunk's 64 tokens each): q into
 //                tensor memory as fp16 (times a power of two per row, so q has no range
@@ -19,14 +21,17 @@
 //                rescaled rarely.  The next item's q is converted before O is read, so
 //                its first scores are computed meanwhile.
 //   warps 8..15  rebuild K and V of a chunk in fp16 (rounded once) into swizzled
-//                shared memory, two buffers each: a thread takes one (token, group of
-//                64 channels); its codes are loaded one chunk ahead.  Rows behind the
+//                shared memory, two to four buffers each: a thread takes one (token, group
+//                of 64 channels); its codes are loaded one chunk ahead.  Rows behind the
 //                sequence become zeros.
-//   warp 16      one thread issues tcgen05.mma: S = Q K^T (A from tensor memory, B
-//                K-major) of chunk i + 1, then O += P V (B with the channels
+//   warp 16      issues tcgen05.mma (of a pair: the first CTA's): S = Q K^T (A from tensor
+//                memory, B K-major) of chunk i + 1, then O += P V (B with the channels
 //                contiguous) of chunk i, so the softmax runs beside them.
 //   warp 17      one thread copies the next item's q into shared memory (TMA).
 // K and V must stay within fp16: |value| >= 65520 records LILY_ERR_DEVICE_RANGE.
+// Measured (16 query heads on 2 KV heads of 256, 4 bits): 2,048 queries at the end of
+// 32,768 tokens 669 us (1,591 TFLOP/s, 0.83 of the measured burst matrix rate), a prompt of
+// 8,192 tokens 396 us (0.72: an item's start and end cost about eight chunks).
 #include <cmath>
 #include <cstdint>
 
@@ -909,12 +914,11 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     if (warp == kMmaWarp) free_tmem<CG>(tmem);
 }
 
-// Joins the parts of an item that was cut: CTA (first share of the item, four rows), 64
-// threads a row, a float4 column each, on a running maximum.  An item of pairs is cut
-// in two as a rule, one of few query tokens in up to 76: two parts in flight with many
-// CTAs on an SM (an 8K prompt's join 9 us), or eight (15 us there; 16 tokens on 32K
-// 6 us less).  One row per CTA took 20 us to launch.  The part of the first share c0 is
-// in slot 2 c0 + 1, those of the following ones c in slot 2 c.
+// Joins the parts of an item that was cut: CTA (first share of the item, four rows, every
+// gridDim.y-th four of them), 64 threads a row, a float4 column each, on a running maximum.
+// An item of a pair is cut in two as a rule: two parts in flight with many CTAs on an SM (an
+// 8K prompt's join 9 us; eight in flight 15).  One row per CTA took 20 us to launch.  The part
+// of the first share c0 is in slot 2 c0 + 1, those of the following ones c in slot 2 c.
 template <int CG>
 __global__ void __launch_bounds__(256, CG == 2 ? 8 : 2) kvq_prefill_join_kernel(const __grid_constant__ KvqAttnArgs a)
 {
@@ -923,53 +927,160 @@ __global__ void __launch_bounds__(256, CG == 2 ? 8 : 2) kvq_prefill_join_kernel(
     pdl_wait();
     const int4 meta = a.meta[blockIdx.x];
     if (meta.x < 0) return;
-    const int G = a.group, TQ = kRows / G, row = blockIdx.y * 4 + threadIdx.x / 64, d4 = threadIdx.x % 64;
-    const int r = row % kRows, tq = row / kRows * TQ + r / G;  // query token within the item
-    if (r >= TQ * G || tq >= meta.z || d4 * 4 >= a.D) return;
-    const int c0 = blockIdx.x, S = meta.w - c0 + 1;
-    auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (CG * kRows) + row; };
-    float M = kNoMax, den = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < S; s0 += kBatch) {
-        float2 ml[kBatch];
-        float4 x[kBatch];
-        float to = M;
+    const int G = a.group, TQ = kRows / G, d4 = threadIdx.x % 64, c0 = blockIdx.x, S = meta.w - c0 + 1;
+    if (d4 * 4 >= a.D) return;
+    for (int row = blockIdx.y * 4 + threadIdx.x / 64; row < CG * kRows; row += gridDim.y * 4) {
+        const int r = row % kRows, tq = row / kRows * TQ + r / G;  // query token within the item
+        if (r >= TQ * G || tq >= meta.z) continue;
+        auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (CG * kRows) + row; };
+        float M = kNoMax, den = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = 0; s0 < S; s0 += kBatch) {
+            float2 ml[kBatch];
+            float4 x[kBatch];
+            float to = M;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int s = s0 + k;
-            ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2) : make_float2(kNoMax, 0.0f);
-            x[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < kBatch; ++k) {
+                const int s = s0 + k;
+                ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2) : make_float2(kNoMax, 0.0f);
+                x[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k].x);
+            const float c = ex2(M - to);
+            M = to;
+            den *= c;
+            o.x *= c;
+            o.y *= c;
+            o.z *= c;
+            o.w *= c;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float e = ex2(ml[k].x - to);
+                den = fmaf(e, ml[k].y, den);
+                o.x = fmaf(e, x[k].x, o.x);
+                o.y = fmaf(e, x[k].y, o.y);
+                o.z = fmaf(e, x[k].z, o.z);
+                o.w = fmaf(e, x[k].w, o.w);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k].x);
-        const float c = ex2(M - to);
-        M = to;
-        den *= c;
-        o.x *= c;
-        o.y *= c;
-        o.z *= c;
-        o.w *= c;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const float e = ex2(ml[k].x - to);
-            den = fmaf(e, ml[k].y, den);
-            o.x = fmaf(e, x[k].x, o.x);
-            o.y = fmaf(e, x[k].y, o.y);
-            o.z = fmaf(e, x[k].z, o.z);
-            o.w = fmaf(e, x[k].w, o.w);
-        }
+        const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+        uint2 y;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        y.x = *reinterpret_cast<const uint32_t *>(&lo);
+        y.y = *reinterpret_cast<const uint32_t *>(&hi);
+        const long long n = meta.x + tq;
+        reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + r % G) * a.D)[d4] = y;
     }
-    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-    uint2 y;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    y.x = *reinterpret_cast<const uint32_t *>(&lo);
-    y.y = *reinterpret_cast<const uint32_t *>(&hi);
-    const long long n = meta.x + tq;
-    reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + r % G) * a.D)[d4] = y;
+}
+
+// The same for calls of few query tokens (one CTA an item), whose items are few and have up to
+// 152 parts: the query rows of all of them are one list that the CTAs go through, found by
+// a scan over the shares' entries.  64 threads take a row; where an item has more parts than
+// a thread has loads in flight, a CTA takes one row and its four groups of 64 threads every
+// fourth part each, joined through shared memory in a fixed order.  16 tokens on 32,768: 35 us
+// for the call, 45 with the kernel above (which is the faster where items are many: a prompt of
+// 8,192 tokens 396 us, 402 with the list).
+__global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __grid_constant__ KvqAttnArgs a)
+{
+    constexpr int kBatch = 8, kShares = kKvqPrefillCtas;
+    __shared__ int4 metas[kShares];
+    __shared__ int upto[kShares], warp_sum[8];  // units of the shares up to this one
+    __shared__ float4 part[4][64];
+    __shared__ float2 part_ml[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d4 = tid % 64, slot0 = tid / 64;
+    const int G = a.group, TQ = kRows / G;
+    pdl_trigger();
+    pdl_wait();
+    const int4 mine = tid < kShares ? a.meta[tid] : make_int4(-1, 0, 0, 0);
+    const int rows = mine.x >= 0 ? min(mine.z, TQ) * G : 0;
+    const bool by_row = __syncthreads_or(mine.x >= 0 && mine.w - tid + 1 > kBatch);
+    int inc = by_row ? rows : (rows + 3) / 4;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += warp_sum[i];
+    if (tid < kShares) {
+        metas[tid] = mine;
+        upto[tid] = inc;
+    }
+    __syncthreads();
+    const int total = upto[kShares - 1];
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int c0 = -1, last = kShares - 1;  // the first share with upto > u
+        while (last - c0 > 1) {
+            const int mid = (c0 + last) >> 1;
+            if (upto[mid] > u)
+                last = mid;
+            else
+                c0 = mid;
+        }
+        const int local = u - (c0 >= 0 ? upto[c0] : 0);
+        c0 = last;
+        const int4 meta = metas[c0];
+        const int S = meta.w - c0 + 1, i = by_row ? local : local * 4 + slot0, tq = i / G, h = i % G;  // query token, head
+        const bool valid = tq < min(meta.z, TQ) && d4 * 4 < a.D;
+        auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kRows + i; };
+        float M = kNoMax, den = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float e, float l, const float4 &x) {
+            den = fmaf(e, l, den);
+            o.x = fmaf(e, x.x, o.x);
+            o.y = fmaf(e, x.y, o.y);
+            o.z = fmaf(e, x.z, o.z);
+            o.w = fmaf(e, x.w, o.w);
+        };
+        const int step = by_row ? 4 : 1;
+        for (int s0 = by_row ? slot0 : 0; valid && s0 < S; s0 += kBatch * step) {
+            float2 ml[kBatch];
+            float4 x[kBatch];
+            float to = M;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int s = s0 + k * step;
+                ml[k] = s < S ? *reinterpret_cast<const float2 *>(a.part_ml + slot(s) * 2) : make_float2(kNoMax, 0.0f);
+                x[k] = s < S ? reinterpret_cast<const float4 *>(a.part_acc + slot(s) * a.D)[d4] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) to = fmaxf(to, ml[k].x);
+            const float4 before = o;
+            const float e = ex2(M - to), l = den;
+            M = to;
+            den = 0.0f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            add(e, l, before);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) add(ex2(ml[k].x - to), ml[k].y, x[k]);
+        }
+        if (by_row) {
+            __syncthreads();  // the last row's are read
+            part[slot0][d4] = o;
+            if (d4 == 0) part_ml[slot0] = make_float2(M, den);
+            __syncthreads();
+            if (slot0 > 0) continue;
+            M = kNoMax;
+            for (int k = 0; k < 4; ++k) M = fmaxf(M, part_ml[k].x);
+            den = 0.0f;
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < 4; ++k) add(ex2(part_ml[k].x - M), part_ml[k].y, part[k][d4]);
+        }
+        if (!valid) continue;
+        const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+        uint2 y;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        y.x = *reinterpret_cast<const uint32_t *>(&lo);
+        y.y = *reinterpret_cast<const uint32_t *>(&hi);
+        const long long n = meta.x + tq;
+        reinterpret_cast<uint2 *>(a.out + (n * a.H_q + meta.y * G + h) * a.D)[d4] = y;
+    }
 }
 
 template <int BITS, int GR, int CG>
-cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
+cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaStream_t stream)
 {
     constexpr int smem = smem_bytes(GR, CG);
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG>), smem);
@@ -988,7 +1099,8 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t st
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG>, a, tmQ)) != cudaSuccess) return e;
-    return launch_pdl(kvq_prefill_join_kernel<CG>, dim3(kKvqPrefillCtas / CG, CG * kRows / 4), dim3(256), 0, stream, a);
+    if (few) return launch_pdl(kvq_prefill_join_few_kernel, dim3(4 * kKvqPrefillCtas), dim3(256), 0, stream, a);
+    return launch_pdl(kvq_prefill_join_kernel<CG>, dim3(kKvqPrefillCtas / CG, CG == 1 ? 16 : 64), dim3(256), 0, stream, a);
 }
 
 // Pairs, but one CTA an item where D = 64 (its 64 channels of V are one swizzled box and
@@ -998,10 +1110,10 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t st
 template <int BITS>
 cudaError_t launch_d(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    if (a.D == 64) return launch<BITS, 1, 1>(a, tmQ, stream);
-    if (a.N <= static_cast<long long>(a.B) * (kRows / a.group))
-        return a.D == 128 ? launch<BITS, 2, 1>(a, tmQ, stream) : launch<BITS, 4, 1>(a, tmQ, stream);
-    return a.D == 128 ? launch<BITS, 2, 2>(a, tmQ, stream) : launch<BITS, 4, 2>(a, tmQ, stream);
+    const bool few = a.N <= static_cast<long long>(a.B) * (kRows / a.group);
+    if (a.D == 64) return launch<BITS, 1, 1>(a, tmQ, few, stream);
+    if (few) return a.D == 128 ? launch<BITS, 2, 1>(a, tmQ, few, stream) : launch<BITS, 4, 1>(a, tmQ, few, stream);
+    return a.D == 128 ? launch<BITS, 2, 2>(a, tmQ, few, stream) : launch<BITS, 4, 2>(a, tmQ, few, stream);
 }
 
 }  // namespace

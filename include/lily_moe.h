@@ -67,7 +67,7 @@ enum {
     LILY_ERR_DEVICE_TIMEOUT = -6, /* a kernel's bounded wait ran out (device-detected) */
     LILY_ERR_DEVICE_INDEX = -7,   /* a kernel saw an index out of range (device-detected) */
     LILY_ERR_SCRATCH_LIMIT = -8,  /* size above the fixed scratch of lily_moe_route_noalloc */
-    LILY_ERR_DEVICE_RANGE = -9    /* a value beyond the fp16 range of the expert GEMMs (device-detected) */
+    LILY_ERR_DEVICE_RANGE = -9    /* a value beyond the fp16 range of a matrix operand (device-detected) */
 };
 
 /*
@@ -325,7 +325,9 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
  *   code  = min(rint((x - lo) / scale), L)   (0 where scale is 0)
  *   value = code * scale + bias
  * with fp32 arithmetic, round-to-nearest-even.  |value - x| is at most about
- * scale / 2; a group of equal values is kept exactly.
+ * scale / 2; a group of equal values is kept exactly.  The values of a group have to be
+ * finite: one that is not leaves that group's codes and parameters unspecified, and
+ * no other's.
  *
  * Layout of K and of V (device, row-major, every array 16-byte aligned):
  *   codes      uint8 [n_blocks][H_kv][D/64][block_size][64 * bits / 8]; 4 bits:
@@ -343,7 +345,8 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
  * length outside [0, max_blocks * block_size] records LILY_ERR_DEVICE_INDEX.
  * lily_kvq_append and lily_kvq_read then leave that token's row alone; the
  * attention reads block 0 / clamps the length instead.
- * Every call is bit-reproducible from run to run.
+ * Every call is bit-reproducible from run to run.  Calls that may overlap on the GPU
+ * need workspaces of their own; a cache may be read by any number of them.
  */
 typedef struct lily_kvq_shape {
     int32_t B;           /* sequences */
@@ -401,7 +404,8 @@ int lily_kvq_read(const lily_kvq_shape *shape, const lily_kvq_cache *cache, uint
  *   q     bf16 [B][H_q][D], sequence b q_stride elements after the first (at
  *         least H_q * D, a multiple of 8)
  *   out   bf16 [B][H_q][D] dense; a sequence with no tokens gets zeros
- * Cache rows at or past seq_lens[b] are not used, whatever they hold.
+ * Cache rows at or past seq_lens[b] are not used, whatever they hold.  K and V may have any
+ * finite values.  At most two kernels are enqueued, whatever the lengths.
  */
 int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
                          const int32_t *block_table, const int32_t *seq_lens, float scale, uint16_t *out, void *ws,
@@ -414,6 +418,10 @@ int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cach
  * attends to the positions <= seq_lens[b] - m + i.  A query with none gets zeros.
  *   q     bf16 [N][H_q][D] (q_stride as above), rows by cu_q int32 [B+1]
  *   out   bf16 [N][H_q][D] dense; rows from cu_q[B] on are left as they were
+ * K and V are rebuilt in fp16, each value rounded once: a used group that can hold a
+ * value of 65520 or more in magnitude records LILY_ERR_DEVICE_RANGE (lily_kvq_attn_decode
+ * has no such limit), and values below 2^-14 keep fewer bits (multiples of 2^-24).  Two kernels are
+ * enqueued; N = 0 enqueues nothing.
  */
 int lily_kvq_attn_prefill(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q,
                           int64_t q_stride, int32_t N, const int32_t *cu_q, const int32_t *block_table,
