@@ -223,6 +223,13 @@ def test_decode_lengths(L):
     _check_decode(_cfg((L,), seed=L), poison=True)
 
 
+@pytest.mark.parametrize("D,H_q,H_kv", [(64, 4, 4), (128, 8, 4), (256, 16, 2)])
+@pytest.mark.parametrize("lens", [(640,), (1024,), (1088,), (1, 1024, 30), (1100,) * 9 + (1, 2000, 64, 0), (1000, 60) * 19, (1100, 3, 64) * 27])
+def test_decode_of_short_and_middle_caches(lens, D, H_q, H_kv):
+    # a CTA for each segment and shares of the list, joins of few and of many segments
+    _check_decode(_cfg(lens, D=D, H_q=H_q, H_kv=H_kv, block_size=32, seed=49 + len(lens)), poison=True)
+
+
 def test_decode_empty_sequences_give_zeros():
     c, out = _check_decode(_cfg((0, 70, 0), D=64, seed=40), poison=True)
     assert (out[0] == 0).all() and (out[2] == 0).all()
@@ -395,6 +402,14 @@ def test_prefill_long_context_and_repeats():
     _check_prefill(KvqConfig("prompt", lens=(3000,), seed=55), rows=np.arange(0, 3000, 97))
     # draft tokens of several sequences
     _check_prefill(KvqConfig("draft", lens=(4096, 5000, 2049, 17), new=(4, 4, 4, 4), seed=56))
+
+
+@pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 4)])
+@pytest.mark.parametrize("lens,new", [((20000,), (3,)), ((9000, 40, 0, 5000), (16, 1, 0, 7)), ((2000, 3000) * 10, (1, 2) * 10)])
+def test_prefill_of_few_tokens_on_long_contexts(lens, new, D, bits):
+    # items with more and with fewer parts than a join's loads in flight
+    c, out = _check_prefill(KvqConfig("few", lens=lens, new=new, D=D, bits=bits, seed=58 + D), poison=True)
+    assert torch.equal(out, _prefill(c))
 
 
 def test_prefill_of_one_token_equals_decode():
