@@ -16,10 +16,10 @@
 // are three butterfly shuffles of one packed register (lo, -hi).  Measured (2 KV heads
 // of 256): 65,536 tokens at 4 bits read in 31.7 us (5.4 TB/s, 0.80 of the measured copy
 // rate; writes are 78% of the bytes); with 4 heads of 128 at 8 bits, 63,251 tokens
-// written and read back in 76.2 us (5.2 TB/s).  The append is bound by issue (~19
-// instructions a value at first, 13 now): with five CTAs an SM (48 registers, some spilled)
-// it takes 3 to 6% less than with four, the read 4% more and at 8 bits 26%; few tokens have
-// nothing to gain from either and keep four.
+// written and read back in 74.1 us (5.4 TB/s).  The append is bound by issue, so its
+// arithmetic takes two values an instruction (10,754 tokens 17.3 us without, 16.5 with), and five
+// CTAs an SM (48 registers, some spilled) are better than four (18.0) or six (19.1); few
+// tokens gain nothing and keep four, and so does the read (31.7 us, five 32.8, six 48.4).
 #include <cstdint>
 
 #include "lily_device.cuh"
@@ -101,15 +101,23 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &w, const GroupScale &g)
     constexpr float L = 255.0f;
     constexpr uint32_t kMagic = 0x4B400000u, kStep = 1u << BITS;
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    const unsigned long long m = pair(g.m, g.m), mlo = pair(g.mlo, g.mlo), h = pair(-g.h, -g.h), r = pair(g.r, g.r);
     uint32_t c[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = j & 1 ? __uint_as_float(ws[j / 2] & 0xFFFF0000u) : __uint_as_float(ws[j / 2] << 16);
-        const float d = fmaf(x, g.m, g.mlo);
-        const float q0 = __fmul_rn(d, g.r);
-        const float q = fmaf(g.r, fmaf(-q0, g.h, d), q0);
+    for (int j = 0; j < 4; ++j) {  // two values an instruction
+        const unsigned long long d = fma2(pair(__uint_as_float(ws[j] << 16), __uint_as_float(ws[j] & 0xFFFF0000u)), m, mlo);
+        const unsigned long long q0 = mul2(d, r);
+        unsigned long long q = fma2(r, fma2(q0, h, d), q0);
         // the scale is rounded by 2^-8 at most, so at 4 bits q stays below 15.06 and needs no limit
-        c[j] = __float_as_uint(__fadd_rn(BITS == 4 ? q : fminf(q, L), 12582912.0f));
+        if constexpr (BITS == 8) {
+            float a, b;
+            unpair(q, a, b);
+            q = pair(fminf(a, L), fminf(b, L));
+        }
+        float a, b;
+        unpair(add2(q, pair(12582912.0f, 12582912.0f)), a, b);
+        c[2 * j] = __float_as_uint(a);
+        c[2 * j + 1] = __float_as_uint(b);
     }
     if (BITS == 4) {
         uint32_t p = c[7], k = kMagic;
