@@ -436,6 +436,13 @@ def _tokens(name: str, t, heads: int, D: int, dev: int):
     return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * D)
 
 
+def _table(t, shape, dev: int) -> int:
+    """Address of the block table: rows of max_blocks entries (a wider table would be read across its rows)."""
+    if t.dim() != 2 or t.shape[0] != shape.B or t.shape[1] != shape.max_blocks:
+        raise ValueError(f"block_table: expected [{shape.B}][{shape.max_blocks}], got {list(t.shape)}")
+    return _dense("block_table", t, torch.int32, shape.B * shape.max_blocks, dev)
+
+
 def _launch_stream(stream, dev: int):
     return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
@@ -451,7 +458,7 @@ def _kvq_copy(fn: str, shape, cache, k, v, cu, starts, block_table, ws, stream, 
     pv, sv = _tokens("v", v, H, D, dev)
     rc = getattr(_lib or load(), fn)(
         ctypes.byref(shape), ctypes.byref(cache), pk, sk, pv, sv, N, _dense("cu", cu, i32, B + 1, dev),
-        _dense("starts", starts, i32, B, dev), _dense("block_table", block_table, i32, B * shape.max_blocks, dev),
+        _dense("starts", starts, i32, B, dev), _table(block_table, shape, dev),
         _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
     return _check(fn, rc) if check else rc
 
@@ -487,7 +494,7 @@ def lily_kvq_attn_decode(shape: lily_kvq_shape, cache: lily_kvq_cache, q, block_
     if q.shape[0] != B:
         raise ValueError(f"q: expected {B} sequences, got {q.shape[0]}")
     rc = (_lib or load()).lily_kvq_attn_decode(
-        ctypes.byref(shape), ctypes.byref(cache), pq, sq, _dense("block_table", block_table, i32, B * shape.max_blocks, dev),
+        ctypes.byref(shape), ctypes.byref(cache), pq, sq, _table(block_table, shape, dev),
         _dense("seq_lens", seq_lens, i32, B, dev), D ** -0.5 if scale is None else scale,
         _dense("out", out, torch.bfloat16, B * H * D, dev), _dense("ws", ws, torch.uint8, 1, dev), ws.numel(),
         _launch_stream(stream, dev))
@@ -504,7 +511,7 @@ def lily_kvq_attn_prefill(shape: lily_kvq_shape, cache: lily_kvq_cache, q, cu_q,
     pq, sq = _tokens("q", q, H, D, dev)
     rc = (_lib or load()).lily_kvq_attn_prefill(
         ctypes.byref(shape), ctypes.byref(cache), pq, sq, N, _dense("cu_q", cu_q, i32, B + 1, dev),
-        _dense("block_table", block_table, i32, B * shape.max_blocks, dev), _dense("seq_lens", seq_lens, i32, B, dev),
+        _table(block_table, shape, dev), _dense("seq_lens", seq_lens, i32, B, dev),
         D ** -0.5 if scale is None else scale, _dense("out", out, torch.bfloat16, N * H * D, dev),
         _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
     return _check("lily_kvq_attn_prefill", rc) if check else rc

@@ -945,7 +945,8 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     int rc;
     if ((rc = kvq_check_shape(shape)) || (rc = kvq_check_cache(*shape, cache))) return rc;
     const lily_kvq_shape s = *shape;
-    if (N < 0 || !std::isfinite(scale)) return LILY_ERR_INVALID;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (N < 0 || !std::isfinite(scale_log2)) return LILY_ERR_INVALID;
     const KvqLayout L = kvq_layout(s, ragged ? N : 0);
     if ((rc = check_ws(ws, ws_bytes, L.total))) return rc;
     if (N == 0) return LILY_OK;
@@ -957,7 +958,7 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     KvqAttnArgs a{};
     a.c = kvq_device_cache(s, *cache);
     a.B = s.B; a.H_q = s.H_q; a.D = s.D; a.group = s.H_q / s.H_kv; a.max_blocks = s.max_blocks; a.N = N;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.q = q; a.q_stride = q_stride;
     a.cu_q = ragged ? cu_q : nullptr;
     a.block_table = block_table; a.seq_lens = seq_lens;

@@ -647,3 +647,24 @@ def test_prefill_on_two_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
     assert all(c.status() == 0 for c in cs)
+
+
+def test_binding_refuses_tensors_of_other_shapes():
+    c = Cache(_cfg((100, 50), D=64, seed=66)).to_gpu()
+    t, q, n = c.d["block_table"], c.d["q"], c.d["seq_lens"]
+    out = torch.empty_like(q)
+
+    def refused(what, **kw):
+        a = {"q": q, "block_table": t, "seq_lens": n, "out": out, "ws": c.ws, **kw}
+        with pytest.raises(ValueError, match=what):
+            lm.lily_kvq_attn_decode(c.shape, c.handle, a["q"], a["block_table"], a["seq_lens"], a["out"], a["ws"])
+
+    refused("block_table", block_table=torch.cat([t, t], 1))   # a wider table
+    refused("block_table", block_table=t.flatten())
+    refused("block_table", block_table=t.long())
+    refused("block_table", block_table=torch.cat([t, t], 1)[:, :t.shape[1]])   # its rows are not contiguous
+    refused("seq_lens", seq_lens=n[:1])
+    refused("out", out=out[:1])
+    refused("sequences", q=q[:1])
+    refused("ws", ws=c.ws.to(torch.int8))
+    assert c.status() == 0

@@ -87,6 +87,7 @@ def test_attention_refusals():
         assert call(s=None) == -1 and call(c=None) == -1
         assert call(s=_shape(H_q=18)) == -2 and call(c=_cache(s, code_bytes=7)) == -1
         assert call(scale=nan) == -1 and call(scale=inf) == -1
+        assert call(scale=3e38) == -1   # times log2(e) it is no fp32 number
         for a in ("q", "tb", "sl", "out", "ws"):
             assert call(**{a: None}) == -1, a
             assert call(**{a: FAKE + 8}) == -3, a
