@@ -1,6 +1,6 @@
 """fp64 CPU oracle of the mixture-of-experts layer, of grouped-query decode
 attention over a fixed-block KV cache and of the Gated DeltaNet scan: ctypes
-wrappers around oracle.c.
+wrappers around oracle.c (the quantised KV cache is in kvq.py).
 
 TEST INFRASTRUCTURE ONLY.  Only tests, the smoke check and the benchmark's
 CPU-baseline leg may import this package.  The CUDA library never calls it and
