@@ -668,3 +668,55 @@ def test_binding_refuses_tensors_of_other_shapes():
     refused("sequences", q=q[:1])
     refused("ws", ws=c.ws.to(torch.int8))
     assert c.status() == 0
+
+
+def test_attention_of_more_sequences_than_threads():
+    rng = np.random.default_rng(67)
+    lens = tuple(int(x) for x in rng.integers(0, 70, 1300))
+    new = tuple(int(min(L, x)) for L, x in zip(lens, rng.integers(0, 4, 1300)))
+    _check_decode(_cfg(lens, D=64, H_q=2, H_kv=1, block_size=32, seed=67), poison=True)
+    _check_prefill(KvqConfig("many", lens=lens, new=new, D=64, H_q=2, H_kv=1, block_size=32, seed=68), poison=True)
+    _check_prefill(KvqConfig("many", lens=lens, new=lens, D=128, H_q=2, H_kv=2, block_size=32, seed=69), poison=True)
+
+
+def test_calls_with_nothing_to_do():
+    # every sequence empty or idle: zeros from decode, untouched rows from prefill
+    cfg = KvqConfig("idle", lens=(0, 0, 90), new=(0, 0, 0), D=128, seed=70)
+    c = Cache(cfg, n_query=8).to_gpu()
+    q = torch.randn((8, cfg.H_q, cfg.D), device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 5.0)
+    lm.lily_kvq_attn_prefill(c.shape, c.handle, q, c.d["cu"], c.d["block_table"], c.d["seq_lens"], out, c.ws)
+    assert (out == 5).all()
+    none = torch.zeros_like(c.d["seq_lens"])
+    lm.lily_kvq_attn_decode(c.shape, c.handle, q[:3], c.d["block_table"], none, out[:3], c.ws)
+    assert (out[:3] == 0).all() and (out[3:] == 5).all()
+    assert c.status() == 0
+
+
+def test_attention_over_a_cache_beyond_four_gigabytes():
+    # the same blocks at the end of arrays of 4.9 GB: the same bits
+    cfg = KvqConfig("far", lens=(300, 77), new=(40, 3), seed=71)
+    c = Cache(cfg, n_query=cfg.N).to_gpu()
+    n, far = c.a["n_blocks"], 300000
+    want = [_prefill(c), _decode(c, q=c.d["q"][:2])]
+    big = {}
+    for k, t in c.t.items():
+        big[k] = torch.empty((far + n,) + t.shape[1:], dtype=t.dtype, device="cuda")
+        big[k][far:] = t
+    assert big["k_q"].numel() > 1 << 32
+    c.handle = lm.make_kvq_cache(big)
+    c.d["block_table"] = torch.where(c.d["block_table"] >= 0, c.d["block_table"] + far, -1).to(torch.int32)
+    assert torch.equal(_prefill(c), want[0]) and torch.equal(_decode(c, q=c.d["q"][:2]), want[1])
+    assert c.status() == 0
+
+
+def test_sequences_that_share_blocks():
+    # a common prefix held once: both tables name the same blocks
+    cfg = _cfg((200, 200), D=128, seed=72)
+    c = Cache(cfg, n_query=2).to_gpu()
+    alone = _decode(c)
+    c.d["block_table"][1] = c.d["block_table"][0]
+    q = c.d["q"][:1].expand(2, -1, -1).contiguous()
+    both = _decode(c, q=q)
+    assert torch.equal(both[0], both[1]) and torch.equal(both[0], alone[0])
+    assert c.status() == 0
