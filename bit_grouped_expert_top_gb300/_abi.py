@@ -395,52 +395,48 @@ def alloc_kvq_workspace(shape: lily_kvq_shape, n_query: int = 0, device="cuda") 
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-# The checks of a call's tensors are written flat: a decode step of short sequences
-# takes the GPU less time than a careless wrapper takes the host.
+# A call's tensors are checked in one flat condition, as a decode step of short sequences takes
+# the GPU less time than a careless wrapper takes the host; where it does not hold,
+# the functions below find out why and raise.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream without a Stream object
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # for callers that hold a CUDA tensor
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 
 
-def _device_of(name: str, t, cache) -> int:
-    """The device of the call's first tensor: the library launches on the current
-    device, so a tensor (or a cache) elsewhere is refused."""
+def _need(ok: bool, message: str) -> None:
+    if not ok:
+        raise ValueError(message)
+
+
+def _need_device(name: str, t, cache) -> int:
+    """The library launches on the current device: a tensor (or a cache) elsewhere is refused."""
     dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if cache.device != dev:
-        raise ValueError(f"the cache is on cuda:{cache.device}, {name} on cuda:{dev}")
+    _need(dev >= 0, f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+    _need(dev == torch.cuda.current_device(),
+          f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _need(cache.device == dev, f"the cache is on cuda:{cache.device}, {name} on cuda:{dev}")
     return dev
 
 
-def _dense(name: str, t, dtype, n: int, dev: int) -> int:
-    """Address of a dense tensor of this dtype and device with at least n elements."""
-    if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
-        if not t.is_cuda:
-            raise ValueError(f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} on cuda:{dev}, got {t.dtype} {list(t.shape)} with "
-                         f"strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+def _need_dense(name: str, t, dtype, n: int, dev: int) -> None:
+    _need(t.is_cuda, f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+    _need(t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous(),
+          f"{name}: expected {n} contiguous {dtype} on cuda:{dev}, got {t.dtype} {list(t.shape)} with "
+          f"strides {t.stride()} on {t.device}")
 
 
-def _tokens(name: str, t, heads: int, D: int, dev: int):
-    """Address and token stride of a bf16 [n][heads][D] tensor whose tokens are dense."""
-    shape = t.shape
-    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise ValueError(f"{name}: expected bfloat16 [n][{heads}][{D}], got {t.dtype} {list(shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: expected a CUDA tensor on cuda:{dev}, got one on {t.device}")
-    stride = t.stride()
-    if stride[2] != 1 or (stride[1] != D and heads > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {stride}")
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * D)
+def _need_tokens(name: str, t, heads: int, D: int, dev: int) -> None:
+    _need(t.dtype is _BF16 and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == D,
+          f"{name}: expected bfloat16 [n][{heads}][{D}], got {t.dtype} {list(t.shape)}")
+    _need(t.get_device() == dev, f"{name}: expected a CUDA tensor on cuda:{dev}, got one on {t.device}")
+    _need(t.stride(2) == 1 and (t.stride(1) == D or heads == 1),
+          f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
 
 
-def _table(t, shape, dev: int) -> int:
-    """Address of the block table: rows of max_blocks entries (a wider table would be read across its rows)."""
-    if t.dim() != 2 or t.shape[0] != shape.B or t.shape[1] != shape.max_blocks:
-        raise ValueError(f"block_table: expected [{shape.B}][{shape.max_blocks}], got {list(t.shape)}")
-    return _dense("block_table", t, torch.int32, shape.B * shape.max_blocks, dev)
+def _need_table(t, shape, dev: int) -> None:
+    _need(t.shape == (shape.B, shape.max_blocks),
+          f"block_table: expected [{shape.B}][{shape.max_blocks}], got {list(t.shape)}")
+    _need_dense("block_table", t, _I32, shape.B * shape.max_blocks, dev)
 
 
 def _launch_stream(stream, dev: int):
@@ -448,18 +444,31 @@ def _launch_stream(stream, dev: int):
 
 
 def _kvq_copy(fn: str, shape, cache, k, v, cu, starts, block_table, ws, stream, check: bool) -> int:
-    N, B, H, D, i32 = k.shape[0], shape.B, shape.H_kv, shape.D, torch.int32
-    if k.dtype is not torch.bfloat16:
-        raise ValueError(f"k: expected bfloat16, got {k.dtype}")
-    if v.shape[0] != N:
-        raise ValueError(f"k has {N} tokens, v {v.shape[0]}")
-    dev = _device_of("k", k, cache)
-    pk, sk = _tokens("k", k, H, D, dev)
-    pv, sv = _tokens("v", v, H, D, dev)
+    B, H, D = shape.B, shape.H_kv, shape.D
+    dev, size, sk, sv = k.get_device(), k.shape, k.stride(), v.stride()
+    if not (k.dtype is _BF16 and v.dtype is _BF16 and v.shape == size and len(size) == 3 and size[1] == H and size[2] == D
+            and sk[2] == 1 and sv[2] == 1 and (H == 1 or (sk[1] == D and sv[1] == D))
+            and cu.dtype is _I32 and cu.numel() > B and cu.is_contiguous()
+            and starts.dtype is _I32 and starts.numel() >= B and starts.is_contiguous()
+            and block_table.dtype is _I32 and block_table.shape == (B, shape.max_blocks) and block_table.is_contiguous()
+            and ws.dtype is _U8 and ws.is_contiguous()
+            and dev >= 0 and dev == _current_device() == cache.device == v.get_device() == cu.get_device()
+            == starts.get_device() == block_table.get_device() == ws.get_device()):
+        _need(k.dtype is _BF16, f"k: expected bfloat16, got {k.dtype}")
+        _need(v.shape[0] == k.shape[0], f"k has {k.shape[0]} tokens, v {v.shape[0]}")
+        dev = _need_device("k", k, cache)
+        _need_tokens("k", k, H, D, dev)
+        _need_tokens("v", v, H, D, dev)
+        _need_dense("cu", cu, _I32, B + 1, dev)
+        _need_dense("starts", starts, _I32, B, dev)
+        _need_table(block_table, shape, dev)
+        _need_dense("ws", ws, _U8, 1, dev)
+        raise ValueError("tensors on different devices")
+    N = size[0]
     rc = getattr(_lib or load(), fn)(
-        ctypes.byref(shape), ctypes.byref(cache), pk, sk, pv, sv, N, _dense("cu", cu, i32, B + 1, dev),
-        _dense("starts", starts, i32, B, dev), _table(block_table, shape, dev),
-        _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
+        ctypes.byref(shape), ctypes.byref(cache), k.data_ptr(), sk[0] if N > 1 else H * D, v.data_ptr(),
+        sv[0] if N > 1 else H * D, N, cu.data_ptr(), starts.data_ptr(), block_table.data_ptr(), ws.data_ptr(), ws.numel(),
+        _launch_stream(stream, dev))
     return _check(fn, rc) if check else rc
 
 
@@ -476,28 +485,43 @@ def lily_kvq_read(shape: lily_kvq_shape, cache: lily_kvq_cache, k, v, cu, starts
     return _kvq_copy("lily_kvq_read", shape, cache, k, v, cu, starts, block_table, ws, stream, check)
 
 
-def _kvq_query(q, H: int, D: int, cache) -> int:
-    if q.dtype is not torch.bfloat16:
-        raise ValueError(f"q: expected bfloat16 [n][{H}][{D}], got {q.dtype} {list(q.shape)}")
-    if q.dim() != 3 or q.shape[1] != H or q.shape[2] != D:
-        raise ValueError(f"q: expected bfloat16 [n][{H}][{D}], got {list(q.shape)}")
-    return _device_of("q", q, cache)
+def _kvq_attention(shape, cache, q, cu_q, block_table, seq_lens, out, ws, scale, stream):
+    """The checks of both attentions (cu_q None: decode).  Device, stream, token stride of q and the scale."""
+    B, H, D = shape.B, shape.H_q, shape.D
+    dev, size, sq = q.get_device(), q.shape, q.stride()
+    if not (q.dtype is _BF16 and len(size) == 3 and size[1] == H and size[2] == D and sq[2] == 1 and (H == 1 or sq[1] == D)
+            and block_table.dtype is _I32 and block_table.shape == (B, shape.max_blocks) and block_table.is_contiguous()
+            and seq_lens.dtype is _I32 and seq_lens.numel() >= B and seq_lens.is_contiguous()
+            and out.dtype is _BF16 and out.numel() >= size[0] * H * D and out.is_contiguous()
+            and ws.dtype is _U8 and ws.is_contiguous()
+            and dev >= 0 and dev == _current_device() == cache.device == block_table.get_device() == seq_lens.get_device()
+            == out.get_device() == ws.get_device()
+            and (size[0] == B if cu_q is None else cu_q.dtype is _I32 and cu_q.numel() > B and cu_q.is_contiguous()
+                 and cu_q.get_device() == dev)):
+        _need(q.dtype is _BF16 and q.dim() == 3 and q.shape[1] == H and q.shape[2] == D,
+              f"q: expected bfloat16 [n][{H}][{D}], got {q.dtype} {list(q.shape)}")
+        dev = _need_device("q", q, cache)
+        _need_tokens("q", q, H, D, dev)
+        if cu_q is None:
+            _need(q.shape[0] == B, f"q: expected {B} sequences, got {q.shape[0]}")
+        else:
+            _need_dense("cu_q", cu_q, _I32, B + 1, dev)
+        _need_table(block_table, shape, dev)
+        _need_dense("seq_lens", seq_lens, _I32, B, dev)
+        _need_dense("out", out, _BF16, q.shape[0] * H * D, dev)
+        _need_dense("ws", ws, _U8, 1, dev)
+        raise ValueError("tensors on different devices")
+    return _launch_stream(stream, dev), sq[0] if size[0] > 1 else H * D, D ** -0.5 if scale is None else scale
 
 
 def lily_kvq_attn_decode(shape: lily_kvq_shape, cache: lily_kvq_cache, q, block_table, seq_lens, out, ws,
                          scale: Optional[float] = None, stream=None, *, check: bool = True) -> int:
     """Decode attention over the quantised cache (see include/lily_moe.h): q and
     out bf16 [B][H_q][D].  scale defaults to 1/sqrt(D)."""
-    B, H, D, i32 = shape.B, shape.H_q, shape.D, torch.int32
-    dev = _kvq_query(q, H, D, cache)
-    pq, sq = _tokens("q", q, H, D, dev)
-    if q.shape[0] != B:
-        raise ValueError(f"q: expected {B} sequences, got {q.shape[0]}")
+    stream, stride, scale = _kvq_attention(shape, cache, q, None, block_table, seq_lens, out, ws, scale, stream)
     rc = (_lib or load()).lily_kvq_attn_decode(
-        ctypes.byref(shape), ctypes.byref(cache), pq, sq, _table(block_table, shape, dev),
-        _dense("seq_lens", seq_lens, i32, B, dev), D ** -0.5 if scale is None else scale,
-        _dense("out", out, torch.bfloat16, B * H * D, dev), _dense("ws", ws, torch.uint8, 1, dev), ws.numel(),
-        _launch_stream(stream, dev))
+        ctypes.byref(shape), ctypes.byref(cache), q.data_ptr(), stride, block_table.data_ptr(), seq_lens.data_ptr(), scale,
+        out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     return _check("lily_kvq_attn_decode", rc) if check else rc
 
 
@@ -506,14 +530,11 @@ def lily_kvq_attn_prefill(shape: lily_kvq_shape, cache: lily_kvq_cache, q, cu_q,
     """Causal attention of a chunk of query tokens per sequence (q, out bf16
     [N][H_q][D], rows by cu_q) over the quantised cache that already holds the
     chunk's keys.  scale defaults to 1/sqrt(D)."""
-    B, H, D, N, i32 = shape.B, shape.H_q, shape.D, q.shape[0], torch.int32
-    dev = _kvq_query(q, H, D, cache)
-    pq, sq = _tokens("q", q, H, D, dev)
+    _need(cu_q is not None, "cu_q: expected a tensor")
+    stream, stride, scale = _kvq_attention(shape, cache, q, cu_q, block_table, seq_lens, out, ws, scale, stream)
     rc = (_lib or load()).lily_kvq_attn_prefill(
-        ctypes.byref(shape), ctypes.byref(cache), pq, sq, N, _dense("cu_q", cu_q, i32, B + 1, dev),
-        _table(block_table, shape, dev), _dense("seq_lens", seq_lens, i32, B, dev),
-        D ** -0.5 if scale is None else scale, _dense("out", out, torch.bfloat16, N * H * D, dev),
-        _dense("ws", ws, torch.uint8, 1, dev), ws.numel(), _launch_stream(stream, dev))
+        ctypes.byref(shape), ctypes.byref(cache), q.data_ptr(), stride, q.shape[0], cu_q.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), scale, out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
     return _check("lily_kvq_attn_prefill", rc) if check else rc
 
 
