@@ -969,7 +969,7 @@ int kvq_attention(const lily_kvq_shape *shape, const lily_kvq_cache *cache, cons
     a.part_acc = at<float>(ws, L.part_acc);
     if (!ragged) return to_status(launch_kvq_decode(a, stream), "quantised-cache attention launch");
     CUtensorMap tmQ;
-    if (!tmap_query(&tmQ, q, N, s.H_q, s.D, q_stride, a.group, kKvqPrefillRows / a.group))
+    if (!tmap_query(&tmQ, q, N, s.H_q, s.D, q_stride, a.group, kvq_prefill_tile_rows(a) / a.group))
         return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled (queries)");
     return to_status(launch_kvq_prefill(a, tmQ, stream), "quantised-cache attention launch");
 }

@@ -47,8 +47,16 @@ constexpr int kChunk = 64;                 // cache tokens per step
 // which the shares of the work list count: an 8K prompt 528 us with 2, 429 with 6, 410
 // with 8, 419 with 12.
 constexpr int kItemCost = 8;
-constexpr int kSoftWarps = 8, kDeqWarps = 8, kMmaWarp = 16, kLoadWarp = 17;
-constexpr int kThreads = (kLoadWarp + 1) * 32;
+// Warps by the quarters NQ of the tile's 128 rows that hold queries: two softmax warps a
+// quarter (a quarter's warps have its index modulo 4, as they reach its lanes of tensor
+// memory), rebuild warps, MMA issuer, query loader.
+template <int NQ>
+struct Roles {
+    static constexpr int soft = 2 * NQ, deq = NQ == 1 ? 16 : 8, mma = soft + deq, load = mma + 1, threads = (load + 1) * 32;
+    __device__ static __forceinline__ bool is_soft(int warp) { return warp < 8 && (warp & 3) < NQ; }
+    __device__ static __forceinline__ int deq_index(int warp) { return NQ == 1 ? (warp < 4 ? warp - 1 : warp - 2) : warp - soft; }
+};
+constexpr int kMaxWarps = Roles<1>::threads / 32;
 constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
 constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
 constexpr int kMaxBufs = 4;                // buffers of K and of V, at most
@@ -59,8 +67,8 @@ struct Fixed {
     uint64_t k_full[kMaxBufs], k_free[kMaxBufs], v_full[kMaxBufs], v_free[kMaxBufs], s_full[2], p_full[2];
     uint64_t pv_done[2], q_full, q_loaded, q_free, o_free, drain;
     uint32_t tmem;
-    int abort, b0, m0, L0;
-    long long pre, per, begin, total, used, sum[kThreads / 32];
+    int abort, b0, m0, L0, q0;
+    long long pre, per, begin, total, used, sum[kMaxWarps];
     float xch[2][2][kRows];  // [chunk parity][half of the columns][row]
 };
 constexpr int kFixed = 4096;
@@ -250,9 +258,8 @@ __device__ __forceinline__ uint64_t join64(uint32_t lo, uint32_t hi)
 }
 
 // ------------------------------------------------------------------ work list
-__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int b)
+__device__ __forceinline__ int length_of(const KvqAttnArgs &a, int L)
 {
-    int L = a.seq_lens[b];
     const int cap = a.max_blocks * a.c.bs;
     if (L < 0 || L > cap) {
         record_error(&a.ctrl->status, kErrDeviceIndex);
@@ -260,10 +267,11 @@ __device__ __forceinline__ int length_of(const KvqAttnArgs &a, int b)
     }
     return L;
 }
-// Query tokens of a sequence (rows outside the call's N are none).
-__device__ __forceinline__ int queries_of(const KvqAttnArgs &a, int b)
+// Query tokens of a sequence from row q0 on (rows outside the call's N are none).
+__device__ __forceinline__ int queries_of(const KvqAttnArgs &a, int b, int &q0)
 {
-    const int q0 = a.cu_q[b], q1 = min(a.cu_q[b + 1], a.N);
+    q0 = a.cu_q[b];
+    const int q1 = min(a.cu_q[b + 1], a.N);
     return q0 < 0 || q1 <= q0 ? 0 : q1 - q0;
 }
 __device__ __forceinline__ int tile_chunks(int m, int L, int t, int TQ)
@@ -305,7 +313,7 @@ __device__ __forceinline__ long long places_before(int m, int L, int t, int TQ)
 
 // A CTA's place in the list: item (b, g, t) from place s0 on, `left` places in all.
 struct Walk {
-    int b, g, t, m, L, s0;
+    int b, g, t, m, L, s0, q0;  // q0: the sequence's first query row
     long long left;
 };
 // Its share of the item: chunks [j0, j0 + n) of nch, `take` places.
@@ -323,70 +331,110 @@ __device__ __forceinline__ Share share_of(const Walk &w, int TQ)
 }
 
 // c of `shares`: which share of the list; TQ: query tokens of an item.
+template <int NT>  // threads of the CTA
 __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int TQ, int c, int shares)
 {
     Walk w{};
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int m = 0, L = 0;
-    long long per = 0, before = 0, all = 0;  // this thread's sequence: places per KV head
-    auto scan = [&](int s0) {
-        m = L = 0;
-        per = 0;
-        if (s0 + tid < a.B && (m = queries_of(a, s0 + tid)) > 0) {
-            L = length_of(a, s0 + tid);
+    long long off, per_head;  // of share c's first place within its sequence; the sequence's places per KV head
+    if (a.B <= 32) {
+        // every warp for itself, a sequence per lane
+        int m = 0, L = 0, q0 = 0;
+        if (lane < a.B) {
+            L = a.seq_lens[lane];
+            m = queries_of(a, lane, q0);
+        }
+        long long per = 0;
+        if (m > 0) {
+            L = length_of(a, L);
             per = places_before(m, L, (m + TQ - 1) / TQ, TQ);
         }
-        const long long n = per * a.c.H_kv;
-        long long inc = n;
+        long long inc = per * a.c.H_kv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long up = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += up;
         }
-        __syncthreads();
-        if (lane == 31) F.sum[warp] = inc;
-        __syncthreads();
-        before = inc - n;
-        all = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < warp) before += F.sum[i];
-            all += F.sum[i];
-        }
-    };
-    long long total = 0;
-    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        scan(s0);
-        total += all;
-    }
-    // no more CTAs than places: every CTA between an item's first and last has a part of it
-    const long long used = min(total, static_cast<long long>(shares));
-    if (c >= used) return w;
-    const long long begin = total * c / used;
-    w.left = total * (c + 1) / used - begin;
-    long long pre = 0;
-    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        if (a.B > kThreads) scan(s0);
-        const long long lo = pre + before;
-        if (begin >= lo && begin < lo + per * a.c.H_kv) {
-            F.b0 = s0 + tid;
-            F.m0 = m;
-            F.L0 = L;
-            F.pre = lo;
-            F.per = per;
+        const long long total = __shfl_sync(0xffffffffu, inc, 31), used = min(total, static_cast<long long>(shares));
+        if (c >= used) return w;
+        const long long begin = total * c / used;
+        w.left = total * (c + 1) / used - begin;
+        w.b = __ffs(__ballot_sync(0xffffffffu, begin < inc)) - 1;
+        w.m = __shfl_sync(0xffffffffu, m, w.b);
+        w.L = __shfl_sync(0xffffffffu, L, w.b);
+        w.q0 = __shfl_sync(0xffffffffu, q0, w.b);
+        per_head = __shfl_sync(0xffffffffu, per, w.b);
+        off = begin - (__shfl_sync(0xffffffffu, inc, w.b) - per_head * a.c.H_kv);
+        if (tid == 0) {
             F.begin = begin;
             F.total = total;
             F.used = used;
         }
-        pre += all;
-        if (begin < pre) break;
+    } else {
+        int m = 0, L = 0, q0 = 0;
+        long long per = 0, before = 0, all = 0;  // this thread's sequence: places per KV head
+        auto scan = [&](int s0) {
+            m = L = 0;
+            per = 0;
+            if (s0 + tid < a.B && (m = queries_of(a, s0 + tid, q0)) > 0) {
+                L = length_of(a, a.seq_lens[s0 + tid]);
+                per = places_before(m, L, (m + TQ - 1) / TQ, TQ);
+            }
+            const long long n = per * a.c.H_kv;
+            long long inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            __syncthreads();
+            if (lane == 31) F.sum[warp] = inc;
+            __syncthreads();
+            before = inc - n;
+            all = 0;
+            for (int i = 0; i < NT / 32; ++i) {
+                if (i < warp) before += F.sum[i];
+                all += F.sum[i];
+            }
+        };
+        long long total = 0;
+        for (int s0 = 0; s0 < a.B; s0 += NT) {
+            scan(s0);
+            total += all;
+        }
+        // no more CTAs than places: every CTA between an item's first and last has a part of it
+        const long long used = min(total, static_cast<long long>(shares));
+        if (c >= used) return w;
+        const long long begin = total * c / used;
+        w.left = total * (c + 1) / used - begin;
+        long long pre = 0;
+        for (int s0 = 0; s0 < a.B; s0 += NT) {
+            if (a.B > NT) scan(s0);
+            const long long lo = pre + before;
+            if (begin >= lo && begin < lo + per * a.c.H_kv) {
+                F.b0 = s0 + tid;
+                F.m0 = m;
+                F.L0 = L;
+                F.q0 = q0;
+                F.pre = lo;
+                F.per = per;
+                F.begin = begin;
+                F.total = total;
+                F.used = used;
+            }
+            pre += all;
+            if (begin < pre) break;
+        }
+        __syncthreads();
+        w.b = F.b0;
+        w.m = F.m0;
+        w.L = F.L0;
+        w.q0 = F.q0;
+        off = begin - F.pre;
+        per_head = F.per;
     }
-    __syncthreads();
-    w.b = F.b0;
-    w.m = F.m0;
-    w.L = F.L0;
-    const long long off = begin - F.pre;
-    w.g = static_cast<int>(off / F.per);
-    const long long r = off % F.per;
+    w.g = static_cast<int>(off / per_head);
+    const long long r = off % per_head;
     // the tile that place r falls into: the last t with places_before(t) <= r, 32 candidates at a time
     int t_lo = 0, t_hi = (w.m + TQ - 1) / TQ;  // places_before(t_lo) <= r < places_before(t_hi)
     while (t_hi - t_lo > 1) {
@@ -412,9 +460,9 @@ __device__ __forceinline__ void advance(const KvqAttnArgs &a, Walk &w, int take,
     if (++w.g < a.c.H_kv) return;
     w.g = 0;
     do {
-        w.m = queries_of(a, ++w.b);
+        w.m = queries_of(a, ++w.b, w.q0);
     } while (w.m == 0 && w.b + 1 < a.B);  // places are still to come, so there is one
-    w.L = length_of(a, w.b);
+    w.L = length_of(a, a.seq_lens[w.b]);
 }
 // From here to an item with chunks for this CTA (only its last item may have none).
 __device__ __forceinline__ bool next_share(const KvqAttnArgs &a, const Walk &w, Share &h, int TQ)
@@ -461,8 +509,8 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
     }
 }
 
-template <int BITS, int GR, int CG>
-__global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a, const __grid_constant__ CUtensorMap tmQ)
+template <int BITS, int GR, int CG, int NQ>
+__global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(const __grid_constant__ KvqAttnArgs a, const __grid_constant__ CUtensorMap tmQ)
 {
     constexpr int D = 64 * GR, GB = 8 * BITS;
     extern __shared__ uint8_t dsm_raw[];
@@ -473,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     const uint32_t k_smem = smem_u32(base) + kFixed, v_smem = k_smem + kBufs * BB, q_smem = v_smem + kBufs * BB;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = CG == 1 ? 0 : static_cast<int>(cluster_rank()), share = blockIdx.x / CG;
-    const int G = a.group, TQ = kRows / G, TI = CG * TQ;  // query tokens of this CTA's 128 rows, of an item
+    using R = Roles<NQ>;
+    const int G = a.group, TQ = 32 * NQ / G, TI = CG * TQ;  // query tokens of this CTA's rows, of an item
     int *status = &a.ctrl->status;
 
     if (threadIdx.x == 0) {
@@ -485,18 +534,18 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&F.s_full[i], 1);
-            mbar_init(&F.p_full[i], CG * kSoftWarps);
+            mbar_init(&F.p_full[i], CG * R::soft);
             mbar_init(&F.pv_done[i], 1);
         }
-        mbar_init(&F.q_full, CG * kSoftWarps);
+        mbar_init(&F.q_full, CG * R::soft);
         mbar_init(&F.q_loaded, 1);
-        mbar_init(&F.q_free, kSoftWarps);
-        mbar_init(&F.o_free, CG * kSoftWarps);
+        mbar_init(&F.q_free, R::soft);
+        mbar_init(&F.o_free, CG * R::soft);
         mbar_init(&F.drain, 1);
         F.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) alloc_tmem<CG>(&F.tmem);
+    if (warp == R::mma) alloc_tmem<CG>(&F.tmem);
     tc_fence_before();
     pair_sync<CG>();
     tc_fence_after();
@@ -504,10 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     pdl_trigger();
     pdl_wait();
     const uint32_t tmem = F.tmem;
-    Walk w = first_item(a, F, TI, share, kKvqPrefillCtas / CG);
+    Walk w = first_item<R::threads>(a, F, TI, share, kKvqPrefillCtas / CG);
     bool ok = true;
 
-    if (warp < kSoftWarps) {
+    if (R::is_soft(warp)) {
         // ------------------------------------------------ two threads per query row
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -658,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
                 named_barrier_sync(kBarPair + quarter, 64);
                 const bool seen = l_run > 0.0f;  // a row that saw nothing has zeros
                 const float r = seen ? 1.0f / l_run : 0.0f;
-                const long long n = a.cu_q[w.b] + tq;
+                const long long n = w.q0 + tq;
                 uint16_t *dst = a.out + (n * a.H_q + head) * D;
                 float *pdst = a.part_acc + part_row * D;
 #pragma unroll 1
@@ -696,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             if (threadIdx.x == 0 && rank == 0 && starts && !ends) {
                 // who joins the parts of an item that starts here and goes on: up to the CTA with its last place
                 const long long last = ((F.begin + done - w.s0 + h.nch + kItemCost) * F.used - 1) / F.total;
-                a.meta[share] = make_int4(a.cu_q[w.b] + w.t * TI, w.g, w.m - w.t * TI, static_cast<int>(last));
+                a.meta[share] = make_int4(w.q0 + w.t * TI, w.g, w.m - w.t * TI, static_cast<int>(last));
                 mine = 0;
             }
             done += h.take;
@@ -706,13 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             more = more2;
         }
         if (threadIdx.x == 0 && rank == 0 && mine) a.meta[share] = make_int4(-1, 0, 0, 0);
-    } else if (warp < kSoftWarps + kDeqWarps) {
+    } else if (warp < R::soft + R::deq) {
         // ------------------------------------------------ K and V of the chunks into shared memory
         // The chunk's (K or V, group, 32 tokens) are dealt to the warps: one each (two for one CTA with D = 256);
         // with fewer of them than warps, the warps take chunks in turn.  Of a pair, this CTA has half of the
         // chunk's tokens of K, and half of the groups of V.
-        constexpr int kItems = 2 * NK > kDeqWarps ? 2 * NK / kDeqWarps : 1, kWarps = 2 * NK / kItems, kTurns = kDeqWarps / kWarps;
-        const int dw = (warp - kSoftWarps) % kWarps, turn = (warp - kSoftWarps) / kWarps;
+        constexpr int kItems = 2 * NK > R::deq ? 2 * NK / R::deq : 1, kWarps = 2 * NK / kItems, kTurns = R::deq / kWarps;
+        const int dw = R::deq_index(warp) % kWarps, turn = R::deq_index(warp) / kWarps;
         struct Item {
             uint32_t addr;  // this lane's row of the group in buffer 0
             int row, group, half;
@@ -788,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
             it += h.n;
             advance(a, w, h.take, TI);
         }
-    } else if (warp == kLoadWarp) {
+    } else if (warp == R::load) {
         // ------------------------------------------------ q of the items, one ahead
         if (lane == 0) {
             prefetch_tmap(&tmQ);
@@ -800,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
 #pragma unroll
                 for (int c = 0; c < GR; ++c)
                     tma_load_3d(base + kFixed + 2 * kBufs * BB + c * kQBox, &tmQ, &F.q_loaded, c * 64, w.g * G,
-                                a.cu_q[w.b] + w.t * TI + rank * TQ);
+                                w.q0 + w.t * TI + rank * TQ);
                 ++items;
                 advance(a, w, h.take, TI);
             }
@@ -888,7 +937,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_prefill_kernel(const __grid_c
     __syncwarp();
     pair_sync<CG>();
     tc_fence_after();
-    if (warp == kMmaWarp) free_tmem<CG>(tmem);
+    if (warp == R::mma) free_tmem<CG>(tmem);
 }
 
 // Joins the parts of an item that was cut: CTA (first share of the item, four rows, every
@@ -958,6 +1007,7 @@ __global__ void __launch_bounds__(256, CG == 2 ? 8 : 2) kvq_prefill_join_kernel(
 // fourth part each, joined through shared memory in a fixed order.  16 tokens on 32,768: 35 us
 // for the call, 45 with the kernel above (which is the faster where items are many: a prompt of
 // 8,192 tokens 396 us, 402 with the list).
+template <int NQ>
 __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __grid_constant__ KvqAttnArgs a)
 {
     constexpr int kBatch = 8, kShares = kKvqPrefillCtas;
@@ -966,7 +1016,7 @@ __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __gr
     __shared__ float4 part[4][64];
     __shared__ float2 part_ml[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d4 = tid % 64, slot0 = tid / 64;
-    const int G = a.group, TQ = kRows / G;
+    const int G = a.group, TQ = 32 * NQ / G;
     pdl_trigger();
     pdl_wait();
     const int4 mine = tid < kShares ? a.meta[tid] : make_int4(-1, 0, 0, 0);
@@ -1056,11 +1106,11 @@ __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __gr
     }
 }
 
-template <int BITS, int GR, int CG>
+template <int BITS, int GR, int CG, int NQ>
 cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaStream_t stream)
 {
     constexpr int smem = smem_bytes(GR, CG);
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG>), smem);
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG, NQ>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1070,13 +1120,13 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaS
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(kKvqPrefillCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Roles<NQ>::threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG>, a, tmQ)) != cudaSuccess) return e;
-    if (few) return launch_pdl(kvq_prefill_join_few_kernel, dim3(4 * kKvqPrefillCtas), dim3(256), 0, stream, a);
+    if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG, NQ>, a, tmQ)) != cudaSuccess) return e;
+    if (few) return launch_pdl(kvq_prefill_join_few_kernel<NQ>, dim3(4 * kKvqPrefillCtas), dim3(256), 0, stream, a);
     return launch_pdl(kvq_prefill_join_kernel<CG>, dim3(kKvqPrefillCtas / CG, CG == 1 ? 16 : 64), dim3(256), 0, stream, a);
 }
 
@@ -1084,16 +1134,24 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaS
 // do not split) and where no sequence need have more query tokens than one CTA's 128
 // rows hold: a pair's second half would idle (eight drafts of four tokens: 28 us against
 // 34; prompts and chunks of 1,024 tokens and more are 1.15 to 1.25 times as fast with pairs).
+// Where 32 rows hold them, a tile has 32 rows and the other quarters' warps rebuild.
+bool few_queries(const KvqAttnArgs &a, int rows) { return a.N <= static_cast<long long>(a.B) * (rows / a.group); }
+template <int BITS, int GR>
+cudaError_t launch_rows(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
+{
+    if (few_queries(a, 32)) return launch<BITS, GR, 1, 1>(a, tmQ, true, stream);
+    if (GR == 1 || few_queries(a, kRows)) return launch<BITS, GR, 1, 4>(a, tmQ, few_queries(a, kRows), stream);
+    return launch<BITS, GR, GR == 1 ? 1 : 2, 4>(a, tmQ, false, stream);
+}
 template <int BITS>
 cudaError_t launch_d(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    const bool few = a.N <= static_cast<long long>(a.B) * (kRows / a.group);
-    if (a.D == 64) return launch<BITS, 1, 1>(a, tmQ, few, stream);
-    if (few) return a.D == 128 ? launch<BITS, 2, 1>(a, tmQ, few, stream) : launch<BITS, 4, 1>(a, tmQ, few, stream);
-    return a.D == 128 ? launch<BITS, 2, 2>(a, tmQ, few, stream) : launch<BITS, 4, 2>(a, tmQ, few, stream);
+    return a.D == 64 ? launch_rows<BITS, 1>(a, tmQ, stream) : a.D == 128 ? launch_rows<BITS, 2>(a, tmQ, stream) : launch_rows<BITS, 4>(a, tmQ, stream);
 }
 
 }  // namespace
+
+int kvq_prefill_tile_rows(const KvqAttnArgs &a) { return few_queries(a, 32) ? 32 : kRows; }
 
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {

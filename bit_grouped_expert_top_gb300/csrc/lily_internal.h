@@ -231,7 +231,9 @@ constexpr int kKvqMaxGroup = 8;      // query heads per KV head
 constexpr int kKvqDecodeCtas = 152, kKvqPrefillCtas = 152;
 constexpr int kKvqPrefillRows = 128;
 cudaError_t launch_kvq_decode(const KvqAttnArgs &a, cudaStream_t stream);
-// tmQ: q as 3-D bf16 [N][H_q][D], box 64 channels x the group's heads x 128 / group tokens, 128-byte swizzle.
+// Query rows (heads x tokens) of a CTA in this prefill call.
+int kvq_prefill_tile_rows(const KvqAttnArgs &a);
+// tmQ: q as 3-D bf16 [N][H_q][D], box 64 channels x the group's heads x rows / group tokens, 128-byte swizzle.
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream);
 
 // Gated DeltaNet scan (gdn.cu): CTA (16-row slice of the state, value head).
