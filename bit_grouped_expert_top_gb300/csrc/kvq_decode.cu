@@ -66,12 +66,14 @@ constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
 
 __host__ __device__ constexpr int merge_row(int D) { return D + 8; }  // floats of a head's row in the join buffer, padded
 __host__ __device__ constexpr int merge_bytes(int D) { return kNW * 8 * merge_row(D) * 4; }
-constexpr int stage_bytes(int D, int bs, int bits) { return 2 * (bs * D * bits / 8 + bs * (D / 64) * 4); }
-int stages_for(int D, int bs, int bits)
+__host__ __device__ constexpr int stage_bytes(int D, int bs, int bits) { return 2 * (bs * D * bits / 8 + bs * (D / 64) * 4); }
+__host__ __device__ constexpr int stages_for(int D, int bs, int bits)
 {
     const int n = (kSmemLimit - kFixed - merge_bytes(D)) / stage_bytes(D, bs, bits);
     return n < kMaxStages ? n : kMaxStages;
 }
+// Tokens that a warp takes at a time: one or two halves of 16.
+__host__ __device__ constexpr int unit_of(int D) { return D == 256 ? 16 : 32; }
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
@@ -303,7 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
     float *merge = reinterpret_cast<float *>(base + kFixed);  // [warp][head][merge_row]
     uint8_t *ring = base + kFixed + merge_bytes(D);
     constexpr int CB = GR * bs * GB, PB = GR * bs * 4, SB = 2 * (CB + PB);  // codes, parameters, stage
-    constexpr int IH = GR == 4 ? 1 : 2, kUnit = 16 * IH;  // a warp takes one or two halves of 16 tokens at a time
+    constexpr int kUnit = unit_of(D), IH = kUnit / 16;
+    // a warp's next unit is kNW units on: no further than the ring's length, so that when its stage has been issued, the
+    // slot's last turn but one is over (the producers have waited for it)
+    static_assert((kNW + bs / kUnit - 1) / (bs / kUnit) <= stages_for(D, bs, BITS), "ring too short");
     const int NS = a.stages, G = a.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gi = lane >> 2, t = lane & 3;
     int *status = &a.ctrl->status;
@@ -454,7 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
 
         for (int u = first; u < units; u += kNW) {
             const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
-            ok = ok && mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
+            // A warp meets a slot only in some of its turns, and copies land in any order: the slot's last turn has to be
+            // over first, or `full` of the turn before, still open, has the parity of this one done.
+            ok = ok && (turn == 0 || mbar_wait(&F.empty[slot], (turn - 1) & 1, &F.abort, status)) &&
+                 mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const uint8_t *kq = ring + static_cast<size_t>(slot) * SB, *kp = kq + CB, *vq = kp + PB, *vp = vq + CB;

@@ -720,3 +720,22 @@ def test_sequences_that_share_blocks():
     both = _decode(c, q=q)
     assert torch.equal(both[0], both[1]) and torch.equal(both[0], alone[0])
     assert c.status() == 0
+
+
+@pytest.mark.parametrize("D,bits,bs", [(256, 8, 64), (256, 8, 128), (256, 4, 64), (128, 8, 128), (128, 4, 64)])
+def test_decode_of_fresh_memory(D, bits, bs):
+    # blocks of memory that the GPU has not touched lately arrive in any order: every call gives the same bits
+    cfg = _cfg((20000, 9000), D=D, bits=bits, block_size=bs, seed=73)
+    c = Cache(cfg).to_gpu()
+    want = _decode(c)
+    host = {k: t.cpu() for k, t in c.t.items()}
+    for i in range(6):
+        c.t = c.handle = None
+        torch.cuda.empty_cache()
+        pad = torch.empty((i + 1) << 22, dtype=torch.uint8, device="cuda")
+        c.t = {k: t.cuda() for k, t in host.items()}
+        c.handle = lm.make_kvq_cache(c.t)
+        torch.cuda.synchronize()
+        assert torch.equal(_decode(c), want)
+        del pad
+    assert c.status() == 0
