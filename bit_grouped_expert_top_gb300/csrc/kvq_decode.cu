@@ -48,9 +48,10 @@
 namespace lily {
 namespace {
 
-// Consumer warps: 6, 8 or 10 take 25.6, 25.7 or 24.8 us for a sequence of 131,072 tokens
-// and 14.2, 14.8 or 14.8 for one of 32,768; 14 are slower (registers).
-constexpr int kNW = 10;
+// Consumer warps: 8 or 10 take 23.5 or 23.8 us for a sequence of 131,072 tokens (2 KV heads of
+// 256), 13.7 or 14.1 for 24 short ones (4 heads of 128, 8 bits); eight long ones with 8 heads of
+// 128 69.8 or 67.1.  6 are slower on long caches, 14 everywhere (registers).
+constexpr int kNW = 8;
 constexpr int kThreads = (kNW + 2) * 32;      // + the producers of K and of V
 constexpr int kMaxStages = 14;                // segments in flight <= stages < named barriers
 constexpr int kSmemLimit = 227 * 1024;
@@ -296,8 +297,9 @@ __device__ __forceinline__ void join_column(const KvqAttnArgs &a, const Fixed &F
     }
 }
 
+// (One warp more in the launch bound than there are: the same 168 registers without 48 bytes of spills.)
 template <int BITS, int GR, int bs>
-__global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
+__global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
 {
     constexpr int D = GR * 64, GB = 8 * BITS;  // bytes of a group's codes in one row
     extern __shared__ __align__(128) uint8_t base[];
@@ -461,10 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1) kvq_decode_kernel(const __grid_co
             const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
             // A warp meets a slot only in some of its turns, and copies land in any order: the slot's last turn has to be
             // over first, or `full` of the turn before, still open, has the parity of this one done.
-            ok = ok && (turn == 0 || mbar_wait(&F.empty[slot], (turn - 1) & 1, &F.abort, status)) &&
-                 mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            // Both are looked at in this order, without waiting in between.
+            const uint32_t over = turn == 0 ? 1u : phase_done(&F.empty[slot], (turn - 1) & 1), here = phase_done(&F.full[slot], turn & 1);
+            if (!ok || !__all_sync(0xffffffffu, over & here)) {
+                ok = ok && (turn == 0 || mbar_wait(&F.empty[slot], (turn - 1) & 1, &F.abort, status)) &&
+                     mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
             const uint8_t *kq = ring + static_cast<size_t>(slot) * SB, *kp = kq + CB, *vq = kp + PB, *vp = vq + CB;
             const int left = w.L - (tok0 + u * kUnit);  // tokens of this unit that exist (may be <= 0, or more than 32)
             const int row = r0 + token_of(gi);          // + 16 i + 8 h: this lane's token rows of S^T
@@ -824,10 +830,10 @@ cudaError_t launch_d(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 // A CTA for each segment, and no join, where no CTA then has much more than an even share
 // of a full cache: with n segments on 152 CTAs, where capacity (1 - n / 152) is at most 640
 // tokens, which cost what cutting and joining does.  Measured, one CTA each against cut (2
-// KV heads of 256): one sequence of 256 tokens 7.1 / 8.0 us, of 512 9.2 / 8.3, of 1,024
-// 12.8 / 8.5; 64 sequences of 1,024 14.5 / 22.3.  (4 heads of 128: 512 tokens 6.1 / 6.7,
-// 64 sequences of 256 7.7 / 11.3 with 128 segments.)  Above 1,024 tokens the lengths of a
-// batch can differ too much from its capacity.
+// KV heads of 256): one sequence of 256 tokens 6.2 / 7.9 us, of 512 8.2 / 7.9, of 1,024
+// 11.8 / 8.1; 64 sequences of 1,024 13.9 / 21.0.  (4 heads of 128: one of 512 tokens 5.6 /
+// 6.6, 16 of 256 4.6 / 7.5.)  Above 1,024 tokens the lengths of a batch can differ too much
+// from its capacity.
 bool one_cta_each(long long segments, long long capacity)
 {
     return segments <= kKvqDecodeCtas && capacity <= 1024 && capacity * (kKvqDecodeCtas - segments) <= 640LL * kKvqDecodeCtas;
