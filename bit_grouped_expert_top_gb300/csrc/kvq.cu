@@ -22,7 +22,7 @@
 // tokens gain nothing and keep four, and so does the read (31.7 us, five 32.8, six 48.4).
 #include <cstdint>
 
-#include "lily_device.cuh"
+#include "kvq_device.cuh"
 #include "lily_internal.h"
 
 namespace lily {

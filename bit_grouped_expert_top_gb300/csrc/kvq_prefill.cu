@@ -35,7 +35,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "lily_device.cuh"
+#include "kvq_device.cuh"
 #include "lily_internal.h"
 
 namespace lily {
@@ -100,20 +100,6 @@ __device__ __forceinline__ constexpr int unpacked(int p)
     return BITS == 4 ? (p < 4 ? 2 * p : 2 * (p - 4) + 1) : (p & 4) + ((p & 3) == 0 ? 0 : (p & 3) == 1 ? 2 : (p & 3) == 2 ? 1 : 3);
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");

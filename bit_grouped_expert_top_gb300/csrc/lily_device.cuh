@@ -181,71 +181,12 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// two fp32 values in one register pair
-__device__ __forceinline__ unsigned long long pair(float x, float y)
-{
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void unpair(unsigned long long v, float &x, float &y)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigned long long y, unsigned long long z)
-{
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigned long long y)
-{
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long x, unsigned long long y)
-{
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-
 // Named barrier over `nthreads` threads (whole warps); the warp is reconverged
 // first, as bar.sync is warp-aligned.
 __device__ __forceinline__ void named_barrier_sync(int id, int nthreads)
 {
     __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-// Whether a phase is complete, without waiting.
-__device__ __forceinline__ uint32_t phase_done(uint64_t *bar, uint32_t parity)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return r;
-}
-
-// A whole warp waits.  Every lane does: what the barrier guards is read by every lane,
-// and a shuffle of one lane's result orders no memory access.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
 }
 
 // ----------------------------------------------------------------- tcgen05 (UMMA + TMEM)
