@@ -47,6 +47,12 @@ constexpr int kChunk = 64;                 // cache tokens per step
 // which the shares of the work list count: an 8K prompt 528 us with 2, 429 with 6, 410
 // with 8, 419 with 12.
 constexpr int kItemCost = 8;
+// Cutting an item costs about sixteen chunks (its parts, their join): where there are no more
+// items than shares, and the longest is not longer by more than that than an even share, each
+// share is an item.  A prompt of 1,024 tokens 43 us cut, 35 with items; of 512 33 and 28.
+// (With a limit of 8 chunks as if cut; with 32, four tokens each on four contexts of 1,000
+// take 30 us instead of 21.)
+constexpr int kUncut = 16;
 // Warps by the quarters NQ of the tile's 128 rows that hold queries: two softmax warps a
 // quarter (a quarter's warps have its index modulo 4, as they reach its lanes of tensor
 // memory), rebuild warps, MMA issuer, query loader.
@@ -342,6 +348,29 @@ __device__ __forceinline__ Walk first_item(const KvqAttnArgs &a, Fixed &F, int T
             if (lane >= o) inc += up;
         }
         const long long total = __shfl_sync(0xffffffffu, inc, 31), used = min(total, static_cast<long long>(shares));
+        // an item for each share, where the longest is not much more than an even share
+        const int tiles = (m + TQ - 1) / TQ;
+        const int longest = __reduce_max_sync(0xffffffffu, m > 0 ? tile_chunks(m, L, tiles - 1, TQ) + kItemCost : 0);
+        const int mine = static_cast<int>(min(static_cast<long long>(tiles) * a.c.H_kv, 4096LL));
+        if (static_cast<int>(__reduce_add_sync(0xffffffffu, mine)) <= shares && longest <= total / shares + kUncut) {
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += up;
+            }
+            const uint32_t in = __ballot_sync(0xffffffffu, c < upto);
+            if (in == 0) return w;
+            w.b = __ffs(in) - 1;
+            w.m = __shfl_sync(0xffffffffu, m, w.b);
+            w.L = __shfl_sync(0xffffffffu, L, w.b);
+            w.q0 = __shfl_sync(0xffffffffu, q0, w.b);
+            const int i = c - __shfl_sync(0xffffffffu, upto - mine, w.b), n = (w.m + TQ - 1) / TQ;
+            w.g = i / n;
+            w.t = i % n;
+            w.left = tile_chunks(w.m, w.L, w.t, TQ) + kItemCost;
+            return w;
+        }
         if (c >= used) return w;
         const long long begin = total * c / used;
         w.left = total * (c + 1) / used - begin;
@@ -986,17 +1015,17 @@ __global__ void __launch_bounds__(256, CG == 2 ? 8 : 2) kvq_prefill_join_kernel(
     }
 }
 
-// The same for calls of few query tokens (one CTA an item), whose items are few and have up to
-// 152 parts: the query rows of all of them are one list that the CTAs go through, found by
+// The same where items are few (no more than shares) and may have up to 152 parts or not be cut
+// at all: the query rows of the cut ones are one list that the CTAs go through, found by
 // a scan over the shares' entries.  64 threads take a row; where an item has more parts than
 // a thread has loads in flight, a CTA takes one row and its four groups of 64 threads every
 // fourth part each, joined through shared memory in a fixed order.  16 tokens on 32,768: 35 us
 // for the call, 45 with the kernel above (which is the faster where items are many: a prompt of
 // 8,192 tokens 396 us, 402 with the list).
-template <int NQ>
+template <int CG, int NQ>
 __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __grid_constant__ KvqAttnArgs a)
 {
-    constexpr int kBatch = 8, kShares = kKvqPrefillCtas;
+    constexpr int kBatch = 8, kShares = kKvqPrefillCtas / CG;
     __shared__ int4 metas[kShares];
     __shared__ int upto[kShares], warp_sum[8];  // units of the shares up to this one
     __shared__ float4 part[4][64];
@@ -1006,7 +1035,7 @@ __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __gr
     pdl_trigger();
     pdl_wait();
     const int4 mine = tid < kShares ? a.meta[tid] : make_int4(-1, 0, 0, 0);
-    const int rows = mine.x >= 0 ? min(mine.z, TQ) * G : 0;
+    const int rows = mine.x >= 0 ? min(mine.z, CG * TQ) * G : 0;
     const bool by_row = __syncthreads_or(mine.x >= 0 && mine.w - tid + 1 > kBatch);
     int inc = by_row ? rows : (rows + 3) / 4;
 #pragma unroll
@@ -1036,8 +1065,9 @@ __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __gr
         c0 = last;
         const int4 meta = metas[c0];
         const int S = meta.w - c0 + 1, i = by_row ? local : local * 4 + slot0, tq = i / G, h = i % G;  // query token, head
-        const bool valid = tq < min(meta.z, TQ) && d4 * 4 < a.D;
-        auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * kRows + i; };
+        const bool valid = tq < min(meta.z, CG * TQ) && d4 * 4 < a.D;
+        const int row = tq / TQ * kRows + tq % TQ * G + h;
+        auto slot = [&](int s) { return static_cast<size_t>(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * (CG * kRows) + row; };
         float M = kNoMax, den = 0.0f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float e, float l, const float4 &x) {
@@ -1092,8 +1122,11 @@ __global__ void __launch_bounds__(256, 2) kvq_prefill_join_few_kernel(const __gr
     }
 }
 
+// Whether no sequence need have more query tokens than `rows` rows hold.
+bool few_queries(const KvqAttnArgs &a, int rows) { return a.N <= static_cast<long long>(a.B) * (rows / a.group); }
+
 template <int BITS, int GR, int CG, int NQ>
-cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaStream_t stream)
+cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
     constexpr int smem = smem_bytes(GR, CG);
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_prefill_kernel<BITS, GR, CG, NQ>), smem);
@@ -1112,7 +1145,9 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaS
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if ((e = cudaLaunchKernelEx(&cfg, kvq_prefill_kernel<BITS, GR, CG, NQ>, a, tmQ)) != cudaSuccess) return e;
-    if (few) return launch_pdl(kvq_prefill_join_few_kernel<NQ>, dim3(4 * kKvqPrefillCtas), dim3(256), 0, stream, a);
+    const long long items = (a.N / (CG * (32 * NQ / a.group)) + static_cast<long long>(a.B)) * a.c.H_kv;  // at most
+    if (few_queries(a, kRows) || items <= kKvqPrefillCtas / CG)
+        return launch_pdl(kvq_prefill_join_few_kernel<CG, NQ>, dim3(4 * kKvqPrefillCtas), dim3(256), 0, stream, a);
     return launch_pdl(kvq_prefill_join_kernel<CG>, dim3(kKvqPrefillCtas / CG, CG == 1 ? 16 : 64), dim3(256), 0, stream, a);
 }
 
@@ -1121,13 +1156,12 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, bool few, cudaS
 // rows hold: a pair's second half would idle (eight drafts of four tokens: 28 us against
 // 34; prompts and chunks of 1,024 tokens and more are 1.15 to 1.25 times as fast with pairs).
 // Where 32 rows hold them, a tile has 32 rows and the other quarters' warps rebuild.
-bool few_queries(const KvqAttnArgs &a, int rows) { return a.N <= static_cast<long long>(a.B) * (rows / a.group); }
 template <int BITS, int GR>
 cudaError_t launch_rows(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
-    if (few_queries(a, 32)) return launch<BITS, GR, 1, 1>(a, tmQ, true, stream);
-    if (GR == 1 || few_queries(a, kRows)) return launch<BITS, GR, 1, 4>(a, tmQ, few_queries(a, kRows), stream);
-    return launch<BITS, GR, GR == 1 ? 1 : 2, 4>(a, tmQ, false, stream);
+    if (few_queries(a, 32)) return launch<BITS, GR, 1, 1>(a, tmQ, stream);
+    if (GR == 1 || few_queries(a, kRows)) return launch<BITS, GR, 1, 4>(a, tmQ, stream);
+    return launch<BITS, GR, GR == 1 ? 1 : 2, 4>(a, tmQ, stream);
 }
 template <int BITS>
 cudaError_t launch_d(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)

@@ -412,6 +412,15 @@ def test_prefill_of_few_tokens_on_long_contexts(lens, new, D, bits):
     assert torch.equal(out, _prefill(c))
 
 
+@pytest.mark.parametrize("D,H_q,H_kv", [(64, 8, 2), (128, 16, 4), (256, 16, 2)])
+@pytest.mark.parametrize("lens,new", [((1000,), None), ((1700,), None), ((700, 300, 0, 61), None), ((2500, 900), (300, 40)), ((40,) * 33, None)])
+def test_prefill_of_short_prompts(lens, new, D, H_q, H_kv):
+    # items that are whole for a share, and cut ones; more sequences than a warp has lanes
+    cfg = KvqConfig("short", lens=lens, new=new, D=D, H_q=H_q, H_kv=H_kv, block_size=32, seed=74 + D)
+    c, out = _check_prefill(cfg, poison=True, rows=np.arange(0, 2500, 23))
+    assert torch.equal(out, _prefill(c))
+
+
 def test_prefill_of_one_token_equals_decode():
     cfg = KvqConfig("one", lens=(800, 90, 1), new=(1, 1, 1), seed=57)
     c = Cache(cfg, n_query=3).to_gpu()
