@@ -12,14 +12,15 @@
 // Bound: HBM (2 + 0.5625 bytes a value at 4 bits, 2 + 1.0625 at 8).  A warp takes
 // four consecutive tokens of one (K or V, head, group): eight threads a token, eight
 // channels each, so that it reads whole 128-byte lines of the bf16 side and touches
-// one 128-byte run of codes; four such steps are in flight per thread.  The extremes
-// are three butterfly shuffles of one packed register (lo, -hi).  Measured (2 KV heads
-// of 256): 65,536 tokens at 4 bits read in 31.7 us (5.4 TB/s, 0.80 of the measured copy
+// one 128-byte run of codes; several such steps are in flight per thread (append 3, read 8).
+// The extremes are three butterfly shuffles of one packed register (lo, -hi).  Measured (2 KV
+// heads of 256): 65,536 tokens at 4 bits read in 31.7 us (5.4 TB/s, 0.80 of the measured copy
 // rate; writes are 78% of the bytes); with 4 heads of 128 at 8 bits, 63,251 tokens
-// written and read back in 74.1 us (5.4 TB/s).  The append is bound by issue, so its
-// arithmetic takes two values an instruction (10,754 tokens 17.3 us without, 16.5 with), and five
-// CTAs an SM (48 registers, some spilled) are better than four (18.0) or six (19.1); few
-// tokens gain nothing and keep four, and so does the read (31.7 us, five 32.8, six 48.4).
+// written and read back in 74.1 us (5.4 TB/s).  The append is near its issue limit, so its
+// arithmetic takes two values an instruction (10,754 tokens written and read 17.3 us without,
+// 16.5 with), and its first loads are issued before the tokens' rows are known (four tokens 4.4 ->
+// 4.2 us).  Four groups in flight spill at five CTAs an SM (16.5 us, 17.9 at four) where
+// three take 16.1 at four; the read with five CTAs takes 32.8 us, with six 48.4.
 #include <cstdint>
 
 #include "kvq_device.cuh"
@@ -163,8 +164,9 @@ struct Place {
 
 // The CTA's 4 QUADS tokens from blockIdx.x 4 QUADS on.  Half of the warps take K,
 // half V; fn(place, group) runs for every group of the warp's four tokens, kBatch at a
-// time: `load` for all of a batch, then `use` (by the whole warp).
-template <int BITS, int QUADS, int kBatch, typename T, typename Load, typename Use>
+// time: `load` for all of a batch, then `use` (by the whole warp).  kEarly: `load` needs
+// only p.row, so the first batch is on its way while the tokens' cache rows are looked up.
+template <int BITS, int QUADS, int kBatch, bool kEarly, typename T, typename Load, typename Use>
 __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &load, const Use &use)
 {
     __shared__ int2 slots[4 * QUADS];
@@ -174,29 +176,36 @@ __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &loa
     if (shared) {
         if (t <= a.B) cu_s[t] = a.cu[t];
         if (t < a.B) starts_s[t] = a.starts[t];
-        __syncthreads();
     }
-    if (t < 4 * QUADS)
-        slots[t] = n0 + t >= a.N ? make_int2(-1, 0) : shared ? token_slot(a, cu_s, starts_s, n0 + t) : token_slot(a, a.cu, a.starts, n0 + t);
-    __syncthreads();
-    const int warp = threadIdx.x / 32, e = threadIdx.x % 8, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8;
-    const int2 slot = slots[tok];
+    constexpr int kStep = kThreads / 32 / QUADS / 2;
+    const int warp = threadIdx.x / 32, e = threadIdx.x % 8, tok = (warp % QUADS) * 4 + (threadIdx.x % 32) / 8, first = warp / QUADS / 2;
     const long long n = n0 + tok;
     const bool isv = (warp / QUADS) & 1;
     Place p;
-    p.act = slot.x >= 0;
     p.bs = a.c.bs;
     p.groups = a.c.H_kv * a.c.groups;
     p.row = (isv ? a.v + n * a.v_stride : a.k + n * a.k_stride) + e * 8;
-    const long long at = p.act ? static_cast<long long>(slot.x) * p.groups * p.bs + slot.y : 0;
-    p.codes = (isv ? a.c.v_q : a.c.k_q) + at * (8 * BITS) + e * BITS;
-    p.params = (isv ? a.c.v_sb : a.c.k_sb) + at * 2;
-    constexpr int kStep = kThreads / 32 / QUADS / 2;
-    for (int g0 = warp / QUADS / 2; g0 < p.groups; g0 += kStep * kBatch) {
-        T v[kBatch];
+    T v[kBatch];
+    auto load_batch = [&](int g0) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (p.act && g0 + i * kStep < p.groups) v[i] = load(p, g0 + i * kStep);
+    };
+    if (kEarly) {
+        p.act = n < a.N;
+        load_batch(first);
+    }
+    if (shared) __syncthreads();
+    if (t < 4 * QUADS)
+        slots[t] = n0 + t >= a.N ? make_int2(-1, 0) : shared ? token_slot(a, cu_s, starts_s, n0 + t) : token_slot(a, a.cu, a.starts, n0 + t);
+    __syncthreads();
+    const int2 slot = slots[tok];
+    p.act = slot.x >= 0;
+    const long long at = p.act ? static_cast<long long>(slot.x) * p.groups * p.bs + slot.y : 0;
+    p.codes = (isv ? a.c.v_q : a.c.k_q) + at * (8 * BITS) + e * BITS;
+    p.params = (isv ? a.c.v_sb : a.c.k_sb) + at * 2;
+    for (int g0 = first; g0 < p.groups; g0 += kStep * kBatch) {
+        if (!kEarly || g0 != first) load_batch(g0);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (g0 + i * kStep < p.groups) use(p, g0 + i * kStep, v[i]);
@@ -204,11 +213,11 @@ __device__ __forceinline__ void for_tokens(const KvqCopyArgs &a, const Load &loa
 }
 
 template <int BITS, int QUADS>
-__global__ void __launch_bounds__(kThreads, QUADS == 1 ? 4 : 5) kvq_append_kernel(const __grid_constant__ KvqCopyArgs a)
+__global__ void __launch_bounds__(kThreads, 4) kvq_append_kernel(const __grid_constant__ KvqCopyArgs a)
 {
     pdl_trigger();
     pdl_wait();
-    for_tokens<BITS, QUADS, 4, uint4>(
+    for_tokens<BITS, QUADS, 3, true, uint4>(
         a, [](const Place &p, int g) { return *reinterpret_cast<const uint4 *>(p.row + g * 64); },
         [](const Place &p, int g, const uint4 &w) {
             const uint32_t lo2 = bf16x2_min(bf16x2_min(w.x, w.y), bf16x2_min(w.z, w.w));
@@ -238,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) kvq_read_kernel(const __grid_cons
         uint2 q;
         uint32_t sb;
     };
-    for_tokens<BITS, QUADS, 8, Codes>(
+    for_tokens<BITS, QUADS, 8, false, Codes>(
         a,
         [](const Place &p, int g) {
             const uint8_t *src = p.codes + g * p.bs * (8 * BITS);

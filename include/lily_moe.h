@@ -379,7 +379,7 @@ size_t lily_kvq_workspace_bytes(const lily_kvq_shape *shape, int32_t n_query);
  *               (so k and v may be slices of a fused projection's output)
  *   cu_new      int32 [B+1] device, ascending from 0: the tokens of sequence b
  *               are rows [cu_new[b], cu_new[b+1]); rows from cu_new[B] on are
- *               padding, neither read nor written
+ *               padding: whatever they hold, nothing is written for them
  *   starts      int32 [B] device: position of each sequence's first new token
  * No two tokens of a call may go to the same cache row.  N = 0 enqueues nothing.
  */
