@@ -12,7 +12,8 @@
 // share evenly (a long prompt's later tiles have more of them); an item cut between pairs
 // leaves partial results that a second kernel joins.
 // Per CTA, with every wait bounded:
-//   warps 0..7   two threads per query row (32 of a chunk's 64 tokens each): q into
+//   warps 0..7   two threads per query row (32 of a chunk's 64 tokens each; four where a
+//                tile has 32 rows, which leaves the warps for the rebuild): q into
 //                tensor memory as fp16 (times a power of two per row, so q has no range
 //                limit), then per chunk S from tensor memory, the softmax weights back
 //                into it as fp16 (the A operand of P V), at the end O out of it.  The
@@ -53,17 +54,18 @@ constexpr int kItemCost = 8;
 // (With a limit of 8 chunks as if cut; with 32, four tokens each on four contexts of 1,000
 // take 30 us instead of 21.)
 constexpr int kUncut = 16;
-// Warps by the quarters NQ of the tile's 128 rows that hold queries: two softmax warps a
-// quarter (a quarter's warps have its index modulo 4, as they reach its lanes of tensor
-// memory), rebuild warps, MMA issuer, query loader.
+// Warps by the quarters NQ of the tile's 128 rows that hold queries: softmax warps (eight:
+// two a quarter; one quarter: four; a quarter's warps have its index modulo 4, as they reach
+// its lanes of tensor memory), rebuild warps, MMA issuer, query loader.
 template <int NQ>
 struct Roles {
-    static constexpr int soft = 2 * NQ, deq = NQ == 1 ? 16 : 8, mma = soft + deq, load = mma + 1, threads = (load + 1) * 32;
-    __device__ static __forceinline__ bool is_soft(int warp) { return warp < 8 && (warp & 3) < NQ; }
-    __device__ static __forceinline__ int deq_index(int warp) { return NQ == 1 ? (warp < 4 ? warp - 1 : warp - 2) : warp - soft; }
+    static constexpr int parts = NQ == 1 ? 4 : 2;  // softmax warps of a quarter: each has 64 / parts of a chunk's tokens
+    static constexpr int soft = parts * NQ, deq = NQ == 1 ? 16 : 8, mma = soft + deq, load = mma + 1, threads = (load + 1) * 32;
+    __device__ static __forceinline__ bool is_soft(int warp) { return warp < 4 * parts && (warp & 3) < NQ; }
+    __device__ static __forceinline__ int deq_index(int warp) { return NQ == 1 ? (warp < 16 ? warp - 1 - warp / 4 : warp - 4) : warp - soft; }
 };
 constexpr int kMaxWarps = Roles<1>::threads / 32;
-constexpr int kBarPair = 1;                // named barriers 1..4: the two warps of 32 rows
+constexpr int kBarPair = 1;                // named barriers 1..4: the softmax warps of 32 rows
 constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128-byte swizzle
 constexpr int kMaxBufs = 4;                // buffers of K and of V, at most
 constexpr uint32_t kTmemCols = 512;
@@ -75,9 +77,9 @@ struct Fixed {
     uint32_t tmem;
     int abort, b0, m0, L0, q0;
     long long pre, per, begin, total, used, sum[kMaxWarps];
-    float xch[2][2][kRows];  // [chunk parity][half of the columns][row]
+    float xch[2][4][kRows];  // [chunk parity][part of the columns][row]
 };
-constexpr int kFixed = 4096;
+constexpr int kFixed = 5120;
 static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
 constexpr int kQBox = kRows * 128;         // [128 rows][64 channels] bf16, 128-byte swizzle
 // CG: the CTAs that share an item's K and V.  The MMAs of a pair read half of K's tokens
@@ -127,6 +129,20 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr)
         : "memory");
 }
+// The same of 16 columns.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld_x32(taddr, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld_x16(taddr, r); }
 // Descriptor of an operand with its M/N side contiguous (128-byte swizzle): boxes of
 // 64 contiguous elements x rows of 128 bytes; `lead` bytes between boxes, 1024 bytes
 // between groups of eight rows.
@@ -150,6 +166,14 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st_x16(taddr, r); }
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[8]) { tmem_st_x8(taddr, r); }
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
 {
     uint4 v;
@@ -572,8 +596,19 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
     bool ok = true;
 
     if (R::is_soft(warp)) {
-        // ------------------------------------------------ two threads per query row
-        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+        // ------------------------------------------------ two or four threads per query row
+        constexpr int NP = R::parts, NC = kChunk / NP;  // of a row, and its columns of a chunk
+        const int quarter = warp & 3, part = warp >> 2, row = quarter * 32 + lane;
+        auto quarter_sync = [&]() { named_barrier_sync(kBarPair + quarter, NP * 32); };
+        // over the row's threads; all of them are done with xch[s] afterwards, if a quarter_sync comes before its next use
+        auto others = [&](int s, float x, auto op) {
+            F.xch[s][part][row] = x;
+            quarter_sync();
+#pragma unroll
+            for (int o = 1; o < NP; ++o) x = op(x, F.xch[s][(part + o) & (NP - 1)][row]);
+            return x;
+        };
+        auto larger = [](float x, float y) { return fmaxf(x, y); };
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         Share h, h2;
         bool more = next_share(a, w, h, TI);
@@ -588,25 +623,23 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
             const int sw = row & 7;
             float big = 0.0f;
 #pragma unroll
-            for (int c = half; c < GR; c += 2)
+            for (int c = part; c < GR; c += NP)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 y = lds128(src + c * kQBox + ((i ^ sw) << 4));
                     big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(y.x)), fabsf(hi_bf16(y.x))), fmaxf(fabsf(lo_bf16(y.y)), fabsf(hi_bf16(y.y)))));
                     big = fmaxf(big, fmaxf(fmaxf(fabsf(lo_bf16(y.z)), fabsf(hi_bf16(y.z))), fmaxf(fabsf(lo_bf16(y.w)), fabsf(hi_bf16(y.w)))));
                 }
-            named_barrier_sync(kBarPair + quarter, 64);  // the other half is done with xch
-            F.xch[0][half][row] = big;
-            named_barrier_sync(kBarPair + quarter, 64);
-            big = fmaxf(big, F.xch[0][half ^ 1][row]);
-            named_barrier_sync(kBarPair + quarter, 64);
+            quarter_sync();  // the others are done with xch
+            big = others(0, big, larger);
+            quarter_sync();
             // times 2^(14 - floor(log2 big)), within the normal numbers, and the sign of the scale
             const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
             const float up = copysignf(__uint_as_float(static_cast<uint32_t>(ef) << 23), a.scale_log2);
             // never 0: a masked score is -inf, and stays it
             mul = fmaxf(fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23), 1.17549435e-38f);
 #pragma unroll
-            for (int c = half; c < GR; c += 2) {
+            for (int c = part; c < GR; c += NP) {
                 uint32_t r[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -645,24 +678,22 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                 ok = ok && warp_wait(&F.s_full[sb], (it >> 1) & 1, &F.abort, status);
                 if (any_row) {
                     tc_fence_after();
-                    const int vis = limit - (h.j0 + i) * kChunk - half * 32;  // of this thread's 32 columns, those the row sees
-                    uint32_t s[32] = {};
-                    if (ok) tmem_ld_x32(lanes + Cols<GR>::S + sb * 64 + half * 32, s);
-                    if (__any_sync(0xffffffffu, vis < 32)) {
+                    const int vis = limit - (h.j0 + i) * kChunk - part * NC;  // of this thread's columns, those the row sees
+                    uint32_t s[NC] = {};
+                    if (ok) tmem_ld_cols(lanes + Cols<GR>::S + sb * 64 + part * NC, s);
+                    if (__any_sync(0xffffffffu, vis < NC)) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
+                        for (int x = 0; x < NC; ++x)
                             if (x >= vis) s[x] = 0xFF800000u;  // -inf
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < 32; x += 2)  // three operands a step
+                    for (int x = 0; x < NC; x += 2)  // three operands a step
                         mx[(x >> 1) & 3] = fmaxf(fmaxf(mx[(x >> 1) & 3], __uint_as_float(s[x])), __uint_as_float(s[x + 1]));
-                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    F.xch[sb][half][row] = top;
-                    named_barrier_sync(kBarPair + quarter, 64);  // also: both halves have S in registers, so P may overwrite it
-                    top = fmaxf(top, F.xch[sb][half ^ 1][row]);
+                    // (after its barrier all of the row's S is in registers, so P may overwrite it)
+                    const float top = others(sb, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), larger);
                     const float mn = top > -INFINITY ? top * item_mul : kNoMax;
-                    if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {  // the same in both halves
+                    if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {  // the same in all parts
                         const float to = fmaxf(m_run, mn), al = ex2(m_run - to);
                         m_run = to;
                         l_run *= al;
@@ -671,7 +702,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                             ok = ok && warp_wait(&F.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, &F.abort, status);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = half; c < D / 32 && ok; c += 2) {
+                            for (int c = part; c < D / 32 && ok; c += NP) {
                                 uint32_t o[32];
                                 tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
 #pragma unroll
@@ -681,11 +712,11 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                             tmem_st_wait();
                         }
                     }
-                    uint32_t p[16];
+                    uint32_t p[NC / 2];
                     unsigned long long sum[2] = {0ull, 0ull};
                     const unsigned long long mul2 = pair(item_mul, item_mul), neg2 = pair(-m_run, -m_run);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
+                    for (int x = 0; x < NC / 2; ++x) {
                         float e0, e1;
                         unpair(fma2(pair(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])), mul2, neg2), e0, e1);
                         e0 = ex2(e0);
@@ -698,7 +729,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                         unpair(add2(sum[0], sum[1]), a0, a1);
                         l_run += a0 + a1;
                     }
-                    if (ok) tmem_st_x16(lanes + Cols<GR>::S + sb * 64 + half * 16, p);
+                    if (ok) tmem_st_cols(lanes + Cols<GR>::S + sb * 64 + part * (NC / 2), p);
                     tmem_st_wait();
                     tc_fence_before();
                 }
@@ -715,18 +746,16 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
             const bool starts = h.j0 == 0, ends = h.j0 + h.n == h.nch;
             const size_t part_row = static_cast<size_t>(2 * share + (starts ? 1 : 0)) * (CG * kRows) + rank * kRows + row;
             if (any_row) {
-                named_barrier_sync(kBarPair + quarter, 64);
-                F.xch[0][half][row] = l_run;
-                named_barrier_sync(kBarPair + quarter, 64);
-                l_run += F.xch[0][half ^ 1][row];
-                named_barrier_sync(kBarPair + quarter, 64);
+                quarter_sync();
+                l_run = others(0, l_run, [](float x, float y) { return x + y; });
+                quarter_sync();
                 const bool seen = l_run > 0.0f;  // a row that saw nothing has zeros
                 const float r = seen ? 1.0f / l_run : 0.0f;
                 const long long n = w.q0 + tq;
                 uint16_t *dst = a.out + (n * a.H_q + head) * D;
                 float *pdst = a.part_acc + part_row * D;
 #pragma unroll 1
-                for (int c = half; c < D / 32 && ok; c += 2) {
+                for (int c = part; c < D / 32 && ok; c += NP) {
                     uint32_t o[32];
                     tmem_ld_x32(lanes + Cols<GR>::O + c * 32, o);
                     if (valid) {
@@ -751,7 +780,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                     }
                     __syncwarp();
                 }
-                if (valid && half == 0 && !(starts && ends))
+                if (valid && part == 0 && !(starts && ends))
                     *reinterpret_cast<float2 *>(a.part_ml + part_row * 2) = make_float2(m_run, l_run);
             }
             tc_fence_before();
@@ -1153,9 +1182,10 @@ cudaError_t launch(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t st
 
 // Pairs, but one CTA an item where D = 64 (its 64 channels of V are one swizzled box and
 // do not split) and where no sequence need have more query tokens than one CTA's 128
-// rows hold: a pair's second half would idle (eight drafts of four tokens: 28 us against
-// 34; prompts and chunks of 1,024 tokens and more are 1.15 to 1.25 times as fast with pairs).
-// Where 32 rows hold them, a tile has 32 rows and the other quarters' warps rebuild.
+// rows hold: a pair's second half would idle (eight drafts of four tokens, without the rule below:
+// 28 us against 34; prompts and chunks of 1,024 tokens and more are 1.15 to 1.25 times as fast with pairs).
+// Where 32 rows hold them, a tile has 32 rows, four threads a row and sixteen rebuild warps
+// (28.3 us with the 128-row tile, 25.0 with two threads a row, 24.7 with four).
 template <int BITS, int GR>
 cudaError_t launch_rows(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream)
 {
