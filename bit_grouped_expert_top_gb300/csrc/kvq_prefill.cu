@@ -45,8 +45,8 @@ namespace {
 constexpr int kRows = 128;                 // query rows of a tile
 constexpr int kChunk = 64;                 // cache tokens per step
 // Taking up an item (its q, the first scores, its output) costs about eight chunks,
-// which the shares of the work list count: an 8K prompt 528 us with 2, 429 with 6, 410
-// with 8, 419 with 12.
+// which the shares of the work list count: an 8K prompt 413 us with 6, 397 with 8, 402
+// with 10, 406 with 12.
 constexpr int kItemCost = 8;
 // Cutting an item costs about sixteen chunks (its parts, their join): where there are no more
 // items than shares, and the longest is not longer by more than that than an even share, each
