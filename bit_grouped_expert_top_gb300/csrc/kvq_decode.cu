@@ -57,6 +57,11 @@ constexpr int kMaxStages = 14;                // segments in flight <= stages < 
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarriers = 15;                 // named barriers 1..15, by segment
 constexpr float kNoMax = -1.7e38f;            // running maximum before any token (finite: -inf - kNoMax = -inf)
+// The factor f of the weights at most (before any token with a scale, and with scales below 2^-107):
+// a weight reaches 2^8 before the running maximum moves, and its product with f stays finite,
+// as times a scale of 0 it has to be 0.
+constexpr int kMaxFactorLog = 111;
+constexpr float kMaxFactor = 0x1p111f;
 
 struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
             mul[0] = __shfl_sync(0xffffffffu, m, 8 * t);
             mul[1] = __shfl_sync(0xffffffffu, m, 8 * t + 4);
         }
-        float acc[GR][4][4], bsum[GR][2], m_run[2] = {kNoMax, kNoMax}, l_run[2] = {0.0f, 0.0f}, f = 0x1p127f;
+        float acc[GR][4][4], bsum[GR][2], m_run[2] = {kNoMax, kNoMax}, l_run[2] = {0.0f, 0.0f}, f = kMaxFactor;
 #pragma unroll
         for (int c = 0; c < GR; ++c) {
             bsum[c][0] = bsum[c][1] = 0.0f;
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
                 for (int o = 1; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
                 float r1 = 1.0f, r2 = 1.0f;
                 if (smax * f > 128.0f) {  // f smax back into [16, 32)
-                    const int ex = min(max(258 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 254);
+                    const int ex = min(max(258 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog);
                     r2 = 1.0f / f;
                     f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
                     r1 = f;

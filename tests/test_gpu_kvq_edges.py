@@ -1,0 +1,97 @@
+"""The quantised cache's kernels at the edges of their range: groups of equal values, scales that no fp16 number holds,
+values and weights of very different size.
+
+What the results may be off by is derived at each test; references are fp64 on the values that the codes stand for."""
+import numpy as np
+import pytest
+import torch
+
+import bit_grouped_expert_top_gb300 as lm
+from bit_grouped_expert_top_gb300.kvq_inputs import KvqConfig
+from helpers import bits as raw
+from kvq_util import Cache, check, error_bound, rounded
+from oracle import kvq
+
+pytestmark = pytest.mark.gpu
+RANGE_ERR = -9  # LILY_ERR_DEVICE_RANGE
+
+
+def _bf16(x):
+    return raw(torch.as_tensor(np.asarray(x, np.float32)).to(torch.bfloat16))
+
+
+def _store(c, n, b, x):
+    """Quantises x [L][H_kv][D] as the whole of sequence b's K or V in the host copy."""
+    code, sb = kvq.quantise(_bf16(x), c.cfg.bits)
+    kvq.write_rows(c.h[n + "_q"], c.table[b], 0, kvq.pack(code, c.cfg.bits))
+    kvq.write_rows(c.h[n + "_sb"], c.table[b], 0, sb)
+
+
+def _queries(c, q):
+    c.a["q"] = torch.from_numpy(np.array(q, np.float32, order="C")).to(torch.bfloat16)
+
+
+def _decode(c, scale=None):
+    out = torch.full((c.cfg.B, c.cfg.H_q, c.cfg.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lm.lily_kvq_attn_decode(c.shape, c.handle, c.d["q"], c.d["block_table"], c.d["seq_lens"], out, c.ws, scale=scale)
+    return out
+
+
+def _prefill(c, scale=None):
+    out = torch.full((c.cfg.N, c.cfg.H_q, c.cfg.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lm.lily_kvq_attn_prefill(c.shape, c.handle, c.d["q"], c.d["cu"], c.d["block_table"], c.d["seq_lens"], out, c.ws, scale=scale)
+    return out
+
+
+def _reference(c, b, rows, limits, scale=None):
+    kk, vv, km, vm = c.sequence(b)
+    return kvq.attend_and_bound(rounded(c.a["q"])[rows], kk, vv, limits, scale, km, vm)
+
+
+# lengths of decode batches: a CTA has one (sequence, KV head) each, several steps a warp; and one that is cut between CTAs
+WHOLE = (1000, 700, 130, 1, 900, 300) * 6 + (1000, 0)
+CUT = (2500, 700, 130)
+
+
+def _one_token(lens, **kw):
+    return KvqConfig("edges", lens=lens, new=(1,) * len(lens), H_q=8, H_kv=4, **kw)
+
+
+def _rising(cfg, seed, rise):
+    """q of one direction for every head, and per sequence keys whose scores rise by `rise` powers of two in 1,000 tokens."""
+    rng = np.random.default_rng(seed)
+    u = rng.choice([-1.0, 1.0], cfg.D)
+    q = np.broadcast_to(u, (cfg.N, cfg.H_q, cfg.D))
+    step = rise / (np.sqrt(cfg.D) * np.log2(np.e)) / 1000
+    keys = [0.05 * rng.standard_normal((L, cfg.H_kv, cfg.D)) + u * (np.arange(L) * step)[:, None, None] for L in cfg.lens]
+    return q, keys, rng
+
+
+def _check_decode(c, scale=None):
+    got = rounded(_decode(c, scale))
+    assert c.status() == 0
+    for b, L in enumerate(c.cfg.lens):
+        ref, mags = _reference(c, b, slice(b, b + 1), [L], scale)
+        check(got[b:b + 1], ref, mags, operand=0.0)
+
+
+# ------------------------------------------------------------------ decode: groups of equal values
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D,bs", [(64, 32), (128, 64), (256, 32), (256, 128)])
+@pytest.mark.parametrize("lens", [WHOLE, CUT])
+@pytest.mark.parametrize("kind", ["zero", "equal", "prefix", "tiny"])
+def test_decode_of_values_without_a_scale(kind, lens, D, bs, bits):
+    # groups of equal values have scale 0; the scores rise, so that weights pass the running maximum
+    cfg = _one_token(lens, D=D, block_size=bs, bits=bits, seed=D + bits)
+    q, keys, rng = _rising(cfg, 11, 20.0)
+    c = Cache(cfg)
+    _queries(c, q)
+    for b, L in enumerate(lens):
+        if L == 0:
+            continue
+        _store(c, "k", b, keys[b])
+        x = rng.standard_normal((L, cfg.H_kv, D))
+        equal = np.repeat(rng.standard_normal((L, cfg.H_kv, D // 64)), 64, -1)
+        _store(c, "v", b, {"zero": 0 * x, "equal": equal, "tiny": x * 2.0 ** -121,
+                           "prefix": np.where((np.arange(L) < L * 2 // 3)[:, None, None], equal, x)}[kind])
+    _check_decode(c.to_gpu())
