@@ -69,8 +69,9 @@ __device__ __forceinline__ int2 token_slot(const KvqCopyArgs &a, const int *cu, 
 // multiply-adds; h has 8 bits, so no quotient of a 24-bit d comes nearer than 2^-33 to
 // a rounding border, and r may be the hardware's approximation.  All of it is computed
 // times m, a power of two that keeps every term within the normal numbers: the range of
-// two finite bf16 values is finite in halves, and where it is below 2^-32 all of the
-// group is below 2^-24 and takes 2^64.
+// two finite bf16 values is finite in halves, and where it is below 2^-32 the group takes
+// 2^64: then either all of it is below 2^-24, or (lo not below 1) its values are equal, at any
+// size; those stay in halves, with a range and a scale of 0.
 struct GroupScale {
     float m, h, r, mlo;
     uint32_t sb;  // scale, bias as stored
@@ -81,7 +82,7 @@ __device__ __forceinline__ GroupScale group_scale(float lo, float hi)
     constexpr float L = BITS == 4 ? 15.0f : 255.0f, rL = 1.0f / L;
     GroupScale g;
     const float half = 0.5f * hi - 0.5f * lo;
-    const bool lift = half < 0x1p-33f;
+    const bool lift = half < 0x1p-33f && fabsf(lo) < 1.0f;
     g.m = lift ? 0x1p64f : 0.5f;
     g.mlo = -lo * g.m;
     const float range = fmaf(hi, g.m, g.mlo);

@@ -95,3 +95,29 @@ def test_decode_of_values_without_a_scale(kind, lens, D, bs, bits):
         _store(c, "v", b, {"zero": 0 * x, "equal": equal, "tiny": x * 2.0 ** -121,
                            "prefix": np.where((np.arange(L) < L * 2 // 3)[:, None, None], equal, x)}[kind])
     _check_decode(c.to_gpu())
+
+
+# ------------------------------------------------------------------ append: equal values of any size
+@pytest.mark.parametrize("bits", [4, 8])
+def test_append_of_equal_values_is_exact(bits):
+    sizes = np.array([2.0 ** 60, 2.0 ** 63, 2.0 ** 64, 2.0 ** 65, 1e25, 1e30, 3.3e38, 2.0 ** -30, 2.0 ** -100, 2.0 ** -126, 2.0 ** -133, 1.0])
+    x = np.repeat(np.concatenate([sizes, -sizes]), 64).reshape(-1, 1, 64).astype(np.float32)
+    near = x.copy()                     # the same, one value a step away
+    near[:, 0, 5] *= np.float32(1 + 2.0 ** -7)
+    xb = torch.from_numpy(np.concatenate([x, near])).to(torch.bfloat16)
+    n = xb.shape[0]
+    s = lm.make_kvq_shape(1, 1, 1, 64, 64, 1, bits)
+    t, ws = lm.alloc_kvq_cache(s, 1), lm.alloc_kvq_workspace(s)
+    one = dict(dtype=torch.int32, device="cuda")
+    cu, zero, table = torch.tensor([0, n], **one), torch.zeros(1, **one), torch.zeros((1, 1), **one)
+    handle = lm.make_kvq_cache(t)
+    lm.lily_kvq_append(s, handle, xb.cuda(), (-xb).cuda(), cu, zero, table, ws)
+    for name, src in (("k", xb), ("v", -xb)):
+        code, sb = kvq.quantise(raw(src), bits)
+        np.testing.assert_array_equal(kvq.bf16_value(raw(t[name + "_sb"]))[0, 0, 0, :n], kvq.bf16_value(sb)[:, 0, 0])
+        np.testing.assert_array_equal(t[name + "_q"].cpu().numpy()[0, 0, 0, :n], kvq.pack(code, bits)[:, 0, 0])
+    k, v = torch.empty_like(xb, device="cuda"), torch.empty_like(xb, device="cuda")
+    lm.lily_kvq_read(s, handle, k, v, cu, zero, table, ws)
+    m = 2 * len(sizes)
+    assert torch.equal(k[:m].cpu(), xb[:m]) and torch.equal(v[:m].cpu(), -xb[:m])
+    assert lm.lily_moe_device_status(ws) == 0
