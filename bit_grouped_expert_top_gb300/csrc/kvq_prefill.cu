@@ -519,17 +519,39 @@ struct Raw {
     uint32_t sb;
 };
 
+// Values in fp16, the multiply-add in fp32.
+template <int BITS>
+__device__ __noinline__ void rebuild_f32(const uint32_t *codes, float s, float b, uint32_t row_addr)
+{
+    constexpr uint32_t L = (1u << BITS) - 1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const unsigned long long w = BITS == 4 ? codes[i] : codes[2 * i] | static_cast<unsigned long long>(codes[2 * i + 1]) << 32;
+        uint32_t v[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int c0 = BITS * unpacked<BITS>(2 * p), c1 = BITS * unpacked<BITS>(2 * p + 1);
+            v[p] = pack_f16(fmaf(__uint2float_rn(static_cast<uint32_t>(w >> c0) & L), s, b),
+                            fmaf(__uint2float_rn(static_cast<uint32_t>(w >> c1) & L), s, b));
+        }
+        sts128(row_addr ^ (i << 4), make_uint4(v[0], v[1], v[2], v[3]));
+    }
+}
+
 // Values code * scale + bias in fp16, each rounded once.  4 bits: the nibbles are e2m3
 // bit patterns of code / 8, which converts exactly, and the multiply-add gets 8 scale (a
 // normal fp16 number down to scales of 2^-17).  8 bits: the code under the exponent of
-// 128 is 128 + code / 8, so 128 is taken off exactly first.
+// 128 is 128 + code / 8, so 128 is taken off exactly first.  That needs 8 scale within
+// fp16, which the test at the end makes sure of (4-bit groups from about -61000 to 61000 have scales
+// of 8190 and more); the rare group that fails it is done over in fp32.  The test comes after
+// the stores so that nothing waits for it (a 2K chunk at the end of 32K 669 us without it, 673 here, 686 with it first).
 template <int BITS>
 __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint32_t row_addr, int *status)
 {
     const uint32_t sb = exists ? raw.sb : 0u;  // rows behind the sequence, whatever they hold
     const float s = lo_bf16(sb), b = hi_bf16(sb);
     constexpr float L = BITS == 4 ? 15.0f : 255.0f;
-    if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(raw.q);
     const __half2 s2 = __float2half2_rn(s * 8.0f), b2 = __float2half2_rn(b);
     auto value = [&](uint32_t w) {
         const uint32_t x = (w & 0x00FF00FFu) | 0x58005800u, off = 0xD800D800u;
@@ -538,13 +560,17 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
     };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(raw.q);
         uint4 v;
         if constexpr (BITS == 4)  // channels (0, 2), (4, 6), (1, 3), (5, 7)
             v = dequant8_f16_e2m3(q[i], s2, b2);
         else                      // channels (0, 2), (1, 3), (4, 6), (5, 7)
             v = make_uint4(value(q[2 * i]), value(q[2 * i] >> 8), value(q[2 * i + 1]), value(q[2 * i + 1] >> 8));
         sts128(row_addr ^ (i << 4), v);
+    }
+    if (!(fmaf(L, fabsf(s), fabsf(b)) < 65504.0f)) {
+        if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
+        Raw<BITS> copy = raw;
+        rebuild_f32<BITS>(reinterpret_cast<const uint32_t *>(copy.q), s, b, row_addr);
     }
 }
 

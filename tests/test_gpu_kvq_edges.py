@@ -121,3 +121,26 @@ def test_append_of_equal_values_is_exact(bits):
     m = 2 * len(sizes)
     assert torch.equal(k[:m].cpu(), xb[:m]) and torch.equal(v[:m].cpu(), -xb[:m])
     assert lm.lily_moe_device_status(ws) == 0
+
+
+# ------------------------------------------------------------------ prefill: scales that fp16 does not hold
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [(30, 1), (200, 40)])
+def test_prefill_of_groups_that_span_the_fp16_range(new, D, bits):
+    # ends within fp16, a step of 8192 and more at 4 bits
+    cfg = KvqConfig("wide", lens=(230, 70), new=new, D=D, bits=bits, seed=80 + D)
+    rng = np.random.default_rng(12)
+    c = Cache(cfg, n_query=cfg.N)
+    for b, L in enumerate(cfg.lens):
+        for n in "kv":
+            x = rng.uniform(-60000, 57000, (L, cfg.H_kv, D))
+            x[:, :, 3::64], x[:, :, 9::64] = (-65280, 57600) if n == "v" else (-65024, 64512)
+            _store(c, n, b, x)
+    c.to_gpu()
+    got = rounded(_prefill(c, scale=1e-6))
+    assert c.status() == 0
+    for b, (L, m) in enumerate(zip(cfg.lens, cfg.news)):
+        n0 = int(c.a["cu"][b])
+        ref, mags = _reference(c, b, slice(n0, n0 + m), L - m + 1 + np.arange(m), 1e-6)
+        check(got[n0:n0 + m], ref, mags)
