@@ -539,12 +539,13 @@ __device__ __noinline__ void rebuild_f32(const uint32_t *codes, float s, float b
 }
 
 // Values code * scale + bias in fp16, each rounded once.  4 bits: the nibbles are e2m3
-// bit patterns of code / 8, which converts exactly, and the multiply-add gets 8 scale (a
-// normal fp16 number down to scales of 2^-17).  8 bits: the code under the exponent of
-// 128 is 128 + code / 8, so 128 is taken off exactly first.  That needs 8 scale within
-// fp16, which the test at the end makes sure of (4-bit groups from about -61000 to 61000 have scales
-// of 8190 and more); the rare group that fails it is done over in fp32.  The test comes after
-// the stores so that nothing waits for it (a 2K chunk at the end of 32K 669 us without it, 673 here, 686 with it first).
+// bit patterns of code / 8, which converts exactly, and the multiply-add gets 8 scale.
+// 8 bits: the code under the exponent of 128 is 128 + code / 8, so 128 is taken off exactly
+// first.  That needs 8 scale and the bias to be fp16 numbers, which the test at the end makes sure of:
+// scales from 2^-20 to 8176 and biases from 2^-17 are (8 significant bits above 2^-24), and 4-bit groups from
+// about -61000 to 61000 have larger scales; what a smaller scale lost the code would multiply, by up to 32.
+// The rare group that fails the test is done over in fp32.  The test comes after the stores
+// so that nothing waits for it (a 2K chunk at the end of 32K 669 us without it, 673 here, 686 with it first).
 template <int BITS>
 __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint32_t row_addr, int *status)
 {
@@ -567,7 +568,7 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
             v = make_uint4(value(q[2 * i]), value(q[2 * i] >> 8), value(q[2 * i + 1]), value(q[2 * i + 1] >> 8));
         sts128(row_addr ^ (i << 4), v);
     }
-    if (!(fmaf(L, fabsf(s), fabsf(b)) < 65504.0f)) {
+    if (!(__low2float(s2) == s * 8.0f && __low2float(b2) == b && fmaf(L, fabsf(s), fabsf(b)) < 65504.0f)) {
         if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
         Raw<BITS> copy = raw;
         rebuild_f32<BITS>(reinterpret_cast<const uint32_t *>(copy.q), s, b, row_addr);

@@ -144,3 +144,28 @@ def test_prefill_of_groups_that_span_the_fp16_range(new, D, bits):
         n0 = int(c.a["cu"][b])
         ref, mags = _reference(c, b, slice(n0, n0 + m), L - m + 1 + np.arange(m), 1e-6)
         check(got[n0:n0 + m], ref, mags)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("gain", [2.0 ** -12, 1e-4, 1e-5, 1e-6, 2.0 ** -22])
+def test_prefill_of_small_values_rounds_them_once(gain, bits):
+    # a value is rounded to fp16: off by 2^-11 of itself, or below 2^-14 by 2^-25; as much for a key, whose score is then off by
+    # scale sum_d |q_d| 2^-25 more, and a weight by e^(2 times that)
+    cfg = KvqConfig("small", lens=(1, 1, 3, 300), new=(1, 1, 3, 40), D=128, bits=bits, seed=81)
+    for k_gain, v_gain in ((1.0, gain), (gain, 1.0)):
+        c = Cache(cfg, n_query=cfg.N)
+        rng = np.random.default_rng(13)
+        for b, L in enumerate(cfg.lens):
+            for n, g in (("k", k_gain), ("v", v_gain)):
+                _store(c, n, b, g * rng.uniform(0.5, 1.5, (L, 1, 1)) * rng.standard_normal((L, cfg.H_kv, 128)))
+        c.to_gpu()
+        scale = 0.08 / k_gain
+        got = rounded(_prefill(c, scale=scale))
+        assert c.status() == 0 and np.isfinite(got).all()
+        for b, (L, m) in enumerate(zip(cfg.lens, cfg.news)):
+            rows = slice(int(c.a["cu"][b]), int(c.a["cu"][b + 1]))
+            ref, mags = _reference(c, b, rows, L - m + 1 + np.arange(m), scale)
+            k_abs = 2.0 ** -25 * scale * np.abs(rounded(c.a["q"])[rows]).sum(-1) * (k_gain < 1)
+            bound = error_bound(ref, mags, 2.0 ** -11) + np.expm1(2 * k_abs)[..., None] * mags["value"] + 2.0 ** -25 * 1.01
+            err = np.abs(got[rows] - ref)
+            assert (err <= bound).all(), (b, (err / bound).max())
