@@ -15,8 +15,10 @@
 // q is scaled per head by a power of two into fp16 (2^14..2^15 at its largest
 // value, so a value keeps its 8 bits down to 2^-24 of that).  The weights
 // p_t sv_{t,c} are rounded to fp16 (2^-11 relative) after a power of two f that
-// keeps the largest scale seen at 16..128: f follows the data as the running
-// maximum of the softmax does, so the cache's values have no range limit.  p is
+// keeps the largest scale seen below 128: f follows the data as the running
+// maximum of the softmax does.  One f does while the scales lie within 2^8 of each other,
+// as a model's do; a warp that meets others (a token or a group of channels of very different size) goes on in
+// units_apart.  p is
 // taken against a running maximum that moves only when a score passes it by 8 (in
 // powers of two), which one vote per step finds; sums are fp32.
 //
@@ -52,7 +54,14 @@ namespace {
 // 256), 13.7 or 14.1 for 24 short ones (4 heads of 128, 8 bits); eight long ones with 8 heads of
 // 128 69.8 or 67.1.  6 are slower on long caches, 14 everywhere (registers).
 constexpr int kNW = 8;
-constexpr int kThreads = (kNW + 2) * 32;      // + the producers of K and of V
+// + the producers of K and of V.  With D = 256 a consumer thread needs more than the 168 registers that ten or twelve
+// warps have each: the producers' warpgroup (two of its warps idle) then gives registers up (168 x 12 warps =
+// 224 x 8 + 56 x 4).  131,072 tokens of 2 heads take 23.3 us so, 24.4 without, at 8 bits 30.7 and 33.9;
+// with D = 64 and 128, which fit in 168, the larger CTA costs 1 to 2.5%.
+__host__ __device__ constexpr bool splits_registers(int D) { return D == 256; }
+__host__ __device__ constexpr int threads_of(int D) { return (kNW + (splits_registers(D) ? 4 : 2)) * 32; }
+constexpr int kProducerRegs = 56, kConsumerRegs = 224;
+constexpr int kMaxThreads = threads_of(256);
 constexpr int kMaxStages = 14;                // segments in flight <= stages < named barriers
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarriers = 15;                 // named barriers 1..15, by segment
@@ -65,7 +74,7 @@ constexpr float kMaxFactor = 0x1p111f;
 
 struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    int abort, b0, len0, pre, begin, total, used, sum[kThreads / 32];
+    int abort, b0, len0, pre, begin, total, used, sum[kMaxThreads / 32];
     alignas(8) float ml[kNW][8][2];
 };
 constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
@@ -92,6 +101,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
+}
+// Registers of a thread from here on, for a warpgroup: more of them come from what another one has given back.
+// The kernel is launched with 168 x 384, which the bounds above make it ask for.
+template <int N, bool kMore>
+__device__ __forceinline__ void set_max_registers()
+{
+    if constexpr (kMore)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // d += a b: m16n8k16, fp16 inputs, fp32 accumulators
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -131,6 +150,7 @@ struct Walk {
     int b, g, j0, L, next, left;  // next: the length of sequence b + 1 as stored (loaded one sequence ahead)
 };
 
+template <int NT>  // threads of the CTA
 __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
 {
     Walk w{};
@@ -191,13 +211,13 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
         before = inc - n;
         all = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
+        for (int i = 0; i < NT / 32; ++i) {
             if (i < warp) before += F.sum[i];
             all += F.sum[i];
         }
     };
     int total = 0;
-    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
+    for (int s0 = 0; s0 < a.B; s0 += NT) {
         scan(s0);
         total += all;
     }
@@ -209,8 +229,8 @@ __device__ __forceinline__ Walk first_segment(const KvqAttnArgs &a, Fixed &F)
     w.left = per * (c + 1) + rest * (c + 1) / used - begin;
     // the sequence that `begin` falls into (with no more sequences than threads, the scan above has it)
     int pre = 0;
-    for (int s0 = 0; s0 < a.B; s0 += kThreads) {
-        if (a.B > kThreads) scan(s0);
+    for (int s0 = 0; s0 < a.B; s0 += NT) {
+        if (a.B > NT) scan(s0);
         const int lo = pre + before, n = s0 + tid < a.B ? blocks_of(len, a.c.bs) * a.c.H_kv : 0;
         if (begin >= lo && begin - lo < n) {
             F.b0 = s0 + tid;
@@ -288,9 +308,187 @@ __device__ __forceinline__ void join_column(const KvqAttnArgs &a, const Fixed &F
     }
 }
 
-// (One warp more in the launch bound than there are: the same 168 registers without 48 bytes of spills.)
+// The pieces of a consumer warp's work (lane = 4 gi + t), which both forms of it below share.
+// q per head times a power of two in fp16: the operand registers of the K steps, and the sums per group.
+template <int GR>
+struct Query {
+    uint32_t b[GR * 4][2];
+    float sum[GR][2], mul[2];
+};
+template <int BITS, int GR>
+__device__ __forceinline__ void load_query(const KvqAttnArgs &a, const Walk &w, int gi, int t, Query<GR> &q)
+{
+    constexpr int D = GR * 64;
+    const uint16_t *qh = a.q + w.b * a.q_stride + static_cast<long long>(w.g * a.group + (gi < a.group ? gi : 0)) * D;
+    uint32_t xs[GR][8];
+    float big = 0.0f;
+#pragma unroll
+    for (int c = 0; c < GR; ++c) {
+        const uint4 x0 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16);
+        const uint4 x1 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16 + 8);
+        xs[c][0] = x0.x; xs[c][1] = x0.y; xs[c][2] = x0.z; xs[c][3] = x0.w;
+        xs[c][4] = x1.x; xs[c][5] = x1.y; xs[c][6] = x1.z; xs[c][7] = x1.w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (gi >= a.group) xs[c][i] = 0u;
+            big = fmaxf(big, fmaxf(fabsf(lo_bf16(xs[c][i])), fabsf(hi_bf16(xs[c][i]))));
+        }
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // 2^(14 - floor(log2 big)): its exponent field, within the normal numbers
+    const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
+    const float up = __uint_as_float(static_cast<uint32_t>(ef) << 23);
+#pragma unroll
+    for (int c = 0; c < GR; ++c) {
+        float ones[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float u = BITS == 4 && (j & 1) ? up * 0.0625f : up;  // those codes carry 2^-20
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int i0 = k_channel<BITS>(j, 2 * r), i1 = k_channel<BITS>(j, 2 * r + 1);
+                q.b[c * 4 + j][r] = pack_f16((i0 & 1 ? hi_bf16(xs[c][i0 / 2]) : lo_bf16(xs[c][i0 / 2])) * u,
+                                            (i1 & 1 ? hi_bf16(xs[c][i1 / 2]) : lo_bf16(xs[c][i1 / 2])) * u);
+            }
+            // the sums over the group, heads 2t and 2t + 1, by a step against ones (16 where q has a sixteenth)
+            const uint32_t one = BITS == 4 && (j & 1) ? 0x4C004C00u : 0x3C003C00u;
+            mma_f16(ones, one, one, one, one, q.b[c * 4 + j][0], q.b[c * 4 + j][1]);
+        }
+        q.sum[c][0] = ones[0] * 0x1p-24f;
+        q.sum[c][1] = ones[1] * 0x1p-24f;
+    }
+    const float m = a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23);
+    q.mul[0] = __shfl_sync(0xffffffffu, m, 8 * t);
+    q.mul[1] = __shfl_sync(0xffffffffu, m, 8 * t + 4);
+}
+
+// Scores of a unit: sc[i][2h + x], tokens row + 16 i + 8 h, heads 2t + x.  One accumulator per (token half,
+// group), four of them between dependent matrix steps.
+template <int BITS, int GR, int bs, int IH>
+__device__ __forceinline__ void score_unit(const uint8_t *kq, const uint8_t *kp, int row, int t, const Query<GR> &q, float (&sc)[IH][4])
+{
+    constexpr int GB = 8 * BITS;
+    constexpr int KW = BITS / 2;
+    uint32_t k0[IH][GR][KW], k1[IH][GR][KW];
+    float d[IH][GR][4];
+#pragma unroll
+    for (int i = 0; i < IH; ++i)
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+            const uint8_t *p0 = kq + (c * bs + row + 16 * i) * GB + t * (GB / 4), *p1 = p0 + 8 * GB;
+            if constexpr (BITS == 4) {
+                const uint2 x0 = *reinterpret_cast<const uint2 *>(p0), x1 = *reinterpret_cast<const uint2 *>(p1);
+                k0[i][c][0] = x0.x; k0[i][c][1] = x0.y;
+                k1[i][c][0] = x1.x; k1[i][c][1] = x1.y;
+            } else {
+                const uint4 x0 = *reinterpret_cast<const uint4 *>(p0), x1 = *reinterpret_cast<const uint4 *>(p1);
+                k0[i][c][0] = x0.x; k0[i][c][1] = x0.y; k0[i][c][2] = x0.z; k0[i][c][3] = x0.w;
+                k1[i][c][0] = x1.x; k1[i][c][1] = x1.y; k1[i][c][2] = x1.z; k1[i][c][3] = x1.w;
+            }
+            d[i][c][0] = d[i][c][1] = d[i][c][2] = d[i][c][3] = 0.0f;
+        }
+#pragma unroll
+    for (int x = 0; x < KW; ++x) {
+#pragma unroll
+        for (int odd = 0; odd < (BITS == 4 ? 2 : 1); ++odd) {
+            const uint32_t M = BITS == 8 ? 0x00FF00FFu : odd ? 0x00F000F0u : 0x000F000Fu;
+            const int j = BITS == 4 ? 2 * x + odd : x;
+#pragma unroll
+            for (int i = 0; i < IH; ++i)
+#pragma unroll
+                for (int c = 0; c < GR; ++c)
+                    mma_f16(d[i][c], k0[i][c][x] & M, k1[i][c][x] & M, (k0[i][c][x] >> 8) & M, (k1[i][c][x] >> 8) & M,
+                            q.b[c * 4 + j][0], q.b[c * 4 + j][1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IH; ++i) {
+        float *s4 = sc[i];
+        s4[0] = s4[1] = s4[2] = s4[3] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+            const uint32_t w0 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i) * 4);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i + 8) * 4);
+            const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
+            s4[0] = fmaf(b0, q.sum[c][0], fmaf(s0, d[i][c][0], s4[0]));
+            s4[1] = fmaf(b0, q.sum[c][1], fmaf(s0, d[i][c][1], s4[1]));
+            s4[2] = fmaf(b1, q.sum[c][0], fmaf(s1, d[i][c][2], s4[2]));
+            s4[3] = fmaf(b1, q.sum[c][1], fmaf(s1, d[i][c][3], s4[3]));
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s4[x] *= q.mul[x & 1];
+    }
+}
+
+// Scale and bias of V, tokens row + 16 i + 8 h; `left` tokens of the unit exist (may be <= 0, or more than 32).  Rows
+// behind the sequence have no weight, whatever they hold, and a scale (`idle`, or the one of the unit's first token) that moves no factor.
+template <int GR, int bs, int IH>
+__device__ __forceinline__ void load_scales(const uint8_t *vp, int row, int gi, int t, int left, uint32_t idle, uint32_t (&vw)[IH][GR][2], float (&sc)[IH][4])
+{
+#pragma unroll
+    for (int i = 0; i < IH; ++i)
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                vw[i][c][h] = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
+    if (left < 16 * IH) {
+        uint32_t first[GR];
+#pragma unroll
+        for (int c = 0; c < GR; ++c) first[c] = __shfl_sync(0xffffffffu, vw[0][c][0], t) & 0xFFFFu;
+#pragma unroll
+        for (int i = 0; i < IH; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (token_of(gi) + 16 * i + 8 * h >= left) {
+                    sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < GR; ++c) vw[i][c][h] = left > 0 ? first[c] : idle;
+                }
+    }
+}
+
+// O^T += V^T P of 16 tokens (row0 the first one's, in the group's codes): the tokens on K, the weights in fp16, w0 the ones of the
+// first eight tokens.
+template <int BITS>
+__device__ __forceinline__ void add_product(const uint8_t *vq, int row0, int gi, int t, uint32_t w0, uint32_t w1, float (&acc)[4][4])
+{
+    constexpr int GB = 8 * BITS;
+    const uint32_t y0 = transpose8x8(w0), y1 = transpose8x8(w1);
+    // lane: channels 8 gi .. 8 gi + 7 of the group, tokens t, t + 4, t + 8, t + 12
+    const uint8_t *pv = vq + (row0 + t) * GB + gi * BITS;
+    uint32_t v[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (BITS == 4) {
+            v[r][0] = *reinterpret_cast<const uint32_t *>(pv + 4 * r * GB);
+        } else {
+            const uint2 x2 = *reinterpret_cast<const uint2 *>(pv + 4 * r * GB);
+            v[r][0] = x2.x;
+            v[r][1] = x2.y;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < BITS / 4; ++x) {
+        const uint32_t za = __byte_perm(v[0][x], v[1][x], 0x5410), zb = __byte_perm(v[2][x], v[3][x], 0x5410);
+        const uint32_t ya = __byte_perm(v[0][x], v[1][x], 0x7632), yb = __byte_perm(v[2][x], v[3][x], 0x7632);
+        const uint32_t za8 = za >> 8, zb8 = zb >> 8, ya8 = ya >> 8, yb8 = yb >> 8;
+        if (BITS == 4) {  // channels (0, 2), (1, 3), (4, 6), (5, 7)
+            mma_f16(acc[0], za & 0x000F000Fu, za8 & 0x000F000Fu, zb & 0x000F000Fu, zb8 & 0x000F000Fu, y0, y1);
+            mma_f16(acc[1], za & 0x00F000F0u, za8 & 0x00F000F0u, zb & 0x00F000F0u, zb8 & 0x00F000F0u, y0, y1);
+            mma_f16(acc[2], ya & 0x000F000Fu, ya8 & 0x000F000Fu, yb & 0x000F000Fu, yb8 & 0x000F000Fu, y0, y1);
+            mma_f16(acc[3], ya & 0x00F000F0u, ya8 & 0x00F000F0u, yb & 0x00F000F0u, yb8 & 0x00F000F0u, y0, y1);
+        } else {          // channels (4x, 4x + 2), (4x + 1, 4x + 3)
+            mma_f16(acc[2 * x], za & 0x00FF00FFu, ya & 0x00FF00FFu, zb & 0x00FF00FFu, yb & 0x00FF00FFu, y0, y1);
+            mma_f16(acc[2 * x + 1], za8 & 0x00FF00FFu, ya8 & 0x00FF00FFu, zb8 & 0x00FF00FFu, yb8 & 0x00FF00FFu, y0, y1);
+        }
+    }
+}
+
+// (Without a split, one warp more in the launch bound than there are: the same 168 registers without 48 bytes of spills.)
 template <int BITS, int GR, int bs>
-__global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
+__global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * GR) ? 0 : 32), 1) kvq_decode_kernel(const __grid_constant__ KvqAttnArgs a)
 {
     constexpr int D = GR * 64, GB = 8 * BITS;  // bytes of a group's codes in one row
     extern __shared__ __align__(128) uint8_t base[];
@@ -317,9 +515,13 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
     pdl_trigger();
     pdl_wait();
     __syncthreads();
-    Walk w = first_segment(a, F);
+    Walk w = first_segment<threads_of(D)>(a, F);
 
     if (warp >= kNW) {
+        if constexpr (splits_registers(D)) {
+            set_max_registers<kProducerRegs, false>();
+            if (warp >= kNW + 2) return;
+        }
         // ------------------------------------------------ producers: K, V (two, as issuing a copy takes ~130 cycles)
         const bool isv = warp > kNW;
         const uint8_t *codes = isv ? a.c.v_q : a.c.k_q;
@@ -375,6 +577,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
     }
 
     // ---------------------------------------------------- consumers
+    if constexpr (splits_registers(D)) set_max_registers<kConsumerRegs, true>();
     if (!a.whole && threadIdx.x == 0 && !a.key_by_segment && w.left == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     constexpr int ups = bs / kUnit;  // units per stage
     int unit = 0, stage0 = 0, bar = 0;  // units and stages of the segments before this one; named barrier
@@ -393,53 +596,8 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
             continue;
         }
 
-        // ---- q: per head a power of two into fp16, the operand registers of the K steps, sums per group
-        uint32_t qb[GR * 4][2];
-        float qsum[GR][2], mul[2];
-        {
-            const uint16_t *qh = a.q + w.b * a.q_stride + static_cast<long long>(w.g * G + (gi < G ? gi : 0)) * D;
-            uint32_t xs[GR][8];
-            float big = 0.0f;
-#pragma unroll
-            for (int c = 0; c < GR; ++c) {
-                const uint4 x0 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16);
-                const uint4 x1 = *reinterpret_cast<const uint4 *>(qh + c * 64 + t * 16 + 8);
-                xs[c][0] = x0.x; xs[c][1] = x0.y; xs[c][2] = x0.z; xs[c][3] = x0.w;
-                xs[c][4] = x1.x; xs[c][5] = x1.y; xs[c][6] = x1.z; xs[c][7] = x1.w;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (gi >= G) xs[c][i] = 0u;
-                    big = fmaxf(big, fmaxf(fabsf(lo_bf16(xs[c][i])), fabsf(hi_bf16(xs[c][i]))));
-                }
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            // 2^(14 - floor(log2 big)): its exponent field, within the normal numbers
-            const int ef = big > 0.0f ? min(268 - max(static_cast<int>(__float_as_uint(big) >> 23), 1), 253) : 127;
-            const float up = __uint_as_float(static_cast<uint32_t>(ef) << 23);
-#pragma unroll
-            for (int c = 0; c < GR; ++c) {
-                float ones[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float u = BITS == 4 && (j & 1) ? up * 0.0625f : up;  // those codes carry 2^-20
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int i0 = k_channel<BITS>(j, 2 * r), i1 = k_channel<BITS>(j, 2 * r + 1);
-                        qb[c * 4 + j][r] = pack_f16((i0 & 1 ? hi_bf16(xs[c][i0 / 2]) : lo_bf16(xs[c][i0 / 2])) * u,
-                                                    (i1 & 1 ? hi_bf16(xs[c][i1 / 2]) : lo_bf16(xs[c][i1 / 2])) * u);
-                    }
-                    // the sums over the group, heads 2t and 2t + 1, by a step against ones (16 where q has a sixteenth)
-                    const uint32_t one = BITS == 4 && (j & 1) ? 0x4C004C00u : 0x3C003C00u;
-                    mma_f16(ones, one, one, one, one, qb[c * 4 + j][0], qb[c * 4 + j][1]);
-                }
-                qsum[c][0] = ones[0] * 0x1p-24f;
-                qsum[c][1] = ones[1] * 0x1p-24f;
-            }
-            const float m = a.scale_log2 * 0x1p24f * __uint_as_float(static_cast<uint32_t>(254 - ef) << 23);
-            mul[0] = __shfl_sync(0xffffffffu, m, 8 * t);
-            mul[1] = __shfl_sync(0xffffffffu, m, 8 * t + 4);
-        }
+        Query<GR> q;
+        load_query<BITS>(a, w, gi, t, q);
         float acc[GR][4][4], bsum[GR][2], m_run[2] = {kNoMax, kNoMax}, l_run[2] = {0.0f, 0.0f}, f = kMaxFactor;
 #pragma unroll
         for (int c = 0; c < GR; ++c) {
@@ -450,7 +608,9 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
                 for (int x = 0; x < 4; ++x) acc[c][m][x] = 0.0f;
         }
 
-        for (int u = first; u < units; u += kNW) {
+        bool apart = false;
+        int u = first;
+        for (; u < units; u += kNW) {
             const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
             // A warp meets a slot only in some of its turns, and copies land in any order: the slot's last turn has to be
             // over first, or `full` of the turn before, still open, has the parity of this one done.
@@ -466,84 +626,13 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
             const int left = w.L - (tok0 + u * kUnit);  // tokens of this unit that exist (may be <= 0, or more than 32)
             const int row = r0 + token_of(gi);          // + 16 i + 8 h: this lane's token rows of S^T
 
-            // ---- scores: sc[i][2h + x], tokens row + 16 i + 8 h, heads 2t + x.  One accumulator per
-            // (token half, group), four of them between dependent matrix steps
-            constexpr int KW = BITS / 2;
             float sc[IH][4];
-            {
-                uint32_t k0[IH][GR][KW], k1[IH][GR][KW];
-                float d[IH][GR][4];
-#pragma unroll
-                for (int i = 0; i < IH; ++i)
-#pragma unroll
-                    for (int c = 0; c < GR; ++c) {
-                        const uint8_t *p0 = kq + (c * bs + row + 16 * i) * GB + t * (GB / 4), *p1 = p0 + 8 * GB;
-                        if constexpr (BITS == 4) {
-                            const uint2 x0 = *reinterpret_cast<const uint2 *>(p0), x1 = *reinterpret_cast<const uint2 *>(p1);
-                            k0[i][c][0] = x0.x; k0[i][c][1] = x0.y;
-                            k1[i][c][0] = x1.x; k1[i][c][1] = x1.y;
-                        } else {
-                            const uint4 x0 = *reinterpret_cast<const uint4 *>(p0), x1 = *reinterpret_cast<const uint4 *>(p1);
-                            k0[i][c][0] = x0.x; k0[i][c][1] = x0.y; k0[i][c][2] = x0.z; k0[i][c][3] = x0.w;
-                            k1[i][c][0] = x1.x; k1[i][c][1] = x1.y; k1[i][c][2] = x1.z; k1[i][c][3] = x1.w;
-                        }
-                        d[i][c][0] = d[i][c][1] = d[i][c][2] = d[i][c][3] = 0.0f;
-                    }
-#pragma unroll
-                for (int x = 0; x < KW; ++x) {
-#pragma unroll
-                    for (int odd = 0; odd < (BITS == 4 ? 2 : 1); ++odd) {
-                        const uint32_t M = BITS == 8 ? 0x00FF00FFu : odd ? 0x00F000F0u : 0x000F000Fu;
-                        const int j = BITS == 4 ? 2 * x + odd : x;
-#pragma unroll
-                        for (int i = 0; i < IH; ++i)
-#pragma unroll
-                            for (int c = 0; c < GR; ++c)
-                                mma_f16(d[i][c], k0[i][c][x] & M, k1[i][c][x] & M, (k0[i][c][x] >> 8) & M, (k1[i][c][x] >> 8) & M,
-                                        qb[c * 4 + j][0], qb[c * 4 + j][1]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < IH; ++i) {
-                    float *s4 = sc[i];
-                    s4[0] = s4[1] = s4[2] = s4[3] = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < GR; ++c) {
-                        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i) * 4);
-                        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(kp + (c * bs + row + 16 * i + 8) * 4);
-                        const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
-                        s4[0] = fmaf(b0, qsum[c][0], fmaf(s0, d[i][c][0], s4[0]));
-                        s4[1] = fmaf(b0, qsum[c][1], fmaf(s0, d[i][c][1], s4[1]));
-                        s4[2] = fmaf(b1, qsum[c][0], fmaf(s1, d[i][c][2], s4[2]));
-                        s4[3] = fmaf(b1, qsum[c][1], fmaf(s1, d[i][c][3], s4[3]));
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) s4[x] *= mul[x & 1];
-                }
-            }
-            uint32_t vw[IH][GR][2];  // scale, bias of V: tokens row + 16 i + 8 h
-#pragma unroll
-            for (int i = 0; i < IH; ++i)
-#pragma unroll
-                for (int c = 0; c < GR; ++c)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vw[i][c][h] = *reinterpret_cast<const uint32_t *>(vp + (c * bs + row + 16 * i + 8 * h) * 4);
-            if (left < kUnit) {
-                // rows behind the sequence: no weight, whatever they hold
-#pragma unroll
-                for (int i = 0; i < IH; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (token_of(gi) + 16 * i + 8 * h >= left) {
-                            sc[i][2 * h] = sc[i][2 * h + 1] = -INFINITY;
-#pragma unroll
-                            for (int c = 0; c < GR; ++c) vw[i][c][h] = 0u;
-                        }
-            }
+            score_unit<BITS, GR, bs>(kq, kp, row, t, q, sc);
+            uint32_t vw[IH][GR][2];
+            load_scales<GR, bs>(vp, row, gi, t, left, (254u << 7) - (__float_as_uint(f) >> 16), vw, sc);
 
             // ---- running maximum, and the power of two of the value scales: both move rarely
-            float top0 = fmaxf(sc[0][0], sc[0][2]), top1 = fmaxf(sc[0][1], sc[0][3]), smax = 0.0f;
+            float top0 = fmaxf(sc[0][0], sc[0][2]), top1 = fmaxf(sc[0][1], sc[0][3]), smax = 0.0f, smin = INFINITY;
             if constexpr (IH == 2) {
                 top0 = fmaxf(top0, fmaxf(sc[IH - 1][0], sc[IH - 1][2]));
                 top1 = fmaxf(top1, fmaxf(sc[IH - 1][1], sc[IH - 1][3]));
@@ -551,9 +640,25 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < IH; ++i)
 #pragma unroll
-                for (int c = 0; c < GR; ++c) smax = fmaxf(smax, fmaxf(fabsf(lo_bf16(vw[i][c][0])), fabsf(lo_bf16(vw[i][c][1]))));
+                for (int c = 0; c < GR; ++c) {
+                    const float s0 = fabsf(lo_bf16(vw[i][c][0])), s1 = fabsf(lo_bf16(vw[i][c][1]));
+                    smax = fmaxf(smax, fmaxf(s0, s1));
+                    smin = fminf(smin, fminf(s0, s1));
+                }
             const bool grew = top0 > m_run[0] + 8.0f || top1 > m_run[1] + 8.0f;
-            if (__any_sync(0xffffffffu, grew || smax * f > 128.0f)) {
+            if (__any_sync(0xffffffffu, grew || smax * f > 128.0f || smin * f < 0.5f)) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
+                    smin = fminf(smin, __shfl_xor_sync(0xffffffffu, smin, o));
+                }
+                float to = f;
+                if (smax * f > 128.0f)  // f smax back into [64, 128)
+                    to = __uint_as_float(static_cast<uint32_t>(min(max(260 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog)) << 23);
+                if (smin * to < 0.5f || (to < f * 0x1p-8f && f < kMaxFactor)) {
+                    apart = true;
+                    break;
+                }
                 float mn0 = top0, mn1 = top1;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
@@ -562,30 +667,22 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
                 }
                 mn0 = fmaxf(mn0, m_run[0]);
                 mn1 = fmaxf(mn1, m_run[1]);
-                const float al0 = ex2(m_run[0] - mn0), al1 = ex2(m_run[1] - mn1);
+                const float r = to < f ? to * (1.0f / f) : 1.0f, al0 = ex2(m_run[0] - mn0), al1 = ex2(m_run[1] - mn1);
+                f = to;
                 m_run[0] = mn0;
                 m_run[1] = mn1;
                 l_run[0] *= al0;
                 l_run[1] *= al1;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
-                float r1 = 1.0f, r2 = 1.0f;
-                if (smax * f > 128.0f) {  // f smax back into [16, 32)
-                    const int ex = min(max(258 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog);
-                    r2 = 1.0f / f;
-                    f = __uint_as_float(static_cast<uint32_t>(ex) << 23);
-                    r1 = f;
-                }
 #pragma unroll
                 for (int c = 0; c < GR; ++c) {
                     bsum[c][0] *= al0;
                     bsum[c][1] *= al1;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        acc[c][m][0] = acc[c][m][0] * al0 * r2 * r1;
-                        acc[c][m][1] = acc[c][m][1] * al1 * r2 * r1;
-                        acc[c][m][2] = acc[c][m][2] * al0 * r2 * r1;
-                        acc[c][m][3] = acc[c][m][3] * al1 * r2 * r1;
+                        acc[c][m][0] = acc[c][m][0] * al0 * r;
+                        acc[c][m][1] = acc[c][m][1] * al1 * r;
+                        acc[c][m][2] = acc[c][m][2] * al0 * r;
+                        acc[c][m][3] = acc[c][m][3] * al1 * r;
                     }
                 }
             }
@@ -605,41 +702,113 @@ __global__ void __launch_bounds__(kThreads + 32, 1) kvq_decode_kernel(const __gr
                     const float s0 = lo_bf16(w0), b0 = hi_bf16(w0), s1 = lo_bf16(w1), b1 = hi_bf16(w1);
                     bsum[c][0] = fmaf(p[0], b0, fmaf(p[2], b1, bsum[c][0]));
                     bsum[c][1] = fmaf(p[1], b0, fmaf(p[3], b1, bsum[c][1]));
-                    const uint32_t y0 = transpose8x8(pack_f16(pf[0] * s0, pf[1] * s0));
-                    const uint32_t y1 = transpose8x8(pack_f16(pf[2] * s1, pf[3] * s1));
-                    // lane: channels 8 gi .. 8 gi + 7 of the group, tokens t, t + 4, t + 8, t + 12
-                    const uint8_t *pv = vq + (c * bs + r0 + 16 * i + t) * GB + gi * BITS;
-                    uint32_t v[4][2];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (BITS == 4) {
-                            v[r][0] = *reinterpret_cast<const uint32_t *>(pv + 4 * r * GB);
-                        } else {
-                            const uint2 x2 = *reinterpret_cast<const uint2 *>(pv + 4 * r * GB);
-                            v[r][0] = x2.x;
-                            v[r][1] = x2.y;
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < BITS / 4; ++x) {
-                        const uint32_t za = __byte_perm(v[0][x], v[1][x], 0x5410), zb = __byte_perm(v[2][x], v[3][x], 0x5410);
-                        const uint32_t ya = __byte_perm(v[0][x], v[1][x], 0x7632), yb = __byte_perm(v[2][x], v[3][x], 0x7632);
-                        const uint32_t za8 = za >> 8, zb8 = zb >> 8, ya8 = ya >> 8, yb8 = yb >> 8;
-                        if (BITS == 4) {  // channels (0, 2), (1, 3), (4, 6), (5, 7)
-                            mma_f16(acc[c][0], za & 0x000F000Fu, za8 & 0x000F000Fu, zb & 0x000F000Fu, zb8 & 0x000F000Fu, y0, y1);
-                            mma_f16(acc[c][1], za & 0x00F000F0u, za8 & 0x00F000F0u, zb & 0x00F000F0u, zb8 & 0x00F000F0u, y0, y1);
-                            mma_f16(acc[c][2], ya & 0x000F000Fu, ya8 & 0x000F000Fu, yb & 0x000F000Fu, yb8 & 0x000F000Fu, y0, y1);
-                            mma_f16(acc[c][3], ya & 0x00F000F0u, ya8 & 0x00F000F0u, yb & 0x00F000F0u, yb8 & 0x00F000F0u, y0, y1);
-                        } else {          // channels (4x, 4x + 2), (4x + 1, 4x + 3)
-                            mma_f16(acc[c][2 * x], za & 0x00FF00FFu, ya & 0x00FF00FFu, zb & 0x00FF00FFu, yb & 0x00FF00FFu, y0, y1);
-                            mma_f16(acc[c][2 * x + 1], za8 & 0x00FF00FFu, ya8 & 0x00FF00FFu, zb8 & 0x00FF00FFu, yb8 & 0x00FF00FFu, y0, y1);
-                        }
-                    }
+                    add_product<BITS>(vq, c * bs + r0 + 16 * i, gi, t, pack_f16(pf[0] * s0, pf[1] * s0), pack_f16(pf[2] * s1, pf[3] * s1), acc[c]);
                 }
             }
             // the last one is given back after the join: no segment then meets another that has its named barrier
             __syncwarp();
             if (lane == 0 && u + kNW < units) mbar_arrive(&F.empty[slot]);
+        }
+
+        // ---- the units from u on, where scales do not lie within 2^8 of each other (or are 0): a factor for each head and group,
+        // which follows the largest p s of that head and group, so that a token without weight in a head, and another
+        // group, take no bits from it
+        if (apart) {
+            float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;  // by head 2t + x and group c: own[x * merge_row(D) + c]
+            if (gi == 0) {
+#pragma unroll
+                for (int c = 0; c < GR; ++c) own[c] = own[merge_row(D) + c] = f;
+            }
+#pragma unroll 1
+            for (; u < units; u += kNW) {
+                const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
+                ok = ok && (turn == 0 || mbar_wait(&F.empty[slot], (turn - 1) & 1, &F.abort, status)) &&
+                     mbar_wait(&F.full[slot], turn & 1, &F.abort, status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint8_t *kq = ring + static_cast<size_t>(slot) * SB, *kp = kq + CB, *vq = kp + PB, *vp = vq + CB;
+                const int row = r0 + token_of(gi);
+                float sc[IH][4], rise[2];
+                uint32_t vw[IH][GR][2];
+                score_unit<BITS, GR, bs>(kq, kp, row, t, q, sc);
+                load_scales<GR, bs>(vp, row, gi, t, w.L - (tok0 + u * kUnit), 0u, vw, sc);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float mn = fmaxf(sc[0][x], sc[0][x + 2]);
+                    if constexpr (IH == 2) mn = fmaxf(mn, fmaxf(sc[IH - 1][x], sc[IH - 1][x + 2]));
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                    mn = fmaxf(mn, m_run[x]);
+                    rise[x] = mn - m_run[x];
+                    m_run[x] = mn;
+                    l_run[x] *= ex2(-rise[x]);
+                }
+#pragma unroll
+                for (int i = 0; i < IH; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        sc[i][x] = ex2(sc[i][x] - m_run[x & 1]);
+                        l_run[x & 1] += sc[i][x];
+                    }
+#pragma unroll
+                for (int c = 0; c < GR; ++c) {
+                    float fc[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float al = ex2(-rise[x]);
+                        float big = 0.0f;
+                        bsum[c][x] *= al;
+#pragma unroll
+                        for (int i = 0; i < IH; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                bsum[c][x] = fmaf(sc[i][2 * h + x], hi_bf16(vw[i][c][h]), bsum[c][x]);
+                                big = fmaxf(big, sc[i][2 * h + x] * fabsf(lo_bf16(vw[i][c][h])));
+                            }
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        // What went in before weighs 2^-rise of what it did, and the factor goes up by as much; then it comes
+                        // down to bring the largest p s f of this unit into [64, 128) where that would reach 2^15.
+                        __syncwarp();
+                        const int was = static_cast<int>(__float_as_uint(own[x * merge_row(D) + c]) >> 23), e = static_cast<int>(__float_as_uint(big) >> 23);
+                        int now = min(was + static_cast<int>(fminf(rise[x], 256.0f)), 127 + kMaxFactorLog);
+                        if (e + now >= 254 + 15) now = 254 + 6 - e;
+                        fc[x] = __uint_as_float(static_cast<uint32_t>(now) << 23);
+                        __syncwarp();
+                        if (gi == 0) own[x * merge_row(D) + c] = fc[x];
+                        // O times 2^(now - was - rise), in two steps as the power of two alone may be no number
+                        const int half = (now - was) / 2;
+                        const float r0 = __uint_as_float(static_cast<uint32_t>(127 + half) << 23);
+                        const float r1 = __uint_as_float(static_cast<uint32_t>(127 + (now - was) - half) << 23) * al;
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            acc[c][m][x] = acc[c][m][x] * r0 * r1;
+                            acc[c][m][x + 2] = acc[c][m][x + 2] * r0 * r1;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < IH; ++i) {
+                        const float s0 = lo_bf16(vw[i][c][0]), s1 = lo_bf16(vw[i][c][1]);
+                        add_product<BITS>(vq, c * bs + r0 + 16 * i, gi, t, pack_f16(sc[i][0] * s0 * fc[0], sc[i][1] * s0 * fc[1]),
+                                          pack_f16(sc[i][2] * s1 * fc[0], sc[i][3] * s1 * fc[1]), acc[c]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0 && u + kNW < units) mbar_arrive(&F.empty[slot]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < GR; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float r = 1.0f / own[x * merge_row(D) + c];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        acc[c][m][x] *= r;
+                        acc[c][m][x + 2] *= r;
+                    }
+                }
+            f = 1.0f;
         }
 
         // ---- the segment's end: this warp's sums over its lanes, then the warps through shared memory
@@ -800,10 +969,20 @@ __global__ void __launch_bounds__(256) kvq_combine_kernel(const __grid_constant_
 template <int BITS, int GR, int bs>
 cudaError_t launch(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 {
+    constexpr int NT = threads_of(64 * GR);
     const size_t smem = kFixed + merge_bytes(64 * GR) + static_cast<size_t>(a.stages) * stage_bytes(64 * GR, bs, BITS);
-    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR, bs>), static_cast<int>(smem));
+    const void *kernel = reinterpret_cast<const void *>(kvq_decode_kernel<BITS, GR, bs>);
+    const cudaError_t e = set_max_dynamic_smem(kernel, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kvq_decode_kernel<BITS, GR, bs>, dim3(ctas), dim3(kThreads), smem, stream, a);
+    if constexpr (splits_registers(64 * GR)) {
+        // the consumers' share has to be there, or they would wait for it without end
+        static const bool fits = [kernel] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs * NT >= (kConsumerRegs * kNW + kProducerRegs * 4) * 32;
+        }();
+        if (!fits) return cudaErrorLaunchOutOfResources;
+    }
+    return launch_pdl(kvq_decode_kernel<BITS, GR, bs>, dim3(ctas), dim3(NT), smem, stream, a);
 }
 template <int BITS, int GR>
 cudaError_t launch_bs(const KvqAttnArgs &a, int ctas, cudaStream_t stream)

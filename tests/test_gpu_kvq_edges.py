@@ -169,3 +169,59 @@ def test_prefill_of_small_values_rounds_them_once(gain, bits):
             bound = error_bound(ref, mags, 2.0 ** -11) + np.expm1(2 * k_abs)[..., None] * mags["value"] + 2.0 ** -25 * 1.01
             err = np.abs(got[rows] - ref)
             assert (err <= bound).all(), (b, (err / bound).max())
+
+
+# ------------------------------------------------------------------ decode: values of very different size
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 333, 999])
+def test_decode_of_a_huge_value_with_no_weight(at, D, bits):
+    # a token whose values are 2^40 times the others' and whose weight is below 2^-90 changes nothing; for one head of
+    # the two it has all of the weight
+    for lens in (WHOLE, CUT):
+        cfg = _one_token(lens, D=D, bits=bits, seed=84)
+        rng = np.random.default_rng(15)
+        c = Cache(cfg)
+        u = rng.choice([-1.0, 1.0], D)
+        q = np.broadcast_to(u, (cfg.N, 8, D)).copy()
+        q[:, 1::2] *= -1
+        _queries(c, q)
+        for b, L in enumerate(lens):
+            if L <= at:
+                continue
+            k, v = 0.05 * rng.standard_normal((L, 4, D)), rng.standard_normal((L, 4, D))
+            k[at] -= 100.0 / (np.sqrt(D) * np.log2(np.e)) * u
+            v[at] *= 2.0 ** 40
+            _store(c, "k", b, k)
+            _store(c, "v", b, v)
+        c.to_gpu()
+        got = rounded(_decode(c))
+        assert c.status() == 0
+        for b, L in enumerate(lens):
+            ref, mags = _reference(c, b, slice(b, b + 1), [L])
+            for h in range(8):   # head by head: the check's norm is one of all that it gets
+                check(got[b:b + 1, h:h + 1], ref[:, h:h + 1], {n: x[:, h:h + 1] for n, x in mags.items()}, operand=0.0)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("lens", [WHOLE, CUT])
+@pytest.mark.parametrize("D", [128, 256])
+def test_decode_of_groups_of_unlike_size(D, lens, bits):
+    # each group of channels on its own, whatever the others hold
+    cfg = _one_token(lens, D=D, bits=bits, seed=85)
+    q, keys, rng = _rising(cfg, 16, 20.0)
+    c = Cache(cfg)
+    _queries(c, q)
+    gain = 2.0 ** np.repeat(np.array([40.0, -20.0, 0.0, -45.0])[:D // 64], 64)
+    for b, L in enumerate(lens):
+        if L:
+            _store(c, "k", b, keys[b])
+            _store(c, "v", b, rng.standard_normal((L, cfg.H_kv, D)) * gain)
+    c.to_gpu()
+    got = rounded(_decode(c))
+    assert c.status() == 0
+    for b, L in enumerate(lens):
+        ref, mags = _reference(c, b, slice(b, b + 1), [L])
+        for g in range(D // 64):
+            cut = slice(64 * g, 64 * g + 64)
+            check(got[b:b + 1, :, cut], ref[..., cut], {"score": mags["score"], "value": mags["value"][..., cut]}, operand=0.0)
