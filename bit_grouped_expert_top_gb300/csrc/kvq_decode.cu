@@ -15,7 +15,7 @@
 // q is scaled per head by a power of two into fp16 (2^14..2^15 at its largest
 // value, so a value keeps its 8 bits down to 2^-24 of that).  The weights
 // p_t sv_{t,c} are rounded to fp16 (2^-11 relative) after a power of two f that
-// keeps the largest scale seen below 128: f follows the data as the running
+// keeps the largest scale seen in range: f follows the data as the running
 // maximum of the softmax does.  One f does while the scales lie within 2^8 of each other,
 // as a model's do; a warp that meets others (a token or a group of channels of very different size) goes on in
 // units_apart.  p is
@@ -56,7 +56,7 @@ namespace {
 constexpr int kNW = 8;
 // + the producers of K and of V.  With D = 256 a consumer thread needs more than the 168 registers that ten or twelve
 // warps have each: the producers' warpgroup (two of its warps idle) then gives registers up (168 x 12 warps =
-// 224 x 8 + 56 x 4).  131,072 tokens of 2 heads take 23.3 us so, 24.4 without, at 8 bits 30.7 and 33.9;
+// 224 x 8 + 56 x 4).  131,072 tokens of 2 heads take 23.2 us so, 24.4 without, at 8 bits 31.0 and 33.9;
 // with D = 64 and 128, which fit in 168, the larger CTA costs 1 to 2.5%.
 __host__ __device__ constexpr bool splits_registers(int D) { return D == 256; }
 __host__ __device__ constexpr int threads_of(int D) { return (kNW + (splits_registers(D) ? 4 : 2)) * 32; }
@@ -66,11 +66,16 @@ constexpr int kMaxStages = 14;                // segments in flight <= stages < 
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kBarriers = 15;                 // named barriers 1..15, by segment
 constexpr float kNoMax = -1.7e38f;            // running maximum before any token (finite: -inf - kNoMax = -inf)
-// The factor f of the weights at most (before any token with a scale, and with scales below 2^-107):
-// a weight reaches 2^8 before the running maximum moves, and its product with f stays finite,
-// as times a scale of 0 it has to be 0.
-constexpr int kMaxFactorLog = 111;
-constexpr float kMaxFactor = 0x1p111f;
+// Weights are taken against the running maximum plus kLift: they reach 2^(8 - kLift) at most, so that sums of
+// 2^24 of them times values of any finite size stay finite.  (Small values end in fp32's smallest
+// numbers instead: outputs below about 2^-100 lose bits.)
+constexpr int kLift = 32;
+// The factor f of the weights at most: before any token with a scale, and with scales below 2^-88.
+constexpr int kMaxFactorLog = 126;
+constexpr float kMaxFactor = 0x1p126f;
+// f times the scales lies in [kLow, kHigh]: times a weight below 2^15, which fp16 holds, and down to
+// 2^-23 of the largest weight above fp16's smallest numbers.
+constexpr float kHigh = 0x1p39f, kLow = 0x1p31f;
 
 struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -609,6 +614,7 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
         }
 
         bool apart = false;
+        float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;  // the second loop's factors, by head 2t + x and group c: own[x * merge_row(D) + c]
         int u = first;
         for (; u < units; u += kNW) {
             const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
@@ -629,7 +635,7 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
             float sc[IH][4];
             score_unit<BITS, GR, bs>(kq, kp, row, t, q, sc);
             uint32_t vw[IH][GR][2];
-            load_scales<GR, bs>(vp, row, gi, t, left, (254u << 7) - (__float_as_uint(f) >> 16), vw, sc);
+            load_scales<GR, bs>(vp, row, gi, t, left, ((254u + kLift) << 7) - (__float_as_uint(f) >> 16), vw, sc);
 
             // ---- running maximum, and the power of two of the value scales: both move rarely
             float top0 = fmaxf(sc[0][0], sc[0][2]), top1 = fmaxf(sc[0][1], sc[0][3]), smax = 0.0f, smin = INFINITY;
@@ -645,17 +651,17 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                     smax = fmaxf(smax, fmaxf(s0, s1));
                     smin = fminf(smin, fminf(s0, s1));
                 }
-            const bool grew = top0 > m_run[0] + 8.0f || top1 > m_run[1] + 8.0f;
-            if (__any_sync(0xffffffffu, grew || smax * f > 128.0f || smin * f < 0.5f)) {
+            const bool grew = top0 > m_run[0] + (8.0f - kLift) || top1 > m_run[1] + (8.0f - kLift);
+            if (__any_sync(0xffffffffu, grew || smax * f > kHigh || smin * f < kLow)) {
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, o));
                     smin = fminf(smin, __shfl_xor_sync(0xffffffffu, smin, o));
                 }
                 float to = f;
-                if (smax * f > 128.0f)  // f smax back into [64, 128)
-                    to = __uint_as_float(static_cast<uint32_t>(min(max(260 - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog)) << 23);
-                if (smin * to < 0.5f || (to < f * 0x1p-8f && f < kMaxFactor)) {
+                if (smax * f > kHigh)  // f smax back into the upper half of it
+                    to = __uint_as_float(static_cast<uint32_t>(min(max(260 + kLift - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog)) << 23);
+                if (smin * to < kLow || (to < f * 0x1p-8f && f < kMaxFactor)) {
                     apart = true;
                     break;
                 }
@@ -665,8 +671,8 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                     mn0 = fmaxf(mn0, __shfl_xor_sync(0xffffffffu, mn0, o));
                     mn1 = fmaxf(mn1, __shfl_xor_sync(0xffffffffu, mn1, o));
                 }
-                mn0 = fmaxf(mn0, m_run[0]);
-                mn1 = fmaxf(mn1, m_run[1]);
+                mn0 = fmaxf(mn0 + kLift, m_run[0]);
+                mn1 = fmaxf(mn1 + kLift, m_run[1]);
                 const float r = to < f ? to * (1.0f / f) : 1.0f, al0 = ex2(m_run[0] - mn0), al1 = ex2(m_run[1] - mn1);
                 f = to;
                 m_run[0] = mn0;
@@ -714,7 +720,6 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
         // which follows the largest p s of that head and group, so that a token without weight in a head, and another
         // group, take no bits from it
         if (apart) {
-            float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;  // by head 2t + x and group c: own[x * merge_row(D) + c]
             if (gi == 0) {
 #pragma unroll
                 for (int c = 0; c < GR; ++c) own[c] = own[merge_row(D) + c] = f;
@@ -738,7 +743,7 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                     if constexpr (IH == 2) mn = fmaxf(mn, fmaxf(sc[IH - 1][x], sc[IH - 1][x + 2]));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                    mn = fmaxf(mn, m_run[x]);
+                    mn = fmaxf(mn + kLift, m_run[x]);
                     rise[x] = mn - m_run[x];
                     m_run[x] = mn;
                     l_run[x] *= ex2(-rise[x]);
@@ -797,18 +802,6 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                 if (lane == 0 && u + kNW < units) mbar_arrive(&F.empty[slot]);
             }
             __syncwarp();
-#pragma unroll
-            for (int c = 0; c < GR; ++c)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float r = 1.0f / own[x * merge_row(D) + c];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        acc[c][m][x] *= r;
-                        acc[c][m][x + 2] *= r;
-                    }
-                }
-            f = 1.0f;
         }
 
         // ---- the segment's end: this warp's sums over its lanes, then the warps through shared memory
@@ -821,7 +814,11 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                 for (int c = 0; c < GR; ++c) bsum[c][x] += __shfl_xor_sync(0xffffffffu, bsum[c][x], o);
             }
         }
-        const float rf = 1.0f / f;
+        float rf[GR][2];  // 1 / f, a power of two
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) rf[c][x] = __uint_as_float((254u << 23) - __float_as_uint(apart ? own[x * merge_row(D) + c] : f));
         const bool starts = w.j0 == 0, ends = w.j0 + n == nblk;
         const int part = 2 * blockIdx.x + (starts ? 1 : 0);
         auto join_sync = [&]() {
@@ -844,7 +841,7 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
             for (int c = 0; c < GR; ++c) {
                 auto out = [&](int m, int h) {
                     const float unit_scale = BITS == 4 && (m & 1) ? 0x1p20f : 0x1p24f;
-                    return fmaf(acc[c][m][2 * h + x] * unit_scale, rf, bsum[c][x]);
+                    return fmaf(acc[c][m][2 * h + x] * unit_scale, rf[c][x], bsum[c][x]);
                 };
                 *reinterpret_cast<float4 *>(dst + c * 64) = make_float4(out(0, 0), out(1, 0), out(0, 1), out(1, 1));
                 *reinterpret_cast<float4 *>(dst + c * 64 + 4) = make_float4(out(2, 0), out(3, 0), out(2, 1), out(3, 1));

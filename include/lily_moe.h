@@ -405,7 +405,8 @@ int lily_kvq_read(const lily_kvq_shape *shape, const lily_kvq_cache *cache, uint
  *         least H_q * D, a multiple of 8)
  *   out   bf16 [B][H_q][D] dense; a sequence with no tokens gets zeros
  * Cache rows at or past seq_lens[b] are not used, whatever they hold.  K and V may have any
- * finite values.  At most two kernels are enqueued, whatever the lengths.
+ * finite values, in any mixture (outputs below 2^-100 lose bits); the scores and scale * |q| * 2^24 have to be
+ * fp32 numbers.  At most two kernels are enqueued, whatever the lengths.
  */
 int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
                          const int32_t *block_table, const int32_t *seq_lens, float scale, uint16_t *out, void *ws,

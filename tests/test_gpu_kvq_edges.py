@@ -225,3 +225,20 @@ def test_decode_of_groups_of_unlike_size(D, lens, bits):
         for g in range(D // 64):
             cut = slice(64 * g, 64 * g + 64)
             check(got[b:b + 1, :, cut], ref[..., cut], {"score": mags["score"], "value": mags["value"][..., cut]}, operand=0.0)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("gain", [2.0 ** 100, 2.0 ** 121, 2.0 ** 126])
+def test_decode_of_the_largest_values(gain, D, bits):
+    # sums of weights times values stay finite up to the end of the type; equal scores, and scores that rise
+    for rise, lens in ((0.0, WHOLE), (20.0, WHOLE), (20.0, CUT)):
+        cfg = _one_token(lens, D=D, bits=bits, seed=86)
+        q, keys, rng = _rising(cfg, 17, rise)
+        c = Cache(cfg)
+        _queries(c, q)
+        for b, L in enumerate(lens):
+            if L:
+                _store(c, "k", b, keys[b])
+                _store(c, "v", b, gain * rng.uniform(0.5, 1.9, (L, cfg.H_kv, D)))
+        _check_decode(c.to_gpu())
