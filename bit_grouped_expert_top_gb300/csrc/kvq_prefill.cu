@@ -29,7 +29,7 @@
 //                memory, B K-major) of chunk i + 1, then O += P V (B with the channels
 //                contiguous) of chunk i, so the softmax runs beside them.
 //   warp 17      one thread copies the next item's q into shared memory (TMA).
-// K and V must stay within fp16: |value| >= 65520 records LILY_ERR_DEVICE_RANGE.
+// K and V must stay within fp16: |value| >= 65520, or one that is no number, records LILY_ERR_DEVICE_RANGE.
 // Measured (16 query heads on 2 KV heads of 256, 4 bits): 2,048 queries at the end of
 // 32,768 tokens 669 us (1,591 TFLOP/s, 0.83 of the measured burst matrix rate), a prompt of
 // 8,192 tokens 396 us (0.72: an item's start and end cost about eight chunks).
@@ -569,7 +569,8 @@ __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint3
         sts128(row_addr ^ (i << 4), v);
     }
     if (!(__low2float(s2) == s * 8.0f && __low2float(b2) == b && fmaf(L, fabsf(s), fabsf(b)) < 65504.0f)) {
-        if (fmaxf(fabsf(b), fabsf(fmaf(L, s, b))) >= 65520.0f) record_error(status, kErrDeviceRange);
+        // (a NaN is in no range)
+        if (!(fabsf(b) < 65520.0f && fabsf(fmaf(L, s, b)) < 65520.0f)) record_error(status, kErrDeviceRange);
         Raw<BITS> copy = raw;
         rebuild_f32<BITS>(reinterpret_cast<const uint32_t *>(copy.q), s, b, row_addr);
     }

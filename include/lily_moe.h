@@ -420,9 +420,9 @@ int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cach
  *   q     bf16 [N][H_q][D] (q_stride as above), rows by cu_q int32 [B+1]
  *   out   bf16 [N][H_q][D] dense; rows from cu_q[B] on are left as they were
  * K and V are rebuilt in fp16, each value rounded once: a used group that can hold a
- * value of 65520 or more in magnitude records LILY_ERR_DEVICE_RANGE (lily_kvq_attn_decode
- * has no such limit), and values below 2^-14 keep fewer bits (multiples of 2^-24).  Two kernels are
- * enqueued; N = 0 enqueues nothing.
+ * value of 65520 or more in magnitude, or whose scale or bias is not finite, records
+ * LILY_ERR_DEVICE_RANGE (lily_kvq_attn_decode has no such limit), and values below 2^-14
+ * keep fewer bits (multiples of 2^-24).  Two kernels are enqueued; N = 0 enqueues nothing.
  */
 int lily_kvq_attn_prefill(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q,
                           int64_t q_stride, int32_t N, const int32_t *cu_q, const int32_t *block_table,

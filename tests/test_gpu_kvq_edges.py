@@ -171,6 +171,23 @@ def test_prefill_of_small_values_rounds_them_once(gain, bits):
             assert (err <= bound).all(), (b, (err / bound).max())
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("n", ["k", "v"])
+@pytest.mark.parametrize("scale,bias", [(0x7FC0, 0x3F80), (0x3F80, 0x7FC0), (0x7F80, 0x3F80), (0x3F80, 0xFF80), (0xFFC0, 0xFFC0)])
+def test_prefill_reports_parameters_that_are_no_numbers(scale, bias, n, bits):
+    cfg = KvqConfig("nan", lens=(200, 100), new=(5, 7), D=64, bits=bits, seed=82)
+    c = Cache(cfg, n_query=cfg.N).to_gpu()
+    _prefill(c)
+    assert c.status() == 0
+    rows = kvq.rows_of(c.h[n + "_sb"], c.table[1], 50, 1)
+    rows[0, 1, 0] = scale, bias
+    kvq.write_rows(c.h[n + "_sb"], c.table[1], 50, rows)
+    c.to_gpu()
+    got = _prefill(c)
+    assert c.status() == RANGE_ERR
+    assert torch.isfinite(got[:5]).all()   # the other sequence is not touched by it
+
+
 # ------------------------------------------------------------------ decode: values of very different size
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("D", [64, 128, 256])
