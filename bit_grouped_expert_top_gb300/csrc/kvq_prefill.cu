@@ -18,7 +18,7 @@
 //                limit), then per chunk S from tensor memory, the softmax weights back
 //                into it as fp16 (the A operand of P V), at the end O out of it.  The
 //                running maximum moves only when a score passes it by 8 (in powers of
-//                two; the weights then stay below 2^8), so O in tensor memory is
+//                two; the weights then stay below 2^15, see kLift), so O in tensor memory is
 //                rescaled rarely.  The next item's q is converted before O is read, so
 //                its first scores are computed meanwhile.
 //   warps 8..15  rebuild K and V of a chunk in fp16 (rounded once) into swizzled
@@ -70,6 +70,10 @@ constexpr int kBox = kChunk * 128;         // [64 tokens][64 channels] fp16, 128
 constexpr int kMaxBufs = 4;                // buffers of K and of V, at most
 constexpr uint32_t kTmemCols = 512;
 constexpr float kNoMax = -1.7e38f;
+// Weights are taken against the running maximum less kLift: a row's largest one is 2^7 to 2^15, so that fp16 rounds
+// the others by 2^-11 of themselves down to 2^-21 of it, and smaller ones by 2^-32 of it at most (as
+// many small weights beside a large one may be all that a row is made of).
+constexpr float kLift = 7.0f;
 
 struct Fixed {
     uint64_t k_full[kMaxBufs], k_free[kMaxBufs], v_full[kMaxBufs], v_free[kMaxBufs], s_full[2], p_full[2];
@@ -720,7 +724,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                         mx[(x >> 1) & 3] = fmaxf(fmaxf(mx[(x >> 1) & 3], __uint_as_float(s[x])), __uint_as_float(s[x + 1]));
                     // (after its barrier all of the row's S is in registers, so P may overwrite it)
                     const float top = others(sb, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), larger);
-                    const float mn = top > -INFINITY ? top * item_mul : kNoMax;
+                    const float mn = top > -INFINITY ? fmaf(top, item_mul, -kLift) : kNoMax;
                     if (__any_sync(0xffffffffu, mn > m_run + 8.0f)) {  // the same in all parts
                         const float to = fmaxf(m_run, mn), al = ex2(m_run - to);
                         m_run = to;

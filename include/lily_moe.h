@@ -422,7 +422,8 @@ int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cach
  * K and V are rebuilt in fp16, each value rounded once: a used group that can hold a
  * value of 65520 or more in magnitude, or whose scale or bias is not finite, records
  * LILY_ERR_DEVICE_RANGE (lily_kvq_attn_decode has no such limit), and values below 2^-14
- * keep fewer bits (multiples of 2^-24).  Two kernels are enqueued; N = 0 enqueues nothing.
+ * keep fewer bits (multiples of 2^-24).  The softmax's weights are rounded to fp16: each is off by
+ * at most 2^-11 of itself or 2^-32 of its row's largest.  Two kernels are enqueued; N = 0 enqueues nothing.
  */
 int lily_kvq_attn_prefill(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q,
                           int64_t q_stride, int32_t N, const int32_t *cu_q, const int32_t *block_table,

@@ -188,6 +188,36 @@ def test_prefill_reports_parameters_that_are_no_numbers(scale, bias, n, bits):
     assert torch.isfinite(got[:5]).all()   # the other sequence is not touched by it
 
 
+# ------------------------------------------------------------------ prefill: small weights
+@pytest.mark.parametrize("gap", [10.3, 18.3, 22.4, 24.5, 26.2])
+@pytest.mark.parametrize("D,new", [(64, 3), (128, 70), (256, 300)])
+def test_prefill_of_many_small_weights_behind_a_large_one(D, new, gap):
+    # one token whose score is `gap` powers of two above all others, and whose value is 0: the output is what thousands
+    # of small weights add up to.  A weight is rounded to fp16 at 2^7 or more for the largest: off by 2^-11 of itself or
+    # by 2^-25 / 2^7 of the largest.
+    L = 4096
+    cfg = KvqConfig("sink", lens=(L,), new=(new,), D=D, seed=83)
+    rng = np.random.default_rng(14)
+    c = Cache(cfg, n_query=cfg.N)
+    _queries(c, np.ones((new, cfg.H_q, D)))
+    k = np.zeros((L, cfg.H_kv, D))
+    k[0] = 1.0
+    v = rng.uniform(0.5, 1.5, (L, cfg.H_kv, D))
+    v[0] = 0.0
+    _store(c, "k", 0, k)
+    _store(c, "v", 0, v)
+    c.to_gpu()
+    scale = gap / (D * np.log2(np.e))
+    got = rounded(_prefill(c, scale=scale))
+    assert c.status() == 0
+    pick = np.unique(np.linspace(0, new - 1, 12).astype(int))
+    ref, mags = _reference(c, 0, pick, L - new + 1 + pick, scale)
+    vm = c.sequence(0)[3]
+    floor = np.repeat(vm.sum(0), cfg.H_q // cfg.H_kv, 0)[None] * 2.0 ** -32
+    err, bound = np.abs(got[pick] - ref), error_bound(ref, mags, 2.0 ** -11) + floor
+    assert np.isfinite(got).all() and (err <= bound).all(), (err / bound).max()
+
+
 # ------------------------------------------------------------------ decode: values of very different size
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("D", [64, 128, 256])
