@@ -67,7 +67,9 @@ class lily_kvq_shape(ctypes.Structure):
 class lily_kvq_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k_q", "k_sb", "v_q", "v_sb")] + [
         (n, ctypes.c_int64) for n in ("n_blocks", "code_bytes")]
-    device = 0  # CUDA device of the arrays (not part of the C struct)
+    # not part of the C struct: CUDA device of the arrays, and the shape of a block's codes (None: not known)
+    device = 0
+    block = None
 
 
 class lily_moe_decode_trace(ctypes.Structure):
@@ -379,6 +381,7 @@ def make_kvq_cache(tensors: Dict[str, torch.Tensor]) -> lily_kvq_cache:
     cache = lily_kvq_cache(_ptr(k_q), _ptr(tensors["k_sb"]), _ptr(tensors["v_q"]), _ptr(tensors["v_sb"]),
                            k_q.shape[0], k_q.numel())
     cache.device = k_q.get_device()
+    cache.block = tuple(k_q.shape[1:])
     return cache
 
 
@@ -433,6 +436,13 @@ def _need_tokens(name: str, t, heads: int, D: int, dev: int) -> None:
           f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
 
 
+def _need_block(shape, cache) -> None:
+    """A cache of other heads, blocks or bits can have as many bytes of codes, but other ones of parameters."""
+    block = (shape.H_kv, shape.D >> 6, shape.block_size, 8 * shape.bits)
+    _need(cache.block in (None, block),
+          f"cache: blocks of {cache.block} (KV heads, groups, tokens, bytes of codes), the shape has {block}")
+
+
 def _need_table(t, shape, dev: int) -> None:
     _need(t.shape == (shape.B, shape.max_blocks),
           f"block_table: expected [{shape.B}][{shape.max_blocks}], got {list(t.shape)}")
@@ -452,8 +462,10 @@ def _kvq_copy(fn: str, shape, cache, k, v, cu, starts, block_table, ws, stream, 
             and starts.dtype is _I32 and starts.numel() >= B and starts.is_contiguous()
             and block_table.dtype is _I32 and block_table.shape == (B, shape.max_blocks) and block_table.is_contiguous()
             and ws.dtype is _U8 and ws.is_contiguous()
+            and cache.block in (None, (H, D >> 6, shape.block_size, 8 * shape.bits))
             and dev >= 0 and dev == _current_device() == cache.device == v.get_device() == cu.get_device()
             == starts.get_device() == block_table.get_device() == ws.get_device()):
+        _need_block(shape, cache)
         _need(k.dtype is _BF16, f"k: expected bfloat16, got {k.dtype}")
         _need(v.shape[0] == k.shape[0], f"k has {k.shape[0]} tokens, v {v.shape[0]}")
         dev = _need_device("k", k, cache)
@@ -494,10 +506,12 @@ def _kvq_attention(shape, cache, q, cu_q, block_table, seq_lens, out, ws, scale,
             and seq_lens.dtype is _I32 and seq_lens.numel() >= B and seq_lens.is_contiguous()
             and out.dtype is _BF16 and out.numel() >= size[0] * H * D and out.is_contiguous()
             and ws.dtype is _U8 and ws.is_contiguous()
+            and cache.block in (None, (shape.H_kv, D >> 6, shape.block_size, 8 * shape.bits))
             and dev >= 0 and dev == _current_device() == cache.device == block_table.get_device() == seq_lens.get_device()
             == out.get_device() == ws.get_device()
             and (size[0] == B if cu_q is None else cu_q.dtype is _I32 and cu_q.numel() > B and cu_q.is_contiguous()
                  and cu_q.get_device() == dev)):
+        _need_block(shape, cache)
         _need(q.dtype is _BF16 and q.dim() == 3 and q.shape[1] == H and q.shape[2] == D,
               f"q: expected bfloat16 [n][{H}][{D}], got {q.dtype} {list(q.shape)}")
         dev = _need_device("q", q, cache)

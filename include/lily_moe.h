@@ -363,7 +363,8 @@ typedef struct lily_kvq_cache {
     uint8_t *v_q;
     uint16_t *v_sb;
     int64_t n_blocks;    /* blocks in each of the four arrays */
-    int64_t code_bytes;  /* bytes of k_q, and of v_q: n_blocks * H_kv * D * block_size * bits / 8 */
+    int64_t code_bytes;  /* bytes of k_q, and of v_q: n_blocks * H_kv * D * block_size * bits / 8 (checked against the
+                            shape; a cache of another layout with as many bytes is not noticed) */
 } lily_kvq_cache;
 
 /*
