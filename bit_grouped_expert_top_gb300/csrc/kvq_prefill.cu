@@ -209,10 +209,12 @@ __device__ __forceinline__ void pair_sync()  // every thread of the CTA, or of b
     else
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on a barrier of the first CTA of the pair.  What it announces has been made
-// visible by its own fences (shared memory: the async proxy's; tensor memory: wait::st and
-// before_thread_sync); a release at cluster scope on top waited for every access in
-// flight, ~1000 cycles a chunk.
+// Arrives on a barrier of the first CTA of the pair.  What it announces is memory of this CTA that the MMAs of
+// the first one read: shared memory, made visible to the tensor cores by the writers' proxy fences, and tensor memory
+// (wait::st and before_thread_sync).  The order across CTAs is the release fence here, at cluster scope and for shared memory, before an
+// arrival at that scope, and the acquire at cluster scope of first_wait.  (An arrival of the plain form releases to its
+// own CTA only; with release.cluster it waits for every access in flight: 2,048 tokens on 32,768 took 676 us
+// with the first, 959 with the second, 686 so.)
 template <int CG>
 __device__ __forceinline__ void arrive_first(uint64_t *bar)
 {
@@ -222,8 +224,40 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar)
         asm volatile(
             "{\n\t.reg .b32 r;\n\t"
             "mapa.shared::cluster.u32 r, %0, 0;\n\t"
-            "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+            "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+            "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
             : "memory");
+}
+// The first CTA's wait for such a barrier, by a whole warp: mbar_wait with acquire at cluster scope.
+template <int CG>
+__device__ __forceinline__ bool first_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status)
+{
+    if constexpr (CG == 1) return warp_wait(bar, parity, abort_flag, status);
+    const uint32_t addr = smem_u32(bar);
+    auto done = [&]() {
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(r)
+            : "r"(addr), "r"(parity), "r"(20000u)
+            : "memory");
+        return r != 0;
+    };
+    bool ok = done();
+    if (!ok) {
+        const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+        while (!(ok = done()) && !*abort_flag) {
+            if (global_timer_ns() - t0 > LILY_WAIT_LIMIT_NS) {
+                record_error(status, kErrDeviceTimeout);
+                *abort_flag = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 template <int CG>
 __device__ __forceinline__ void alloc_tmem(uint32_t *dst)
@@ -953,12 +987,12 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
         Share h;
         while (rank == 0 && ok && next_share(a, w, h, TI)) {
             const int n = __shfl_sync(0xffffffffu, h.n, 0);
-            if (!(ok = warp_wait(&F.q_full, items & 1, &F.abort, status))) break;
+            if (!(ok = first_wait<CG>(&F.q_full, items & 1, &F.abort, status))) break;
             tc_fence_after();
             for (int i = 0; i <= n && ok; ++i) {
                 if (i < n) {
                     const int x = it + i, buf = x % kBufs, sb = x & 1;
-                    if (!(ok = warp_wait(&F.k_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
+                    if (!(ok = first_wait<CG>(&F.k_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t lo = static_cast<uint32_t>(kd) + buf * (BB >> 4), hi = static_cast<uint32_t>(kd >> 32);
@@ -975,9 +1009,9 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                 }
                 if (i > 0) {
                     const int x = it + i - 1, buf = x % kBufs, sb = x & 1;
-                    if (i == 1 && items > 0 && !(ok = warp_wait(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
-                    if (!(ok = warp_wait(&F.v_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
-                    if (!(ok = warp_wait(&F.p_full[sb], (x >> 1) & 1, &F.abort, status))) break;
+                    if (i == 1 && items > 0 && !(ok = first_wait<CG>(&F.o_free, (items - 1) & 1, &F.abort, status))) break;
+                    if (!(ok = first_wait<CG>(&F.v_full[buf], (x / kBufs) & 1, &F.abort, status))) break;
+                    if (!(ok = first_wait<CG>(&F.p_full[sb], (x >> 1) & 1, &F.abort, status))) break;
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t lo = static_cast<uint32_t>(vd) + buf * (BB >> 4), hi = static_cast<uint32_t>(vd >> 32);
