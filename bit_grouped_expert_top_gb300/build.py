@@ -6,8 +6,9 @@ skipped when the library is newer than every source and header.
 
 Besides the product library there is one test-only variant,
 ``liblily_moe_stalltest.so``, built from the same sources with two macros: the
-pipeline waits of the grouped GEMM give up after 1 ms instead of 2 s, and for
-T == 77 the epilogue first waits on a barrier that nothing completes.  The
+pipeline waits of the kernels give up after 1 ms instead of 2 s, and for T == 77
+(tokens, sequences of a quantised-cache decode, query tokens of a prefill) the
+epilogue, or the first unit, first waits on a barrier that nothing completes.  The
 failure-path tests use it to make a bounded wait run out on purpose and check
 that the kernel reports LILY_ERR_DEVICE_TIMEOUT, drains its in-flight work and
 leaves the GPU usable.  The product library is never built with these macros.

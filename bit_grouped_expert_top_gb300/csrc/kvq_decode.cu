@@ -81,6 +81,9 @@ struct Fixed {
     uint64_t full[kMaxStages], empty[kMaxStages];
     int abort, b0, len0, pre, begin, total, used, sum[kMaxThreads / 32];
     alignas(8) float ml[kNW][8][2];
+#ifdef LILY_TEST_STALL_T
+    uint64_t never;  // test builds only: a barrier nothing arrives on
+#endif
 };
 constexpr int kFixed = (sizeof(Fixed) + 127) / 128 * 128;
 
@@ -514,6 +517,9 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
             mbar_init(&F.full[i], 2);
             mbar_init(&F.empty[i], bs / kUnit);
         }
+#ifdef LILY_TEST_STALL_T
+        mbar_init(&F.never, 1);
+#endif
         F.abort = 0;
         fence_mbar_init();
     }
@@ -613,6 +619,11 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                 for (int x = 0; x < 4; ++x) acc[c][m][x] = 0.0f;
         }
 
+#ifdef LILY_TEST_STALL_T
+        // Test builds only: with that many sequences the first CTA's first unit waits for a barrier that nothing completes, so
+        // that the wait runs out and every role gives up.
+        if (a.N == LILY_TEST_STALL_T && blockIdx.x == 0 && unit + first == 0) ok = warp_wait(&F.never, 0, &F.abort, status);
+#endif
         bool apart = false;
         float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;  // the second loop's factors, by head 2t + x and group c: own[x * merge_row(D) + c]
         int u = first;

@@ -82,6 +82,9 @@ struct Fixed {
     int abort, b0, m0, L0, q0;
     long long pre, per, begin, total, used, sum[kMaxWarps];
     float xch[2][4][kRows];  // [chunk parity][part of the columns][row]
+#ifdef LILY_TEST_STALL_T
+    uint64_t never;  // test builds only: a barrier nothing arrives on
+#endif
 };
 constexpr int kFixed = 5120;
 static_assert(sizeof(Fixed) <= kFixed, "barriers and scratch");
@@ -647,6 +650,9 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
         mbar_init(&F.q_free, R::soft);
         mbar_init(&F.o_free, CG * R::soft);
         mbar_init(&F.drain, 1);
+#ifdef LILY_TEST_STALL_T
+        mbar_init(&F.never, 1);
+#endif
         F.abort = 0;
         fence_mbar_init();
     }
@@ -741,6 +747,11 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
             const float item_mul = mul;
             for (int i = 0; i < h.n; ++i, ++it) {
                 const int sb = it & 1;
+#ifdef LILY_TEST_STALL_T
+                // Test builds only: with that many query tokens the first chunk of every second CTA waits for a barrier that
+                // nothing completes, so that the wait runs out and every role of its pair gives up.
+                if (a.N == LILY_TEST_STALL_T && blockIdx.x % 2 == 0 && threadIdx.x < 32 && it == 0) ok = ok && warp_wait(&F.never, 0, &F.abort, status);
+#endif
                 ok = ok && warp_wait(&F.s_full[sb], (it >> 1) & 1, &F.abort, status);
                 if (any_row) {
                     tc_fence_after();
