@@ -575,9 +575,9 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
             advance(a, w, n);
         }
         // no copy into this CTA's shared memory may still be in flight at exit
+        const uint64_t t0 = global_timer_ns();
         for (int i = issued > NS ? issued - NS : 0; i < issued; ++i) {
             const uint32_t addr = smem_u32(&F.full[i % NS]);
-            const uint64_t t0 = global_timer_ns();
             while (!mbar_try_wait(addr, (i / NS) & 1))
                 if (global_timer_ns() - t0 > LILY_DRAIN_LIMIT_NS) {
                     record_error(status, kErrDeviceTimeout);
