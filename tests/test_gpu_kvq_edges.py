@@ -289,3 +289,30 @@ def test_decode_of_the_largest_values(gain, D, bits):
                 _store(c, "k", b, keys[b])
                 _store(c, "v", b, gain * rng.uniform(0.5, 1.9, (L, cfg.H_kv, D)))
         _check_decode(c.to_gpu())
+
+
+@pytest.mark.parametrize("gap", [10.3, 18.3, 22.4, 24.5])
+@pytest.mark.parametrize("D,bits", [(64, 4), (128, 8), (256, 4)])
+def test_decode_of_many_small_weights_behind_a_large_one(D, bits, gap):
+    # as for prefill above; the scales of the values lie within 2^7 of each other and the small weights have the larger ones:
+    # a weight times a scale is 2^5 or more in fp16 where the largest weight has it, so off by 2^-25 / 2^5 of the largest at most
+    cfg = _one_token((4096, 900) * 5, D=D, bits=bits, seed=87)
+    rng = np.random.default_rng(18)
+    c = Cache(cfg)
+    _queries(c, np.ones((cfg.N, cfg.H_q, D)))
+    for b, L in enumerate(cfg.lens):
+        k = np.zeros((L, cfg.H_kv, D))
+        k[0] = 1.0
+        v = rng.uniform(0.5, 1.5, (L, cfg.H_kv, D))
+        v[0] *= 0.02
+        _store(c, "k", b, k)
+        _store(c, "v", b, v)
+    c.to_gpu()
+    scale = gap / (D * np.log2(np.e))
+    got = rounded(_decode(c, scale))
+    assert c.status() == 0
+    for b, L in enumerate(cfg.lens):
+        ref, mags = _reference(c, b, slice(b, b + 1), [L], scale)
+        floor = np.repeat(c.sequence(b)[3].sum(0), cfg.H_q // cfg.H_kv, 0)[None] * 2.0 ** -30
+        err, bound = np.abs(got[b:b + 1] - ref), error_bound(ref, mags, 0.0) + floor
+        assert np.isfinite(got).all() and (err <= bound).all(), (err / bound).max()
