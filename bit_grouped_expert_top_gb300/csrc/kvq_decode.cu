@@ -17,10 +17,11 @@
 // p_t sv_{t,c} are rounded to fp16 (2^-11 relative) after a power of two f that
 // keeps the largest scale seen in range: f follows the data as the running
 // maximum of the softmax does.  One f does while the scales lie within 2^8 of each other,
-// as a model's do; a warp that meets others (a token or a group of channels of very different size) goes on in
-// units_apart.  p is
+// as a model's do; a warp that meets others (a token or a group of channels of very
+// different size) goes on in a second loop with a factor for each head and group (131,072
+// tokens 30.5 us where every V has a scale of 0, 23.5 else).  p is
 // taken against a running maximum that moves only when a score passes it by 8 (in
-// powers of two), which one vote per step finds; sums are fp32.
+// powers of two), which the vote that looks at the scales finds too; sums are fp32.
 //
 // Bound: the cache's bytes (36 per 64 values at 4 bits).  Work split: the cache
 // blocks of all (sequence, KV head) segments form one list that the CTAs (one per
@@ -73,8 +74,9 @@ constexpr int kLift = 32;
 // The factor f of the weights at most: before any token with a scale, and with scales below 2^-88.
 constexpr int kMaxFactorLog = 126;
 constexpr float kMaxFactor = 0x1p126f;
-// f times the scales lies in [kLow, kHigh]: times a weight below 2^15, which fp16 holds, and down to
-// 2^-23 of the largest weight above fp16's smallest numbers.
+// f times the scales lies in [kLow, kHigh]: times a weight it is 2^15 at most, which fp16 holds, and times the largest
+// weight 2^-1 at least (2^6 for the largest scales).  fp16 rounds the product by 2^-11 of itself, or by 2^-24
+// (2^-31) of what the largest weight would have there.
 constexpr float kHigh = 0x1p39f, kLow = 0x1p31f;
 
 struct Fixed {
@@ -1006,7 +1008,8 @@ cudaError_t launch_d(const KvqAttnArgs &a, int ctas, cudaStream_t stream)
 }  // namespace
 
 // A CTA for each segment, and no join, where no CTA then has much more than an even share
-// of a full cache: with n segments on 152 CTAs, where capacity (1 - n / 152) is at most 640
+// of a full cache (by the table's width, as the lengths are on the device: short sequences under a wide
+// table take the cut form): with n segments on 152 CTAs, where capacity (1 - n / 152) is at most 640
 // tokens, which cost what cutting and joining does.  Measured, one CTA each against cut (2
 // KV heads of 256): one sequence of 256 tokens 6.2 / 7.9 us, of 512 8.2 / 7.9, of 1,024
 // 11.8 / 8.1; 64 sequences of 1,024 13.9 / 21.0.  (4 heads of 128: one of 512 tokens 5.6 /

@@ -6,9 +6,10 @@
 // The tensor cores bound this one: 4 D operations per (query head, token) pair.  A CTA
 // takes 128 query rows, the G query heads of a KV head for TQ = 128 / G tokens (one
 // rebuilt K and V serves them all), against the cache in chunks of 64 tokens; a pair of
-// CTAs shares an item of 2 TQ tokens and each rebuilds half of K and V, since the rebuild
-// and not the MMAs bounds a CTA alone (2,048 queries on 32,768 tokens: 669 us with pairs,
-// 835 without).  The chunks of all items form one list that the pairs, one per two SMs,
+// CTAs shares an item of 2 TQ tokens and each rebuilds half of K and V, since with D = 256 the
+// rebuild and not the MMAs bounds a CTA alone (2,048 queries on 32,768 tokens at the time: 669 us with
+// pairs, 835 without; with D = 64 and 128 it is the chain of a tile's scores, softmax and product, which takes
+// as long as with 256).  The chunks of all items form one list that the pairs, one per two SMs,
 // share evenly (a long prompt's later tiles have more of them); an item cut between pairs
 // leaves partial results that a second kernel joins.
 // Per CTA, with every wait bounded:
@@ -31,8 +32,8 @@
 //   warp 17      one thread copies the next item's q into shared memory (TMA).
 // K and V must stay within fp16: |value| >= 65520, or one that is no number, records LILY_ERR_DEVICE_RANGE.
 // Measured (16 query heads on 2 KV heads of 256, 4 bits): 2,048 queries at the end of
-// 32,768 tokens 669 us (1,591 TFLOP/s, 0.83 of the measured burst matrix rate), a prompt of
-// 8,192 tokens 396 us (0.72: an item's start and end cost about eight chunks).
+// 32,768 tokens 683 us (1,558 TFLOP/s, 0.81 of the measured burst matrix rate), a prompt of
+// 8,192 tokens 402 us (0.71: an item's start and end cost about eight chunks).
 #include <cmath>
 #include <cstdint>
 
@@ -586,7 +587,8 @@ __device__ __noinline__ void rebuild_f32(const uint32_t *codes, float s, float b
 // scales from 2^-20 to 8176 and biases from 2^-17 are (8 significant bits above 2^-24), and 4-bit groups from
 // about -61000 to 61000 have larger scales; what a smaller scale lost the code would multiply, by up to 32.
 // The rare group that fails the test is done over in fp32.  The test comes after the stores
-// so that nothing waits for it (a 2K chunk at the end of 32K 669 us without it, 673 here, 686 with it first).
+// so that nothing waits for it (a 2K chunk at the end of 32K 669 us without it, 673 here, 686 with it first).  Where
+// every group fails it (V of 2^-24), that chunk takes 1.3 times as long.
 template <int BITS>
 __device__ __forceinline__ void rebuild(const Raw<BITS> &raw, bool exists, uint32_t row_addr, int *status)
 {

@@ -325,7 +325,8 @@ int lily_attn_decode(const lily_attn_shape *shape, const uint16_t *q, const uint
  *   code  = min(rint((x - lo) / scale), L)   (0 where scale is 0)
  *   value = code * scale + bias
  * with fp32 arithmetic, round-to-nearest-even.  |value - x| is at most about
- * scale / 2; a group of equal values is kept exactly.  The values of a group have to be
+ * scale / 2 at 4 bits; at 8 bits up to one scale at the group's upper end, as the scale is
+ * rounded by up to 2^-8 of itself.  A group of equal values is kept exactly.  The values of a group have to be
  * finite: one that is not leaves that group's codes and parameters unspecified, and
  * no other's.
  *
@@ -407,7 +408,9 @@ int lily_kvq_read(const lily_kvq_shape *shape, const lily_kvq_cache *cache, uint
  *   out   bf16 [B][H_q][D] dense; a sequence with no tokens gets zeros
  * Cache rows at or past seq_lens[b] are not used, whatever they hold.  K and V may have any
  * finite values, in any mixture (outputs below 2^-100 lose bits); the scores and scale * |q| * 2^24 have to be
- * fp32 numbers.  At most two kernels are enqueued, whatever the lengths.
+ * fp32 numbers.  A token's weight times a group's scale is rounded to fp16: off by at most 2^-11 of itself
+ * or 2^-24 of what the head's largest weight would have there.  At most two kernels are enqueued,
+ * whatever the lengths.
  */
 int lily_kvq_attn_decode(const lily_kvq_shape *shape, const lily_kvq_cache *cache, const uint16_t *q, int64_t q_stride,
                          const int32_t *block_table, const int32_t *seq_lens, float scale, uint16_t *out, void *ws,
