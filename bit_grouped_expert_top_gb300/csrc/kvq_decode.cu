@@ -627,7 +627,8 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
         if (a.N == LILY_TEST_STALL_T && blockIdx.x == 0 && unit + first == 0) ok = warp_wait(&F.never, 0, &F.abort, status);
 #endif
         bool apart = false;
-        float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;  // the second loop's factors, by head 2t + x and group c: own[x * merge_row(D) + c]
+        // the second loop's factors, in the padding of the warp's rows: of head 2t + x and group c own[x * merge_row(D) + c]
+        float *own = merge + (warp * 8 + 2 * t) * merge_row(D) + D;
         int u = first;
         for (; u < units; u += kNW) {
             const int st = stage0 + u / ups, turn = __umulhi(st, a.stages_inv), slot = st - turn * NS, r0 = (u % ups) * kUnit;
@@ -672,8 +673,10 @@ __global__ void __launch_bounds__(threads_of(64 * GR) + (splits_registers(64 * G
                     smin = fminf(smin, __shfl_xor_sync(0xffffffffu, smin, o));
                 }
                 float to = f;
-                if (smax * f > kHigh)  // f smax back into the upper half of it
-                    to = __uint_as_float(static_cast<uint32_t>(min(max(260 + kLift - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog)) << 23);
+                if (smax * f > kHigh) {  // f smax back into [kHigh / 2, kHigh)
+                    const int ex = min(max(260 + kLift - static_cast<int>(__float_as_uint(smax) >> 23), 1), 127 + kMaxFactorLog);
+                    to = __uint_as_float(static_cast<uint32_t>(ex) << 23);
+                }
                 if (smin * to < kLow || (to < f * 0x1p-8f && f < kMaxFactor)) {
                     apart = true;
                     break;

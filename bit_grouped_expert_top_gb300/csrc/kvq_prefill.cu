@@ -32,8 +32,8 @@
 //   warp 17      one thread copies the next item's q into shared memory (TMA).
 // K and V must stay within fp16: |value| >= 65520, or one that is no number, records LILY_ERR_DEVICE_RANGE.
 // Measured (16 query heads on 2 KV heads of 256, 4 bits): 2,048 queries at the end of
-// 32,768 tokens 683 us (1,558 TFLOP/s, 0.81 of the measured burst matrix rate), a prompt of
-// 8,192 tokens 402 us (0.71: an item's start and end cost about eight chunks).
+// 32,768 tokens 677 us (1,573 TFLOP/s, 0.82 of the measured burst matrix rate), a prompt of
+// 8,192 tokens 400 us (0.72: an item's start and end cost about eight chunks).
 #include <cmath>
 #include <cstdint>
 
@@ -213,24 +213,26 @@ __device__ __forceinline__ void pair_sync()  // every thread of the CTA, or of b
     else
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives on a barrier of the first CTA of the pair.  What it announces is memory of this CTA that the MMAs of
-// the first one read: shared memory, made visible to the tensor cores by the writers' proxy fences, and tensor memory
-// (wait::st and before_thread_sync).  The order across CTAs is the release fence here, at cluster scope and for shared memory, before an
-// arrival at that scope, and the acquire at cluster scope of first_wait.  (An arrival of the plain form releases to its
-// own CTA only; with release.cluster it waits for every access in flight: 2,048 tokens on 32,768 took 676 us
-// with the first, 959 with the second, 686 so.)
-template <int CG>
+// Arrives on a barrier of the first CTA of the pair.  What it announces is memory of this CTA that the MMAs of the
+// first one read, so the arrival and the wait for it are of cluster scope.  Tensor memory needs no more than that between
+// before_thread_sync and after_thread_sync.  For shared memory (kShared; made visible to the tensor cores by the
+// writers' proxy fences) a release fence comes before the arrival, restricted to shared memory, and first_wait acquires.
+// (An arrival of the plain form releases to its own CTA only; release.cluster waits for every access in flight:
+// 2,048 tokens on 32,768 took 676 us with the first, 959 with the second, 686 with this fence before every arrival,
+// 677 so.)
+template <int CG, bool kShared>
 __device__ __forceinline__ void arrive_first(uint64_t *bar)
 {
-    if constexpr (CG == 1)
+    if constexpr (CG == 1) {
         mbar_arrive(bar);
-    else
+    } else {
+        if constexpr (kShared) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
         asm volatile(
             "{\n\t.reg .b32 r;\n\t"
             "mapa.shared::cluster.u32 r, %0, 0;\n\t"
-            "fence.release.sync_restrict::shared::cta.cluster;\n\t"
             "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
             : "memory");
+    }
 }
 // The first CTA's wait for such a barrier, by a whole warp: mbar_wait with acquire at cluster scope.
 template <int CG>
@@ -734,7 +736,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                arrive_first<CG>(&F.q_full);
+                arrive_first<CG, false>(&F.q_full);
                 mbar_arrive(&F.q_free);
             }
         };
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) arrive_first<CG>(&F.p_full[sb]);
+                if (lane == 0) arrive_first<CG, false>(&F.p_full[sb]);
             }
             // ---- the item's end.  The next item's q first: the last scores of this one are in (S is full), so Q is free
             Walk w2 = w;
@@ -864,7 +866,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_first<CG>(&F.o_free);
+            if (lane == 0) arrive_first<CG, false>(&F.o_free);
             if (threadIdx.x == 0 && rank == 0 && starts && !ends) {
                 // who joins the parts of an item that starts here and goes on: up to the CTA with its last place
                 const long long last = ((F.begin + done - w.s0 + h.nch + kItemCost) * F.used - 1) / F.total;
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(Roles<NQ>::threads, 1) kvq_prefill_kernel(cons
                     rebuild<BITS>(raw[y], j * kChunk + row < w.L, item[y].addr + buf * BB, status);
                     fence_async_shared();
                     __syncwarp();
-                    if (lane == 0) arrive_first<CG>(item[y].isv ? &F.v_full[buf] : &F.k_full[buf]);
+                    if (lane == 0) arrive_first<CG, true>(item[y].isv ? &F.v_full[buf] : &F.k_full[buf]);
                     if (j + kTurns < end) fetch(y, j + kTurns, next);
                 }
             }
