@@ -40,6 +40,8 @@ class lily_moe_shape(ctypes.Structure):
 
 class lily_q4(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+    # not part of the C struct: the matrix's size and CUDA device, as make_q4 found them
+    rows = K = device = -1
 
 
 class lily_moe_weights(ctypes.Structure):
@@ -70,6 +72,26 @@ class lily_kvq_cache(ctypes.Structure):
     # not part of the C struct: CUDA device of the arrays, and the shape of a block's codes (None: not known)
     device = 0
     block = None
+
+
+class lily_norm_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H", "d", "x_type", "h_type", "w_type")]
+
+
+class lily_q4_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "rows", "K", "x_type", "out_type")]
+
+
+class lily_rope_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("N", "H_q", "H_k", "D", "rot", "interleaved")]
+
+
+class lily_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(n, ctypes.c_double) for n in ("theta", "factor", "original", "low", "high")]
+
+
+class lily_draft_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "N", "V")]
 
 
 class lily_moe_decode_trace(ctypes.Structure):
@@ -111,6 +133,15 @@ def _configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.lily_kvq_attn_decode.argtypes = [PQ, PC, P, I64, P, P, ctypes.c_float, P, P, S, P]
     L.lily_kvq_attn_prefill.argtypes = [PQ, PC, P, I64, ctypes.c_int32, P, P, P, ctypes.c_float, P, P, S, P]
     for n in ("lily_kvq_append", "lily_kvq_read", "lily_kvq_attn_decode", "lily_kvq_attn_prefill"):
+        getattr(L, n).restype = I32
+    F = ctypes.c_float
+    L.lily_rms_norm.argtypes = [ctypes.POINTER(lily_norm_shape), P, I64, P, P, P, F, F, P, P, P, P]
+    L.lily_q4_matvec.argtypes = [ctypes.POINTER(lily_q4_shape), ctypes.POINTER(lily_q4), P, I64, P, P, P]
+    L.lily_rope.argtypes = [ctypes.POINTER(lily_rope_shape), P, I64, P, I64, P, P, F, P, I64, P, I64, P]
+    L.lily_rope_frequencies.argtypes = [ctypes.POINTER(lily_rope_scaling), ctypes.c_int32, P]
+    L.lily_rope_table.argtypes = [P, ctypes.c_int32, P]
+    L.lily_draft_verify.argtypes = [ctypes.POINTER(lily_draft_shape), P, I64, P, I64, P, P, P, P, P, P, P, S, P]
+    for n in ("lily_rms_norm", "lily_q4_matvec", "lily_rope", "lily_rope_frequencies", "lily_rope_table", "lily_draft_verify"):
         getattr(L, n).restype = I32
     L.lily_moe_device_status.argtypes = [P, P]
     L.lily_moe_clear_status.argtypes = [P, P]
@@ -565,3 +596,249 @@ def lily_gdn_scan(q, k, v, alpha, beta, out, state_out, state_in=None, scale: Op
     rc = load().lily_gdn_scan(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state_in),
                               float(scale), _ptr(out), _ptr(state_out), _stream(stream))
     return _check("lily_gdn_scan", rc) if check else rc
+
+
+# ------------------------------------------------------------------ around the attention and the expert layers
+_F32, _E4M3, _I64 = torch.float32, torch.float8_e4m3fn, torch.int64
+_TYPE = {_BF16: 0, _F32: 1, _E4M3: 2}  # LILY_BF16, LILY_F32, LILY_E4M3
+
+
+def _need_here(name: str, t) -> int:
+    """Device of a call's first tensor, which has to be the current one."""
+    dev = t.get_device()
+    _need(dev >= 0, f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+    _need(dev == torch.cuda.current_device(),
+          f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _need_type(name: str, t, *types) -> None:
+    _need(t.dtype in types, f"{name}: expected {' or '.join(str(x) for x in types)}, got {t.dtype}")
+
+
+def _need_array(name: str, t, dtype, shape, dev: int) -> None:
+    """A dense tensor of just this shape and type on the call's device."""
+    _need(t.is_cuda, f"expected a CUDA tensor, got one on {t.device} ({name}, shape {tuple(t.shape)})")
+    _need(t.dtype is dtype and tuple(t.shape) == tuple(shape) and t.get_device() == dev and t.is_contiguous(),
+          f"{name}: expected contiguous {dtype} {list(shape)} on cuda:{dev}, got {t.dtype} {list(t.shape)} with "
+          f"strides {t.stride()} on {t.device}")
+
+
+def lily_rms_norm(x, weight=None, y=None, y8=None, y8_scale=None, residual=None, h=None, eps: float = 1e-6,
+                  weight_offset: float = 0.0, stream=None, *, check: bool = True) -> int:
+    """Root-mean-square norm with the residual's addition (see include/lily_moe.h): x [N][d], or [N][H][d] for the heads
+    of N tokens (any token stride), bf16 or fp32; y bf16 and y8 (float8_e4m3fn, with y8_scale fp32 [..., d/64]) of x's
+    shape.  The channel's factor is weight + weight_offset (weight None: weight_offset)."""
+    size, dev, st, xt = x.shape, x.get_device(), x.stride(), x.dtype
+    n = len(size)
+    H, d = (1, size[1]) if n == 2 else (size[1], size[2]) if n == 3 else (0, 0)
+    first = y if y is not None else y8
+    if not (H > 0 and (xt is _BF16 or xt is _F32) and st[-1] == 1 and (n == 2 or H == 1 or st[1] == d) and first is not None
+            and (weight is None or ((weight.dtype is _BF16 or weight.dtype is _F32) and weight.shape == (d,)
+                                    and weight.is_contiguous() and weight.get_device() == dev))
+            and (y is None or (y.dtype is _BF16 and y.shape == size and y.is_contiguous() and y.get_device() == dev))
+            and (y8 is None) == (y8_scale is None)
+            and (y8 is None or (y8.dtype is _E4M3 and y8.shape == size and y8.is_contiguous() and y8.get_device() == dev
+                                and d & 63 == 0 and y8_scale.dtype is _F32 and y8_scale.shape == size[:-1] + (d >> 6,)
+                                and y8_scale.is_contiguous() and y8_scale.get_device() == dev))
+            and (residual is None) == (h is None)
+            and (residual is None or ((residual.dtype is _BF16 or residual.dtype is _F32) and h.dtype is residual.dtype
+                                      and residual.shape == size and h.shape == size and residual.is_contiguous()
+                                      and h.is_contiguous() and residual.get_device() == dev and h.get_device() == dev))
+            and dev >= 0 and dev == _current_device()):
+        _need(H > 0, f"x: expected [N][d] or [N][H][d] with H > 0, got {list(size)}")
+        _need_type("x", x, _BF16, _F32)
+        dev = _need_here("x", x)
+        _need(st[-1] == 1 and (n == 2 or H == 1 or st[1] == d), f"x: the channels of a token must be contiguous, got strides {st}")
+        _need(first is not None, "expected y or y8 (with y8_scale)")
+        if weight is not None:
+            _need_type("weight", weight, _BF16, _F32)
+            _need_array("weight", weight, weight.dtype, (d,), dev)
+        if y is not None:
+            _need_array("y", y, _BF16, size, dev)
+        _need((y8 is None) == (y8_scale is None), "y8 and y8_scale go together")
+        if y8 is not None:
+            _need(d % 64 == 0, f"y8: groups of 64 channels, x has {d}")
+            _need_array("y8", y8, _E4M3, size, dev)
+            _need_array("y8_scale", y8_scale, _F32, size[:-1] + (d // 64,), dev)
+        _need((residual is None) == (h is None), "residual and h go together")
+        if residual is not None:
+            _need_type("residual", residual, _BF16, _F32)
+            _need_array("residual", residual, residual.dtype, size, dev)
+            _need_array("h", h, residual.dtype, size, dev)
+        raise ValueError("tensors on different devices")
+    N = size[0]
+    shape = lily_norm_shape(N, H, d, _TYPE[xt], 0 if residual is None else _TYPE[residual.dtype],
+                            0 if weight is None else _TYPE[weight.dtype])
+    rc = (_lib or load()).lily_rms_norm(
+        shape, x.data_ptr(), st[0] if N > 1 else H * d, None if residual is None else residual.data_ptr(),
+        None if h is None else h.data_ptr(), None if weight is None else weight.data_ptr(), weight_offset, eps,
+        None if y is None else y.data_ptr(), None if y8 is None else y8.data_ptr(),
+        None if y8_scale is None else y8_scale.data_ptr(), _launch_stream(stream, dev))
+    return _check("lily_rms_norm", rc) if check else rc
+
+
+def make_q4(q, scale, bias) -> lily_q4:
+    """One 4-bit matrix of its codes (uint8 [rows][K/2]) and its bf16 scales and biases ([rows][K/64]); the
+    caller keeps the tensors alive."""
+    rows, half = q.shape if q.dim() == 2 else (0, 0)
+    _need(q.dtype is _U8 and rows > 0 and half % 32 == 0 and half > 0,
+          f"q: expected uint8 [rows][K/2], K a multiple of 64, got {q.dtype} {list(q.shape)}")
+    dev = q.get_device()
+    _need(dev >= 0 and q.is_contiguous(), f"q: expected a contiguous CUDA tensor, got strides {q.stride()} on {q.device}")
+    _need_array("scale", scale, _BF16, (rows, half // 32), dev)
+    _need_array("bias", bias, _BF16, (rows, half // 32), dev)
+    w = lily_q4(q.data_ptr(), scale.data_ptr(), bias.data_ptr())
+    w.rows, w.K, w.device = rows, 2 * half, dev
+    return w
+
+
+def lily_q4_matvec(w: lily_q4, x, out, x_scale=None, stream=None, *, check: bool = True) -> int:
+    """Up to 32 tokens times the 4-bit matrix of make_q4 (see include/lily_moe.h): x bf16 [T][K], or float8_e4m3fn
+    with x_scale fp32 [T][K/64] (lily_rms_norm's y8); out bf16 or fp32 [T][rows]."""
+    rows, K = w.rows, w.K
+    dev, size, st, xt, ot = x.get_device(), x.shape, x.stride(), x.dtype, out.dtype
+    if not (len(size) == 2 and size[1] == K and st[1] == 1 and (ot is _BF16 or ot is _F32) and out.shape == (size[0], rows)
+            and out.is_contiguous()
+            and (xt is _BF16 and x_scale is None or xt is _E4M3 and x_scale is not None and x_scale.dtype is _F32
+                 and x_scale.shape == (size[0], K >> 6) and x_scale.is_contiguous() and x_scale.get_device() == dev)
+            and dev >= 0 and dev == _current_device() == w.device == out.get_device()):
+        _need(x.dim() == 2 and size[1] == K, f"x: expected [T][{K}], got {list(size)}")
+        _need_type("x", x, _BF16, _E4M3)
+        dev = _need_here("x", x)
+        _need(w.device == dev, f"the matrix is on cuda:{w.device}, x on cuda:{dev}")
+        _need(st[1] == 1, f"x: the channels of a token must be contiguous, got strides {st}")
+        _need((xt is _E4M3) == (x_scale is not None), "x_scale goes with x in float8_e4m3fn, and only with it")
+        if x_scale is not None:
+            _need_array("x_scale", x_scale, _F32, (size[0], K // 64), dev)
+        _need_type("out", out, _BF16, _F32)
+        _need_array("out", out, ot, (size[0], rows), dev)
+        raise ValueError("tensors on different devices")
+    T = size[0]
+    rc = (_lib or load()).lily_q4_matvec(
+        lily_q4_shape(T, rows, K, _TYPE[xt], _TYPE[ot]), w, x.data_ptr(), st[0] if T > 1 else K,
+        None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _launch_stream(stream, dev))
+    return _check("lily_q4_matvec", rc) if check else rc
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                     low: float = 1.0, high: float = 32.0) -> torch.Tensor:
+    """Angle of each of the rot / 2 pairs a position (fp64, on the host), scaled for contexts longer than the trained
+    one: "none", "linear", "base" or "parts" (see lily_rope_frequencies in include/lily_moe.h)."""
+    _need(scaling in ROPE_SCALING, f"scaling: expected one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    out = torch.empty(max(rot // 2, 1), dtype=torch.float64)
+    c = lily_rope_scaling(ROPE_SCALING[scaling], theta, factor, original, low, high)
+    _check("lily_rope_frequencies", load().lily_rope_frequencies(c, rot, out.data_ptr()))
+    return out
+
+
+def make_rope_table(frequencies, device="cuda") -> torch.Tensor:
+    """Device table of lily_rope for these angles a position (fp64, in [0, 2 pi))."""
+    f = torch.as_tensor(frequencies, dtype=torch.float64, device="cpu").contiguous()
+    _need(f.dim() == 1 and f.numel() > 0, f"frequencies: expected a vector, got {list(f.shape)}")
+    out = torch.empty(f.numel(), dtype=_I64)
+    _check("lily_rope_table", load().lily_rope_table(f.data_ptr(), f.numel(), out.data_ptr()))
+    return out.to(device)
+
+
+def _rope_heads(name: str, t, dev: int) -> None:
+    _need(t.dtype is _BF16 and t.dim() == 3, f"{name}: expected bfloat16 [N][H][D], got {t.dtype} {list(t.shape)}")
+    _need(t.get_device() == dev, f"{name}: expected a CUDA tensor on cuda:{dev}, got one on {t.device}")
+    _need(t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1),
+          f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+
+
+def lily_rope(q, k, positions, table, q_out=None, k_out=None, interleaved: bool = False, amplitude: float = 1.0, stream=None,
+              *, check: bool = True) -> int:
+    """Rotary positions (see include/lily_moe.h): q [N][H_q][D] and k [N][H_k][D] (None: queries only) bf16 with any token
+    stride; the first 2 * len(table) channels of each head turn.  q_out and k_out default to q and k (in place)."""
+    if q_out is None:
+        q_out = q
+    if k_out is None:
+        k_out = k
+    dev, qs, st, so = q.get_device(), q.shape, q.stride(), q_out.stride()
+    D = qs[-1]
+    if k is not None and k_out is not None:
+        ks, kst, kso = k.shape, k.stride(), k_out.stride()
+        k_ok = (k.dtype is _BF16 and k_out.dtype is _BF16 and len(ks) == 3 and k_out.shape == ks and ks[0] == qs[0] and ks[2] == D
+                and ks[1] > 0 and kst[2] == 1 and kso[2] == 1 and (ks[1] == 1 or (kst[1] == D and kso[1] == D))
+                and k.get_device() == dev and k_out.get_device() == dev)
+    else:
+        k_ok = k is None and k_out is None
+    if not (k_ok and q.dtype is _BF16 and q_out.dtype is _BF16 and len(qs) == 3 and q_out.shape == qs and st[2] == 1 and so[2] == 1
+            and (qs[1] == 1 or (st[1] == D and so[1] == D)) and q_out.get_device() == dev
+            and positions.dtype is _I32 and positions.shape == (qs[0],) and positions.is_contiguous() and positions.get_device() == dev
+            and table.dtype is _I64 and table.dim() == 1 and table.is_contiguous() and table.get_device() == dev
+            and dev >= 0 and dev == _current_device()):
+        _need(q.dtype is _BF16 and q.dim() == 3, f"q: expected bfloat16 [N][H][D], got {q.dtype} {list(q.shape)}")
+        dev = _need_here("q", q)
+        _need((k is None) == (k_out is None), "k and k_out go together")
+        for name, t, like in (("q", q, q), ("q_out", q_out, q), ("k", k, k), ("k_out", k_out, k)):
+            if t is not None:
+                _rope_heads(name, t, dev)
+                _need(t.shape == like.shape and t.shape[0] == qs[0] and t.shape[2] == D and t.shape[1] > 0,
+                      f"{name}: {list(t.shape)} beside q {list(qs)}")
+        _need_array("positions", positions, _I32, (qs[0],), dev)
+        _need(table.dim() == 1, f"table: expected a vector, got {list(table.shape)}")
+        _need_array("table", table, _I64, table.shape, dev)
+        raise ValueError("tensors on different devices")
+    N, H_q = qs[0], qs[1]
+    H_k = 0 if k is None else ks[1]
+    dense_q, dense_k = H_q * D, H_k * D
+    rc = (_lib or load()).lily_rope(
+        lily_rope_shape(N, H_q, H_k, D, 2 * table.shape[0], 1 if interleaved else 0), q.data_ptr(), st[0] if N > 1 else dense_q,
+        None if k is None else k.data_ptr(), 0 if k is None else kst[0] if N > 1 else dense_k, positions.data_ptr(),
+        table.data_ptr(), amplitude, q_out.data_ptr(), so[0] if N > 1 else dense_q, None if k is None else k_out.data_ptr(),
+        0 if k is None else kso[0] if N > 1 else dense_k, _launch_stream(stream, dev))
+    return _check("lily_rope", rc) if check else rc
+
+
+LILY_DRAFT_WORKSPACE_BYTES = 256
+
+
+def alloc_draft_workspace(device="cuda") -> torch.Tensor:
+    """Workspace of lily_draft_verify (its status word)."""
+    return torch.zeros(LILY_DRAFT_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def lily_draft_verify(p, q, drafts, cu, u, r, accepted, tokens, ws, stream=None, *, check: bool = True) -> int:
+    """Accepts or refuses the N drafted tokens of B sequences and draws the token after them (see include/lily_moe.h): p
+    fp32 [N + B][V] (the target's probabilities), q fp32 [N][V] or None (drafts without probabilities), any row
+    stride; drafts int32 [N], rows by cu int32 [B+1]; uniform numbers u [N] and r [B]; accepted int32 [B] and tokens int32 [N + B]."""
+    dev, ps, st = p.get_device(), p.shape, p.stride()
+    B, N = r.shape[0] if r.dim() else 0, drafts.shape[0] if drafts.dim() else 0
+    if not (p.dtype is _F32 and len(ps) == 2 and ps[0] == N + B and st[1] == 1 and ps[1] > 0
+            and (q is None or (q.dtype is _F32 and q.shape == (N, ps[1]) and q.stride(1) == 1 and q.get_device() == dev))
+            and drafts.dtype is _I32 and drafts.dim() == 1 and drafts.is_contiguous()
+            and cu.dtype is _I32 and cu.shape == (B + 1,) and cu.is_contiguous()
+            and u.dtype is _F32 and u.shape == (N,) and u.is_contiguous() and r.dtype is _F32 and r.dim() == 1 and r.is_contiguous()
+            and accepted.dtype is _I32 and accepted.shape == (B,) and accepted.is_contiguous()
+            and tokens.dtype is _I32 and tokens.shape == (N + B,) and tokens.is_contiguous()
+            and ws.dtype is _U8 and ws.is_contiguous()
+            and dev >= 0 and dev == _current_device() == drafts.get_device() == cu.get_device() == u.get_device() == r.get_device()
+            == accepted.get_device() == tokens.get_device() == ws.get_device()):
+        _need(p.dtype is _F32 and p.dim() == 2 and ps[0] == N + B and ps[1] > 0,
+              f"p: expected float32 [{N + B}][V], got {p.dtype} {list(ps)}")
+        dev = _need_here("p", p)
+        _need(st[1] == 1, f"p: the values of a row must be contiguous, got strides {st}")
+        if q is not None:
+            _need(q.dtype is _F32 and q.shape == (N, ps[1]) and q.stride(1) == 1 and q.get_device() == dev,
+                  f"q: expected float32 [{N}][{ps[1]}] with contiguous rows on cuda:{dev}, got {q.dtype} {list(q.shape)} with "
+                  f"strides {q.stride()} on {q.device}")
+        _need_array("drafts", drafts, _I32, (N,), dev)
+        _need_array("cu", cu, _I32, (B + 1,), dev)
+        _need_array("u", u, _F32, (N,), dev)
+        _need_array("r", r, _F32, (B,), dev)
+        _need_array("accepted", accepted, _I32, (B,), dev)
+        _need_array("tokens", tokens, _I32, (N + B,), dev)
+        _need_dense("ws", ws, _U8, 1, dev)
+        raise ValueError("tensors on different devices")
+    V = ps[1]
+    rc = (_lib or load()).lily_draft_verify(
+        lily_draft_shape(B, N, V), p.data_ptr(), st[0] if N + B > 1 else V, None if q is None or N == 0 else q.data_ptr(),
+        V if q is None or N <= 1 else q.stride(0), drafts.data_ptr() if N else None, cu.data_ptr(), u.data_ptr() if N else None,
+        r.data_ptr(), accepted.data_ptr(), tokens.data_ptr(), ws.data_ptr(), ws.numel(), _launch_stream(stream, dev))
+    return _check("lily_draft_verify", rc) if check else rc

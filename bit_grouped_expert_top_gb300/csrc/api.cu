@@ -48,7 +48,7 @@ namespace {
 
 using namespace lily;
 
-constexpr int kVersion = 10200;  // 1.2.0
+constexpr int kVersion = 10300;  // 1.3.0
 
 // Unique id of the CUDA context current on this thread (the runtime's primary
 // context of the current device), 0 if none is current yet.  Caches of
@@ -349,6 +349,13 @@ int check_ws(const void *ws, size_t ws_bytes, size_t need)
     if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return LILY_ERR_MISALIGNED;
     if (ws_bytes < need) return LILY_ERR_WORKSPACE;
     return LILY_OK;
+}
+
+// A stride in elements: at least `dense`, a multiple of `of`.
+int check_stride(int64_t stride, int64_t dense, int64_t of)
+{
+    if (stride < dense || stride > (int64_t(1) << 31)) return LILY_ERR_INVALID;
+    return stride % of == 0 ? LILY_OK : LILY_ERR_MISALIGNED;
 }
 
 // ------------------------------------------------------------------ device properties
@@ -1031,6 +1038,166 @@ int lily_gdn_scan(const lily_gdn_shape *shape, const uint16_t *q, const uint16_t
     a.q = q; a.k = k; a.v = v; a.alpha = alpha; a.beta = beta;
     a.state_in = state_in; a.out = out; a.state_out = state_out;
     return to_status(launch_gdn_scan(a, stream), "Gated DeltaNet scan launch");
+}
+
+int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride, const void *residual, void *h,
+                  const void *weight, float weight_offset, float eps, uint16_t *y, uint8_t *y8, float *y8_scale,
+                  cudaStream_t stream)
+{
+    if (!shape) return LILY_ERR_INVALID;
+    const lily_norm_shape s = *shape;
+    const int64_t rows = static_cast<int64_t>(s.N) * s.H;
+    if (s.N < 0 || s.H < 1 || s.d < 1 || !(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(weight_offset))
+        return LILY_ERR_INVALID;
+    for (int t : {s.x_type, s.h_type, s.w_type})
+        if (t != LILY_BF16 && t != LILY_F32) return LILY_ERR_UNSUPPORTED;
+    if (s.d % (y8 ? 64 : 8) != 0 || s.d > 16384 || rows >= (int64_t(1) << 31)) return LILY_ERR_UNSUPPORTED;
+    int rc;
+    if ((rc = check_stride(x_stride, static_cast<int64_t>(s.H) * s.d, 8))) return rc;
+    if (s.N == 0) return LILY_OK;  // the arrays are empty and may be NULL
+    if ((rc = check_ptr(x))) return rc;
+    if (!y && !y8) return LILY_ERR_INVALID;
+    if (!y8 != !y8_scale || !residual != !h) return LILY_ERR_INVALID;
+    for (const void *p : {residual, static_cast<const void *>(h), weight, static_cast<const void *>(y),
+                          static_cast<const void *>(y8), static_cast<const void *>(y8_scale)})
+        if (p && !aligned16(p)) return LILY_ERR_MISALIGNED;
+    NormArgs a{};
+    a.rows = rows; a.H = s.H; a.d = s.d;
+    a.x = x; a.x_stride = x_stride;
+    a.residual = residual; a.h = h; a.weight = weight;
+    a.x_f32 = s.x_type == LILY_F32; a.h_f32 = s.h_type == LILY_F32; a.w_f32 = s.w_type == LILY_F32;
+    a.w_offset = weight_offset; a.eps = eps; a.inv_d = 1.0f / static_cast<float>(s.d);
+    a.y = y; a.y8 = y8; a.y8_scale = y8_scale;
+    return to_status(launch_norm(a, stream), "norm launch");
+}
+
+int lily_q4_matvec(const lily_q4_shape *shape, const lily_q4 *w, const void *x, int64_t x_stride, const float *x_scale,
+                   void *out, cudaStream_t stream)
+{
+    if (!shape || !w) return LILY_ERR_INVALID;
+    const lily_q4_shape s = *shape;
+    if (s.T < 0 || s.rows < 1 || s.K < 1) return LILY_ERR_INVALID;
+    if ((s.x_type != LILY_BF16 && s.x_type != LILY_E4M3) || (s.out_type != LILY_BF16 && s.out_type != LILY_F32))
+        return LILY_ERR_UNSUPPORTED;
+    if (s.T > kMatvecMaxT || s.K % 64 != 0 || s.K > kMatvecMaxK || s.rows >= (1 << 30)) return LILY_ERR_UNSUPPORTED;
+    const bool codes = s.x_type == LILY_E4M3;
+    int rc;
+    if ((rc = check_q4(*w))) return rc;
+    if (s.T == 0) return LILY_OK;
+    if ((rc = check_ptr(x)) || (rc = check_ptr(out))) return rc;
+    if (codes ? (rc = check_ptr(x_scale)) : x_scale != nullptr) return codes ? rc : LILY_ERR_INVALID;
+    if ((rc = check_stride(x_stride, s.K, codes ? 16 : 8))) return rc;
+    const int sms = num_sms_current();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "device query");
+    MatvecArgs a{};
+    a.T = s.T; a.rows = s.rows; a.K = s.K;
+    a.w = w->q; a.s = w->scale; a.b = w->bias;
+    a.x = x; a.x_stride = x_stride; a.x_scale = x_scale;
+    a.out = out; a.out_f32 = s.out_type == LILY_F32;
+    return to_status(launch_matvec(a, sms, stream), "4-bit matrix-vector launch");
+}
+
+int lily_rope(const lily_rope_shape *shape, const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+              const int32_t *positions, const uint64_t *table, float amplitude, uint16_t *q_out, int64_t q_out_stride,
+              uint16_t *k_out, int64_t k_out_stride, cudaStream_t stream)
+{
+    if (!shape) return LILY_ERR_INVALID;
+    const lily_rope_shape s = *shape;
+    if (s.N < 0 || s.H_q < 1 || s.H_k < 0 || s.D < 1 || s.rot < 1 || s.rot > s.D || !std::isfinite(amplitude))
+        return LILY_ERR_INVALID;
+    if (s.interleaved != 0 && s.interleaved != 1) return LILY_ERR_INVALID;
+    if (s.D % 16 != 0 || s.D > 512 || s.rot % 16 != 0) return LILY_ERR_UNSUPPORTED;
+    const int64_t heads = static_cast<int64_t>(s.H_q) + s.H_k;
+    if (heads >= (1 << 20) || s.N * heads >= (int64_t(1) << 34) / s.D) return LILY_ERR_UNSUPPORTED;
+    if (s.N == 0) return LILY_OK;
+    int rc;
+    for (const void *p : {static_cast<const void *>(q), static_cast<const void *>(positions),
+                          static_cast<const void *>(table), static_cast<const void *>(q_out)})
+        if ((rc = check_ptr(p))) return rc;
+    if ((rc = check_stride(q_stride, static_cast<int64_t>(s.H_q) * s.D, 8)) ||
+        (rc = check_stride(q_out_stride, static_cast<int64_t>(s.H_q) * s.D, 8)))
+        return rc;
+    if (q_out == q && q_out_stride != q_stride) return LILY_ERR_INVALID;
+    if (s.H_k > 0) {
+        if ((rc = check_ptr(k)) || (rc = check_ptr(k_out))) return rc;
+        if ((rc = check_stride(k_stride, static_cast<int64_t>(s.H_k) * s.D, 8)) ||
+            (rc = check_stride(k_out_stride, static_cast<int64_t>(s.H_k) * s.D, 8)))
+            return rc;
+        if (k_out == k && k_out_stride != k_stride) return LILY_ERR_INVALID;
+    }
+    RopeArgs a{};
+    a.N = s.N; a.H_q = s.H_q; a.H_k = s.H_k; a.D = s.D; a.rot = s.rot;
+    a.next = s.interleaved != 0;
+    a.copy = q_out != q || (s.H_k > 0 && k_out != k);
+    a.amplitude = amplitude;
+    a.q = q; a.k = k; a.q_out = q_out; a.k_out = k_out;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
+    a.positions = positions;
+    a.table = reinterpret_cast<const unsigned long long *>(table);
+    return to_status(launch_rope(a, stream), "rotary positions launch");
+}
+
+int lily_rope_frequencies(const lily_rope_scaling *scaling, int32_t rot, double *freq)
+{
+    if (!scaling || !freq || rot < 2 || rot % 2 != 0) return LILY_ERR_INVALID;
+    const lily_rope_scaling c = *scaling;
+    if (c.kind < LILY_ROPE_PLAIN || c.kind > LILY_ROPE_PARTS) return LILY_ERR_UNSUPPORTED;
+    if (!(c.theta > 0.0) || !std::isfinite(c.theta)) return LILY_ERR_INVALID;
+    if (c.kind != LILY_ROPE_PLAIN && (!(c.factor > 0.0) || !std::isfinite(c.factor))) return LILY_ERR_INVALID;
+    const double two_pi = 2.0 * 3.14159265358979323846;
+    if (c.kind == LILY_ROPE_PARTS &&
+        (!(c.original > 0.0) || !std::isfinite(c.original) || !(c.high > c.low) || !std::isfinite(c.high - c.low)))
+        return LILY_ERR_INVALID;
+    double theta = c.theta;
+    if (c.kind == LILY_ROPE_BASE && rot > 2) theta *= std::pow(c.factor, static_cast<double>(rot) / (rot - 2));
+    for (int32_t i = 0; i < rot / 2; ++i) {
+        double f = std::pow(theta, -2.0 * i / rot);
+        if (c.kind == LILY_ROPE_LINEAR) f /= c.factor;
+        if (c.kind == LILY_ROPE_PARTS) {
+            const double keep = std::min(1.0, std::max(0.0, (c.original * f / two_pi - c.low) / (c.high - c.low)));
+            f *= keep + (1.0 - keep) / c.factor;
+        }
+        freq[i] = f;
+    }
+    return LILY_OK;
+}
+
+int lily_rope_table(const double *freq, int32_t n, uint64_t *table)
+{
+    if (n < 0 || (n > 0 && (!freq || !table))) return LILY_ERR_INVALID;
+    const double two_pi = 2.0 * 3.14159265358979323846;
+    for (int32_t i = 0; i < n; ++i) {
+        const double turns = freq[i] / two_pi;
+        if (!(turns >= 0.0) || turns >= 1.0) return LILY_ERR_INVALID;
+        table[i] = static_cast<uint64_t>(std::round(std::ldexp(turns, 64)));  // 53 bits: below 2^64
+    }
+    return LILY_OK;
+}
+
+int lily_draft_verify(const lily_draft_shape *shape, const float *p, int64_t p_stride, const float *q, int64_t q_stride,
+                      const int32_t *drafts, const int32_t *cu, const float *u, const float *r, int32_t *accepted,
+                      int32_t *tokens, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!shape) return LILY_ERR_INVALID;
+    const lily_draft_shape s = *shape;
+    if (s.B < 0 || s.N < 0 || s.V < 1) return LILY_ERR_INVALID;
+    if (s.B > 65536 || s.V > (1 << 24) || static_cast<int64_t>(s.N) + s.B >= (int64_t(1) << 31)) return LILY_ERR_UNSUPPORTED;
+    int rc;
+    if ((rc = check_ws(ws, ws_bytes, sizeof(Ctrl)))) return rc;
+    if (s.B == 0) return LILY_OK;
+    for (const void *t : {static_cast<const void *>(p), static_cast<const void *>(cu), static_cast<const void *>(r),
+                          static_cast<const void *>(accepted), static_cast<const void *>(tokens)})
+        if ((rc = check_ptr(t))) return rc;
+    if (s.N > 0 && ((rc = check_ptr(drafts)) || (rc = check_ptr(u)))) return rc;
+    if (q && !aligned16(q)) return LILY_ERR_MISALIGNED;
+    if ((rc = check_stride(p_stride, s.V, 1)) || (q && (rc = check_stride(q_stride, s.V, 1)))) return rc;
+    VerifyArgs a{};
+    a.B = s.B; a.N = s.N; a.V = s.V;
+    a.p = p; a.q = q; a.p_stride = p_stride; a.q_stride = q_stride;
+    a.drafts = drafts; a.cu = cu; a.u = u; a.r = r;
+    a.accepted = accepted; a.tokens = tokens;
+    a.ctrl = at<Ctrl>(ws, 0);
+    return to_status(launch_verify(a, stream), "draft verification launch");
 }
 
 int lily_moe_route_noalloc(const lily_moe_shape *shape, const lily_moe_weights *w, const uint16_t *x,

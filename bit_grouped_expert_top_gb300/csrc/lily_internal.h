@@ -236,6 +236,69 @@ int kvq_prefill_tile_rows(const KvqAttnArgs &a);
 // tmQ: q as 3-D bf16 [N][H_q][D], box 64 channels x the group's heads x rows / group tokens, 128-byte swizzle.
 cudaError_t launch_kvq_prefill(const KvqAttnArgs &a, const CUtensorMap &tmQ, cudaStream_t stream);
 
+// Root-mean-square norm with the residual's addition (norm.cu).
+struct NormArgs {
+    long long rows;            // N * H
+    int H, d;
+    const void *x;             // [N][H][d], token stride x_stride
+    long long x_stride;
+    const void *residual;      // [N][H][d] or NULL
+    void *h;                   // the sum, in the residual's type
+    const void *weight;        // [d] or NULL (zeros)
+    bool x_f32, h_f32, w_f32;  // fp32 (else bf16)
+    float w_offset, eps, inv_d;
+    uint16_t *y;               // bf16 [N][H][d] or NULL
+    uint8_t *y8;               // e4m3 [N][H][d] or NULL
+    float *y8_scale;           // [N][H][d/64]
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
+
+// Rotary positions (rope.cu).
+struct RopeArgs {
+    int N, H_q, H_k, D, rot;
+    bool next;                 // pairs (2i, 2i + 1), else (i, i + rot/2)
+    bool copy;                 // some output is not its input: the channels from rot on are copied
+    float amplitude;
+    const uint16_t *q, *k;     // bf16, token strides below
+    uint16_t *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+    const int *positions;      // [N]
+    const unsigned long long *table;  // [rot/2]: f_i / 2 pi in units of 2^-64 turns
+    int heads_each;            // heads of a thread (set by launch_rope)
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
+
+// A few tokens times a 4-bit matrix (q4_matvec.cu).
+struct MatvecArgs {
+    int T, rows, K;
+    const uint8_t *w;          // [rows][K/2]
+    const uint16_t *s, *b;     // bf16 [rows][K/64]
+    const void *x;             // bf16, or e4m3, [T][K], token stride x_stride
+    long long x_stride;
+    const float *x_scale;      // [T][K/64] (e4m3) or NULL (bf16)
+    void *out;                 // [T][rows]
+    bool out_f32;
+    // set by launch_matvec
+    int wk_log;                // log2 of the warps of a CTA that share a row tile's K
+};
+constexpr int kMatvecMaxT = 32, kMatvecMaxK = 16384;
+cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream);
+
+// Draft verification (verify.cu).
+struct VerifyArgs {
+    int B, N, V;
+    const float *p;            // [N + B][V], row stride p_stride
+    const float *q;            // [N][V], row stride q_stride, or NULL
+    long long p_stride, q_stride;
+    const int *drafts;         // [N]
+    const int *cu;             // [B+1]
+    const float *u, *r;        // [N], [B]
+    int *accepted;             // [B]
+    int *tokens;               // [N + B]
+    Ctrl *ctrl;
+};
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream);
+
 // Gated DeltaNet scan (gdn.cu): CTA (16-row slice of the state, value head).
 struct GdnArgs {
     int T, H_k, H_v, d_k, d_v;

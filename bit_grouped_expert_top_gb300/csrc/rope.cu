@@ -1,0 +1,96 @@
+// Rotary positions on queries and keys, for sm_103a.
+//
+// Pair i of a head is turned by the angle pos * f_i:
+//   (a, b) -> amplitude * (a cos - b sin, a sin + b cos)
+// with the pair's channels (i, i + rot/2) or (2i, 2i + 1) of the first `rot`.
+// f_i / 2 pi is held as a 64-bit fraction of a turn, so the turns of a position modulo one are an
+// integer product modulo 2^64: exact but for the fraction's own 2^-65, at any position.  Its top 32 bits, an
+// angle off by at most 2^-32 half-turns, go to sincospif.  In fp32, pos * f_i alone would be
+// off by 2^-5 at position 2^20.
+//
+// Bound: HBM (4 bytes a channel) for a prompt, latency for a step.  A thread has the 16 channels of a pair of
+// 16-byte vectors (eight pairs to turn, or a piece of the tail to copy), and takes
+// `heads_each` heads with the sines and cosines that it works out once.
+#include <cstdint>
+
+#include "lily_internal.h"
+
+namespace lily {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <bool NEXT>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
+{
+    pdl_trigger();
+    const int parts = (a.copy ? a.D : a.rot) / 16, turn = a.rot / 16;
+    const unsigned unit = blockIdx.x * kThreads + threadIdx.x;
+    const int part = unit % parts;
+    const int heads = a.H_q + a.H_k, slices = (heads + a.heads_each - 1) / a.heads_each;
+    const int slice = unit / parts % slices;
+    const long long n = unit / parts / slices;
+    if (n >= a.N) return;
+    const bool turns = part < turn;
+    // the two vectors of this part, in channels from the head's first
+    const int v0 = turns ? part * 8 : a.rot + (part - turn) * 8;
+    const int v1 = v0 + (turns ? a.rot : a.D - a.rot) / 2;
+    pdl_wait();
+    float c[8], s[8];
+    if (turns) {
+        const long long pos = a.positions[n];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // half: pairs v0 .. v0 + 7; next: four pairs from each vector
+            const int pair = NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j;
+            const unsigned long long fraction = static_cast<unsigned long long>(pos) * a.table[pair];
+            const float half_turns = static_cast<float>(static_cast<int>(fraction >> 32)) * 0x1p-31f;
+            sincospif(half_turns, &s[j], &c[j]);
+            s[j] *= a.amplitude;
+            c[j] *= a.amplitude;
+        }
+    }
+    const int last = min(heads, (slice + 1) * a.heads_each);
+#pragma unroll 2
+    for (int h = slice * a.heads_each; h < last; ++h) {
+        const bool is_q = h < a.H_q;
+        const uint16_t *src = is_q ? a.q + n * a.q_stride + h * a.D : a.k + n * a.k_stride + (h - a.H_q) * a.D;
+        uint16_t *dst = is_q ? a.q_out + n * a.q_out_stride + h * a.D : a.k_out + n * a.k_out_stride + (h - a.H_q) * a.D;
+        const uint4 x = *reinterpret_cast<const uint4 *>(src + v0), y = *reinterpret_cast<const uint4 *>(src + v1);
+        uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        if (turns) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x0 = __uint_as_float(xs[j] << 16), x1 = __uint_as_float(xs[j] & 0xFFFF0000u);
+                const float y0 = __uint_as_float(ys[j] << 16), y1 = __uint_as_float(ys[j] & 0xFFFF0000u);
+                __nv_bfloat162 p, q;
+                if (NEXT) {  // (x0, x1) is pair j of the first vector, (y0, y1) of the second
+                    p = __floats2bfloat162_rn(x0 * c[j] - x1 * s[j], x0 * s[j] + x1 * c[j]);
+                    q = __floats2bfloat162_rn(y0 * c[j + 4] - y1 * s[j + 4], y0 * s[j + 4] + y1 * c[j + 4]);
+                } else {  // (x0, y0) and (x1, y1) are pairs 2j and 2j + 1
+                    p = __floats2bfloat162_rn(x0 * c[2 * j] - y0 * s[2 * j], x1 * c[2 * j + 1] - y1 * s[2 * j + 1]);
+                    q = __floats2bfloat162_rn(x0 * s[2 * j] + y0 * c[2 * j], x1 * s[2 * j + 1] + y1 * c[2 * j + 1]);
+                }
+                xs[j] = *reinterpret_cast<const uint32_t *>(&p);
+                ys[j] = *reinterpret_cast<const uint32_t *>(&q);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst + v0) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+        *reinterpret_cast<uint4 *>(dst + v1) = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &args, cudaStream_t stream)
+{
+    RopeArgs a = args;
+    const int heads = a.H_q + a.H_k;
+    a.heads_each = 1;
+    const long long units = static_cast<long long>(a.N) * ((a.copy ? a.D : a.rot) / 16) * ((heads + a.heads_each - 1) / a.heads_each);
+    const dim3 grid(static_cast<unsigned>((units + kThreads - 1) / kThreads)), block(kThreads);
+    return a.next ? launch_pdl(rope_kernel<true>, grid, block, 0, stream, a)
+                  : launch_pdl(rope_kernel<false>, grid, block, 0, stream, a);
+}
+
+}  // namespace lily

@@ -469,6 +469,146 @@ int lily_gdn_scan(const lily_gdn_shape *shape, const uint16_t *q, const uint16_t
                   float *state_out, cudaStream_t stream);
 
 /*
+ * Around the attention and the expert layers: the operators of a serving step between them
+ * (norms, projections, rotary positions) and after them (verification of drafted tokens).
+ *
+ * Method: the page "Perplexity libera o Lily" (noticiai.com.br) describes the expert layer, the
+ * attention and the scan, and leaves these to the model; the 4-bit format is the page's
+ * (section "Prefill e decode: onde estao os ganhos").
+ *
+ * All of them: row-major device arrays, 16-byte aligned, strides in elements; asynchronous on
+ * `stream`, one kernel each, bit-reproducible; no tokens enqueue nothing.  Outputs may overlap neither
+ * inputs nor other outputs, except where a call says so.
+ */
+enum { LILY_BF16 = 0, LILY_F32 = 1, LILY_E4M3 = 2 };  /* element types of the calls below */
+
+/*
+ * Root-mean-square norm of rows of d channels, with the residual's addition:
+ *   h = x + residual (x where there is none)
+ *   y = h / sqrt(mean_c h_c^2 + eps) * (weight + weight_offset)
+ * in fp32; the norm goes by h before it is rounded.
+ *   x          x_type [N][H][d], token n x_stride elements after the first: at least H * d; a multiple of 8
+ *              (so x may be the heads of a slice of a fused projection's output; H = 1 for hidden states)
+ *   residual   h_type [N][H][d] dense, or NULL; h: the sum, rounded once to h_type, dense; NULL if and only if
+ *              residual is.  h may be residual itself.
+ *   weight     w_type [d], or NULL (zeros: the factor is weight_offset)
+ *   y          bf16 [N][H][d] dense, or NULL
+ *   y8         e4m3 [N][H][d] dense, with y8_scale f32 [N][H][d/64], or both NULL.  Per group of 64 channels, by the
+ *              unrounded y: scale = max |y| / 448, code = e4m3(y * (448 / max |y|)), value = code * scale;
+ *              a group with max |y| < 2^-100 has codes and scale zero.
+ * At least one of y and y8 is given.  eps >= 0; a row of zeros with eps = 0 gives zeros.  Any finite x whose
+ * sum with the residual is an fp32 number: squares beyond the fp32 range are taken care of.
+ * x_type, h_type and w_type are LILY_BF16 or LILY_F32.  d a multiple of 8 (with y8 of 64) in [8, 16384]; N * H < 2^31.
+ */
+typedef struct lily_norm_shape {
+    int32_t N, H, d;                 /* tokens, rows of a token, channels of a row */
+    int32_t x_type, h_type, w_type;
+} lily_norm_shape;
+
+int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride, const void *residual, void *h,
+                  const void *weight, float weight_offset, float eps, uint16_t *y, uint8_t *y8, float *y8_scale,
+                  cudaStream_t stream);
+
+/*
+ * A few tokens times one 4-bit matrix (a projection, a vocabulary's logits):
+ *   out[t][n] = sum_k x[t][k] W[n][k],   W as in lily_q4, K = the matrix's columns.
+ *   x         x_type [T][K], token stride x_stride: at least K; a multiple of 8 (bf16) or 16 (e4m3)
+ *   x_scale   f32 [T][K/64] dense with LILY_E4M3 (lily_rms_norm's y8 and y8_scale), NULL with LILY_BF16
+ *   out       out_type (LILY_BF16, LILY_F32) [T][rows] dense
+ * Weights, codes and bf16 x enter the products unrounded, but for x below 2^-31 of its group's (64 channels of
+ * a token) largest magnitude, which is off by at most 2^-36 of that; sums are fp32.  A token with values that are
+ * not finite leaves only its own outputs unspecified, a weight row only its own row.  Intermediate sums
+ * are held over 2^24: inputs below 2^-90 lose bits.
+ * Supported: 0 <= T <= 32 (in whole groups of 8: five tokens cost what eight do); K a multiple of 64 in [64, 16384];
+ * 1 <= rows < 2^30.
+ */
+typedef struct lily_q4_shape {
+    int32_t T, rows, K;
+    int32_t x_type, out_type;
+} lily_q4_shape;
+
+int lily_q4_matvec(const lily_q4_shape *shape, const lily_q4 *w, const void *x, int64_t x_stride, const float *x_scale,
+                   void *out, cudaStream_t stream);
+
+/*
+ * Rotary positions on queries and keys: the pairs of the first `rot` channels of each head are turned by
+ * angle = positions[n] * f_i, i = 0 .. rot/2 - 1, the other channels copied:
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos),
+ * with (a, b) the channels (i, i + rot/2), or (2i, 2i + 1) where `interleaved` is not 0.
+ *   q, k       bf16 [N][H_q][D], [N][H_k][D], token strides at least H * D, multiples of 8; k and k_out may be NULL with H_k = 0
+ *   positions  int32 [N], any values
+ *   table      device, uint64 [rot/2]: round(f_i / (2 pi) * 2^64) of each pair, as lily_rope_table makes it (on the host)
+ *   q_out, k_out  as q and k, with their own strides; either may be its input itself (with the same stride)
+ * The angle is exact to 2^-31 half-turns at every position.  fp32 arithmetic, each output rounded once.
+ * Supported: D a multiple of 16 in [16, 512], rot a multiple of 16 in [16, D]; N * (H_q + H_k) * D < 2^34.
+ */
+typedef struct lily_rope_shape {
+    int32_t N, H_q, H_k, D, rot;
+    int32_t interleaved;
+} lily_rope_shape;
+
+int lily_rope(const lily_rope_shape *shape, const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+              const int32_t *positions, const uint64_t *table, float amplitude, uint16_t *q_out, int64_t q_out_stride,
+              uint16_t *k_out, int64_t k_out_stride, cudaStream_t stream);
+
+/*
+ * The frequencies f_i = theta^(-2i / rot) of lily_rope, scaled for contexts longer than the trained one
+ * (HOST arrays, fp64):
+ *   LILY_ROPE_PLAIN   as they are
+ *   LILY_ROPE_LINEAR  f_i / factor
+ *   LILY_ROPE_BASE    with theta * factor^(rot / (rot - 2))
+ *   LILY_ROPE_PARTS   by the turns r_i = original * f_i / (2 pi) that a pair makes over the original context: with
+ *                     keep = clamp((r_i - low) / (high - low), 0, 1), f_i (keep + (1 - keep) / factor)
+ * freq: [rot/2].  rot even, >= 2; theta > 0; factor > 0; PARTS: original > 0, high > low.
+ */
+enum { LILY_ROPE_PLAIN = 0, LILY_ROPE_LINEAR = 1, LILY_ROPE_BASE = 2, LILY_ROPE_PARTS = 3 };
+
+typedef struct lily_rope_scaling {
+    int32_t kind;
+    double theta, factor, original, low, high;  /* original, low, high: LILY_ROPE_PARTS only */
+} lily_rope_scaling;
+
+int lily_rope_frequencies(const lily_rope_scaling *scaling, int32_t rot, double *freq);
+
+/* table[i] = round(freq[i] / (2 pi) * 2^64), for n frequencies in [0, 2 pi) (HOST arrays). */
+int lily_rope_table(const double *freq, int32_t n, uint64_t *table);
+
+/*
+ * Verification of drafted tokens.  Sequence b has the m = cu[b+1] - cu[b] drafts x_i = drafts[cu[b] + i], the
+ * target's probabilities p_i = p[cu[b] + b + i] for i = 0 .. m (row i is what the target expects after i drafts), the draft
+ * model's q_i = q[cu[b] + i] and uniform numbers u[cu[b] + i] and r[b] in [0, 1).  Draft i is accepted if
+ * those before it are and
+ *   u_i * q_i(x_i) < p_i(x_i)     (compared exactly);
+ * with n drafts accepted, the token after them is drawn from weight = max(p_n - q_n, 0) if n < m (from p_n if that is
+ * zero everywhere), from weight = p_m if n = m: the smallest v with
+ *   sum_{w <= v} weight(w) > r_b * sum_w weight(w).
+ * Without draft probabilities (q NULL: drafts that were looked up, or the draft model's likeliest) q_i is 1 at x_i and
+ * 0 elsewhere.  The tokens are distributed as the target's own.
+ *   p         f32 [N + B][V], row stride p_stride >= V;  q  f32 [N][V], row stride q_stride >= V, or NULL
+ *   drafts    int32 [N];  cu  int32 [B+1], ascending from 0;  u  f32 [N];  r  f32 [B].  N is at least cu[B]; drafts, q and u
+ *             may be NULL with N = 0
+ *   accepted  int32 [B]: n
+ *   tokens    int32 [N + B]: those of sequence b at cu[b] + b + i: the accepted drafts (i < n), the drawn token
+ *             (i = n), -1 (n < i <= m).  Entries from cu[B] + B on are left as they were.
+ *   ws        at least LILY_DRAFT_WORKSPACE_BYTES, for the status word
+ * Probabilities are in [0, 1] and a row's sum below 4; they count in units of 2^-62, rounded down, and their sums
+ * are exact.  (Values below 0 and NaN count as 0, above 1 as 1.)
+ * Device-detected: a draft outside [0, V) records LILY_ERR_DEVICE_INDEX and counts as refused (with q NULL, nothing is
+ * then taken out of p); bounds in cu that descend, or leave [0, N], record it and leave that sequence's outputs alone; a row
+ * without any weight records LILY_ERR_DEVICE_RANGE and gives the token -1.
+ * Supported: 0 <= B <= 65536, N >= 0, N + B < 2^31, 1 <= V <= 2^24.
+ */
+#define LILY_DRAFT_WORKSPACE_BYTES 256
+
+typedef struct lily_draft_shape {
+    int32_t B, N, V;    /* sequences, drafts of all of them, vocabulary */
+} lily_draft_shape;
+
+int lily_draft_verify(const lily_draft_shape *shape, const float *p, int64_t p_stride, const float *q, int64_t q_stride,
+                      const int32_t *drafts, const int32_t *cu, const float *u, const float *r, int32_t *accepted,
+                      int32_t *tokens, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * Routing without a caller workspace.  The method has no counterpart: this entry
  * point exists for callers that may not allocate device memory when they call
  * the layer, e.g. a plugin that runs inside another engine's fixed memory
