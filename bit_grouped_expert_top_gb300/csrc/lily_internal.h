@@ -279,7 +279,7 @@ struct MatvecArgs {
     void *out;                 // [T][rows]
     bool out_f32;
     // set by launch_matvec
-    int ranks;                 // CTAs of a cluster that share K
+    int ranks, stages;         // CTAs of a cluster that share K, stages of a warp's ring
     int wk_log;                // log2 of the warps of a CTA that share a row tile's K
 };
 constexpr int kMatvecMaxT = 32, kMatvecMaxK = 16384;

@@ -31,27 +31,32 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPitch = 20;  // floats between tokens of a joined tile: the fragment's stores meet no bank twice
+constexpr int kPitch = 20;      // floats between tokens of a joined tile: the fragment's stores meet no bank twice
+constexpr int kTileBytes = 2560;  // a quad of 16 rows in the ring: 128 bytes of codes, 16 of scales, 16 of biases a row
+static_assert(kTileBytes >= 4 * 8 * kPitch * 4, "a tile's sums of 32 tokens fit its slot");
+constexpr int kMaxSmem = 226 * 1024;
 
-__device__ __forceinline__ uint2 ld_w2(const void *p)
+// BYTES of which `n` are read, the rest zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy(uint32_t to, const void *from, int n)
 {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(n) : "memory");
 }
 
-__device__ __forceinline__ uint32_t ld_w1(const void *p)
-{
-    uint32_t v;
-    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
-}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-__device__ __forceinline__ uint32_t ld_u16(const uint16_t *p)
+// All but the newest `stages - 2` groups of copies are there.
+__device__ __forceinline__ void copy_wait(int stages)
 {
-    uint16_t v;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    return v;
+    if (stages == 4)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 3)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4])
@@ -83,22 +88,19 @@ __device__ __forceinline__ float bf16_of(const uint2 &v, int j)
 }
 
 // Shared memory of a CTA that holds `quads` quads of x.
-//   xf  [8 NT tokens / 8][group][word w][32 lanes] of 16 bytes: the fragment of lane 4 g + t: channels 16 t + 8 w .. + 7 of
-//       the group of token g, in the order 0 4 1 5 2 6 3 7, the odd ones of which are over 16
-//   xs  [quad][NT][t][j][2]: the factors of the quad's four groups for tokens 2 t and 2 t + 1
-//   xb  [quad][NT][32 lanes] of 8 bytes: the fragment of the sums
-//   join  the warps' sums;  part: a CTA's sums, for its cluster
-template <int NT, int MT, int WARPS>
+//   xf    [8 NT tokens / 8][group][word w][32 lanes] of 16 bytes: the fragment of lane 4 g + t: channels 16 t + 8 w .. + 7 of
+//         the group of token g, in the order 0 4 1 5 2 6 3 7, the odd ones of which are over 16
+//   xs    [quad][NT][t][j][2]: the factors of the quad's four groups for tokens 2 t and 2 t + 1
+//   xb    [quad][NT][32 lanes] of 8 bytes: the fragment of the sums
+//   part  a CTA's sums, for its cluster
+//   ring  [warp][stage][MT] tiles
 struct Layout {
-    static constexpr int kJoinBuffers = NT <= 2 ? 2 : 1;
-    static constexpr size_t kJoin = static_cast<size_t>(WARPS) * MT * 8 * NT * kPitch * 4;
-    int quads, ranks, unit_rows;
-    __host__ __device__ size_t xs() const { return static_cast<size_t>(quads) * NT * 4096; }
-    __host__ __device__ size_t xb() const { return xs() + static_cast<size_t>(quads) * NT * 128; }
-    __host__ __device__ size_t join() const { return xb() + static_cast<size_t>(quads) * NT * 256; }
-    __host__ __device__ size_t part() const { return join() + kJoinBuffers * kJoin; }
-    __host__ __device__ size_t part_bytes() const { return ranks > 1 ? static_cast<size_t>(unit_rows) * 8 * NT * 4 : 0; }
-    __host__ __device__ size_t total() const { return part() + 2 * part_bytes(); }
+    int quads, nt, part_bytes, ring_bytes;
+    __host__ __device__ int xs() const { return quads * nt * 4096; }
+    __host__ __device__ int xb() const { return xs() + quads * nt * 128; }
+    __host__ __device__ int part() const { return xb() + quads * nt * 256; }
+    __host__ __device__ int ring() const { return part() + 2 * part_bytes; }
+    __host__ __device__ int total() const { return ring() + ring_bytes; }
 };
 
 // Stages x of this CTA's quads (groups past g_last count as zeros).  Columns of tokens past T are left as they are: a
@@ -194,15 +196,11 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, int g_first, int g_
     }
 }
 
-// CTAs an SM, by registers.
-template <int NT, int MT>
-constexpr int kPerSm = NT * MT == 1 ? 3 : NT <= 2 ? 2 : 1;
-
 template <int NT, int MT, int WARPS, bool VEC, bool CODES>
-__global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(const __grid_constant__ MatvecArgs a)
+__global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecArgs a)
 {
-    constexpr int kThreads = WARPS * 32;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kThreads = WARPS * 32, kStage = MT * kTileBytes;
+    extern __shared__ __align__(128) unsigned char smem[];
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = a.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
@@ -213,65 +211,64 @@ __global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(cons
     const int wk = 1 << a.wk_log, wm = WARPS >> a.wk_log;        // warps along K, along rows
     const int k_warp = warp & (wk - 1), m_warp = warp >> a.wk_log;
     const int unit_rows = wm * MT * 16, units = (a.rows + unit_rows - 1) / unit_rows;
-    const Layout<NT, MT, WARPS> L{(all_quads + ranks - 1) / ranks, ranks, unit_rows};
+    const Layout L{(all_quads + ranks - 1) / ranks, NT, ranks > 1 ? unit_rows * 8 * NT * 4 : 0, 0};
     uint4 *xf = reinterpret_cast<uint4 *>(smem);
     float *xs = reinterpret_cast<float *>(smem + L.xs());
     uint2 *xb = reinterpret_cast<uint2 *>(smem + L.xb());
+    unsigned char *ring = smem + L.ring() + warp * a.stages * kStage;
     const int stride = gridDim.x / ranks;
     int unit = blockIdx.x / ranks;
 
-    // A quad: rows g and g + 8 of each of MT tiles, channels [16 t, 16 t + 16) of four groups, their scales, and two of
-    // their biases (groups 0 1 where t is even, 2 3 where it is odd).
-    uint2 w[MT][2][4], s[MT][2];
-    uint32_t b[MT][2];
-    const uint8_t *at_w[MT][2];
-    const uint16_t *at_s[MT][2];
-    long long to_b = a.b - a.s;
-    int next_g = 0;  // first group of the quad that is being loaded
-    auto aim = [&](int u, int q) {
-        next_g = (q_first + q) * 4;
+    // The copies of a quad.  Codes: lane l takes the 16-byte pieces l % 8 of rows l / 8 + 4 i, which go to the place
+    // that keeps the reads below (rows 0-3, then 4-7, of a pair of pieces) off each other's banks.  Parameters: lanes 0-15 the
+    // scales of a row, 16-31 the biases: one piece of eight bytes, or, where rows are not
+    // aligned to that, the three words that hold them.
+    int load_unit = unit, load_q = k_warp, load_slot = 0;
+    const int piece = lane % 8, row_w = lane / 8, row_p = lane % 16;
+    const uint16_t *params = lane < 16 ? a.s : a.b;
+    const long long param_end = static_cast<long long>(a.rows) * groups;
+    auto load = [&]() {
+        if (k_warp < quads && load_unit < units) {
+            const int q = q_first + load_q;
+            const uint32_t to = smem_u32(ring + load_slot * kStage);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
+                const int row0 = (load_unit * wm + m_warp) * (MT * 16) + m * 16;
+                const uint8_t *from = a.w + static_cast<long long>(row0 + row_w) * (a.K / 2) + q * 128 + piece * 16;
+                const int most = VEC || q * 8 + piece < groups * 2 ? 16 : 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const long long row = min((u * wm + m_warp) * (MT * 16) + 16 * m + 8 * h + g, a.rows - 1);
-                at_w[m][h] = a.w + row * (a.K / 2) + next_g * 32 + t * 8;
-                at_s[m][h] = a.s + row * groups + next_g;
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row_w + 4 * i;
+                    const bool on = row0 + r < a.rows && most;
+                    copy<16>(to + m * kTileBytes + r * 128 + ((piece >> 1 ^ r & 3) * 2 + (piece & 1)) * 16, on ? from + i * 4 * (a.K / 2) : a.w, on ? 16 : 0);
+                }
+                const int row = row0 + row_p;
+                const long long at = static_cast<long long>(row) * groups + q * 4;
+                const uint32_t to_p = to + m * kTileBytes + 2048 + lane * 16;
+                if (VEC) {
+                    copy<8>(to_p, row < a.rows ? params + at : params, row < a.rows ? 8 : 0);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const long long word = (at & ~1ll) + 2 * k, left = row < a.rows ? param_end - word : 0;
+                        copy<4>(to_p + 4 * k, left > 0 ? params + word : params, left <= 0 ? 0 : left < 2 ? 2 : 4);
+                    }
+                }
             }
+            load_slot = load_slot + 1 == a.stages ? 0 : load_slot + 1;
+            load_q += wk;
+            if (load_q >= quads) {
+                load_q = k_warp;
+                load_unit += stride;
+            }
+        }
+        copy_commit();
     };
-    auto load_w = [&](int j) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) w[m][h][j] = VEC || next_g + j < groups ? ld_w2(at_w[m][h] + 32 * j) : make_uint2(0, 0);
-    };
-    auto pair = [&](const uint16_t *p, int j) -> uint32_t {  // values j and j + 1 of a quad's parameters
-        if (VEC) return ld_w1(p + j);
-        return (next_g + j < groups ? ld_u16(p + j) : 0) | (next_g + j + 1 < groups ? ld_u16(p + j + 1) << 16 : 0);
-    };
-    auto load_s = [&](int half) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) (half ? s[m][h].y : s[m][h].x) = pair(at_s[m][h], 2 * half);
-    };
-    auto load_b = [&]() {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) b[m][h] = pair(at_s[m][h] + to_b, t % 2 * 2);
-    };
-    if (k_warp < quads && unit < units) {  // the matrix is never written by a kernel of the library: ahead of the wait
-        aim(unit, k_warp);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_w(j);
-        load_b();
-        load_s(0);
-        load_s(1);
-    }
+    for (int i = 0; i < a.stages - 1; ++i) load();  // the matrix is never written by a kernel of the library: ahead of the wait
     pdl_wait();
     stage_x<NT, kThreads, CODES>(a, q_first * 4, min((q_first + quads) * 4, groups), quads, xf, xs, reinterpret_cast<uint16_t *>(xb));
     __syncthreads();
+    int slot = 0;
     for (int turn = 0; unit < units; unit += stride, turn ^= 1) {
         float out[NT][MT][4];
 #pragma unroll
@@ -280,32 +277,64 @@ __global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(cons
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) out[n][m][i] = 0.0f;
+        unsigned char *tile = ring;
         for (int q = k_warp; q < quads; q += wk) {
-            const bool here = q + wk < quads, more = here || unit + stride < units;
-            if (more) aim(here ? unit : unit + stride, here ? q + wk : k_warp);
+            copy_wait(a.stages);
+            __syncwarp();  // this quad is there for all lanes, and all are done with the one before
+            load();
+            tile = ring + slot * kStage;
+            slot = slot + 1 == a.stages ? 0 : slot + 1;
+            uint2 s[MT][2];
+            uint32_t b[MT][2];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned char *p = tile + m * kTileBytes + 2048 + (g + 8 * h) * 16;
+                    if (VEC) {
+                        s[m][h] = *reinterpret_cast<const uint2 *>(p);
+                        b[m][h] = *reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
+                    } else {
+                        const int row = (unit * wm + m_warp) * (MT * 16) + m * 16 + g + 8 * h;
+                        const int odd = (row & groups & 1) * 16;  // the first of the row's groups is in the upper half (a quad's first group is even)
+                        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                        const uint32_t *c = reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
+                        s[m][h] = make_uint2(__funnelshift_r(v.x, v.y, odd), __funnelshift_r(v.y, v.z, odd));
+                        b[m][h] = __funnelshift_r(c[0], c[1], odd);
+                        // groups past the row's end hold the next row's parameters: their sums and factors are zeros, and so
+                        // are theirs
+                        const int left = groups - (q_first + q) * 4;
+                        if (left < 4) {
+                            s[m][h].y = left > 2 ? s[m][h].y & 0xFFFFu : 0;
+                            s[m][h].x = left > 1 ? s[m][h].x : s[m][h].x & 0xFFFFu;
+                            const int mine = left - t % 2 * 2;
+                            b[m][h] = mine > 1 ? b[m][h] : mine > 0 ? b[m][h] & 0xFFFFu : 0;
+                        }
+                    }
+                }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint2 x = xb[(q * NT + n) * 32 + lane];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) mma_bf16(out[n][m], b[m][0], b[m][1], x.x, x.y);
             }
-            if (more) load_b();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t c[MT][2][2][4];  // [tile][word][half of the word]: codes as a fragment
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(tile + m * kTileBytes + (g + 8 * h) * 128 + ((j ^ g & 3) * 32 + t * 8));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t v = k ? w[m][h][j].y : w[m][h][j].x, u = v >> 8;
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t v = k ? w.y : w.x, u = v >> 8;
                             c[m][k][0][h] = v & 0x000F000Fu;
                             c[m][k][0][2 + h] = v & 0x00F000F0u;
                             c[m][k][1][h] = u & 0x000F000Fu;
                             c[m][k][1][2 + h] = u & 0x00F000F0u;
                         }
-                if (more) load_w(j);
+                    }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const uint4 *x = xf + ((n * quads + q) * 4 + j) * 64 + lane;
@@ -329,25 +358,28 @@ __global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(cons
                         }
                     }
                 }
-                if (more && j == 1) load_s(0);
-                if (more && j == 3) load_s(1);
             }
         }
-        // join: [warp][tile][token][row]
-        float *join = reinterpret_cast<float *>(smem + L.join() + (L.kJoinBuffers == 2 ? turn * L.kJoin : 0));
+        // Join.  A warp's sums, [tile][token][row], go to the slot that it used last (its first, if it has no part of K).
+        __syncwarp();
+        {
+            float *to = reinterpret_cast<float *>(tile);
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    join[((warp * MT + m) * 8 * NT + n * 8 + t * 2 + i % 2) * kPitch + i / 2 * 8 + g] = out[n][m][i];
+                    for (int i = 0; i < 4; ++i)
+                        to[m * (kTileBytes / 4) + (n * 8 + t * 2 + i % 2) * kPitch + i / 2 * 8 + g] = out[n][m][i];
+        }
+        __shared__ float *joined[WARPS];
+        if (lane == 0) joined[warp] = reinterpret_cast<float *>(tile);
         __syncthreads();
         auto local = [&](int n, int token) {  // sum of the warps that share row n of the unit
-            const float *from = join + (((n / (16 * MT) << a.wk_log) * MT + n / 16 % MT) * 8 * NT + token) * kPitch + n % 16;
+            const int first = n / (16 * MT) << a.wk_log, at = n / 16 % MT * (kTileBytes / 4) + token * kPitch + n % 16;
             float sum = 0.0f;
 #pragma unroll 4
-            for (int k = 0; k < wk; ++k) sum += from[k * (MT * 8 * NT * kPitch)];
+            for (int k = 0; k < wk; ++k) sum += joined[first + k][at];
             return sum;
         };
         auto store = [&](int n, int token, float sum) {
@@ -364,7 +396,7 @@ __global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(cons
             for (int i = threadIdx.x; i < items; i += kThreads) store(i & (unit_rows - 1), i >> rows_log, local(i & (unit_rows - 1), i >> rows_log));
         } else {
             // two buffers: the barrier of the next unit stands between a rank's reads of this one and its next writes
-            float *part = reinterpret_cast<float *>(smem + L.part() + turn * L.part_bytes());
+            float *part = reinterpret_cast<float *>(smem + L.part() + turn * L.part_bytes);
             for (int i = threadIdx.x; i < items; i += kThreads) part[i] = local(i & (unit_rows - 1), i >> rows_log);
             cluster.sync();
             for (int i = threadIdx.x + rank * kThreads; i < items; i += kThreads * ranks) {
@@ -374,28 +406,38 @@ __global__ void __launch_bounds__(WARPS * 32, kPerSm<NT, MT>) matvec_kernel(cons
                 store(i & (unit_rows - 1), i >> rows_log, sum);
             }
         }
-        if (L.kJoinBuffers == 1) __syncthreads();
+        __syncthreads();  // the slots may be filled again
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (ranks > 1) cluster.sync();  // nobody leaves while another reads
 }
 
 template <int NT, int MT, int WARPS, bool VEC, bool CODES>
 cudaError_t launch(MatvecArgs a, int num_sms, cudaStream_t stream)
 {
-    const int quads = (a.K / 64 + 3) / 4, per = (quads + a.ranks - 1) / a.ranks;
-    a.wk_log = 0;
-    while ((2 << a.wk_log) <= WARPS && (2 << a.wk_log) <= per) ++a.wk_log;
-    const int unit_rows = (WARPS >> a.wk_log) * MT * 16, units = (a.rows + unit_rows - 1) / unit_rows;
-    const size_t smem = Layout<NT, MT, WARPS>{per, a.ranks, unit_rows}.total();
+    const int quads = (a.K / 64 + 3) / 4;
+    // CTAs of a cluster along K: as few as leave three stages of the ring beside x
+    Layout L{};
+    int unit_rows = 0;
+    for (a.ranks = 1;; a.ranks *= 2) {
+        const int per = (quads + a.ranks - 1) / a.ranks;
+        a.wk_log = 0;
+        while ((2 << a.wk_log) <= WARPS && (2 << a.wk_log) <= per) ++a.wk_log;
+        unit_rows = (WARPS >> a.wk_log) * MT * 16;
+        L = Layout{per, NT, a.ranks > 1 ? unit_rows * 8 * NT * 4 : 0, 0};
+        a.stages = std::min(4, (kMaxSmem - L.total()) / (WARPS * MT * kTileBytes));
+        if (a.stages >= (NT == 4 ? 2 : 3) || a.ranks == 8) break;
+    }
+    L.ring_bytes = a.stages * WARPS * MT * kTileBytes;
+    const int units = (a.rows + unit_rows - 1) / unit_rows;
     auto kernel = matvec_kernel<NT, MT, WARPS, VEC, CODES>;
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), static_cast<int>(smem));
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), L.total());
     if (e != cudaSuccess) return e;
-    const int per_sm = std::max(1, std::min<int>(kPerSm<NT, MT>, 227 * 1024 / static_cast<int>(smem + 1024)));
-    const int clusters = std::min(units, std::max(1, num_sms * per_sm / a.ranks));
+    const int clusters = std::min(units, std::max(1, num_sms / a.ranks));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(clusters * a.ranks);
     cfg.blockDim = dim3(WARPS * 32);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = L.total();
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -422,15 +464,19 @@ cudaError_t launch(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 cudaError_t launch_matvec(const MatvecArgs &args, int num_sms, cudaStream_t stream)
 {
     MatvecArgs a = args;
-    const int NT = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    // CTAs of a cluster along K: as many as x needs shared memory for
-    a.ranks = 1;
-    while (a.ranks < 8 && NT * ((a.K + a.ranks - 1) / a.ranks) > 8192) a.ranks *= 2;
-    // two tiles a warp (each piece of x read from shared memory serves both) where they fill the GPU
-    const bool two = a.rows >= 32 * 2 * num_sms;
-    if (NT == 1) return two ? launch<1, 2, 8>(a, num_sms, stream) : launch<1, 1, 8>(a, num_sms, stream);
-    if (NT == 2) return two ? launch<2, 2, 8>(a, num_sms, stream) : launch<2, 1, 8>(a, num_sms, stream);
-    return launch<4, 2, 8>(a, num_sms, stream);
+    if (a.T <= 8) return launch<1, 1, 16>(a, num_sms, stream);
+    if (a.T <= 16) return launch<2, 2, 8>(a, num_sms, stream);
+    if (a.K <= 8192) return launch<4, 2, 8>(a, num_sms, stream);
+    // x of 32 tokens and two stages do not fit eight CTAs: the tokens in two calls
+    MatvecArgs b = a;
+    b.T = 16;
+    a.T -= 16;
+    const size_t x_bytes = a.x_scale ? 1 : 2, out_bytes = a.out_f32 ? 4 : 2;
+    a.x = static_cast<const char *>(a.x) + 16 * a.x_stride * x_bytes;
+    if (a.x_scale) a.x_scale += 16 * (a.K / 64);
+    a.out = static_cast<char *>(a.out) + 16 * static_cast<size_t>(a.rows) * out_bytes;
+    const cudaError_t e = launch_matvec(b, num_sms, stream);
+    return e != cudaSuccess ? e : launch_matvec(a, num_sms, stream);
 }
 
 }  // namespace lily
