@@ -38,7 +38,7 @@ constexpr int kMaxSmem = 226 * 1024;
 
 // BYTES of which `n` are read, the rest zeros.
 template <int BYTES>
-__device__ __forceinline__ void copy(uint32_t to, const void *from, int n)
+__device__ __forceinline__ void copy(uint32_t to, const void *from, int n = BYTES)
 {
     if (BYTES == 16)
         asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
@@ -88,23 +88,26 @@ __device__ __forceinline__ float bf16_of(const uint2 &v, int j)
 }
 
 // Shared memory of a CTA that holds `quads` quads of x.
-//   xf    [8 NT tokens / 8][group][word w][32 lanes] of 16 bytes: the fragment of lane 4 g + t: channels 16 t + 8 w .. + 7 of
-//         the group of token g, in the order 0 4 1 5 2 6 3 7, the odd ones of which are over 16
+//   xf    [group][word w][token][t] of 16 bytes, the fragments: channels 16 t + 8 w .. + 7 of the group, in the order
+//         0 4 1 5 2 6 3 7, the odd ones of which are over 16
 //   xs    [quad][NT][t][j][2]: the factors of the quad's four groups for tokens 2 t and 2 t + 1
 //   xb    [quad][NT][32 lanes] of 8 bytes: the fragment of the sums
-//   part  a CTA's sums, for its cluster
+//   part  two of a CTA's sums, [token][row], for its cluster
+//   join  two of the warps' sums, where the ring's slots do not hold them
 //   ring  [warp][stage][MT] tiles
 struct Layout {
-    int quads, nt, part_bytes, ring_bytes;
-    __host__ __device__ int xs() const { return quads * nt * 4096; }
+    int quads, T, nt, part_bytes, join_bytes, ring_bytes;
+    __host__ __device__ int xs() const { return quads * T * 512; }
     __host__ __device__ int xb() const { return xs() + quads * nt * 128; }
     __host__ __device__ int part() const { return xb() + quads * nt * 256; }
-    __host__ __device__ int ring() const { return part() + 2 * part_bytes; }
+    __host__ __device__ int join() const { return part() + 2 * part_bytes; }
+    __host__ __device__ int ring() const { return join() + join_bytes; }
     __host__ __device__ int total() const { return ring() + ring_bytes; }
 };
 
-// Stages x of this CTA's quads (groups past g_last count as zeros).  Columns of tokens past T are left as they are: a
-// column of an mma's product depends on its own token alone, and theirs is not stored.
+// Stages x of this CTA's quads (groups past g_last count as zeros).  Columns of tokens past T take the last token's
+// fragments, and factors and sums that are left as they are: a column of an mma's product depends on
+// its own token alone, and theirs is not stored.
 template <int NT, int THREADS, bool CODES>
 __device__ __forceinline__ void stage_x(const MatvecArgs &a, int g_first, int g_last, int quads, uint4 *xf, float *xs, uint16_t *xb)
 {
@@ -172,7 +175,7 @@ __device__ __forceinline__ void stage_x(const MatvecArgs &a, int g_first, int g_
                 const __half2 p = __floats2half2_rn(x[j] * f, x[j + 4] * f);
                 h[j] = *reinterpret_cast<const uint32_t *>(&p);
             }
-            xf[((t / 8 * quads * 4 + g) * 2 + v % 2) * 32 + t % 8 * 4 + v / 2] = make_uint4(h[0], h[1], h[2], h[3]);
+            xf[((g * 2 + v % 2) * a.T + t) * 4 + v / 2] = make_uint4(h[0], h[1], h[2], h[3]);
             if (v == 0) {
                 const int q = g / 4, j = g % 4, tile = q * NT + t / 8;
                 // the sums are held times 2^-12, the products with codes (2^-24 of them) times 2^12
@@ -200,7 +203,10 @@ template <int NT, int MT, int WARPS, bool VEC, bool CODES>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecArgs a)
 {
     constexpr int kThreads = WARPS * 32, kStage = MT * kTileBytes;
+    constexpr int kTokenFloats = 8 * NT * kPitch;        // a tile's sums
+    constexpr bool kOwnJoin = NT == 1;                   // two buffers for the sums, else the slots of the ring
     extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ const float *joined[WARPS];
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = a.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     const int wk = 1 << a.wk_log, wm = WARPS >> a.wk_log;        // warps along K, along rows
     const int k_warp = warp & (wk - 1), m_warp = warp >> a.wk_log;
     const int unit_rows = wm * MT * 16, units = (a.rows + unit_rows - 1) / unit_rows;
-    const Layout L{(all_quads + ranks - 1) / ranks, NT, ranks > 1 ? unit_rows * 8 * NT * 4 : 0, 0};
+    const Layout L{(all_quads + ranks - 1) / ranks, a.T, NT, ranks > 1 ? unit_rows * a.T * 4 : 0, kOwnJoin ? 2 * WARPS * MT * kTokenFloats * 4 : 0, 0};
     uint4 *xf = reinterpret_cast<uint4 *>(smem);
     float *xs = reinterpret_cast<float *>(smem + L.xs());
     uint2 *xb = reinterpret_cast<uint2 *>(smem + L.xb());
@@ -223,43 +229,67 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     // that keeps the reads below (rows 0-3, then 4-7, of a pair of pieces) off each other's banks.  Parameters: lanes 0-15 the
     // scales of a row, 16-31 the biases: one piece of eight bytes, or, where rows are not
     // aligned to that, the three words that hold them.
-    int load_unit = unit, load_q = k_warp, load_slot = 0;
-    const int piece = lane % 8, row_w = lane / 8, row_p = lane % 16;
+    const int piece = lane % 8, row_w = lane / 8;
+    const long long half = a.K / 2, param_end = static_cast<long long>(a.rows) * groups;
     const uint16_t *params = lane < 16 ? a.s : a.b;
-    const long long param_end = static_cast<long long>(a.rows) * groups;
+    const uint32_t ring_to = smem_u32(ring), to_w = row_w * 128 + ((piece >> 1 ^ row_w) * 2 + (piece & 1)) * 16, to_p = 2048 + lane * 16;
+    int load_row = (unit * wm + m_warp) * (MT * 16), load_q = k_warp;
+    uint32_t load_to = ring_to;
+    const uint8_t *from_w = a.w + (load_row + row_w) * half + (q_first + load_q) * 128 + piece * 16;
+    long long from_p = static_cast<long long>(load_row + lane % 16) * groups + (q_first + load_q) * 4;
+    const int row_step = stride * unit_rows;
+    const bool works = k_warp < quads;
     auto load = [&]() {
-        if (k_warp < quads && load_unit < units) {
-            const int q = q_first + load_q;
-            const uint32_t to = smem_u32(ring + load_slot * kStage);
+        if (works && load_row < a.rows) {
+            const bool whole = load_row + MT * 16 <= a.rows && (VEC || q_first + load_q < all_quads - 1);
+            if (whole) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int row0 = (load_unit * wm + m_warp) * (MT * 16) + m * 16;
-                const uint8_t *from = a.w + static_cast<long long>(row0 + row_w) * (a.K / 2) + q * 128 + piece * 16;
-                const int most = VEC || q * 8 + piece < groups * 2 ? 16 : 0;
+                for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = row_w + 4 * i;
-                    const bool on = row0 + r < a.rows && most;
-                    copy<16>(to + m * kTileBytes + r * 128 + ((piece >> 1 ^ r & 3) * 2 + (piece & 1)) * 16, on ? from + i * 4 * (a.K / 2) : a.w, on ? 16 : 0);
+                    for (int i = 0; i < 4; ++i) copy<16>(load_to + to_w + m * kTileBytes + i * 512, from_w + (16 * m + 4 * i) * half);
+                    const uint16_t *p = params + from_p + 16 * m * groups;
+                    if (VEC) {
+                        copy<8>(load_to + to_p + m * kTileBytes, p);
+                    } else {
+                        const long long at = from_p + 16 * m * groups;
+                        p = params + (at & ~1ll);
+                        copy<4>(load_to + to_p + m * kTileBytes, p);
+                        copy<4>(load_to + to_p + m * kTileBytes + 4, p + 2);
+                        if (at & 1) copy<4>(load_to + to_p + m * kTileBytes + 8, p + 4, 2);  // the row's fourth
+                    }
                 }
-                const int row = row0 + row_p;
-                const long long at = static_cast<long long>(row) * groups + q * 4;
-                const uint32_t to_p = to + m * kTileBytes + 2048 + lane * 16;
-                if (VEC) {
-                    copy<8>(to_p, row < a.rows ? params + at : params, row < a.rows ? 8 : 0);
-                } else {
+            } else {  // rows past the end and, in the last quad, groups past the end are zeros
+                const int pieces = (groups - (q_first + load_q) * 4) * 2;
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const long long word = (at & ~1ll) + 2 * k, left = row < a.rows ? param_end - word : 0;
-                        copy<4>(to_p + 4 * k, left > 0 ? params + word : params, left <= 0 ? 0 : left < 2 ? 2 : 4);
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool on = load_row + 16 * m + 4 * i + row_w < a.rows && piece < pieces;
+                        copy<16>(load_to + to_w + m * kTileBytes + i * 512, on ? from_w + (16 * m + 4 * i) * half : a.w, on ? 16 : 0);
+                    }
+                    const bool row_on = load_row + 16 * m + lane % 16 < a.rows;
+                    const long long at = from_p + 16 * m * groups;
+                    if (VEC) {
+                        copy<8>(load_to + to_p + m * kTileBytes, row_on ? params + at : params, row_on ? 8 : 0);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const long long word = (at & ~1ll) + 2 * k, left = row_on ? param_end - word : 0;
+                            copy<4>(load_to + to_p + m * kTileBytes + 4 * k, left > 0 ? params + word : params, left <= 0 ? 0 : left < 2 ? 2 : 4);
+                        }
                     }
                 }
             }
-            load_slot = load_slot + 1 == a.stages ? 0 : load_slot + 1;
+            load_to += kStage;
+            if (load_to == ring_to + a.stages * kStage) load_to = ring_to;
             load_q += wk;
+            from_w += wk * 128;
+            from_p += wk * 4;
             if (load_q >= quads) {
+                from_w += row_step * half - (load_q - k_warp) * 128;
+                from_p += static_cast<long long>(row_step) * groups - (load_q - k_warp) * 4;
                 load_q = k_warp;
-                load_unit += stride;
+                load_row += row_step;
             }
         }
         copy_commit();
@@ -268,6 +298,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     pdl_wait();
     stage_x<NT, kThreads, CODES>(a, q_first * 4, min((q_first + quads) * 4, groups), quads, xf, xs, reinterpret_cast<uint16_t *>(xb));
     __syncthreads();
+    // this lane's fragments of a group: token g of each eight, the last one for tokens past T
+    const uint4 *x_lane = xf + g * 4 + t, *x_last = xf + (min(8 * NT - 8 + g, a.T - 1) * 4 + t);
     int slot = 0;
     for (int turn = 0; unit < units; unit += stride, turn ^= 1) {
         float out[NT][MT][4];
@@ -301,8 +333,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         const uint32_t *c = reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
                         s[m][h] = make_uint2(__funnelshift_r(v.x, v.y, odd), __funnelshift_r(v.y, v.z, odd));
                         b[m][h] = __funnelshift_r(c[0], c[1], odd);
-                        // groups past the row's end hold the next row's parameters: their sums and factors are zeros, and so
-                        // are theirs
+                        // groups past the row's end hold the next row's parameters, of any value: they count as zeros
                         const int left = groups - (q_first + q) * 4;
                         if (left < 4) {
                             s[m][h].y = left > 2 ? s[m][h].y & 0xFFFFu : 0;
@@ -318,8 +349,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 #pragma unroll
                 for (int m = 0; m < MT; ++m) mma_bf16(out[n][m], b[m][0], b[m][1], x.x, x.y);
             }
+            const float *factors = xs + q * NT * 32 + t * 8;
+            const int x_word = a.T * 4;
+            int x_at = q * 8 * x_word;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j, x_at += 2 * x_word) {
                 uint32_t c[MT][2][2][4];  // [tile][word][half of the word]: codes as a fragment
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -337,9 +371,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                     }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint4 *x = xf + ((n * quads + q) * 4 + j) * 64 + lane;
-                    const uint4 x0 = x[0], x1 = x[32];
-                    const float2 f = *reinterpret_cast<const float2 *>(xs + (q * NT + n) * 32 + t * 8 + j * 2);
+                    const uint4 *x = (n == NT - 1 ? x_last : x_lane + n * 32) + x_at;
+                    const uint4 x0 = x[0], x1 = x[x_word];
+                    const float2 f = *reinterpret_cast<const float2 *>(factors + n * 32 + j * 2);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -360,75 +394,93 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                 }
             }
         }
-        // Join.  A warp's sums, [tile][token][row], go to the slot that it used last (its first, if it has no part of K).
-        __syncwarp();
-        {
-            float *to = reinterpret_cast<float *>(tile);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        to[m * (kTileBytes / 4) + (n * 8 + t * 2 + i % 2) * kPitch + i / 2 * 8 + g] = out[n][m][i];
+        // Join.  A warp's sums, [tile][token][row], go to a buffer, or to the slot that it used last (its first, if it has no part
+        // of K).
+        float *sums;
+        if (kOwnJoin) {
+            sums = reinterpret_cast<float *>(smem + L.join()) + (turn * WARPS + warp) * (MT * kTokenFloats);
+        } else {
+            __syncwarp();
+            sums = reinterpret_cast<float *>(tile);
+            if (lane == 0) joined[warp] = sums;
         }
-        __shared__ float *joined[WARPS];
-        if (lane == 0) joined[warp] = reinterpret_cast<float *>(tile);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[m * kTokenFloats + (n * 8 + t * 2 + i % 2) * kPitch + i / 2 * 8 + g] = out[n][m][i];
         __syncthreads();
-        auto local = [&](int n, int token) {  // sum of the warps that share row n of the unit
-            const int first = n / (16 * MT) << a.wk_log, at = n / 16 % MT * (kTileBytes / 4) + token * kPitch + n % 16;
-            float sum = 0.0f;
+        // A thread takes four rows of a token: items of [token][row / 4].
+        const int fours_log = 29 - __clz(unit_rows), items = a.T << fours_log;  // a unit's rows are a power of two
+        auto local = [&](int i) {
+            const int n = (i & (1 << fours_log) - 1) * 4, first = n / (16 * MT) << a.wk_log;
+            const int at = n / 16 % MT * kTokenFloats + (i >> fours_log) * kPitch + n % 16;
+            const float *own = reinterpret_cast<const float *>(smem + L.join()) + (turn * WARPS + first) * (MT * kTokenFloats) + at;
+            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-            for (int k = 0; k < wk; ++k) sum += joined[first + k][at];
+            for (int k = 0; k < wk; ++k) {
+                const float4 v = *reinterpret_cast<const float4 *>(kOwnJoin ? own + k * (MT * kTokenFloats) : joined[first + k] + at);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
             return sum;
         };
-        auto store = [&](int n, int token, float sum) {
-            const long long row = static_cast<long long>(unit) * unit_rows + n;
-            if (row >= a.rows) return;
-            const long long o = static_cast<long long>(token) * a.rows + row;
-            if (a.out_f32)
-                static_cast<float *>(a.out)[o] = sum * 0x1p12f;
-            else
-                static_cast<__nv_bfloat16 *>(a.out)[o] = __float2bfloat16_rn(sum * 0x1p12f);
+        auto store = [&](int i, const float4 &sum) {
+            const int row = unit * unit_rows + (i & (1 << fours_log) - 1) * 4;
+            const float v[4] = {sum.x * 0x1p12f, sum.y * 0x1p12f, sum.z * 0x1p12f, sum.w * 0x1p12f};
+            const long long o = static_cast<long long>(i >> fours_log) * a.rows + row;
+            if (a.rows % 4 == 0) {
+                if (row >= a.rows) return;
+                if (a.out_f32) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]), r = __floats2bfloat162_rn(v[2], v[3]);
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&r));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (row + k < a.rows) {
+                        if (a.out_f32)
+                            static_cast<float *>(a.out)[o + k] = v[k];
+                        else
+                            static_cast<__nv_bfloat16 *>(a.out)[o + k] = __float2bfloat16_rn(v[k]);
+                    }
+            }
         };
-        const int rows_log = 31 - __clz(unit_rows), items = a.T << rows_log;  // a unit's rows are a power of two
         if (ranks == 1) {
-            for (int i = threadIdx.x; i < items; i += kThreads) store(i & (unit_rows - 1), i >> rows_log, local(i & (unit_rows - 1), i >> rows_log));
+            for (int i = threadIdx.x; i < items; i += kThreads) store(i, local(i));
         } else {
             // two buffers: the barrier of the next unit stands between a rank's reads of this one and its next writes
-            float *part = reinterpret_cast<float *>(smem + L.part() + turn * L.part_bytes);
-            for (int i = threadIdx.x; i < items; i += kThreads) part[i] = local(i & (unit_rows - 1), i >> rows_log);
+            float4 *part = reinterpret_cast<float4 *>(smem + L.part() + turn * L.part_bytes);
+            for (int i = threadIdx.x; i < items; i += kThreads) part[i] = local(i);
             cluster.sync();
             for (int i = threadIdx.x + rank * kThreads; i < items; i += kThreads * ranks) {
-                float sum = 0.0f;
+                float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-                for (int r = 0; r < ranks; ++r) sum += cluster.map_shared_rank(part, r)[i];
-                store(i & (unit_rows - 1), i >> rows_log, sum);
+                for (int r = 0; r < ranks; ++r) {
+                    const float4 v = cluster.map_shared_rank(part, r)[i];
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                }
+                store(i, sum);
             }
         }
-        __syncthreads();  // the slots may be filled again
+        if (!kOwnJoin) __syncthreads();  // the slots may be filled again
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (ranks > 1) cluster.sync();  // nobody leaves while another reads
 }
 
 template <int NT, int MT, int WARPS, bool VEC, bool CODES>
-cudaError_t launch(MatvecArgs a, int num_sms, cudaStream_t stream)
+cudaError_t launch(MatvecArgs a, const Layout &L, int unit_rows, int num_sms, cudaStream_t stream)
 {
-    const int quads = (a.K / 64 + 3) / 4;
-    // CTAs of a cluster along K: as few as leave three stages of the ring beside x
-    Layout L{};
-    int unit_rows = 0;
-    for (a.ranks = 1;; a.ranks *= 2) {
-        const int per = (quads + a.ranks - 1) / a.ranks;
-        a.wk_log = 0;
-        while ((2 << a.wk_log) <= WARPS && (2 << a.wk_log) <= per) ++a.wk_log;
-        unit_rows = (WARPS >> a.wk_log) * MT * 16;
-        L = Layout{per, NT, a.ranks > 1 ? unit_rows * 8 * NT * 4 : 0, 0};
-        a.stages = std::min(4, (kMaxSmem - L.total()) / (WARPS * MT * kTileBytes));
-        if (a.stages >= (NT == 4 ? 2 : 3) || a.ranks == 8) break;
-    }
-    L.ring_bytes = a.stages * WARPS * MT * kTileBytes;
     const int units = (a.rows + unit_rows - 1) / unit_rows;
     auto kernel = matvec_kernel<NT, MT, WARPS, VEC, CODES>;
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), L.total());
@@ -451,32 +503,46 @@ cudaError_t launch(MatvecArgs a, int num_sms, cudaStream_t stream)
 }
 
 template <int NT, int MT, int WARPS>
-cudaError_t launch(const MatvecArgs &a, int num_sms, cudaStream_t stream)
+cudaError_t launch(MatvecArgs a, int num_sms, cudaStream_t stream)
 {
+    const int quads = (a.K / 64 + 3) / 4;
+    // CTAs of a cluster along K: as few as leave the ring enough stages beside x
+    Layout L{};
+    int unit_rows = 0;
+    for (a.ranks = 1;; a.ranks *= 2) {
+        const int per = (quads + a.ranks - 1) / a.ranks;
+        a.wk_log = 0;
+        while ((2 << a.wk_log) <= WARPS && (2 << a.wk_log) <= per) ++a.wk_log;
+        unit_rows = (WARPS >> a.wk_log) * MT * 16;
+        L = Layout{per, a.T, NT, a.ranks > 1 ? unit_rows * a.T * 4 : 0, NT == 1 ? 2 * WARPS * MT * 8 * NT * kPitch * 4 : 0, 0};
+        a.stages = std::min(4, (kMaxSmem - L.total()) / (WARPS * MT * kTileBytes));
+        if (a.stages >= (NT >= 3 ? 2 : 3)) break;
+        if (a.ranks == 8) {  // the tokens do not fit: in two calls
+            MatvecArgs b = a;
+            b.T = a.T / 2;
+            a.T -= b.T;
+            a.x = static_cast<const char *>(a.x) + b.T * a.x_stride * (a.x_scale ? 1 : 2);
+            if (a.x_scale) a.x_scale += b.T * (a.K / 64);
+            a.out = static_cast<char *>(a.out) + b.T * static_cast<size_t>(a.rows) * (a.out_f32 ? 4 : 2);
+            const cudaError_t e = launch_matvec(b, num_sms, stream);
+            return e != cudaSuccess ? e : launch_matvec(a, num_sms, stream);
+        }
+    }
+    L.ring_bytes = a.stages * WARPS * MT * kTileBytes;
     const bool vec = a.K % 256 == 0;
     if (a.x_scale)
-        return vec ? launch<NT, MT, WARPS, true, true>(a, num_sms, stream) : launch<NT, MT, WARPS, false, true>(a, num_sms, stream);
-    return vec ? launch<NT, MT, WARPS, true, false>(a, num_sms, stream) : launch<NT, MT, WARPS, false, false>(a, num_sms, stream);
+        return vec ? launch<NT, MT, WARPS, true, true>(a, L, unit_rows, num_sms, stream) : launch<NT, MT, WARPS, false, true>(a, L, unit_rows, num_sms, stream);
+    return vec ? launch<NT, MT, WARPS, true, false>(a, L, unit_rows, num_sms, stream) : launch<NT, MT, WARPS, false, false>(a, L, unit_rows, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_matvec(const MatvecArgs &args, int num_sms, cudaStream_t stream)
+cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 {
-    MatvecArgs a = args;
     if (a.T <= 8) return launch<1, 1, 16>(a, num_sms, stream);
     if (a.T <= 16) return launch<2, 2, 8>(a, num_sms, stream);
-    if (a.K <= 8192) return launch<4, 2, 8>(a, num_sms, stream);
-    // x of 32 tokens and two stages do not fit eight CTAs: the tokens in two calls
-    MatvecArgs b = a;
-    b.T = 16;
-    a.T -= 16;
-    const size_t x_bytes = a.x_scale ? 1 : 2, out_bytes = a.out_f32 ? 4 : 2;
-    a.x = static_cast<const char *>(a.x) + 16 * a.x_stride * x_bytes;
-    if (a.x_scale) a.x_scale += 16 * (a.K / 64);
-    a.out = static_cast<char *>(a.out) + 16 * static_cast<size_t>(a.rows) * out_bytes;
-    const cudaError_t e = launch_matvec(b, num_sms, stream);
-    return e != cudaSuccess ? e : launch_matvec(a, num_sms, stream);
+    if (a.T <= 24) return launch<3, 2, 8>(a, num_sms, stream);
+    return launch<4, 2, 8>(a, num_sms, stream);
 }
 
 }  // namespace lily
