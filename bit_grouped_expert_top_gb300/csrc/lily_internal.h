@@ -279,7 +279,8 @@ struct MatvecArgs {
     void *out;                 // [T][rows]
     bool out_f32;
     // set by launch_matvec
-    int ranks, stages;         // CTAs of a cluster that share K, stages of a warp's ring
+    int ranks;                 // CTAs of a cluster that share K
+    int tiles_log;             // log2 of a warp's tiles between joins
     int wk_log;                // log2 of the warps of a CTA that share a row tile's K
 };
 constexpr int kMatvecMaxT = 32, kMatvecMaxK = 16384;

@@ -3,21 +3,22 @@
 //
 // Per group g of 64 channels, with c = q[n][k]:
 //   out[t][n] = sum_g scale[n][g] (sum_k c x[t][k]) + bias[n][g] (sum_k x[t][k])
-// The inner products run on the tensor cores (mma.sync m16n8k16, the 16 rows a tile of the matrix,
-// the 8 columns tokens), with nothing rebuilt: a code in the low bits of an fp16 pattern is
-// the number code * 2^-24 (bits 0-3) or code * 2^-20 (bits 4-7), so eight codes are four
-// masks and a shift.  x is brought to fp16 by a power of two for each token and group that puts
-// the group's largest magnitude into [2^14, 2^15): its eight significant bits survive down to 2^-31 of
-// that magnitude, and what is smaller is off by at most 2^-36 of it.  e4m3 tokens are fp16
-// numbers already.  Sums are fp32, scaled and joined a group at a time.  The biases of four groups are one more mma,
-// on bf16: their 16 columns are the four sums of x, each as three bf16 numbers that add up to it exactly.
+// The inner products run on the tensor cores (mma.sync m16n8k16 on fp16, the 16 rows a tile of the matrix, the 8
+// columns tokens), with nothing rebuilt: a code in the low bits of an fp16 pattern is the number code * 2^-24 (bits 0-3) or
+// code * 2^-20 (bits 4-7), so eight codes are four masks and a shift.  (The e4m3 form of mma.sync would take them with two
+// masks, but here it is slower: 27 cycles a sub-core for twice the channels against 10, operands that change.)  bf16
+// tokens are taken times a power of two that brings the largest of the 256 channels of a token that a warp holds into
+// [2^14, 2^15): their eight significant bits survive down to 2^-31 of that largest magnitude, and what is smaller is off by at
+// most 2^-36 of it.  The norm's e4m3 tokens are fp16 numbers already.  Sums are fp32, scaled and joined a group at a
+// time.  The biases of four groups are one more mma, on bf16: their 16 columns are the four sums of x, each as three
+// bf16 numbers that add up to it exactly.
 //
 // Bound: HBM (0.5625 bytes a weight).  The order of the channels within an mma is free as
-// long as both sides agree: a thread takes 16 consecutive channels of a group (8 bytes), so the four
-// threads of a row read 32 bytes, and the four groups (a quad) that a warp takes at a time a whole line.  A quad stays in
-// registers; as soon as a group of it is used, the same registers are loaded with the next quad's.
-// The warps of a CTA share a row tile's K and join their sums in shared memory; a K whose x does
-// not fit is cut over the CTAs of a cluster, joined through distributed shared memory.
+// long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the fragments of its four groups
+// (a quad: 256 channels) of x in registers for the whole call and takes the rows' pieces of that quad past them, one tile
+// of 16 rows after another, through a ring of asynchronous copies of its own; the warps of
+// a CTA share a row's K and join their sums in shared memory.  A K of more quads than a CTA has warps for is cut over
+// the CTAs of a cluster, which join through distributed shared memory.
 #include <algorithm>
 #include <cstdint>
 
@@ -31,9 +32,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kPitch = 20;      // floats between tokens of a joined tile: the fragment's stores meet no bank twice
+constexpr int kPitch = 20;        // floats between tokens of a joined tile: the fragment's stores meet no bank twice
 constexpr int kTileBytes = 2560;  // a quad of 16 rows in the ring: 128 bytes of codes, 16 of scales, 16 of biases a row
-static_assert(kTileBytes >= 4 * 8 * kPitch * 4, "a tile's sums of 32 tokens fit its slot");
 constexpr int kMaxSmem = 226 * 1024;
 
 // BYTES of which `n` are read, the rest zeros.
@@ -48,29 +48,25 @@ __device__ __forceinline__ void copy(uint32_t to, const void *from, int n = BYTE
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// All but the newest `stages - 2` groups of copies are there.
-__device__ __forceinline__ void copy_wait(int stages)
+// All but the newest `STAGES - 2` groups of copies are there.
+template <int STAGES>
+__device__ __forceinline__ void copy_wait()
 {
-    if (stages == 4)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (stages == 3)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, const float (&c)[4])
 {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, const float (&c)[4])
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%5}, {%6,%7}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%5}, {%6,%7}, {%8,%9,%10,%11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 // Two products at once: (a0, a1) * (b0, b1).
@@ -87,145 +83,158 @@ __device__ __forceinline__ float bf16_of(const uint2 &v, int j)
     return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
 }
 
-// Shared memory of a CTA that holds `quads` quads of x.
-//   xf    [group][word w][token][t] of 16 bytes, the fragments: channels 16 t + 8 w .. + 7 of the group, in the order
-//         0 4 1 5 2 6 3 7, the odd ones of which are over 16
-//   xs    [quad][NT][t][j][2]: the factors of the quad's four groups for tokens 2 t and 2 t + 1
-//   xb    [quad][NT][32 lanes] of 8 bytes: the fragment of the sums
-//   part  two of a CTA's sums, [token][row], for its cluster
-//   join  two of the warps' sums, where the ring's slots do not hold them
-//   ring  [warp][stage][MT] tiles
-struct Layout {
-    int quads, T, nt, part_bytes, join_bytes, ring_bytes;
-    __host__ __device__ int xs() const { return quads * T * 512; }
-    __host__ __device__ int xb() const { return xs() + quads * nt * 128; }
-    __host__ __device__ int part() const { return xb() + quads * nt * 256; }
-    __host__ __device__ int join() const { return part() + 2 * part_bytes; }
-    __host__ __device__ int ring() const { return join() + join_bytes; }
-    __host__ __device__ int total() const { return ring() + ring_bytes; }
+__device__ __forceinline__ uint32_t f16x2(float a, float b)
+{
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ float2 of_e4m3x2(uint32_t v)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// A lane's part of a quad of x (lane 4 g + t): channels [16 t, 16 t + 16) of the quad's four groups of tokens 8 n + g, and
+// the fragment of their sums.
+template <int NT, bool CODES>
+struct Tokens {
+    uint32_t x[NT][4][8];             // [4 w + ..]: word w's channels 0 4, 1 5, 2 6, 3 7, the odd pairs over 16
+    uint32_t sums[NT][2];
+    float factor[CODES ? 1 : NT][2];  // bf16: of tokens 2 t and 2 t + 1
 };
 
-// Stages x of this CTA's quads (groups past g_last count as zeros).  Columns of tokens past T take the last token's
-// fragments, and factors and sums that are left as they are: a column of an mma's product depends on
-// its own token alone, and theirs is not stored.
-template <int NT, int THREADS, bool CODES>
-__device__ __forceinline__ void stage_x(const MatvecArgs &a, int g_first, int g_last, int quads, uint4 *xf, float *xs, uint16_t *xb)
+// Loads a quad of x (its groups from g_last on, and tokens past T, as zeros).  CODES: leaves the factors of its groups for
+// tokens 2 t and 2 t + 1, [n][t][j][2], at `factors`.
+template <int NT, bool CODES>
+__device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecArgs &a, int g_first, int g_last, int lane, float *factors)
 {
-    // eight threads a group of a token, eight channels each; kBatch loads in flight
-    constexpr int kBatch = 4;
-    const int per_token = quads * 32, total = a.T * per_token;
-    for (int i0 = threadIdx.x; i0 - threadIdx.x % 32 < total; i0 += kBatch * THREADS) {
-        uint4 raw[kBatch];
-        float scale[kBatch];
+    const int t = lane % 4;
 #pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-            const int i = i0 + r * THREADS, t = i / per_token, g = g_first + i % per_token / 8;
-            raw[r] = make_uint4(0, 0, 0, 0);
-            scale[r] = 0.0f;
-            if (i < total && g < g_last) {
-                const long long at = t * a.x_stride + g * 64 + i % 8 * 8;
+    for (int n = 0; n < NT; ++n) {
+        const int token = 8 * n + lane / 4;
+        uint4 raw[4][2];
+        float scale[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            raw[j][0] = raw[j][1] = make_uint4(0, 0, 0, 0);
+            scale[j] = 0.0f;
+            if (token < a.T && g_first + j < g_last) {
+                const long long at = token * a.x_stride + (g_first + j) * 64 + 16 * t;
                 if (CODES) {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.x) + at);
-                    raw[r].x = c.x;
-                    raw[r].y = c.y;
-                    scale[r] = a.x_scale[static_cast<long long>(t) * (a.K / 64) + g];
+                    raw[j][0] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.x) + at);
+                    scale[j] = a.x_scale[static_cast<long long>(token) * (a.K / 64) + g_first + j];
                 } else {
-                    raw[r] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at);
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at);
+                    raw[j][0] = p[0];
+                    raw[j][1] = p[1];
                 }
             }
         }
-#pragma unroll
-        for (int r = 0; r < kBatch; ++r) {
-            const int i = i0 + r * THREADS, t = i / per_token, g = i % per_token / 8, v = i % 8;
-            float x[8], by;
-            if (CODES) {
-                by = 64.0f;  // the largest code, 448, is 28,672
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = j < 2 ? raw[r].x : raw[r].y;
-                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * (j & 1))), __NV_E4M3);
-                    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                    x[2 * j] = p.x;
-                    x[2 * j + 1] = p.y;
-                }
-            } else {
-                const uint32_t u[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
-                float most = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[2 * j] = __uint_as_float(u[j] << 16);
-                    x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-                    most = fmaxf(most, fmaxf(fabsf(x[2 * j]), fabsf(x[2 * j + 1])));
-                }
-#pragma unroll
-                for (int o = 1; o < 8; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-                // 2^(14 - floor(log2 most)), at most 2^127
-                const int e = max(static_cast<int>(__float_as_uint(most) >> 23), 14);
-                by = __uint_as_float(static_cast<uint32_t>(268 - min(e, 254)) << 23);
-                scale[r] = 1.0f;
-            }
-            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (i >= total) continue;  // whole warps: a token has a multiple of 32 of them
-            uint32_t h[4];
+        float sum[4], by = 64.0f;  // the largest code, 448, is 28,672
+        if (!CODES) {
+            float most = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float f = j & 1 ? by * 0.0625f : by;
-                const __half2 p = __floats2half2_rn(x[j] * f, x[j + 4] * f);
-                h[j] = *reinterpret_cast<const uint32_t *>(&p);
-            }
-            xf[((g * 2 + v % 2) * a.T + t) * 4 + v / 2] = make_uint4(h[0], h[1], h[2], h[3]);
-            if (v == 0) {
-                const int q = g / 4, j = g % 4, tile = q * NT + t / 8;
-                // the sums are held times 2^-12, the products with codes (2^-24 of them) times 2^12
-                xs[tile * 32 + t % 8 / 2 * 8 + j * 2 + t % 2] = scale[r] * 0x1p12f / by;
-                float rest = sum * scale[r] * 0x1p-12f;
-                uint16_t part[3];
+                const uint32_t u[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w, raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {  // what is left of 24 bits after eight more
-                    const __nv_bfloat16 p = __float2bfloat16_rn(rest);
-                    part[k] = __bfloat16_as_ushort(p);
-                    rest -= __bfloat162float(p);
+                for (int i = 0; i < 8; ++i)
+                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(u[i] << 16)), fabsf(__uint_as_float(u[i] & 0xFFFF0000u))));
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            // x times 2^(14 - e), e = floor(log2 most) in [-113, 127]
+            const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23) - 127, -113), 127);
+            const float factor = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            by = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) to.factor[CODES ? 0 : n][i] = __shfl_sync(0xffffffffu, factor, (2 * t + i) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t u[8] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w, raw[j][1].x, raw[j][1].y, raw[j][1].z, raw[j][1].w};
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 p = CODES ? of_e4m3x2(u[i / 2] >> (16 * (i & 1)) & 0xFFFFu)
+                                       : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+                x[2 * i] = p.x * by;
+                x[2 * i + 1] = p.y * by;
+            }
+            sum[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[j] += x[i];
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = i & 1 ? 0.0625f : 1.0f;
+                    to.x[n][j][4 * w + i] = f16x2(x[8 * w + i] * f, x[8 * w + i + 4] * f);
                 }
-                // columns: (first, second) of groups 0 1 | 2 3, then (third, nothing)
-                uint16_t *to = xb + (tile * 32 + t % 8 * 4 + j / 2) * 4 + j % 2;
-                to[0] = part[0];
-                to[8] = part[1];
-                to[2] = part[2];
-                to[10] = 0;
+            // products with codes are times 2^-24 and `by`
+            if (CODES && t == 0) factors[((n * 4 + lane / 8) * 4 + j) * 2 + lane / 4 % 2] = scale[j] * 0x1p18f;
+        }
+        uint32_t part[4][3];  // the groups' sums as three bf16 numbers
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+            float rest = sum[j] * (CODES ? scale[j] * 0.015625f : 0x1p-24f);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {  // what is left of 24 bits after eight more
+                const __nv_bfloat16 p = __float2bfloat16_rn(rest);
+                part[j][k] = __bfloat16_as_ushort(p);
+                rest -= __bfloat162float(p);
             }
         }
+        // columns 2 t, 2 t + 1: the first numbers of groups 0 1 | 2 3, then the second; columns 8 + 2 t: the third, nothing
+        const int j = t % 2 * 2;
+        uint32_t pair[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) pair[k] = j ? part[2][k] | part[3][k] << 16 : part[0][k] | part[1][k] << 16;
+        to.sums[n][0] = t < 2 ? pair[0] : pair[1];
+        to.sums[n][1] = t < 2 ? pair[2] : 0;
     }
 }
 
-template <int NT, int MT, int WARPS, bool VEC, bool CODES>
+// Stages of a warp's ring: what shared memory leaves beside the joins, for two tiles a unit.
+template <int NT, int WARPS>
+constexpr int kStages = WARPS == 16 ? (NT == 1 ? 4 : 3) : 6;
+
+// Shared memory: the factors [warp][QPW][NT][4][4][2]; for a cluster two of a CTA's sums, [token][row]; two of the warps' sums,
+// [tile of the unit][warp][token][row]; the ring [warp][stage] of tiles.
+struct Layout {
+    int warps, quads_a_warp, nt, part_bytes, tiles_log, stages;
+    __host__ __device__ int part() const { return warps * quads_a_warp * nt * 128; }
+    __host__ __device__ int join() const { return part() + 2 * part_bytes; }
+    __host__ __device__ int join_bytes() const { return (warps * 8 * nt * kPitch * 4) << tiles_log; }
+    __host__ __device__ int ring() const { return join() + 2 * join_bytes(); }
+    __host__ __device__ int total() const { return ring() + warps * stages * kTileBytes; }
+};
+
+template <int NT, int QPW, int WARPS, bool VEC, bool CODES>
 __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_constant__ MatvecArgs a)
 {
-    constexpr int kThreads = WARPS * 32, kStage = MT * kTileBytes;
-    constexpr int kTokenFloats = 8 * NT * kPitch;        // a tile's sums
-    constexpr bool kOwnJoin = NT == 1;                   // two buffers for the sums, else the slots of the ring
+    constexpr int kThreads = WARPS * 32, kSums = 8 * NT * kPitch, kS = kStages<NT, WARPS>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ const float *joined[WARPS];
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = a.ranks, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    // this CTA's quads of K
+    // this CTA's quads of K; those of this warp are q_first + k_warp + i wk
     const int groups = a.K / 64, all_quads = (groups + 3) / 4;
     const int q_first = all_quads * rank / ranks, quads = all_quads * (rank + 1) / ranks - q_first;
     const int wk = 1 << a.wk_log, wm = WARPS >> a.wk_log;        // warps along K, along rows
     const int k_warp = warp & (wk - 1), m_warp = warp >> a.wk_log;
-    const int unit_rows = wm * MT * 16, units = (a.rows + unit_rows - 1) / unit_rows;
-    const Layout L{(all_quads + ranks - 1) / ranks, a.T, NT, ranks > 1 ? unit_rows * a.T * 4 : 0, kOwnJoin ? 2 * WARPS * MT * kTokenFloats * 4 : 0, 0};
-    uint4 *xf = reinterpret_cast<uint4 *>(smem);
-    float *xs = reinterpret_cast<float *>(smem + L.xs());
-    uint2 *xb = reinterpret_cast<uint2 *>(smem + L.xb());
-    unsigned char *ring = smem + L.ring() + warp * a.stages * kStage;
+    const int my_quads = k_warp < quads ? (quads - k_warp + wk - 1) >> a.wk_log : 0;  // at most QPW
+    const int tiles_log = a.tiles_log, unit_rows = wm * 16 << tiles_log, units = (a.rows + unit_rows - 1) / unit_rows;
+    const Layout L{WARPS, QPW, NT, ranks > 1 ? unit_rows * a.T * 4 : 0, tiles_log, kS};
+    float *factors = reinterpret_cast<float *>(smem) + warp * (QPW * NT * 32);
+    unsigned char *ring = smem + L.ring() + warp * kS * kTileBytes;
     const int stride = gridDim.x / ranks;
     int unit = blockIdx.x / ranks;
 
-    // The copies of a quad.  Codes: lane l takes the 16-byte pieces l % 8 of rows l / 8 + 4 i, which go to the place
+    // The copies of a tile.  Codes: lane l takes the 16-byte pieces l % 8 of rows l / 8 + 4 i, which go to the place
     // that keeps the reads below (rows 0-3, then 4-7, of a pair of pieces) off each other's banks.  Parameters: lanes 0-15 the
     // scales of a row, 16-31 the biases: one piece of eight bytes, or, where rows are not
     // aligned to that, the three words that hold them.
@@ -233,194 +242,170 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     const long long half = a.K / 2, param_end = static_cast<long long>(a.rows) * groups;
     const uint16_t *params = lane < 16 ? a.s : a.b;
     const uint32_t ring_to = smem_u32(ring), to_w = row_w * 128 + ((piece >> 1 ^ row_w) * 2 + (piece & 1)) * 16, to_p = 2048 + lane * 16;
-    int load_row = (unit * wm + m_warp) * (MT * 16), load_q = k_warp;
+    // steps from a row tile's first quad to the next tile's, within a unit and to the next unit
+    const int rows_unit = stride * unit_rows - (16 << tiles_log) + 16;
+    const long long w_tile = 16 * half, w_unit = rows_unit * half;
+    const int p_tile = 16 * groups;
+    const long long p_unit = static_cast<long long>(rows_unit) * groups;
+    int load_row = (unit * wm + m_warp) * 16 << tiles_log, load_tile = 0, load_i = 0;
     uint32_t load_to = ring_to;
-    const uint8_t *from_w = a.w + (load_row + row_w) * half + (q_first + load_q) * 128 + piece * 16;
-    long long from_p = static_cast<long long>(load_row + lane % 16) * groups + (q_first + load_q) * 4;
-    const int row_step = stride * unit_rows;
-    const bool works = k_warp < quads;
+    const uint8_t *from_w = a.w + (load_row + row_w) * half + (q_first + k_warp) * 128 + piece * 16;
+    long long from_p = static_cast<long long>(load_row + lane % 16) * groups + (q_first + k_warp) * 4;
     auto load = [&]() {
-        if (works && load_row < a.rows) {
-            const bool whole = load_row + MT * 16 <= a.rows && (VEC || q_first + load_q < all_quads - 1);
-            if (whole) {
+        if (my_quads > 0 && load_row < a.rows) {
+            const int q = q_first + k_warp + (load_i << a.wk_log);
+            const uint8_t *w = from_w + load_i * (wk * 128);
+            const long long at = from_p + load_i * (wk * 4);
+            if (load_row + 16 <= a.rows && (VEC || q < all_quads - 1)) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) copy<16>(load_to + to_w + m * kTileBytes + i * 512, from_w + (16 * m + 4 * i) * half);
-                    const uint16_t *p = params + from_p + 16 * m * groups;
-                    if (VEC) {
-                        copy<8>(load_to + to_p + m * kTileBytes, p);
-                    } else {
-                        const long long at = from_p + 16 * m * groups;
-                        p = params + (at & ~1ll);
-                        copy<4>(load_to + to_p + m * kTileBytes, p);
-                        copy<4>(load_to + to_p + m * kTileBytes + 4, p + 2);
-                        if (at & 1) copy<4>(load_to + to_p + m * kTileBytes + 8, p + 4, 2);  // the row's fourth
-                    }
+                for (int i = 0; i < 4; ++i) copy<16>(load_to + to_w + i * 512, w + 4 * i * half);
+                if (VEC) {
+                    copy<8>(load_to + to_p, params + at);
+                } else {
+                    const uint16_t *p = params + (at & ~1ll);
+                    copy<4>(load_to + to_p, p);
+                    copy<4>(load_to + to_p + 4, p + 2);
+                    if (at & 1) copy<4>(load_to + to_p + 8, p + 4, 2);  // the row's fourth
                 }
             } else {  // rows past the end and, in the last quad, groups past the end are zeros
-                const int pieces = (groups - (q_first + load_q) * 4) * 2;
+                const int pieces = (groups - q * 4) * 2;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int i = 0; i < 4; ++i) {
+                    const bool on = load_row + 4 * i + row_w < a.rows && piece < pieces;
+                    copy<16>(load_to + to_w + i * 512, on ? w + 4 * i * half : a.w, on ? 16 : 0);
+                }
+                const bool on = load_row + lane % 16 < a.rows;
+                if (VEC) {
+                    copy<8>(load_to + to_p, on ? params + at : params, on ? 8 : 0);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool on = load_row + 16 * m + 4 * i + row_w < a.rows && piece < pieces;
-                        copy<16>(load_to + to_w + m * kTileBytes + i * 512, on ? from_w + (16 * m + 4 * i) * half : a.w, on ? 16 : 0);
-                    }
-                    const bool row_on = load_row + 16 * m + lane % 16 < a.rows;
-                    const long long at = from_p + 16 * m * groups;
-                    if (VEC) {
-                        copy<8>(load_to + to_p + m * kTileBytes, row_on ? params + at : params, row_on ? 8 : 0);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const long long word = (at & ~1ll) + 2 * k, left = row_on ? param_end - word : 0;
-                            copy<4>(load_to + to_p + m * kTileBytes + 4 * k, left > 0 ? params + word : params, left <= 0 ? 0 : left < 2 ? 2 : 4);
-                        }
+                    for (int k = 0; k < 3; ++k) {
+                        const long long word = (at & ~1ll) + 2 * k, left = on ? param_end - word : 0;
+                        copy<4>(load_to + to_p + 4 * k, left > 0 ? params + word : params, left <= 0 ? 0 : left < 2 ? 2 : 4);
                     }
                 }
             }
-            load_to += kStage;
-            if (load_to == ring_to + a.stages * kStage) load_to = ring_to;
-            load_q += wk;
-            from_w += wk * 128;
-            from_p += wk * 4;
-            if (load_q >= quads) {
-                from_w += row_step * half - (load_q - k_warp) * 128;
-                from_p += static_cast<long long>(row_step) * groups - (load_q - k_warp) * 4;
-                load_q = k_warp;
-                load_row += row_step;
+            load_to += kTileBytes;
+            if (load_to == ring_to + kS * kTileBytes) load_to = ring_to;
+            if (QPW == 1 || ++load_i == my_quads) {
+                const bool last = ++load_tile >> tiles_log;
+                load_tile = last ? 0 : load_tile;
+                load_row += last ? rows_unit : 16;
+                from_w += last ? w_unit : w_tile;
+                from_p += last ? p_unit : p_tile;
+                load_i = 0;
             }
         }
         copy_commit();
     };
-    for (int i = 0; i < a.stages - 1; ++i) load();  // the matrix is never written by a kernel of the library: ahead of the wait
+    for (int i = 0; i < kS - 1; ++i) load();  // the matrix is never written by a kernel of the library: ahead of the wait
     pdl_wait();
-    stage_x<NT, kThreads, CODES>(a, q_first * 4, min((q_first + quads) * 4, groups), quads, xf, xs, reinterpret_cast<uint16_t *>(xb));
-    __syncthreads();
-    // this lane's fragments of a group: token g of each eight, the last one for tokens past T
-    const uint4 *x_lane = xf + g * 4 + t, *x_last = xf + (min(8 * NT - 8 + g, a.T - 1) * 4 + t);
-    int slot = 0;
+    Tokens<NT, CODES> x[QPW];
+#pragma unroll
+    for (int i = 0; i < QPW; ++i)
+        if (i < my_quads)
+            load_tokens<NT, CODES>(x[i], a, (q_first + k_warp + (i << a.wk_log)) * 4, groups, lane, factors + i * NT * 32);
+    __syncwarp();
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const unsigned char *tile = ring;
+    const unsigned char *const ring_end = ring + kS * kTileBytes;
+    const int fours_log = 29 - __clz(unit_rows), items = a.T << fours_log;  // items of the join: [token][row / 4]
     for (int turn = 0; unit < units; unit += stride, turn ^= 1) {
-        float out[NT][MT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[n][m][i] = 0.0f;
-        unsigned char *tile = ring;
-        for (int q = k_warp; q < quads; q += wk) {
-            copy_wait(a.stages);
-            __syncwarp();  // this quad is there for all lanes, and all are done with the one before
-            load();
-            tile = ring + slot * kStage;
-            slot = slot + 1 == a.stages ? 0 : slot + 1;
-            uint2 s[MT][2];
-            uint32_t b[MT][2];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const unsigned char *p = tile + m * kTileBytes + 2048 + (g + 8 * h) * 16;
-                    if (VEC) {
-                        s[m][h] = *reinterpret_cast<const uint2 *>(p);
-                        b[m][h] = *reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
-                    } else {
-                        const int row = (unit * wm + m_warp) * (MT * 16) + m * 16 + g + 8 * h;
-                        const int odd = (row & groups & 1) * 16;  // the first of the row's groups is in the upper half (a quad's first group is even)
-                        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                        const uint32_t *c = reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
-                        s[m][h] = make_uint2(__funnelshift_r(v.x, v.y, odd), __funnelshift_r(v.y, v.z, odd));
-                        b[m][h] = __funnelshift_r(c[0], c[1], odd);
-                        // groups past the row's end hold the next row's parameters, of any value: they count as zeros
-                        const int left = groups - (q_first + q) * 4;
-                        if (left < 4) {
-                            s[m][h].y = left > 2 ? s[m][h].y & 0xFFFFu : 0;
-                            s[m][h].x = left > 1 ? s[m][h].x : s[m][h].x & 0xFFFFu;
-                            const int mine = left - t % 2 * 2;
-                            b[m][h] = mine > 1 ? b[m][h] : mine > 0 ? b[m][h] & 0xFFFFu : 0;
-                        }
-                    }
-                }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint2 x = xb[(q * NT + n) * 32 + lane];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) mma_bf16(out[n][m], b[m][0], b[m][1], x.x, x.y);
-            }
-            const float *factors = xs + q * NT * 32 + t * 8;
-            const int x_word = a.T * 4;
-            int x_at = q * 8 * x_word;
-#pragma unroll
-            for (int j = 0; j < 4; ++j, x_at += 2 * x_word) {
-                uint32_t c[MT][2][2][4];  // [tile][word][half of the word]: codes as a fragment
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(tile + m * kTileBytes + (g + 8 * h) * 128 + ((j ^ g & 3) * 32 + t * 8));
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t v = k ? w.y : w.x, u = v >> 8;
-                            c[m][k][0][h] = v & 0x000F000Fu;
-                            c[m][k][0][2 + h] = v & 0x00F000F0u;
-                            c[m][k][1][h] = u & 0x000F000Fu;
-                            c[m][k][1][2 + h] = u & 0x00F000F0u;
-                        }
-                    }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 *x = (n == NT - 1 ? x_last : x_lane + n * 32) + x_at;
-                    const uint4 x0 = x[0], x1 = x[x_word];
-                    const float2 f = *reinterpret_cast<const float2 *>(factors + n * 32 + j * 2);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        float acc[4];
-                        mma_f16(acc, c[m][0][0], x0.x, x0.y, zero);
-                        mma_f16(acc, c[m][0][1], x0.z, x0.w, acc);
-                        mma_f16(acc, c[m][1][0], x1.x, x1.y, acc);
-                        mma_f16(acc, c[m][1][1], x1.z, x1.w, acc);
-                        mul2(acc[0], acc[1], f.x, f.y);
-                        mul2(acc[2], acc[3], f.x, f.y);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float by = bf16_of(s[m][h], j);
-                            out[n][m][2 * h] = fmaf(by, acc[2 * h], out[n][m][2 * h]);
-                            out[n][m][2 * h + 1] = fmaf(by, acc[2 * h + 1], out[n][m][2 * h + 1]);
-                        }
-                    }
-                }
-            }
-        }
-        // Join.  A warp's sums, [tile][token][row], go to a buffer, or to the slot that it used last (its first, if it has no part
-        // of K).
-        float *sums;
-        if (kOwnJoin) {
-            sums = reinterpret_cast<float *>(smem + L.join()) + (turn * WARPS + warp) * (MT * kTokenFloats);
-        } else {
-            __syncwarp();
-            sums = reinterpret_cast<float *>(tile);
-            if (lane == 0) joined[warp] = sums;
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
+        float *sums = reinterpret_cast<float *>(smem + L.join() + turn * L.join_bytes()) + warp * kSums + t * (2 * kPitch) + g;
+        int row0 = (unit * wm + m_warp) * 16 << tiles_log;
+        for (int r = 0; r < 1 << tiles_log; ++r, sums += WARPS * kSums, row0 += 16) {
+            float out[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sums[m * kTokenFloats + (n * 8 + t * 2 + i % 2) * kPitch + i / 2 * 8 + g] = out[n][m][i];
+                for (int i = 0; i < 4; ++i) out[n][i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < QPW; ++i) {
+                if (i >= my_quads || row0 >= a.rows) break;
+                copy_wait<kS>();
+                __syncwarp();  // this tile is there for all lanes, and all are done with the one before
+                load();
+                uint2 s[2];
+                uint32_t b[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned char *p = tile + 2048 + (g + 8 * h) * 16;
+                    if (VEC) {
+                        s[h] = *reinterpret_cast<const uint2 *>(p);
+                        b[h] = *reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
+                    } else {
+                        // the first of the row's groups may be in the upper half of its word (a quad's first group is even)
+                        const int odd = (row0 + g + 8 * h & groups & 1) * 16;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+                        const uint32_t *c = reinterpret_cast<const uint32_t *>(p + 256 + t % 2 * 4);
+                        s[h] = make_uint2(__funnelshift_r(v.x, v.y, odd), __funnelshift_r(v.y, v.z, odd));
+                        b[h] = __funnelshift_r(c[0], c[1], odd);
+                        // groups past the row's end hold the next row's parameters, of any value: they count as zeros
+                        const int left = groups - (q_first + k_warp + (i << a.wk_log)) * 4;
+                        if (left < 4) {
+                            s[h].y = left > 2 ? s[h].y & 0xFFFFu : 0;
+                            s[h].x = left > 1 ? s[h].x : s[h].x & 0xFFFFu;
+                            const int mine = left - t % 2 * 2;
+                            b[h] = mine > 1 ? b[h] : mine > 0 ? b[h] & 0xFFFFu : 0;
+                        }
+                    }
+                }
+                float part[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_bf16(part[n], b[0], b[1], x[i].sums[n][0], x[i].sums[n][1], zero);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t c[4][4];  // [word and half of it]: codes as a fragment
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(tile + (g + 8 * h) * 128 + ((j ^ g & 3) * 32 + t * 8));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t v = k ? w.y : w.x, u = v >> 8;
+                            c[2 * k][h] = v & 0x000F000Fu;
+                            c[2 * k][2 + h] = v & 0x00F000F0u;
+                            c[2 * k + 1][h] = u & 0x000F000Fu;
+                            c[2 * k + 1][2 + h] = u & 0x00F000F0u;
+                        }
+                    }
+                    const float by[2] = {bf16_of(s[0], j), bf16_of(s[1], j)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float acc[4];
+                        mma_f16(acc, c[0], x[i].x[n][j][0], x[i].x[n][j][1], zero);
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) mma_f16(acc, c[k], x[i].x[n][j][2 * k], x[i].x[n][j][2 * k + 1], acc);
+                        if (CODES) {
+                            const float2 f = *reinterpret_cast<const float2 *>(factors + ((i * NT + n) * 4 + t) * 8 + j * 2);
+                            mul2(acc[0], acc[1], f.x, f.y);
+                            mul2(acc[2], acc[3], f.x, f.y);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) part[n][k] = fmaf(by[k / 2], acc[k], part[n][k]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) out[n][k] = CODES ? out[n][k] + part[n][k] : fmaf(part[n][k], x[i].factor[CODES ? 0 : n][k % 2], out[n][k]);
+                tile += kTileBytes;
+                if (tile == ring_end) tile = ring;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[(n * 8 + i % 2) * kPitch + i / 2 * 8] = out[n][i];
+        }
+        // Join.  Two buffers: the barrier of the next unit stands between this one's reads and the next but one's writes.
         __syncthreads();
-        // A thread takes four rows of a token: items of [token][row / 4].
-        const int fours_log = 29 - __clz(unit_rows), items = a.T << fours_log;  // a unit's rows are a power of two
-        auto local = [&](int i) {
-            const int n = (i & (1 << fours_log) - 1) * 4, first = n / (16 * MT) << a.wk_log;
-            const int at = n / 16 % MT * kTokenFloats + (i >> fours_log) * kPitch + n % 16;
-            const float *own = reinterpret_cast<const float *>(smem + L.join()) + (turn * WARPS + first) * (MT * kTokenFloats) + at;
-            float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = 0; k < wk; ++k) {
-                const float4 v = *reinterpret_cast<const float4 *>(kOwnJoin ? own + k * (MT * kTokenFloats) : joined[first + k] + at);
+        const float *joined = reinterpret_cast<const float *>(smem + L.join() + turn * L.join_bytes());
+        auto local = [&](int token, int n) {  // four rows of a token
+            const int m = n >> (4 + tiles_log), r = n >> 4 & (1 << tiles_log) - 1;
+            const float *from = joined + (r * WARPS + (m << a.wk_log)) * kSums + token * kPitch + n % 16;
+            float4 sum = *reinterpret_cast<const float4 *>(from);
+#pragma unroll 8
+            for (int k = 1; k < wk; ++k) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + k * kSums);
                 sum.x += v.x;
                 sum.y += v.y;
                 sum.z += v.z;
@@ -428,18 +413,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             }
             return sum;
         };
-        auto store = [&](int i, const float4 &sum) {
-            const int row = unit * unit_rows + (i & (1 << fours_log) - 1) * 4;
-            const float v[4] = {sum.x * 0x1p12f, sum.y * 0x1p12f, sum.z * 0x1p12f, sum.w * 0x1p12f};
-            const long long o = static_cast<long long>(i >> fours_log) * a.rows + row;
+        auto store = [&](int token, int n, const float4 &sum) {
+            const int row = unit * unit_rows + n;
+            constexpr float kUnit = CODES ? 1.0f : 1024.0f;  // bf16: codes times 2^-24, x times 2^14 over its factor
+            const float v[4] = {sum.x * kUnit, sum.y * kUnit, sum.z * kUnit, sum.w * kUnit};
+            const long long o = static_cast<long long>(token) * a.rows + row;
             if (a.rows % 4 == 0) {
                 if (row >= a.rows) return;
                 if (a.out_f32) {
                     *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
                 } else {
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]), r = __floats2bfloat162_rn(v[2], v[3]);
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[0], v[1]), q = __floats2bfloat162_rn(v[2], v[3]);
                     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + o) =
-                        make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&r));
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&p), *reinterpret_cast<const uint32_t *>(&q));
                 }
             } else {
 #pragma unroll
@@ -452,12 +438,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                     }
             }
         };
+        const int in_row = (1 << fours_log) - 1;
         if (ranks == 1) {
-            for (int i = threadIdx.x; i < items; i += kThreads) store(i, local(i));
+            for (int i = threadIdx.x; i < items; i += kThreads) store(i >> fours_log, (i & in_row) * 4, local(i >> fours_log, (i & in_row) * 4));
         } else {
-            // two buffers: the barrier of the next unit stands between a rank's reads of this one and its next writes
             float4 *part = reinterpret_cast<float4 *>(smem + L.part() + turn * L.part_bytes);
-            for (int i = threadIdx.x; i < items; i += kThreads) part[i] = local(i);
+            for (int i = threadIdx.x; i < items; i += kThreads) part[i] = local(i >> fours_log, (i & in_row) * 4);
             cluster.sync();
             for (int i = threadIdx.x + rank * kThreads; i < items; i += kThreads * ranks) {
                 float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -469,20 +455,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                     sum.z += v.z;
                     sum.w += v.w;
                 }
-                store(i, sum);
+                store(i >> fours_log, (i & in_row) * 4, sum);
             }
         }
-        if (!kOwnJoin) __syncthreads();  // the slots may be filled again
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (ranks > 1) cluster.sync();  // nobody leaves while another reads
 }
 
-template <int NT, int MT, int WARPS, bool VEC, bool CODES>
-cudaError_t launch(MatvecArgs a, const Layout &L, int unit_rows, int num_sms, cudaStream_t stream)
+template <int NT, int QPW, int WARPS, bool VEC, bool CODES>
+cudaError_t launch(const MatvecArgs &a, const Layout &L, int unit_rows, int num_sms, cudaStream_t stream)
 {
     const int units = (a.rows + unit_rows - 1) / unit_rows;
-    auto kernel = matvec_kernel<NT, MT, WARPS, VEC, CODES>;
+    auto kernel = matvec_kernel<NT, QPW, WARPS, VEC, CODES>;
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), L.total());
     if (e != cudaSuccess) return e;
     const int clusters = std::min(units, std::max(1, num_sms / a.ranks));
@@ -502,47 +487,35 @@ cudaError_t launch(MatvecArgs a, const Layout &L, int unit_rows, int num_sms, cu
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int NT, int MT, int WARPS>
-cudaError_t launch(MatvecArgs a, int num_sms, cudaStream_t stream)
+template <int NT, int QPW, int WARPS>
+cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
 {
+    MatvecArgs a = args;
     const int quads = (a.K / 64 + 3) / 4;
-    // CTAs of a cluster along K: as few as leave the ring enough stages beside x
-    Layout L{};
-    int unit_rows = 0;
-    for (a.ranks = 1;; a.ranks *= 2) {
-        const int per = (quads + a.ranks - 1) / a.ranks;
-        a.wk_log = 0;
-        while ((2 << a.wk_log) <= WARPS && (2 << a.wk_log) <= per) ++a.wk_log;
-        unit_rows = (WARPS >> a.wk_log) * MT * 16;
-        L = Layout{per, a.T, NT, a.ranks > 1 ? unit_rows * a.T * 4 : 0, NT == 1 ? 2 * WARPS * MT * 8 * NT * kPitch * 4 : 0, 0};
-        a.stages = std::min(4, (kMaxSmem - L.total()) / (WARPS * MT * kTileBytes));
-        if (a.stages >= (NT >= 3 ? 2 : 3)) break;
-        if (a.ranks == 8) {  // the tokens do not fit: in two calls
-            MatvecArgs b = a;
-            b.T = a.T / 2;
-            a.T -= b.T;
-            a.x = static_cast<const char *>(a.x) + b.T * a.x_stride * (a.x_scale ? 1 : 2);
-            if (a.x_scale) a.x_scale += b.T * (a.K / 64);
-            a.out = static_cast<char *>(a.out) + b.T * static_cast<size_t>(a.rows) * (a.out_f32 ? 4 : 2);
-            const cudaError_t e = launch_matvec(b, num_sms, stream);
-            return e != cudaSuccess ? e : launch_matvec(a, num_sms, stream);
-        }
-    }
-    L.ring_bytes = a.stages * WARPS * MT * kTileBytes;
+    for (a.ranks = 1; (quads + a.ranks - 1) / a.ranks > QPW * WARPS;) a.ranks *= 2;  // at most 8: 64 quads
+    const int per = (quads + a.ranks - 1) / a.ranks;
+    a.wk_log = 0;
+    while ((1 << a.wk_log) < WARPS && (1 << a.wk_log) * QPW < per) ++a.wk_log;
+    // two tiles a unit halve the barriers, where there are units enough
+    const int wm = WARPS >> a.wk_log;
+    a.tiles_log = static_cast<long long>(a.rows) * a.ranks >= 4ll * 32 * wm * num_sms ? 1 : 0;
+    const int unit_rows = wm * 16 << a.tiles_log;
+    const Layout L{WARPS, QPW, NT, a.ranks > 1 ? unit_rows * a.T * 4 : 0, a.tiles_log, kStages<NT, WARPS>};
+    if (L.total() > kMaxSmem) return cudaErrorInvalidConfiguration;
     const bool vec = a.K % 256 == 0;
     if (a.x_scale)
-        return vec ? launch<NT, MT, WARPS, true, true>(a, L, unit_rows, num_sms, stream) : launch<NT, MT, WARPS, false, true>(a, L, unit_rows, num_sms, stream);
-    return vec ? launch<NT, MT, WARPS, true, false>(a, L, unit_rows, num_sms, stream) : launch<NT, MT, WARPS, false, false>(a, L, unit_rows, num_sms, stream);
+        return vec ? launch<NT, QPW, WARPS, true, true>(a, L, unit_rows, num_sms, stream) : launch<NT, QPW, WARPS, false, true>(a, L, unit_rows, num_sms, stream);
+    return vec ? launch<NT, QPW, WARPS, true, false>(a, L, unit_rows, num_sms, stream) : launch<NT, QPW, WARPS, false, false>(a, L, unit_rows, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 {
-    if (a.T <= 8) return launch<1, 1, 16>(a, num_sms, stream);
-    if (a.T <= 16) return launch<2, 2, 8>(a, num_sms, stream);
-    if (a.T <= 24) return launch<3, 2, 8>(a, num_sms, stream);
-    return launch<4, 2, 8>(a, num_sms, stream);
+    if (a.T <= 8) return a.K <= 4096 ? launch<1, 1, 16>(a, num_sms, stream) : launch<1, 2, 16>(a, num_sms, stream);
+    if (a.T <= 16) return launch<2, 1, 16>(a, num_sms, stream);
+    if (a.T <= 24) return launch<3, 1, 8>(a, num_sms, stream);
+    return launch<4, 1, 8>(a, num_sms, stream);
 }
 
 }  // namespace lily

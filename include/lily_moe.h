@@ -515,10 +515,9 @@ int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride,
  *   x         x_type [T][K], token stride x_stride: at least K; a multiple of 8 (bf16) or 16 (e4m3)
  *   x_scale   f32 [T][K/64] dense with LILY_E4M3 (lily_rms_norm's y8 and y8_scale), NULL with LILY_BF16
  *   out       out_type (LILY_BF16, LILY_F32) [T][rows] dense
- * Weights, codes and bf16 x enter the products unrounded, but for x below 2^-31 of its group's (64 channels of
- * a token) largest magnitude, which is off by at most 2^-36 of that; sums are fp32.  A token with values that are
- * not finite leaves only its own outputs unspecified, a weight row only its own row.  Intermediate sums
- * are held over 2^24: inputs below 2^-90 lose bits.
+ * Weights and e4m3 x enter the products unrounded, bf16 x too, but for values below 2^-27 of the largest of the 256 channels
+ * [256 i, 256 i + 256) of their token, which are off by at most 2^-35 of that largest; sums are fp32.  A token with values that
+ * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 may lose bits.
  * Supported: 0 <= T <= 32 (in whole groups of 8: five tokens cost what eight do); K a multiple of 64 in [64, 16384];
  * 1 <= rows < 2^30.
  */

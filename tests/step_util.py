@@ -66,11 +66,17 @@ def matvec(q, scale, bias, x, x_scale=None):
     want = x @ (code * s + b).T
     # every product and sum on the way is at most this much, in magnitudes
     most = x.abs() @ (code * s.abs() + b.abs()).T
-    # roundings on one path: 4 mma of 17 terms (an mma may cut what it adds, so 2 each), x's sum (6), factor and
-    # scale (3), 2 a group, the join of 64 at most, and the last factor
-    rounds = 4 * 17 * 2 + 6 + 3 + 2 * (x.shape[1] // 64) + 64 + 1
-    group = x.abs().unflatten(-1, (-1, 64)).amax(-1).repeat_interleave(64, -1)  # what is far below its group's largest
-    return want, most * rounds * 2.0 ** -24 + (2.0 ** -36 * group) @ (code * s.abs()).T
+    # roundings on one path: 4 mma of 17 terms (an mma may cut what it adds, so 2 each), x's sum (18), factors and
+    # scale (5), 2 a group, the join of 64 at most, and the last factor
+    rounds = 4 * 17 * 2 + 18 + 5 + 2 * (x.shape[1] // 64) + 64 + 1
+    error = most * rounds * 2.0 ** -24
+    if x_scale is None:
+        # x as fp16 times a power of two that brings the largest of 256 channels into [2^14, 2^15), odd channels over 16: what is not a
+        # multiple of fp16's 2^-24 after that is off by at most 16 * 2^-25, 2^-35 of the largest
+        pad = -x.shape[1] % 256
+        largest = torch.nn.functional.pad(x.abs(), (0, pad)).unflatten(-1, (-1, 256)).amax(-1).repeat_interleave(256, -1)[:, :x.shape[1]]
+        error = error + (2.0 ** -35 * largest) @ (code * s.abs()).T
+    return want, error
 
 
 def make_matrix(rows, K, seed=0, device="cuda"):
