@@ -281,6 +281,7 @@ struct MatvecArgs {
     // set by launch_matvec
     int ranks;                 // CTAs of a cluster that share K
     int tiles_log;             // log2 of a warp's tiles between joins
+    int steps_each, steps_more;  // steps of each cluster; the first `more` clusters have one more
     int wk_log;                // log2 of the warps of a CTA that share a row tile's K
 };
 constexpr int kMatvecMaxT = 32, kMatvecMaxK = 16384;

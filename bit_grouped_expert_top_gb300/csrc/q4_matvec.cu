@@ -224,15 +224,17 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     // this CTA's quads of K; those of this warp are q_first + k_warp + i wk
     const int groups = a.K / 64, all_quads = (groups + 3) / 4;
     const int q_first = all_quads * rank / ranks, quads = all_quads * (rank + 1) / ranks - q_first;
-    const int wk = 1 << a.wk_log, wm = WARPS >> a.wk_log;        // warps along K, along rows
+    const int wk = 1 << a.wk_log, wm = WARPS >> a.wk_log, wm_log = 31 - __clz(wm);  // warps along K, along rows
     const int k_warp = warp & (wk - 1), m_warp = warp >> a.wk_log;
     const int my_quads = k_warp < quads ? (quads - k_warp + wk - 1) >> a.wk_log : 0;  // at most QPW
-    const int tiles_log = a.tiles_log, unit_rows = wm * 16 << tiles_log, units = (a.rows + unit_rows - 1) / unit_rows;
+    // a step is a tile of each of the warps along rows; a unit, between joins, 2^tiles_log steps; a cluster takes steps that follow one another
+    const int tiles_log = a.tiles_log, step_rows = wm * 16, unit_rows = step_rows << tiles_log;
+    const int cluster_id = blockIdx.x / ranks;
+    int step = cluster_id * a.steps_each + min(cluster_id, a.steps_more);
+    const int last_step = step + a.steps_each + (cluster_id < a.steps_more ? 1 : 0);
     const Layout L{WARPS, QPW, NT, ranks > 1 ? unit_rows * a.T * 4 : 0, tiles_log, kS};
     float *factors = reinterpret_cast<float *>(smem) + warp * (QPW * NT * 32);
     unsigned char *ring = smem + L.ring() + warp * kS * kTileBytes;
-    const int stride = gridDim.x / ranks;
-    int unit = blockIdx.x / ranks;
 
     // The copies of a tile.  Codes: lane l takes the 16-byte pieces l % 8 of rows l / 8 + 4 i, which go to the place
     // that keeps the reads below (rows 0-3, then 4-7, of a pair of pieces) off each other's banks.  Parameters: lanes 0-15 the
@@ -242,17 +244,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     const long long half = a.K / 2, param_end = static_cast<long long>(a.rows) * groups;
     const uint16_t *params = lane < 16 ? a.s : a.b;
     const uint32_t ring_to = smem_u32(ring), to_w = row_w * 128 + ((piece >> 1 ^ row_w) * 2 + (piece & 1)) * 16, to_p = 2048 + lane * 16;
-    // steps from a row tile's first quad to the next tile's, within a unit and to the next unit
-    const int rows_unit = stride * unit_rows - (16 << tiles_log) + 16;
-    const long long w_tile = 16 * half, w_unit = rows_unit * half;
-    const int p_tile = 16 * groups;
-    const long long p_unit = static_cast<long long>(rows_unit) * groups;
-    int load_row = (unit * wm + m_warp) * 16 << tiles_log, load_tile = 0, load_i = 0;
+    const long long w_step = step_rows * half;
+    const int p_step = step_rows * groups, last_row = min(last_step * step_rows, a.rows);  // past this cluster's rows
+    int load_row = step * step_rows + m_warp * 16, load_i = 0;
     uint32_t load_to = ring_to;
     const uint8_t *from_w = a.w + (load_row + row_w) * half + (q_first + k_warp) * 128 + piece * 16;
     long long from_p = static_cast<long long>(load_row + lane % 16) * groups + (q_first + k_warp) * 4;
     auto load = [&]() {
-        if (my_quads > 0 && load_row < a.rows) {
+        if (my_quads > 0 && load_row < last_row) {
             const int q = q_first + k_warp + (load_i << a.wk_log);
             const uint8_t *w = from_w + load_i * (wk * 128);
             const long long at = from_p + load_i * (wk * 4);
@@ -288,11 +287,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             load_to += kTileBytes;
             if (load_to == ring_to + kS * kTileBytes) load_to = ring_to;
             if (QPW == 1 || ++load_i == my_quads) {
-                const bool last = ++load_tile >> tiles_log;
-                load_tile = last ? 0 : load_tile;
-                load_row += last ? rows_unit : 16;
-                from_w += last ? w_unit : w_tile;
-                from_p += last ? p_unit : p_tile;
+                load_row += step_rows;
+                from_w += w_step;
+                from_p += p_step;
                 load_i = 0;
             }
         }
@@ -310,10 +307,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     const unsigned char *tile = ring;
     const unsigned char *const ring_end = ring + kS * kTileBytes;
     const int fours_log = 29 - __clz(unit_rows), items = a.T << fours_log;  // items of the join: [token][row / 4]
-    for (int turn = 0; unit < units; unit += stride, turn ^= 1) {
+    for (int turn = 0; step < last_step; turn ^= 1) {
         float *sums = reinterpret_cast<float *>(smem + L.join() + turn * L.join_bytes()) + warp * kSums + t * (2 * kPitch) + g;
-        int row0 = (unit * wm + m_warp) * 16 << tiles_log;
-        for (int r = 0; r < 1 << tiles_log; ++r, sums += WARPS * kSums, row0 += 16) {
+        const int first_row = step * step_rows, steps = min(1 << tiles_log, last_step - step);
+        for (int r = 0; r < steps; ++r, ++step, sums += WARPS * kSums) {
+            const int row0 = step * step_rows + m_warp * 16;
             float out[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -369,19 +367,22 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         }
                     }
                     const float by[2] = {bf16_of(s[0], j), bf16_of(s[1], j)};
+                    float acc[NT][4];  // the tokens' chains side by side: one alone waits 22 cycles for each mma
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(acc[n], c[0], x[i].x[n][j][0], x[i].x[n][j][1], zero);
+#pragma unroll
+                    for (int k = 1; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(acc[n], c[k], x[i].x[n][j][2 * k], x[i].x[n][j][2 * k + 1], acc[n]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float acc[4];
-                        mma_f16(acc, c[0], x[i].x[n][j][0], x[i].x[n][j][1], zero);
-#pragma unroll
-                        for (int k = 1; k < 4; ++k) mma_f16(acc, c[k], x[i].x[n][j][2 * k], x[i].x[n][j][2 * k + 1], acc);
                         if (CODES) {
                             const float2 f = *reinterpret_cast<const float2 *>(factors + ((i * NT + n) * 4 + t) * 8 + j * 2);
-                            mul2(acc[0], acc[1], f.x, f.y);
-                            mul2(acc[2], acc[3], f.x, f.y);
+                            mul2(acc[n][0], acc[n][1], f.x, f.y);
+                            mul2(acc[n][2], acc[n][3], f.x, f.y);
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) part[n][k] = fmaf(by[k / 2], acc[k], part[n][k]);
+                        for (int k = 0; k < 4; ++k) part[n][k] = fmaf(by[k / 2], acc[n][k], part[n][k]);
                     }
                 }
 #pragma unroll
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         __syncthreads();
         const float *joined = reinterpret_cast<const float *>(smem + L.join() + turn * L.join_bytes());
         auto local = [&](int token, int n) {  // four rows of a token
-            const int m = n >> (4 + tiles_log), r = n >> 4 & (1 << tiles_log) - 1;
+            const int m = n >> 4 & wm - 1, r = n / 16 >> wm_log;
             const float *from = joined + (r * WARPS + (m << a.wk_log)) * kSums + token * kPitch + n % 16;
             float4 sum = *reinterpret_cast<const float4 *>(from);
 #pragma unroll 8
@@ -413,13 +414,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             }
             return sum;
         };
+        const int end_row = min(first_row + steps * step_rows, a.rows);
         auto store = [&](int token, int n, const float4 &sum) {
-            const int row = unit * unit_rows + n;
+            const int row = first_row + n;
             constexpr float kUnit = CODES ? 1.0f : 1024.0f;  // bf16: codes times 2^-24, x times 2^14 over its factor
             const float v[4] = {sum.x * kUnit, sum.y * kUnit, sum.z * kUnit, sum.w * kUnit};
             const long long o = static_cast<long long>(token) * a.rows + row;
             if (a.rows % 4 == 0) {
-                if (row >= a.rows) return;
+                if (row >= end_row) return;
                 if (a.out_f32) {
                     *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o) = make_float4(v[0], v[1], v[2], v[3]);
                 } else {
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (row + k < a.rows) {
+                    if (row + k < end_row) {
                         if (a.out_f32)
                             static_cast<float *>(a.out)[o + k] = v[k];
                         else
@@ -464,13 +466,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
 }
 
 template <int NT, int QPW, int WARPS, bool VEC, bool CODES>
-cudaError_t launch(const MatvecArgs &a, const Layout &L, int unit_rows, int num_sms, cudaStream_t stream)
+cudaError_t launch(MatvecArgs a, const Layout &L, int num_sms, cudaStream_t stream)
 {
-    const int units = (a.rows + unit_rows - 1) / unit_rows;
+    const int step_rows = (WARPS >> a.wk_log) * 16, steps = (a.rows + step_rows - 1) / step_rows;
     auto kernel = matvec_kernel<NT, QPW, WARPS, VEC, CODES>;
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kernel), L.total());
     if (e != cudaSuccess) return e;
-    const int clusters = std::min(units, std::max(1, num_sms / a.ranks));
+    const int clusters = std::min(steps, std::max(1, num_sms / a.ranks));
+    a.steps_each = steps / clusters;
+    a.steps_more = steps % clusters;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(clusters * a.ranks);
     cfg.blockDim = dim3(WARPS * 32);
@@ -504,8 +508,8 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
     if (L.total() > kMaxSmem) return cudaErrorInvalidConfiguration;
     const bool vec = a.K % 256 == 0;
     if (a.x_scale)
-        return vec ? launch<NT, QPW, WARPS, true, true>(a, L, unit_rows, num_sms, stream) : launch<NT, QPW, WARPS, false, true>(a, L, unit_rows, num_sms, stream);
-    return vec ? launch<NT, QPW, WARPS, true, false>(a, L, unit_rows, num_sms, stream) : launch<NT, QPW, WARPS, false, false>(a, L, unit_rows, num_sms, stream);
+        return vec ? launch<NT, QPW, WARPS, true, true>(a, L, num_sms, stream) : launch<NT, QPW, WARPS, false, true>(a, L, num_sms, stream);
+    return vec ? launch<NT, QPW, WARPS, true, false>(a, L, num_sms, stream) : launch<NT, QPW, WARPS, false, false>(a, L, num_sms, stream);
 }
 
 }  // namespace
