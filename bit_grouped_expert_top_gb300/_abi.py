@@ -600,7 +600,6 @@ def lily_gdn_scan(q, k, v, alpha, beta, out, state_out, state_in=None, scale: Op
 
 # ------------------------------------------------------------------ around the attention and the expert layers
 _F32, _E4M3, _I64 = torch.float32, torch.float8_e4m3fn, torch.int64
-_TYPE = {_BF16: 0, _F32: 1, _E4M3: 2}  # LILY_BF16, LILY_F32, LILY_E4M3
 
 
 def _need_here(name: str, t) -> int:
@@ -632,19 +631,20 @@ def lily_rms_norm(x, weight=None, y=None, y8=None, y8_scale=None, residual=None,
     size, dev, st, xt = x.shape, x.get_device(), x.stride(), x.dtype
     n = len(size)
     H, d = (1, size[1]) if n == 2 else (size[1], size[2]) if n == 3 else (0, 0)
-    first = y if y is not None else y8
+    first, wt, rt = y if y is not None else y8, weight, residual  # the latter two: then their types
     if not (H > 0 and (xt is _BF16 or xt is _F32) and st[-1] == 1 and (n == 2 or H == 1 or st[1] == d) and first is not None
-            and (weight is None or ((weight.dtype is _BF16 or weight.dtype is _F32) and weight.shape == (d,)
-                                    and weight.is_contiguous() and weight.get_device() == dev))
+            and (weight is None or ((wt := weight.dtype) is _BF16 or wt is _F32) and weight.numel() == d and weight.dim() == 1
+                 and weight.is_contiguous() and weight.get_device() == dev)
             and (y is None or (y.dtype is _BF16 and y.shape == size and y.is_contiguous() and y.get_device() == dev))
             and (y8 is None) == (y8_scale is None)
             and (y8 is None or (y8.dtype is _E4M3 and y8.shape == size and y8.is_contiguous() and y8.get_device() == dev
-                                and d & 63 == 0 and y8_scale.dtype is _F32 and y8_scale.shape == size[:-1] + (d >> 6,)
-                                and y8_scale.is_contiguous() and y8_scale.get_device() == dev))
+                                and d & 63 == 0 and y8_scale.dtype is _F32 and y8_scale.dim() == n and y8_scale.shape[-1] == d >> 6
+                                and y8_scale.numel() == size[0] * H * (d >> 6) and y8_scale.is_contiguous()
+                                and y8_scale.get_device() == dev))
             and (residual is None) == (h is None)
-            and (residual is None or ((residual.dtype is _BF16 or residual.dtype is _F32) and h.dtype is residual.dtype
-                                      and residual.shape == size and h.shape == size and residual.is_contiguous()
-                                      and h.is_contiguous() and residual.get_device() == dev and h.get_device() == dev))
+            and (residual is None or ((rt := residual.dtype) is _BF16 or rt is _F32) and h.dtype is rt and residual.shape == size
+                 and h.shape == size and residual.is_contiguous() and h.is_contiguous() and residual.get_device() == dev
+                 and h.get_device() == dev)
             and dev >= 0 and dev == _current_device()):
         _need(H > 0, f"x: expected [N][d] or [N][H][d] with H > 0, got {list(size)}")
         _need_type("x", x, _BF16, _F32)
@@ -668,10 +668,8 @@ def lily_rms_norm(x, weight=None, y=None, y8=None, y8_scale=None, residual=None,
             _need_array("h", h, residual.dtype, size, dev)
         raise ValueError("tensors on different devices")
     N = size[0]
-    shape = lily_norm_shape(N, H, d, _TYPE[xt], 0 if residual is None else _TYPE[residual.dtype],
-                            0 if weight is None else _TYPE[weight.dtype])
     rc = (_lib or load()).lily_rms_norm(
-        shape, x.data_ptr(), st[0] if N > 1 else H * d, None if residual is None else residual.data_ptr(),
+        lily_norm_shape(N, H, d, xt is _F32, rt is _F32, wt is _F32), x.data_ptr(), st[0] if N > 1 else H * d, None if residual is None else residual.data_ptr(),
         None if h is None else h.data_ptr(), None if weight is None else weight.data_ptr(), weight_offset, eps,
         None if y is None else y.data_ptr(), None if y8 is None else y8.data_ptr(),
         None if y8_scale is None else y8_scale.data_ptr(), _launch_stream(stream, dev))
@@ -716,7 +714,7 @@ def lily_q4_matvec(w: lily_q4, x, out, x_scale=None, stream=None, *, check: bool
         raise ValueError("tensors on different devices")
     T = size[0]
     rc = (_lib or load()).lily_q4_matvec(
-        lily_q4_shape(T, rows, K, _TYPE[xt], _TYPE[ot]), w, x.data_ptr(), st[0] if T > 1 else K,
+        lily_q4_shape(T, rows, K, 2 if xt is _E4M3 else 0, ot is _F32), w, x.data_ptr(), st[0] if T > 1 else K,
         None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _launch_stream(stream, dev))
     return _check("lily_q4_matvec", rc) if check else rc
 
@@ -809,14 +807,13 @@ def lily_draft_verify(p, q, drafts, cu, u, r, accepted, tokens, ws, stream=None,
     fp32 [N + B][V] (the target's probabilities), q fp32 [N][V] or None (drafts without probabilities), any row
     stride; drafts int32 [N], rows by cu int32 [B+1]; uniform numbers u [N] and r [B]; accepted int32 [B] and tokens int32 [N + B]."""
     dev, ps, st = p.get_device(), p.shape, p.stride()
-    B, N = r.shape[0] if r.dim() else 0, drafts.shape[0] if drafts.dim() else 0
+    B, N = r.numel(), drafts.numel()
     if not (p.dtype is _F32 and len(ps) == 2 and ps[0] == N + B and st[1] == 1 and ps[1] > 0
             and (q is None or (q.dtype is _F32 and q.shape == (N, ps[1]) and q.stride(1) == 1 and q.get_device() == dev))
-            and drafts.dtype is _I32 and drafts.dim() == 1 and drafts.is_contiguous()
-            and cu.dtype is _I32 and cu.shape == (B + 1,) and cu.is_contiguous()
-            and u.dtype is _F32 and u.shape == (N,) and u.is_contiguous() and r.dtype is _F32 and r.dim() == 1 and r.is_contiguous()
-            and accepted.dtype is _I32 and accepted.shape == (B,) and accepted.is_contiguous()
-            and tokens.dtype is _I32 and tokens.shape == (N + B,) and tokens.is_contiguous()
+            and drafts.dtype is _I32 and drafts.is_contiguous() and cu.dtype is _I32 and cu.numel() == B + 1 and cu.is_contiguous()
+            and u.dtype is _F32 and u.numel() == N and u.is_contiguous() and r.dtype is _F32 and r.is_contiguous()
+            and accepted.dtype is _I32 and accepted.numel() == B and accepted.is_contiguous()
+            and tokens.dtype is _I32 and tokens.numel() == N + B and tokens.is_contiguous()
             and ws.dtype is _U8 and ws.is_contiguous()
             and dev >= 0 and dev == _current_device() == drafts.get_device() == cu.get_device() == u.get_device() == r.get_device()
             == accepted.get_device() == tokens.get_device() == ws.get_device()):

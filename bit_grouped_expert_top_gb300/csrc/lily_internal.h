@@ -264,7 +264,9 @@ struct RopeArgs {
     long long q_stride, k_stride, q_out_stride, k_out_stride;
     const int *positions;      // [N]
     const unsigned long long *table;  // [rot/2]: f_i / 2 pi in units of 2^-64 turns
-    int heads_each;            // heads of a thread (set by launch_rope)
+    // set by launch_rope
+    int heads_each, slices;    // heads of a thread, threads that share a token's heads
+    unsigned turn_blocks;      // CTAs that turn
 };
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
 
@@ -299,6 +301,7 @@ struct VerifyArgs {
     int *accepted;             // [B]
     int *tokens;               // [N + B]
     Ctrl *ctrl;
+    int ranks;                 // CTAs of a sequence (set by launch_verify)
 };
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream);
 

@@ -19,7 +19,9 @@
 namespace lily {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a CTA whose rows have TPR threads each: one row, where that is more than a warp.
+template <int TPR>
+constexpr int kThreads = TPR > 32 ? TPR : 256;
 
 // A load that stays before pdl_wait (a plain one may be moved past it): the weight is
 // never written by a kernel of the library.
@@ -89,25 +91,24 @@ __device__ __forceinline__ float over_row(float v, float *part)
     for (int o = 1; o < (TPR < 32 ? TPR : 32); o <<= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
     if (TPR > 32) {
         constexpr int kWarps = TPR / 32;
-        const int warp = threadIdx.x / 32, first = warp / kWarps * kWarps;
         __syncthreads();
-        if (threadIdx.x % 32 == 0) part[warp] = v;
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = part[first];
+        v = part[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v = join(v, part[first + w]);
+        for (int w = 1; w < kWarps; ++w) v = join(v, part[w]);
     }
     return v;
 }
 
 template <int TPR, int PER, bool XF32, int RES>  // RES: 0 none, 1 bf16, 2 fp32
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kThreads<TPR>) norm_kernel(const __grid_constant__ NormArgs a)
 {
     constexpr bool kWeightEarly = PER <= 2;
-    __shared__ float part[kThreads / 32];
+    __shared__ float part[kThreads<TPR> / 32];
     pdl_trigger();
     const int lane = threadIdx.x % TPR, vecs = a.d / 8;
-    const long long row = static_cast<long long>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
+    const long long row = static_cast<long long>(blockIdx.x) * (kThreads<TPR> / TPR) + threadIdx.x / TPR;
     const bool live = row < a.rows;
     const long long n = live ? row : 0;
     uint4 w[PER][2];
@@ -173,7 +174,6 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
             }
         return over_row<TPR, false>(s, part);
     };
-    static_assert(TPR <= 32 || TPR == kThreads, "a row's threads are part of a warp or the CTA");
     const float sum = squares(1.0f);
     float r = 1.0f / sqrtf(sum * a.inv_d + a.eps), by = 1.0f;
     // Squares that leave the fp32 range: the row is taken times a power of two that brings the larger
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
 template <int TPR, int PER>
 cudaError_t launch(const NormArgs &a, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((a.rows + kThreads / TPR - 1) / (kThreads / TPR))), block(kThreads);
+    const dim3 grid(static_cast<unsigned>((a.rows + kThreads<TPR> / TPR - 1) / (kThreads<TPR> / TPR))), block(kThreads<TPR>);
     const int res = !a.residual ? 0 : a.h_f32 ? 2 : 1;
     if (a.x_f32)
         return res == 0   ? launch_pdl(norm_kernel<TPR, PER, true, 0>, grid, block, 0, stream, a)
@@ -261,12 +261,22 @@ cudaError_t launch(const NormArgs &a, cudaStream_t stream)
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
     const int vecs = a.d / 8;
+    // Many rows: a few threads a row, with more vectors in flight each, up to 512 channels, then one vector a thread (32,784 rows
+    // of 256 heads' channels: 8.5 us with 16 threads a row, 10.3 with 32; 16,384 rows of 512: 16.7 with 16, 17.6 with 64, 41.8 with
+    // 256; 8,192 rows of 1,024: 14.1 with 128, 20.9 with 32; 4,096 of 4,096: 29.5 with 512, 31.3 with 256; 1,024 of 16,384: 34.4 with
+    // 512, 38.3 with 1,024, 46.0 with 256).  Few rows: as many threads as a row has vectors (8 rows of 512: 1.6 us with 128, 3.3 with 16).
+    const bool few = a.rows < 2048;
     if (vecs <= 8) return launch<8, 1>(a, stream);
-    if (vecs <= 32) return launch<32, 1>(a, stream);
+    if (few && vecs <= 32) return launch<32, 1>(a, stream);
+    if (few && vecs <= 128) return launch<128, 1>(a, stream);
+    if (vecs <= 16) return launch<8, 2>(a, stream);
+    if (vecs <= 32) return launch<16, 2>(a, stream);
+    if (vecs <= 64) return launch<16, 4>(a, stream);
+    if (vecs <= 128) return launch<128, 1>(a, stream);
     if (vecs <= 256) return launch<256, 1>(a, stream);
-    if (vecs <= 512) return launch<256, 2>(a, stream);
+    if (vecs <= 512) return launch<512, 1>(a, stream);
     if (vecs <= 1024) return launch<256, 4>(a, stream);
-    return launch<256, 8>(a, stream);
+    return launch<512, 4>(a, stream);
 }
 
 }  // namespace lily

@@ -9,8 +9,9 @@
 // off by 2^-5 at position 2^20.
 //
 // Bound: HBM (4 bytes a channel) for a prompt, latency for a step.  A thread has the 16 channels of a pair of
-// 16-byte vectors (eight pairs to turn, or a piece of the tail to copy), and takes
-// `heads_each` heads with the sines and cosines that it works out once.
+// 16-byte vectors (eight pairs to turn, or a piece of the tail to copy), and takes `heads_each` heads with the sines and
+// cosines that it works out once: with one head a thread a prompt is bound by its instructions.  The threads that turn
+// come first, so that no warp does both.
 #include <cstdint>
 
 #include "lily_internal.h"
@@ -24,26 +25,37 @@ template <bool NEXT>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a)
 {
     pdl_trigger();
-    const int parts = (a.copy ? a.D : a.rot) / 16, turn = a.rot / 16;
-    const unsigned unit = blockIdx.x * kThreads + threadIdx.x;
+    const int turn = a.rot / 16, tail = a.copy ? (a.D - a.rot) / 16 : 0;
+    const int heads = a.H_q + a.H_k, slices = a.slices;
+    // units of (token, slice of the heads, part): the parts that turn, then, from a block's border on, the tail
+    unsigned unit = blockIdx.x * kThreads + threadIdx.x;
+    const bool turns = blockIdx.x < a.turn_blocks;
+    if (!turns) unit -= a.turn_blocks * kThreads;
+    const unsigned parts = turns ? turn : tail;
     const int part = unit % parts;
-    const int heads = a.H_q + a.H_k, slices = (heads + a.heads_each - 1) / a.heads_each;
-    const int slice = unit / parts % slices;
-    const long long n = unit / parts / slices;
+    const unsigned rest = unit / parts;
+    const long long n = rest / slices;
+    const int slice = rest % slices;
     if (n >= a.N) return;
-    const bool turns = part < turn;
     // the two vectors of this part, in channels from the head's first
-    const int v0 = turns ? part * 8 : a.rot + (part - turn) * 8;
+    const int v0 = turns ? part * 8 : a.rot + part * 8;
     const int v1 = v0 + (turns ? a.rot : a.D - a.rot) / 2;
+    unsigned long long f[8];
+    if (turns) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // half: pairs v0 .. v0 + 7; next: four pairs from each vector
+            const unsigned long long *p = a.table + (NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j);
+            asm volatile("ld.global.nc.u64 %0, [%1];" : "=l"(f[j]) : "l"(p));  // never written by a kernel of the library
+        }
+    }
     pdl_wait();
     float c[8], s[8];
     if (turns) {
         const long long pos = a.positions[n];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // half: pairs v0 .. v0 + 7; next: four pairs from each vector
-            const int pair = NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j;
-            const unsigned long long fraction = static_cast<unsigned long long>(pos) * a.table[pair];
+            const unsigned long long fraction = static_cast<unsigned long long>(pos) * f[j];
             const float half_turns = static_cast<float>(static_cast<int>(fraction >> 32)) * 0x1p-31f;
             sincospif(half_turns, &s[j], &c[j]);
             s[j] *= a.amplitude;
@@ -51,32 +63,45 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         }
     }
     const int last = min(heads, (slice + 1) * a.heads_each);
-#pragma unroll 2
-    for (int h = slice * a.heads_each; h < last; ++h) {
-        const bool is_q = h < a.H_q;
-        const uint16_t *src = is_q ? a.q + n * a.q_stride + h * a.D : a.k + n * a.k_stride + (h - a.H_q) * a.D;
-        uint16_t *dst = is_q ? a.q_out + n * a.q_out_stride + h * a.D : a.k_out + n * a.k_out_stride + (h - a.H_q) * a.D;
-        const uint4 x = *reinterpret_cast<const uint4 *>(src + v0), y = *reinterpret_cast<const uint4 *>(src + v1);
-        uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-        if (turns) {
+    constexpr int kBatch = 3;
+    for (int h0 = slice * a.heads_each; h0 < last; h0 += kBatch) {
+        uint4 in[kBatch][2];
+        uint16_t *dst[kBatch];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x0 = __uint_as_float(xs[j] << 16), x1 = __uint_as_float(xs[j] & 0xFFFF0000u);
-                const float y0 = __uint_as_float(ys[j] << 16), y1 = __uint_as_float(ys[j] & 0xFFFF0000u);
-                __nv_bfloat162 p, q;
-                if (NEXT) {  // (x0, x1) is pair j of the first vector, (y0, y1) of the second
-                    p = __floats2bfloat162_rn(x0 * c[j] - x1 * s[j], x0 * s[j] + x1 * c[j]);
-                    q = __floats2bfloat162_rn(y0 * c[j + 4] - y1 * s[j + 4], y0 * s[j + 4] + y1 * c[j + 4]);
-                } else {  // (x0, y0) and (x1, y1) are pairs 2j and 2j + 1
-                    p = __floats2bfloat162_rn(x0 * c[2 * j] - y0 * s[2 * j], x1 * c[2 * j + 1] - y1 * s[2 * j + 1]);
-                    q = __floats2bfloat162_rn(x0 * s[2 * j] + y0 * c[2 * j], x1 * s[2 * j + 1] + y1 * c[2 * j + 1]);
-                }
-                xs[j] = *reinterpret_cast<const uint32_t *>(&p);
-                ys[j] = *reinterpret_cast<const uint32_t *>(&q);
-            }
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = h0 + i;
+            if (h >= last) break;
+            const bool is_q = h < a.H_q;
+            const uint16_t *src = is_q ? a.q + n * a.q_stride + h * a.D : a.k + n * a.k_stride + (h - a.H_q) * a.D;
+            dst[i] = is_q ? a.q_out + n * a.q_out_stride + h * a.D : a.k_out + n * a.k_out_stride + (h - a.H_q) * a.D;
+            in[i][0] = *reinterpret_cast<const uint4 *>(src + v0);
+            in[i][1] = *reinterpret_cast<const uint4 *>(src + v1);
         }
-        *reinterpret_cast<uint4 *>(dst + v0) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-        *reinterpret_cast<uint4 *>(dst + v1) = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (h0 + i >= last) break;
+            const uint4 x = in[i][0], y = in[i][1];
+            uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            if (turns) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x0 = __uint_as_float(xs[j] << 16), x1 = __uint_as_float(xs[j] & 0xFFFF0000u);
+                    const float y0 = __uint_as_float(ys[j] << 16), y1 = __uint_as_float(ys[j] & 0xFFFF0000u);
+                    __nv_bfloat162 p, q;
+                    if (NEXT) {  // (x0, x1) is pair j of the first vector, (y0, y1) of the second
+                        p = __floats2bfloat162_rn(x0 * c[j] - x1 * s[j], x0 * s[j] + x1 * c[j]);
+                        q = __floats2bfloat162_rn(y0 * c[j + 4] - y1 * s[j + 4], y0 * s[j + 4] + y1 * c[j + 4]);
+                    } else {  // (x0, y0) and (x1, y1) are pairs 2j and 2j + 1
+                        p = __floats2bfloat162_rn(x0 * c[2 * j] - y0 * s[2 * j], x1 * c[2 * j + 1] - y1 * s[2 * j + 1]);
+                        q = __floats2bfloat162_rn(x0 * s[2 * j] + y0 * c[2 * j], x1 * s[2 * j + 1] + y1 * c[2 * j + 1]);
+                    }
+                    xs[j] = *reinterpret_cast<const uint32_t *>(&p);
+                    ys[j] = *reinterpret_cast<const uint32_t *>(&q);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst[i] + v0) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+            *reinterpret_cast<uint4 *>(dst[i] + v1) = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+        }
     }
 }
 
@@ -86,9 +111,16 @@ cudaError_t launch_rope(const RopeArgs &args, cudaStream_t stream)
 {
     RopeArgs a = args;
     const int heads = a.H_q + a.H_k;
-    a.heads_each = 1;
-    const long long units = static_cast<long long>(a.N) * ((a.copy ? a.D : a.rot) / 16) * ((heads + a.heads_each - 1) / a.heads_each);
-    const dim3 grid(static_cast<unsigned>((units + kThreads - 1) / kThreads)), block(kThreads);
+    // As many heads a thread as leave 512 threads an SM that turn.  8,192 tokens of 18 heads of 256, a quarter of which turns: 24.9 us
+    // (6.1 TB/s); 33.6 with 2,048 threads an SM, 25.6 with 1,024, 28.1 with 128.
+    const long long wave = 152 * 512, turning = static_cast<long long>(a.N) * (a.rot / 16);
+    const long long most = turning * heads / wave;
+    a.heads_each = static_cast<int>(most < 1 ? 1 : most < heads ? most : heads);
+    a.slices = (heads + a.heads_each - 1) / a.heads_each;
+    a.heads_each = (heads + a.slices - 1) / a.slices;
+    auto blocks = [&](int parts) { return static_cast<unsigned>((static_cast<long long>(a.N) * a.slices * parts + kThreads - 1) / kThreads); };
+    a.turn_blocks = blocks(a.rot / 16);
+    const dim3 grid(a.turn_blocks + (a.copy ? blocks((a.D - a.rot) / 16) : 0)), block(kThreads);
     return a.next ? launch_pdl(rope_kernel<true>, grid, block, 0, stream, a)
                   : launch_pdl(rope_kernel<false>, grid, block, 0, stream, a);
 }

@@ -9,10 +9,11 @@
 // product of two fp32 numbers is exact.
 //
 // Bound: latency (the acceptance is a chain of three dependent loads), then HBM: only the
-// two rows that the next token is drawn from are read.  A cluster of kRanks CTAs takes one
+// two rows that the next token is drawn from are read.  A cluster of up to eight CTAs takes one
 // sequence; a warp sums one contiguous span of the row, the totals meet in distributed
 // shared memory, and the CTA that holds the threshold looks through that one span again (from L2).
 #include <cstdint>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -23,18 +24,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kRanks = 8;
+constexpr int kMaxRanks = 8;
 using u64 = unsigned long long;
 
-// p in [0, 1] in units of 2^-62, rounded down (exact from 2^-38 on); 0 for NaN and below 0.
+// p in [0, 1] in units of 2^-62, rounded down (exact from 2^-38 on); 0 for NaN and below 0, 1 above 1.  With e
+// the exponent's bits and m the 24-bit mantissa it is (m << 39) >> (127 - e): two words, by shifts that give 0 from 32 on.
 __device__ __forceinline__ u64 fixed62(float p)
 {
-    if (!(p > 0.0f)) return 0;
-    p = fminf(p, 1.0f);
-    const uint32_t bits = __float_as_uint(p);
-    const int e = static_cast<int>(bits >> 23);          // value = mantissa * 2^(e - 150)
-    const u64 m = (bits & 0x7FFFFFu) | 0x800000u;        // subnormals are far below 2^-62: 0 all the same
-    return e >= 88 ? m << (e - 88) : e >= 64 ? m >> (88 - e) : 0;
+    const uint32_t bits = __float_as_uint(fminf(fmaxf(p, 0.0f), 1.0f));
+    const uint32_t m = (bits & 0x7FFFFFu | 0x800000u) << 7, k = 127 - (bits >> 23);  // subnormals are far below 2^-62: 0 all the same
+    uint32_t hi, lo, low;
+    asm("shr.u32 %0, %1, %2;" : "=r"(hi) : "r"(m), "r"(k));
+    asm("shl.b32 %0, %1, %2;" : "=r"(lo) : "r"(m), "r"(32 - k));
+    asm("shr.u32 %0, %1, %2;" : "=r"(low) : "r"(m), "r"(k - 32));
+    return static_cast<u64>(hi) << 32 | lo | low;
 }
 
 // r in [0, 1) in units of 2^-64 (values outside: the nearest).
@@ -55,146 +58,217 @@ __device__ __forceinline__ u64 warp_sum(u64 v)
     return v;
 }
 
+// Sum over the lanes up to this one.
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+
 // Weight of token v: max(p - q, 0), or p where there is no q; `gone` has none.
 struct Row {
     const float *p, *q;
     int gone;
-    __device__ __forceinline__ u64 weight(float pv, float qv, int v) const
+    static __device__ __forceinline__ u64 above(float pv, float qv)
     {
-        const u64 a = fixed62(pv), b = q ? fixed62(qv) : 0;
-        return a > b && v != gone ? a - b : 0;
+        const u64 a = fixed62(pv), b = fixed62(qv);
+        return a > b ? a - b : 0;
     }
-    __device__ __forceinline__ u64 operator()(int v) const { return weight(p[v], q ? q[v] : 0.0f, v); }
+    __device__ __forceinline__ u64 operator()(int v) const
+    {
+        if (q) return above(p[v], q[v]);
+        return v == gone ? 0 : fixed62(p[v]);
+    }
 };
 
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
+// fixed62() by additions: p + 2, cut to the 2^-22 that its last bit is there, leaves 22 bits of p in the low bits of the pattern;
+// the rest, times 2^22 and then 2^40, 22 and 18 more.  (Half as many cycles as the shifts: fp32 additions have twice the rate
+// of integer shifts.)
+struct Pieces {
+    int a, b, c;
+};
+
+__device__ __forceinline__ Pieces pieces(float v)
+{
+    const float p = __saturatef(v);  // 0 for NaN
+    const float a = __fadd_rz(p, 2.0f), r = p - (a - 2.0f);
+    const float b = __fmaf_rz(r, 0x1p22f, 2.0f), s = fmaf(b - 2.0f, -0x1p-22f, r);
+    const float c = __fmaf_rz(s, 0x1p40f, 2.0f);
+    return {static_cast<int>(__float_as_uint(a)), static_cast<int>(__float_as_uint(b)), static_cast<int>(__float_as_uint(c))};
+}
+
+// A lane's part of the weights of [v0, v1): every 32nd, UNROLL loads of each row in flight.
+template <int UNROLL, bool Q>
+__device__ __forceinline__ u64 lane_sum(const Row &row, int v0, int v1, int lane)
+{
+    constexpr int kTwo = 0x40000000;  // the pattern of 2
+    u64 sum = 0;
+    for (int v = v0 + lane; v < v1; v += 32 * UNROLL) {
+        float pv[UNROLL], qv[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const bool on = v + 32 * j < v1;
+            pv[j] = on ? row.p[v + 32 * j] : 0.0f;
+            if (Q) qv[j] = on ? row.q[v + 32 * j] : 0.0f;
+        }
+        int a = 0, b = 0, c = 0;  // UNROLL differences of at most 2^22
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) {
+            const Pieces p = pieces(pv[j]);
+            if (Q) {
+                const Pieces q = pieces(qv[j]);
+                if (pv[j] > qv[j] || qv[j] != qv[j]) {  // above() in floats: a q of NaN counts as 0
+                    a += p.a - q.a;
+                    b += p.b - q.b;
+                    c += p.c - q.c;
+                }
+            } else if (v + 32 * j != row.gone) {
+                a += p.a - kTwo;
+                b += p.b - kTwo;
+                c += p.c - kTwo;
+            }
+        }
+        sum += static_cast<u64>(static_cast<long long>(a) << 40) + static_cast<u64>(static_cast<long long>(b) << 18) + static_cast<u64>(static_cast<long long>(c));
+    }
+    return sum;
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
     verify_kernel(const __grid_constant__ VerifyArgs a)
 {
+    constexpr int kWarps = THREADS / 32;
     __shared__ int first_refused;
-    __shared__ u64 span_sum[kWarps], total_s, scan_s[kWarps];
+    __shared__ u64 span_sum[32], scan_s[32], total_s[2];
     pdl_trigger();
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank()), b = blockIdx.x / kRanks, tid = threadIdx.x;
+    const int ranks = a.ranks, rank = static_cast<int>(cluster.block_rank()), b = blockIdx.x / ranks, tid = threadIdx.x;
     const int warp = tid / 32, lane = tid % 32;
     if (tid == 0) first_refused = 0x7FFFFFFF;
+    if (tid < 32) span_sum[tid] = scan_s[tid] = 0;
     __syncthreads();
     pdl_wait();
 
     const int c0 = a.cu[b], c1 = a.cu[b + 1], m = c1 - c0;
+    const float r = a.r[b];
     if (c0 < 0 || c1 < c0 || c1 > a.N) {  // all CTAs of the cluster agree
         if (tid == 0) record_error(&a.ctrl->status, kErrDeviceIndex);
         return;
     }
-    const float r = a.r[b];
-    for (int i = tid; i < m; i += kThreads) {
+    for (int i = tid; i < m; i += THREADS) {
         const int x = a.drafts[c0 + i];
+        const float u = a.u[c0 + i];
         bool ok = false;
         if (x < 0 || x >= a.V) {
             record_error(&a.ctrl->status, kErrDeviceIndex);
         } else {
             const double px = a.p[(static_cast<long long>(c0) + b + i) * a.p_stride + x];
             const double qx = a.q ? a.q[(static_cast<long long>(c0) + i) * a.q_stride + x] : 1.0f;
-            ok = static_cast<double>(a.u[c0 + i]) * qx < px;
+            ok = static_cast<double>(u) * qx < px;
         }
         if (!ok) atomicMin(&first_refused, i);
     }
     __syncthreads();
     const int n = min(first_refused, m);
     const bool refused = n < m;
-    if (rank == 0) {
-        if (tid == 0) a.accepted[b] = n;
-        for (int i = tid; i <= m; i += kThreads)
-            if (i != n) a.tokens[c0 + b + i] = i < n ? a.drafts[c0 + i] : -1;
-    }
-
     Row row;
     row.p = a.p + (static_cast<long long>(c0) + b + n) * a.p_stride;
     row.q = refused && a.q ? a.q + (static_cast<long long>(c0) + n) * a.q_stride : nullptr;
     row.gone = refused && !a.q ? a.drafts[c0 + n] : -1;
-    // the warp's span: [V s / S, V (s + 1) / S) of S = kRanks kWarps
-    const int s = rank * kWarps + warp;
-    auto bound = [&](int i) { return static_cast<int>(static_cast<long long>(a.V) * i / (kRanks * kWarps)); };
-    const int v0 = bound(s), v1 = bound(s + 1);
+    // the warp's span: [V s / S, V (s + 1) / S) of S = ranks kWarps
+    auto bound = [&](int i) { return static_cast<int>(static_cast<long long>(a.V) * i / (ranks * kWarps)); };
+    const int s = rank * kWarps + warp, v0 = bound(s), v1 = bound(s + 1);
     u64 total = 0, before = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        u64 sum = 0;
-        constexpr int kUnroll = 8;
-        int v = v0 + lane;
-        for (; v + 32 * (kUnroll - 1) < v1; v += 32 * kUnroll) {
-            float pv[kUnroll], qv[kUnroll];
-#pragma unroll
-            for (int j = 0; j < kUnroll; ++j) {
-                pv[j] = row.p[v + 32 * j];
-                qv[j] = row.q ? row.q[v + 32 * j] : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < kUnroll; ++j) sum += row.weight(pv[j], qv[j], v + 32 * j);
-        }
-        for (; v < v1; v += 32) sum += row(v);
-        sum = warp_sum(sum);
+        const u64 sum = warp_sum(row.q ? lane_sum<8, true>(row, v0, v1, lane) : lane_sum<16, false>(row, v0, v1, lane));
         if (lane == 0) span_sum[warp] = sum;
         __syncthreads();
         if (warp == 0) {
-            const u64 t = warp_sum(lane < kWarps ? span_sum[lane] : 0);
-            if (lane == 0) total_s = t;
+            const u64 t = warp_sum(span_sum[lane]);
+            if (lane == 0) total_s[pass] = t;
         }
         cluster.sync();
         total = before = 0;
-        for (int k = 0; k < kRanks; ++k) {
-            const u64 t = *cluster.map_shared_rank(&total_s, k);
+#pragma unroll
+        for (int k = 0; k < kMaxRanks; ++k) {
+            if (k >= ranks) break;
+            const u64 t = cluster.map_shared_rank(total_s, k)[pass];
             if (k < rank) before += t;
             total += t;
         }
-        cluster.sync();  // nobody writes or leaves while another reads
         if (total || (!row.q && row.gone < 0)) break;
         // p nowhere above q (as sums that are rounded can give): the token comes from p itself
         row.q = nullptr;
         row.gone = -1;
     }
-    if (total == 0) {
-        if (rank == 0 && tid == 0) {
+    auto done = cluster.barrier_arrive();  // nobody leaves while another reads
+    if (rank == 0) {
+        if (tid == 0) a.accepted[b] = n;
+        for (int i = tid; i <= m; i += THREADS)
+            if (i != n) a.tokens[c0 + b + i] = i < n ? a.drafts[c0 + i] : -1;
+        if (total == 0 && tid == 0) {
             a.tokens[c0 + b + n] = -1;
             record_error(&a.ctrl->status, kErrDeviceRange);
         }
-        return;
     }
-    // the token is the first whose running sum passes `below`
+    // the token is the first whose running sum passes `below`; the CTA that has it looks through its warp's span again, a
+    // contiguous piece for each thread
     const u64 below = __umul64hi(total, fixed64(r));
-    if (below < before || below - before >= total_s) return;  // another CTA has it
-    int w = 0;
-    for (; w < kWarps - 1 && below - before >= span_sum[w]; ++w) before += span_sum[w];
-    // that span again, a contiguous piece for each thread
-    const int u0 = bound(rank * kWarps + w), u1 = bound(rank * kWarps + w + 1);
-    const int each = (u1 - u0 + kThreads - 1) / kThreads;
-    const int a0 = min(u0 + tid * each, u1), a1 = min(a0 + each, u1);
-    u64 mine = 0;
-    for (int v = a0; v < a1; ++v) mine += row(v);
-    u64 upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += t;
-    }
-    if (lane == 31) scan_s[warp] = upto;
-    __syncthreads();
-    for (int k = 0; k < warp; ++k) before += scan_s[k];
-    before += upto - mine;
-    if (below >= before && below - before < mine) {
-        for (int v = a0; v < a1; ++v) {
-            before += row(v);
-            if (before > below) {
-                a.tokens[c0 + b + n] = v;
-                break;
+    const u64 upto = warp_scan(span_sum[lane], lane);
+    const unsigned passed = __ballot_sync(0xffffffffu, before <= below && below - before < upto);
+    if (total && passed) {
+        const int w = __ffs(passed) - 1;
+        before += w ? __shfl_sync(0xffffffffu, upto, w - 1) : 0;
+        const int u0 = bound(rank * kWarps + w), u1 = bound(rank * kWarps + w + 1);
+        const int each = (u1 - u0 + THREADS - 1) / THREADS;
+        const int a0 = min(u0 + tid * each, u1), a1 = min(a0 + each, u1);
+        u64 mine = 0;
+        for (int v = a0; v < a1; ++v) mine += row(v);
+        const u64 in_warp = warp_scan(mine, lane);
+        if (lane == 31) scan_s[warp] = in_warp;
+        __syncthreads();
+        before += warp_sum(lane < warp ? scan_s[lane] : 0) + in_warp - mine;
+        if (below >= before && below - before < mine) {
+            for (int v = a0; v < a1; ++v) {
+                before += row(v);
+                if (before > below) {
+                    a.tokens[c0 + b + n] = v;
+                    break;
+                }
             }
         }
     }
+    cluster.barrier_wait(std::move(done));
 }
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream)
+cudaError_t launch_verify(const VerifyArgs &args, cudaStream_t stream)
 {
-    return launch_pdl(verify_kernel, dim3(a.B * kRanks), dim3(kThreads), 0, stream, a);
+    VerifyArgs a = args;
+    // One wave of CTAs (a CTA's time is a chain of loads and barriers, and clusters leave gaps between waves: 200 sequences of 20,000
+    // tokens take 14.6 us with one CTA each, 20.4 with two, 69 with eight), in as many as that allows.
+    for (a.ranks = kMaxRanks; a.ranks > 1 && a.B * a.ranks > 152;) a.ranks /= 2;
+    // twice the threads for a CTA's part of a long row (64 rows of 131,072 in two parts 12.9 us against 15.2, eight of 100,003 in
+    // eight parts 9.2 against 8.4)
+    const bool wide = a.V / a.ranks >= 32768;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.B * a.ranks);
+    cfg.blockDim = dim3(wide ? 1024 : 512);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.ranks > 1 ? 2 : 1;
+    return wide ? cudaLaunchKernelEx(&cfg, verify_kernel<1024>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<512>, a);
 }
 
 }  // namespace lily
