@@ -281,9 +281,9 @@ struct MatvecArgs {
     void *out;                 // [T][rows]
     bool out_f32;
     // set by launch_matvec
-    int ranks;                 // CTAs of a cluster that share K
+    int per_chunk, block_steps;  // quads of K at a time; steps that have all their chunks one after another
     int tiles_log;             // log2 of a warp's tiles between joins
-    int steps_each, steps_more;  // steps of each cluster; the first `more` clusters have one more
+    int steps_each, steps_more;  // steps of each CTA; the first `more` CTAs have one more
     int wk_log;                // log2 of the warps of a CTA that share a row tile's K
 };
 constexpr int kMatvecMaxT = 32, kMatvecMaxK = 16384;
