@@ -23,15 +23,6 @@ namespace {
 template <int TPR>
 constexpr int kThreads = TPR > 32 ? TPR : 256;
 
-// A load that stays before pdl_wait (a plain one may be moved past it): the weight is
-// never written by a kernel of the library.
-__device__ __forceinline__ uint4 ld_weight(const void *p)
-{
-    uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8])
 {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -116,15 +107,15 @@ __global__ void __launch_bounds__(kThreads<TPR>) norm_kernel(const __grid_consta
         const int c = lane + i * TPR;
         if (c < vecs && a.weight) {
             const char *p = static_cast<const char *>(a.weight) + static_cast<size_t>(c) * (a.w_f32 ? 32 : 16);
-            w[i][0] = ld_weight(p);
-            if (a.w_f32) w[i][1] = ld_weight(p + 16);
+            w[i][0] = __ldg(reinterpret_cast<const uint4 *>(p));
+            if (a.w_f32) w[i][1] = __ldg(reinterpret_cast<const uint4 *>(p + 16));
         }
     };
+    pdl_wait();
     if (kWeightEarly) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) load_weight(i);
     }
-    pdl_wait();
 
     const long long x_at = n / a.H * a.x_stride + n % a.H * a.d, at = n * a.d;
     float h[PER][8];

@@ -40,22 +40,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     // the two vectors of this part, in channels from the head's first
     const int v0 = turns ? part * 8 : a.rot + part * 8;
     const int v1 = v0 + (turns ? a.rot : a.D - a.rot) / 2;
-    unsigned long long f[8];
-    if (turns) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // half: pairs v0 .. v0 + 7; next: four pairs from each vector
-            const unsigned long long *p = a.table + (NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j);
-            asm volatile("ld.global.nc.u64 %0, [%1];" : "=l"(f[j]) : "l"(p));  // never written by a kernel of the library
-        }
-    }
     pdl_wait();
     float c[8], s[8];
     if (turns) {
         const long long pos = a.positions[n];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const unsigned long long fraction = static_cast<unsigned long long>(pos) * f[j];
+            // half: pairs v0 .. v0 + 7; next: four pairs from each vector
+            const int pair = NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j;
+            const unsigned long long fraction = static_cast<unsigned long long>(pos) * __ldg(a.table + pair);
             const float half_turns = static_cast<float>(static_cast<int>(fraction >> 32)) * 0x1p-31f;
             sincospif(half_turns, &s[j], &c[j]);
             s[j] *= a.amplitude;

@@ -92,20 +92,20 @@ struct Pieces {
     int a, b, c;
 };
 
-__device__ __forceinline__ Pieces pieces(float v)
+__device__ __forceinline__ Pieces pieces(float p)  // p in [0, 1]
 {
-    const float p = __saturatef(v);  // 0 for NaN
     const float a = __fadd_rz(p, 2.0f), r = p - (a - 2.0f);
     const float b = __fmaf_rz(r, 0x1p22f, 2.0f), s = fmaf(b - 2.0f, -0x1p-22f, r);
     const float c = __fmaf_rz(s, 0x1p40f, 2.0f);
     return {static_cast<int>(__float_as_uint(a)), static_cast<int>(__float_as_uint(b)), static_cast<int>(__float_as_uint(c))};
 }
 
-// A lane's part of the weights of [v0, v1): every 32nd, UNROLL loads of each row in flight.
+// A lane's part of the weights of [v0, v1): every 32nd, UNROLL loads of each row in flight.  (`gone` is taken off elsewhere.)
 template <int UNROLL, bool Q>
 __device__ __forceinline__ u64 lane_sum(const Row &row, int v0, int v1, int lane)
 {
-    constexpr int kTwo = 0x40000000;  // the pattern of 2
+    // The patterns' own 2^30 vanishes where a multiple of four of them is added in 32 bits, zeros past the end among them.
+    static_assert(Q || UNROLL % 4 == 0, "");
     u64 sum = 0;
     for (int v = v0 + lane; v < v1; v += 32 * UNROLL) {
         float pv[UNROLL], qv[UNROLL];
@@ -118,18 +118,20 @@ __device__ __forceinline__ u64 lane_sum(const Row &row, int v0, int v1, int lane
         int a = 0, b = 0, c = 0;  // UNROLL differences of at most 2^22
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
-            const Pieces p = pieces(pv[j]);
+            const float ps = __saturatef(pv[j]);  // 0 for NaN
+            const Pieces p = pieces(ps);
             if (Q) {
-                const Pieces q = pieces(qv[j]);
-                if (pv[j] > qv[j] || qv[j] != qv[j]) {  // above() in floats: a q of NaN counts as 0
+                const float qs = __saturatef(qv[j]);
+                const Pieces q = pieces(qs);
+                if (ps > qs) {
                     a += p.a - q.a;
                     b += p.b - q.b;
                     c += p.c - q.c;
                 }
-            } else if (v + 32 * j != row.gone) {
-                a += p.a - kTwo;
-                b += p.b - kTwo;
-                c += p.c - kTwo;
+            } else {
+                a += p.a;
+                b += p.b;
+                c += p.c;
             }
         }
         sum += static_cast<u64>(static_cast<long long>(a) << 40) + static_cast<u64>(static_cast<long long>(b) << 18) + static_cast<u64>(static_cast<long long>(c));
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int s = rank * kWarps + warp, v0 = bound(s), v1 = bound(s + 1);
     u64 total = 0, before = 0;
     for (int pass = 0; pass < 2; ++pass) {
-        const u64 sum = warp_sum(row.q ? lane_sum<8, true>(row, v0, v1, lane) : lane_sum<16, false>(row, v0, v1, lane));
+        u64 sum = warp_sum(row.q ? lane_sum<8, true>(row, v0, v1, lane) : lane_sum<16, false>(row, v0, v1, lane));
+        if (row.gone >= v0 && row.gone < v1) sum -= fixed62(row.p[row.gone]);
         if (lane == 0) span_sum[warp] = sum;
         __syncthreads();
         if (warp == 0) {
