@@ -8,12 +8,14 @@
 // code * 2^-20 (bits 4-7), so eight codes are four masks and a shift.  (The e4m3 form of mma.sync would take them with two
 // masks, but here it is slower: 27 cycles a sub-core for twice the channels against 10, operands that change.)  bf16
 // tokens are taken times a power of two that brings the largest of the 256 channels of a token that a warp holds into
-// [2^14, 2^15): their eight significant bits survive down to 2^-31 of that largest magnitude, and what is smaller is off by at
-// most 2^-36 of it.  The norm's e4m3 tokens are fp16 numbers already.  Sums are fp32, scaled and joined a group at a
+// [2^14, 2^15): their eight significant bits survive down to 2^-27 of that largest magnitude, and what is smaller is off by at
+// most 2^-35 of it.  The norm's e4m3 tokens are fp16 numbers already.  Sums are fp32, scaled and joined a group at a
 // time.  The biases of four groups are one more mma, on bf16: their 16 columns are the four sums of x, each as three
 // bf16 numbers that add up to it exactly.
 //
-// Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions.  The order of the
+// Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
+// cost 11.8 us for 1 token (6.4 TB/s), 12.1 for 8, 18.7 for 16, 31.4 for 32; launch, x and the last tiles 4 to 5 us (9 for 32
+// tokens).  130,001 rows and 4 tokens: 29.3 us; 5,120 rows and 1 token: 4.4.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and

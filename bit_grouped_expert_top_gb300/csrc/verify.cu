@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (x < 0 || x >= a.V) {
             record_error(&a.ctrl->status, kErrDeviceIndex);
         } else {
-            const double px = a.p[(static_cast<long long>(c0) + b + i) * a.p_stride + x];
-            const double qx = a.q ? a.q[(static_cast<long long>(c0) + i) * a.q_stride + x] : 1.0f;
+            const double px = __saturatef(a.p[(static_cast<long long>(c0) + b + i) * a.p_stride + x]);
+            const double qx = a.q ? __saturatef(a.q[(static_cast<long long>(c0) + i) * a.q_stride + x]) : 1.0f;
             ok = static_cast<double>(u) * qx < px;
         }
         if (!ok) atomicMin(&first_refused, i);

@@ -125,7 +125,11 @@ def rope(x, positions, f, interleaved, amplitude=1.0):
 # ------------------------------------------------------------------ drafts
 def units(p):
     """p in units of 2^-62, rounded down, as Python integers."""
-    return [int(math.ldexp(min(max(float(v), 0.0), 1.0), 62)) if v == v else 0 for v in p]
+    return [int(math.ldexp(_clamped(v), 62)) for v in p]
+
+
+def _clamped(v):
+    return min(max(float(v), 0.0), 1.0) if v == v else 0.0
 
 
 def verify(p, q, drafts, cu, u, r):
@@ -139,8 +143,8 @@ def verify(p, q, drafts, cu, u, r):
             x = int(drafts[c0 + n])
             if not 0 <= x < V:
                 break
-            qx = 1.0 if q is None else float(q[c0 + n, x])
-            if not float(u[c0 + n]) * qx < float(p[c0 + b + n, x]):
+            qx = 1.0 if q is None else _clamped(q[c0 + n, x])
+            if not float(u[c0 + n]) * qx < _clamped(p[c0 + b + n, x]):
                 break
             n += 1
         whole = units(p[c0 + b + n])

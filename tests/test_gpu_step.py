@@ -259,6 +259,61 @@ def test_matvec_tokens_do_not_touch_each_other():
         assert torch.equal(out[keep], clean[keep])
 
 
+@pytest.mark.parametrize("K", [256, 320, 64 * 19])
+def test_matvec_rows_do_not_touch_each_other(K):
+    """Parameters that are not finite: a row's own output alone, also where rows share words of them."""
+    q, s, b = su.make_matrix(40, K, seed=8)
+    x, clean, out = _rand(3, K), torch.empty(3, 40, device="cuda"), torch.empty(3, 40, device="cuda")
+    lm.lily_q4_matvec(lm.make_q4(q, s, b), x, clean)
+    s, b = s.clone(), b.clone()
+    s[7], b[18], s[19, 0], b[39, -1] = float("nan"), float("inf"), float("inf"), float("nan")
+    lm.lily_q4_matvec(lm.make_q4(q, s, b), x, out)
+    keep = [n for n in range(40) if n not in (7, 18, 19, 39)]
+    assert torch.equal(out[:, keep], clean[:, keep]) and not bool(torch.isfinite(out[:, [7, 18, 19, 39]]).any())
+
+
+def test_offsets_beyond_32_bits():
+    """Arrays of more than 2^32 bytes: the last rows, tokens and probabilities."""
+    rows, K = 540001, 16384       # 4.4 GB of codes
+    part = su.make_matrix(65, K, seed=9)
+    q = torch.zeros((rows, K // 2), dtype=torch.uint8, device="cuda")
+    s, b = (torch.zeros((rows, K // 64), dtype=BF, device="cuda") for _ in "sb")
+    q[-65:], s[-65:], b[-65:] = part
+    for T in (3, 20):
+        x, out, small = _rand(T, K), torch.empty(T, rows, device="cuda"), torch.empty(T, 65, device="cuda")
+        lm.lily_q4_matvec(lm.make_q4(q, s, b), x, out)
+        lm.lily_q4_matvec(lm.make_q4(*part), x, small)
+        want, bound = su.matvec(*part, x)
+        su.near(out[:, -65:], want, bound * 2 + want.abs() * 2.0 ** -20)
+        su.near(small, want, bound * 2 + want.abs() * 2.0 ** -20)
+        assert float(out[:, :-65].abs().max()) == 0
+    del q, s, b, out
+    N, d = 270001, 8192           # 4.4 GB of bf16
+    x = torch.zeros(N, d, dtype=BF, device="cuda")
+    x[-3:] = _rand(3, d)
+    y = torch.empty_like(x)
+    lm.lily_rms_norm(x, None, y=y, weight_offset=1.0)
+    su.check_norm(su.norm(x[-3:], None, 1.0, 1e-6), y=y[-3:])
+    assert float(y[:-3].abs().max()) == 0
+    # the same memory as heads of 64 channels
+    heads, pos = x.view(N, d // 64, 64), torch.arange(N, dtype=torch.int32, device="cuda")
+    f = lm.rope_frequencies(64)
+    before = heads[-3:].clone()
+    lm.lily_rope(heads, None, pos, lm.make_rope_table(f))
+    su.near(heads[-3:].cpu(), *su.rope(before, pos[-3:], f, False))
+    del x, y, heads
+    V = 1 << 20                   # rows 4.8 GB apart
+    p, _, drafts, cu, u, r = _case([1], V, seed=4)
+    far = torch.zeros(1200000000 + V, device="cuda").as_strided((2, V), (1200000000, 1))
+    far.copy_(p.cuda())
+    acc, tok, ws = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda"), lm.alloc_draft_workspace()
+    for v in (0.0, 0.999999):
+        u[0] = v
+        lm.lily_draft_verify(far, None, drafts.cuda(), cu.cuda(), u.cuda(), r.cuda(), acc, tok, ws)
+        want = su.verify(p.numpy(), None, drafts.numpy(), cu.numpy(), u.numpy(), r.numpy())
+        assert np.array_equal(acc.cpu().numpy(), want[0]) and np.array_equal(tok.cpu().numpy(), want[1])
+
+
 def test_matvec_refusals_of_the_binding():
     parts = su.make_matrix(64, 256)
     w, x, out = lm.make_q4(*parts), _rand(4, 256), torch.empty(4, 64, device="cuda")
@@ -453,6 +508,19 @@ def test_verify_tiny_and_odd_probabilities():
     p[2, 11] = 1e-45
     _verify(p, q, drafts, cu, u, r)
     _verify(p, None, drafts, cu, u, r)
+
+
+def test_verify_of_drafts_without_a_probability():
+    """At the draft itself: NaN and what is below 0 count as 0, what is above 1 as 1."""
+    nan, inf = float("nan"), float("inf")
+    odd = [(0.5, nan), (nan, 0.5), (0.0, -1.0), (-1.0, 0.0), (nan, nan), (0.25, inf), (inf, 0.25), (0.0, 0.0), (1e-30, 0.0), (3.0, 2.0)]
+    p, q = _distributions(2 * len(odd), 64, 1), _distributions(len(odd), 64, 2)
+    for i, (a, b) in enumerate(odd):
+        p[2 * i, 7], q[i, 7] = a, b
+    n = len(odd)
+    for u in (0.0, 0.3, 0.999):
+        _verify(p, q, torch.full((n,), 7, dtype=torch.int32), torch.arange(n + 1, dtype=torch.int32), torch.full((n,), u), torch.full((n,), 0.4))
+        _verify(p, None, torch.full((n,), 7, dtype=torch.int32), torch.arange(n + 1, dtype=torch.int32), torch.full((n,), u), torch.full((n,), 0.4))
 
 
 def test_verify_where_the_target_is_nowhere_above_the_draft():
