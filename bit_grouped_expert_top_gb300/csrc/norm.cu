@@ -19,9 +19,10 @@
 namespace lily {
 namespace {
 
-// Threads of a CTA whose rows have TPR threads each: one row, where that is more than a warp.
+// Threads of a CTA whose rows have TPR threads each: one row, where that is more than a warp, else 128 (with 256 the last CTAs end
+// later: 60,000 rows of 128 13.5 us against 12.7, 32,784 of 256 14.8 against 13.9).
 template <int TPR>
-constexpr int kThreads = TPR > 32 ? TPR : 256;
+constexpr int kThreads = TPR > 32 ? TPR : 128;
 
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8])
 {
@@ -253,7 +254,7 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
 {
     const int vecs = a.d / 8;
     // Many rows: a few threads a row, with more vectors in flight each, up to 512 channels, then one vector a thread (32,784 rows
-    // of 256 heads' channels: 8.5 us with 16 threads a row, 10.3 with 32; 16,384 rows of 512: 16.7 with 16, 17.6 with 64, 41.8 with
+    // of 256 heads' channels: 8.3 us with 16 threads a row, 10.3 with 32; 16,384 rows of 512: 16.5 with 16, 17.6 with 64, 41.8 with
     // 256; 8,192 rows of 1,024: 14.1 with 128, 20.9 with 32; 4,096 of 4,096: 29.5 with 512, 31.3 with 256; 1,024 of 16,384: 34.4 with
     // 512, 38.3 with 1,024, 46.0 with 256).  Few rows: as many threads as a row has vectors (8 rows of 512: 1.6 us with 128, 3.3 with 16).
     const bool few = a.rows < 2048;
