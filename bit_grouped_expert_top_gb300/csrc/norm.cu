@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kThreads<TPR>) norm_kernel(const __grid_consta
         const int c = lane + i * TPR;
         if (c < vecs && a.weight) {
             const char *p = static_cast<const char *>(a.weight) + static_cast<size_t>(c) * (a.w_f32 ? 32 : 16);
-            w[i][0] = __ldg(reinterpret_cast<const uint4 *>(p));
-            if (a.w_f32) w[i][1] = __ldg(reinterpret_cast<const uint4 *>(p + 16));
+            w[i][0] = *reinterpret_cast<const uint4 *>(p);
+            if (a.w_f32) w[i][1] = *reinterpret_cast<const uint4 *>(p + 16);
         }
     };
     pdl_wait();

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         for (int j = 0; j < 8; ++j) {
             // half: pairs v0 .. v0 + 7; next: four pairs from each vector
             const int pair = NEXT ? (j < 4 ? v0 / 2 + j : v1 / 2 + j - 4) : v0 + j;
-            const unsigned long long fraction = static_cast<unsigned long long>(pos) * __ldg(a.table + pair);
+            const unsigned long long fraction = static_cast<unsigned long long>(pos) * a.table[pair];
             const float half_turns = static_cast<float>(static_cast<int>(fraction >> 32)) * 0x1p-31f;
             sincospif(half_turns, &s[j], &c[j]);
             s[j] *= a.amplitude;
