@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     const int n = min(first_refused, m);
     const bool refused = n < m;
+    if (rank == 0 && tid == 0) a.tokens[c0 + b + n] = -1;  // stays where no weight is; ahead of the cluster's barrier, behind which the token comes
     Row row;
     row.p = a.p + (static_cast<long long>(c0) + b + n) * a.p_stride;
     row.q = refused && a.q ? a.q + (static_cast<long long>(c0) + n) * a.q_stride : nullptr;
@@ -213,10 +214,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (tid == 0) a.accepted[b] = n;
         for (int i = tid; i <= m; i += THREADS)
             if (i != n) a.tokens[c0 + b + i] = i < n ? a.drafts[c0 + i] : -1;
-        if (total == 0 && tid == 0) {
-            a.tokens[c0 + b + n] = -1;
-            record_error(&a.ctrl->status, kErrDeviceRange);
-        }
+        if (total == 0 && tid == 0) record_error(&a.ctrl->status, kErrDeviceRange);
     }
     // the token is the first whose running sum passes `below`; the CTA that has it looks through its warp's span again, a
     // contiguous piece for each thread

@@ -591,7 +591,7 @@ int lily_rope_table(const double *freq, int32_t n, uint64_t *table);
  *             (i = n), -1 (n < i <= m).  Entries from cu[B] + B on are left as they were.
  *   ws        at least LILY_DRAFT_WORKSPACE_BYTES, for the status word
  * Probabilities are in [0, 1] and a row's sum below 4; they count in units of 2^-62, rounded down, and their sums
- * are exact.  (Values below 0 and NaN count as 0, above 1 as 1.)
+ * are exact.  (Values below 0 and NaN count as 0, above 1 as 1.  A row that sums to 4 or more gives any token of [0, V), or -1.)
  * Device-detected: a draft outside [0, V) records LILY_ERR_DEVICE_INDEX and counts as refused (with q NULL, nothing is
  * then taken out of p); bounds in cu that descend, or leave [0, N], record it and leave that sequence's outputs alone; a row
  * without any weight records LILY_ERR_DEVICE_RANGE and gives the token -1.

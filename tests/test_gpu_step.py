@@ -570,6 +570,23 @@ def test_verify_reports_rows_without_weight():
     _verify(p, q, drafts, cu, u, r, status=-9)
 
 
+@pytest.mark.parametrize("V", [1000, 1001, 100003])
+@pytest.mark.parametrize("draft", [False, True])
+def test_verify_rows_that_are_no_distributions(V, draft):
+    """A sum beyond the fixed point's range still writes a token of the vocabulary, or -1, and nothing else."""
+    B, N = 7, 7 if draft else 0
+    p = torch.ones((N + B, V), device="cuda")
+    q = torch.full((N, V), 0.25, device="cuda") if draft else None
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * (1 if draft else 0)
+    drafts = torch.full((N,), 3, dtype=torch.int32, device="cuda")
+    u = torch.full((N,), 8.0, device="cuda")  # refused: 8 / 4 > 1
+    acc, tok = (torch.full((n + 8,), -7, dtype=torch.int32, device="cuda") for n in (B, N + B))
+    lm.lily_draft_verify(p, q, drafts, cu, u, torch.linspace(0, 0.999, B, device="cuda"), acc[:B], tok[:N + B], lm.alloc_draft_workspace())
+    acc, tok = acc.tolist(), tok.tolist()
+    assert acc == [0] * B + [-7] * 8 and tok[N + B:] == [-7] * 8
+    assert all(-1 <= t < V for t in tok[:N + B])
+
+
 def test_verify_refusals_of_the_binding():
     p, q, drafts, cu, u, r = (t.cuda() for t in _case([2, 1], 50))
     acc, tok, ws = torch.empty(2, dtype=torch.int32, device="cuda"), torch.empty(5, dtype=torch.int32, device="cuda"), lm.alloc_draft_workspace()
