@@ -15,7 +15,7 @@
 //
 // Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
 // cost 11.8 us for 1 token (6.4 TB/s), 12.1 for 8, 18.7 for 16, 31.4 for 32; launch, x and the last tiles 4 to 5 us (9 for 32
-// tokens).  130,001 rows and 4 tokens: 29.3 us; 5,120 rows and 1 token: 4.4.  The order of the
+// tokens).  130,001 rows and 4 tokens: 28.9 us; 5,120 rows and 1 token: 3.8.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and
@@ -33,6 +33,7 @@ namespace lily {
 namespace {
 
 constexpr int kPitch = 20;        // floats between tokens of a joined tile: the fragment's stores meet no bank twice
+constexpr int kSkew = 16;         // floats more between the two steps of a unit: the join reads both at once, off each other's banks
 constexpr int kTileBytes = 2560;  // a quad of 16 rows in the ring: 128 bytes of codes, 16 of scales, 16 of biases a row
 constexpr int kMaxSmem = 226 * 1024;
 
@@ -210,7 +211,7 @@ constexpr int kStages = WARPS == 16 ? 4 : NT <= 2 ? 6 : 5;
 struct Layout {
     int warps, nt, tiles_log, stages, block_bytes;
     __host__ __device__ int join() const { return warps * nt * 128; }
-    __host__ __device__ int join_bytes() const { return (warps * 8 * nt * kPitch * 4) << tiles_log; }
+    __host__ __device__ int join_bytes() const { return ((warps * 8 * nt * kPitch + kSkew) * 4) << tiles_log; }
     __host__ __device__ int ring() const { return join() + 2 * join_bytes(); }
     __host__ __device__ int block() const { return ring() + warps * stages * kTileBytes; }
     __host__ __device__ int total() const { return block() + block_bytes; }
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             for (int step = block; step < block_end; turn ^= 1) {
                 float *sums = reinterpret_cast<float *>(smem + L.join() + turn * L.join_bytes()) + warp * kSums + t * (2 * kPitch) + g;
                 const int unit_step = step, steps = min(1 << tiles_log, block_end - step);
-                for (int r = 0; r < steps; ++r, ++step, sums += WARPS * kSums) {
+                for (int r = 0; r < steps; ++r, ++step, sums += WARPS * kSums + kSkew) {
                     const int row0 = step * step_rows + m_warp * 16;
                     float part[NT][4];
 #pragma unroll
@@ -422,7 +423,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                 for (int i = threadIdx.x; i < items; i += kThreads) {
                     const int token = i >> fours_log, n = (i & (1 << fours_log) - 1) * 4, row = unit_step * step_rows + n;
                     if (row >= end_row) continue;
-                    const float *from = joined + ((n / 16 >> wm_log) * WARPS + ((n >> 4 & wm - 1) << a.wk_log)) * kSums + token * kPitch + n % 16;
+                    const int of_unit = n / 16 >> wm_log;  // step of the unit
+                    const float *from = joined + (of_unit * WARPS + ((n >> 4 & wm - 1) << a.wk_log)) * kSums + of_unit * kSkew + token * kPitch + n % 16;
                     float4 sum = *reinterpret_cast<const float4 *>(from);
 #pragma unroll 8
                     for (int k = 1; k < wk; ++k) {
@@ -464,6 +466,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+int log2_at_least(int n)
+{
+    int log = 0;
+    while ((1 << log) < n) ++log;
+    return log;
+}
+
 template <int NT, int WARPS, bool VEC, bool CODES>
 cudaError_t launch(MatvecArgs a, const Layout &L, int num_sms, cudaStream_t stream)
 {
@@ -481,11 +490,11 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
     MatvecArgs a = args;
     const int quads = (a.K / 64 + 3) / 4, chunks = (quads + WARPS - 1) / WARPS;
     a.per_chunk = (quads + chunks - 1) / chunks;
-    a.wk_log = 0;
-    while ((1 << a.wk_log) < a.per_chunk) ++a.wk_log;
-    // two steps a unit halve the barriers, where there are steps enough
+    a.wk_log = log2_at_least(a.per_chunk);
+    // Two steps a unit halve the barriers: where some CTA has two, with more than 16 tokens where each has (4,096 rows of 16,384: 15.0 us
+    // against 16.2 for 1 token, 62.0 against 58.9 for 32; 16,384 of 8,192 18.8 against 20.7 for 1, 31.2 against 35.7 for 16).
     const int step_rows = (WARPS >> a.wk_log) * 16;
-    a.tiles_log = a.rows >= 4ll * 2 * step_rows * num_sms ? 1 : 0;
+    a.tiles_log = a.rows > (NT <= 2 ? 1ll : 2ll) * step_rows * num_sms ? 1 : 0;
     Layout L{WARPS, NT, a.tiles_log, kStages<NT, WARPS>, 0};
     a.block_steps = 1 << 30;
     if (chunks > 1) {
@@ -501,6 +510,10 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
 
 cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 {
+    // Up to 8 tokens half the warps start sooner and join less, where they hold all of K and a CTA has a few steps (1,024 rows
+    // of 1,024: 2.35 us against 3.13; 5,120 of 2,048 3.82 against 4.26; 10,240 of 2,048 5.45 against 5.57; 12,288 6.31 against 6.00).
+    const int quads = (a.K + 255) / 256;
+    if (a.T <= 8 && quads <= 8 && a.rows <= 4ll * (8 >> log2_at_least(quads)) * 16 * num_sms) return launch<1, 8>(a, num_sms, stream);
     if (a.T <= 8) return launch<1, 16>(a, num_sms, stream);
     if (a.T <= 16) return launch<2, 8>(a, num_sms, stream);
     if (a.T <= 24) return launch<3, 8>(a, num_sms, stream);

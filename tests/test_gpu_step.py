@@ -196,6 +196,18 @@ def test_matvec_large(T):
     assert all(torch.equal(first, out[:, i * 16251:(i + 1) * 16251]) for i in range(1, 8))
 
 
+@pytest.mark.parametrize("K,rows", [(2048, 9720), (2048, 9729), (1984, 9728), (1984, 9731), (320, 38912), (320, 38997), (64, 77811), (64, 77824),
+                                    (2112, 2431), (2112, 2435), (4096, 2433), (8256, 2500)])
+@pytest.mark.parametrize("T", [1, 8, 16, 24])
+def test_matvec_around_the_steps_of_a_block(K, rows, T):
+    """Rows where a block has few steps, or more, of either size."""
+    parts = su.make_matrix(rows, K, seed=rows)
+    x = _rand(T, K)
+    _matvec(parts, x, F32)
+    y8, sc = _codes(x)
+    _matvec(parts, y8, BF, sc)
+
+
 def test_matvec_strided_tokens():
     parts = su.make_matrix(130, 512)
     x = _rand(6, 2048)[:, 512:1024]
