@@ -105,48 +105,47 @@ struct Tokens {
     float factor[CODES ? 1 : NT][2];  // bf16: of tokens 2 t and 2 t + 1
 };
 
-// Loads a quad of x (its groups from g_last on, and tokens past T, as zeros).  CODES: leaves the factors of its groups for
+__device__ __forceinline__ void load16(uint32_t *to, const char *p)
+{
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3]) : "l"(p) : "memory");
+}
+
+// Loads a quad of x (its groups from g_last on as zeros).  CODES: leaves the factors of its groups for
 // tokens 2 t and 2 t + 1, [n][t][j][2], at `factors`.
-template <int NT, bool CODES>
+template <int NT, bool VEC, bool CODES>
 __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecArgs &a, int g_first, int g_last, int lane, float *factors)
 {
     const int t = lane % 4;
-    // all loads first, to where their fp16 form goes
-    float scale[CODES ? NT : 1][4];
+    // All loads first, to where their fp16 form goes: as asm, or the compiler puts some off until others are converted, which costs another
+    // round trip (2,048 rows of 4,096, 24 tokens: 8.9 us against 10.3).  Tokens past T are the last one again: their columns are not stored.
+    float scale[CODES ? NT : 1];  // of group t
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        const long long token = min(8 * n + lane / 4, a.T - 1);
+        const char *p = static_cast<const char *>(a.x) + (token * a.x_stride + g_first * 64 + 16 * t) * (CODES ? 1 : 2);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int token = 8 * n + lane / 4;
-            uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-            float f = 0.0f;
-            if (token < a.T && g_first + j < g_last) {
-                const long long at = token * a.x_stride + (g_first + j) * 64 + 16 * t;
-                if (CODES) {
-                    r0 = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.x) + at);
-                    f = a.x_scale[static_cast<long long>(token) * (a.K / 64) + g_first + j];
-                } else {
-                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at);
-                    r0 = p[0];
-                    r1 = p[1];
-                }
-            }
             uint32_t *x = to.x[n][j];
-            x[0] = r0.x; x[1] = r0.y; x[2] = r0.z; x[3] = r0.w;
-            x[4] = r1.x; x[5] = r1.y; x[6] = r1.z; x[7] = r1.w;
-            if (CODES) scale[CODES ? n : 0][j] = f;
+            if (VEC || g_first + j < g_last) {
+                load16(x, p + j * (CODES ? 64 : 128));
+                if (!CODES) load16(x + 4, p + j * 128 + 16);
+            } else {
+#pragma unroll
+                for (int i = 0; i < (CODES ? 4 : 8); ++i) x[i] = 0;
+            }
         }
+        if (CODES) scale[CODES ? n : 0] = VEC || g_first + t < g_last ? a.x_scale[token * (a.K / 64) + g_first + t] : 0.0f;
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float sum[4], by = 64.0f;  // the largest code, 448, is 28,672
         if (!CODES) {
-            // the largest magnitude: bf16 patterns without their signs order as the numbers do
-            uint32_t most2 = 0;
+            __nv_bfloat162 most2 = __floats2bfloat162_rn(0.0f, 0.0f);  // NaN leaves it
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) most2 = __vmaxu2(most2, to.x[n][j][i] & 0x7FFF7FFFu);
-            uint32_t most = max(most2 & 0xFFFFu, most2 >> 16);
+                for (int i = 0; i < 8; ++i) most2 = __hmax2(most2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&to.x[n][j][i])));
+            uint32_t most = max(static_cast<uint32_t>(__bfloat16_as_ushort(most2.x)), static_cast<uint32_t>(__bfloat16_as_ushort(most2.y)));
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
             // x times 2^(14 - e), e = floor(log2 most) in [-113, 127]
@@ -176,29 +175,27 @@ __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecA
             for (int w = 0; w < 2; ++w)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) to.x[n][j][4 * w + i] = f16x2(x[8 * w + i], x[8 * w + i + 4]);
-            // products with codes are times 2^-24 and `by`
-            if (CODES && t == 0) factors[((n * 4 + lane / 8) * 4 + j) * 2 + lane / 4 % 2] = scale[CODES ? n : 0][j] * 0x1p18f;
         }
-        uint32_t part[4][3];  // the groups' sums as three bf16 numbers
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-            float rest = sum[j] * (CODES ? scale[CODES ? n : 0][j] * 0.015625f : 0x1p-24f);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) {  // what is left of 24 bits after eight more
-                const __nv_bfloat16 p = __float2bfloat16_rn(rest);
-                part[j][k] = __bfloat16_as_ushort(p);
-                rest -= __bfloat162float(p);
-            }
-        }
+        // the four lanes' sums of four groups: lane t gets the whole of group t's
+        const float keep0 = (t & 1 ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[0] : sum[1], 1);
+        const float keep1 = (t & 1 ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[2] : sum[3], 1);
+        float rest = (t & 2 ? keep1 : keep0) + __shfl_xor_sync(0xffffffffu, t & 2 ? keep0 : keep1, 2);
+        rest *= CODES ? scale[CODES ? n : 0] * 0.015625f : 0x1p-24f;
+        // products with codes are times 2^-24 and `by`
+        if (CODES) factors[((n * 4 + lane / 8) * 4 + t) * 2 + lane / 4 % 2] = scale[CODES ? n : 0] * 0x1p18f;
+        // as three bf16 numbers: what is left of 24 bits after eight more
+        const __nv_bfloat16 p0 = __float2bfloat16_rn(rest);
+        rest -= __bfloat162float(p0);
+        const __nv_bfloat16 p1 = __float2bfloat16_rn(rest);
+        rest -= __bfloat162float(p1);
+        const uint32_t first = __bfloat16_as_ushort(p0) | static_cast<uint32_t>(__bfloat16_as_ushort(p1)) << 16;
+        const uint32_t last = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
         // columns 2 t, 2 t + 1: the first numbers of groups 0 1 | 2 3, then the second; columns 8 + 2 t: the third, nothing
-        const int j = t % 2 * 2;
-        uint32_t pair[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) pair[k] = j ? part[2][k] | part[3][k] << 16 : part[0][k] | part[1][k] << 16;
-        to.sums[n][0] = t < 2 ? pair[0] : pair[1];
-        to.sums[n][1] = t < 2 ? pair[2] : 0;
+        const int from = lane & ~3 | t % 2 * 2;
+        const uint32_t first0 = __shfl_sync(0xffffffffu, first, from), first1 = __shfl_sync(0xffffffffu, first, from + 1);
+        const uint32_t last0 = __shfl_sync(0xffffffffu, last, from), last1 = __shfl_sync(0xffffffffu, last, from + 1);
+        to.sums[n][0] = __byte_perm(first0, first1, t < 2 ? 0x5410 : 0x7632);
+        to.sums[n][1] = t < 2 ? last0 | last1 << 16 : 0;
     }
 }
 
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
             const bool works = k_warp < per_chunk && c0 + k_warp < all_quads;
             if (works) {
                 __syncwarp();  // all lanes are done with the factors before
-                load_tokens<NT, CODES>(x, a, (c0 + k_warp) * 4, groups, lane, factors);
+                load_tokens<NT, VEC, CODES>(x, a, (c0 + k_warp) * 4, groups, lane, factors);
                 __syncwarp();
             }
             const int block_end = min(block + a.block_steps, last_step);
