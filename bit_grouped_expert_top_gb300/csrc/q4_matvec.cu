@@ -14,8 +14,8 @@
 // bf16 numbers that add up to it exactly.
 //
 // Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
-// cost 11.8 us for 1 token (6.4 TB/s), 12.1 for 8, 18.7 for 16, 31.4 for 32; launch, x and the last tiles 4 to 5 us (9 for 32
-// tokens).  130,001 rows and 4 tokens: 28.9 us; 5,120 rows and 1 token: 3.8.  The order of the
+// cost 12.2 us for 1 token (6.2 TB/s), 12.6 for 8, 18.9 for 16, 30.7 for 32; launch, x and the last tiles 4 to 5 us (7 for 32
+// tokens).  130,001 rows and 4 tokens: 28.9 us; 5,120 rows and 1 token: 3.7.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and
