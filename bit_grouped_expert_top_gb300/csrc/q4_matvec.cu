@@ -207,9 +207,10 @@ __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecA
     }
 }
 
-// Stages of a warp's ring: what shared memory leaves beside the joins of two steps a unit, and some sums so far.
+// Stages of a warp's ring: what its memory time needs, and no more (65,536 rows of 2,048: 1 token 16.0 us with three, 16.5 with four; 16
+// tokens 23.5 with four, 24.0 with six; 32 tokens 37.8 with five, 38.3 with four).
 template <int NT, int WARPS>
-constexpr int kStages = WARPS == 16 ? 4 : NT <= 2 ? 6 : 5;
+constexpr int kStages = WARPS == 16 ? 3 : NT <= 3 ? 4 : 5;
 
 // Shared memory: the factors [warp][NT][4][4][2]; two of the warps' sums, [step of the unit][warp][token][row]; the ring
 // [warp][stage] of tiles; where K is more than a chunk, the sums so far of a block's steps, [step][token][row].
