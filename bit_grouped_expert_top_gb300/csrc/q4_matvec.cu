@@ -14,8 +14,8 @@
 // bf16 numbers that add up to it exactly.
 //
 // Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
-// cost 12.2 us for 1 token (6.2 TB/s), 12.6 for 8, 18.9 for 16, 30.7 for 32; launch, x and the last tiles 4 to 5 us (7 for 32
-// tokens).  130,001 rows and 4 tokens: 28.9 us; 5,120 rows and 1 token: 3.7.  The order of the
+// cost 11.6 us for 1 token (6.5 TB/s), 12.0 for 8, 19.1 for 16, 30.7 for 32; launch, x and the last tiles 3 to 5 us (7 for 32
+// tokens).  130,001 rows and 4 tokens: 27.8 us; 5,120 rows and 1 token: 3.6.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and
@@ -505,10 +505,12 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
     const int quads = (a.K / 64 + 3) / 4, chunks = (quads + WARPS - 1) / WARPS;
     a.per_chunk = (quads + chunks - 1) / chunks;
     a.wk_log = log2_at_least(a.per_chunk);
-    // Two steps a unit halve the barriers: where some CTA has two, with more than 16 tokens where each has (4,096 rows of 16,384: 15.0 us
-    // against 16.2 for 1 token, 62.0 against 58.9 for 32; 16,384 of 8,192 18.8 against 20.7 for 1, 31.2 against 35.7 for 16).
+    // A unit is as many steps as some CTA has, up to four, which leaves a quarter of the barriers (8,192 rows of 2,048 and 1 token: 4.4 us
+    // against 4.7 with two; 130,001 of 2,048 and 4 tokens 27.8 against 28.8; 4,096 of 16,384 15.0 against 16.2 with one); above 8 tokens
+    // shared memory has room for two, and above 16 they pay where each CTA has two (32 tokens on 4,096 of 16,384: 62.0 us against 58.9).
     const int step_rows = (WARPS >> a.wk_log) * 16;
-    a.tiles_log = a.rows > (NT <= 2 ? 1ll : 2ll) * step_rows * num_sms ? 1 : 0;
+    const long long wave = static_cast<long long>(step_rows) * num_sms;
+    a.tiles_log = NT == 1 && a.rows > 2 * wave ? 2 : a.rows > (NT <= 2 ? 1 : 2) * wave ? 1 : 0;
     Layout L{WARPS, NT, a.tiles_log, kStages<NT, WARPS>, 0};
     a.block_steps = 1 << 30;
     if (chunks > 1) {
@@ -524,10 +526,10 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
 
 cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 {
-    // Up to 8 tokens half the warps start sooner and join less, where they hold all of K and a CTA has a few steps (1,024 rows
-    // of 1,024: 2.35 us against 3.13; 5,120 of 2,048 3.82 against 4.26; 10,240 of 2,048 5.45 against 5.57; 12,288 6.31 against 6.00).
+    // Up to 8 tokens half the warps start sooner and join less, where they hold all of K and a CTA has up to eight steps (1,024 rows
+    // of 1,024: 2.3 us against 3.1; 10,240 of 2,048 4.8 against 5.3; 16,384 6.2 against 6.3; 65,536 19.5 against 16.7).
     const int quads = (a.K + 255) / 256;
-    if (a.T <= 8 && quads <= 8 && a.rows <= 4ll * (8 >> log2_at_least(quads)) * 16 * num_sms) return launch<1, 8>(a, num_sms, stream);
+    if (a.T <= 8 && quads <= 8 && a.rows <= 8ll * (8 >> log2_at_least(quads)) * 16 * num_sms) return launch<1, 8>(a, num_sms, stream);
     if (a.T <= 8) return launch<1, 16>(a, num_sms, stream);
     if (a.T <= 16) return launch<2, 8>(a, num_sms, stream);
     if (a.T <= 24) return launch<3, 8>(a, num_sms, stream);

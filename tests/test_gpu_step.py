@@ -197,7 +197,8 @@ def test_matvec_large(T):
 
 
 @pytest.mark.parametrize("K,rows", [(2048, 9720), (2048, 9729), (1984, 9728), (1984, 9731), (320, 38912), (320, 38997), (64, 77811), (64, 77824),
-                                    (2112, 2431), (2112, 2435), (4096, 2433), (8256, 2500)])
+                                    (2112, 2431), (2112, 2435), (4096, 2433), (8256, 2500),
+                                    (2048, 4870), (1984, 19456), (2048, 19457), (1984, 19500), (192, 77830), (4096, 4870), (4160, 5003)])
 @pytest.mark.parametrize("T", [1, 8, 16, 24])
 def test_matvec_around_the_steps_of_a_block(K, rows, T):
     """Rows where a block has few steps, or more, of either size."""
