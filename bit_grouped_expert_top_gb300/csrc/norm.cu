@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads<TPR>) norm_kernel(const __grid_consta
         const float mean = squares(pow2) * a.inv_d + a.eps * pow2 * pow2;
         if (far) {
             by = pow2;
-            r = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;  // eps = 0 and a row of zeros: zeros
+            r = mean == 0.0f ? 0.0f : 1.0f / sqrtf(mean);  // eps = 0 and a row of zeros: zeros (a NaN stays one)
         }
     }
 #pragma unroll

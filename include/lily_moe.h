@@ -497,7 +497,8 @@ enum { LILY_BF16 = 0, LILY_F32 = 1, LILY_E4M3 = 2 };  /* element types of the ca
  *              unrounded y: scale = max |y| / 448, code = e4m3(y * (448 / max |y|)), value = code * scale;
  *              a group with max |y| < 2^-100 has codes and scale zero.
  * At least one of y and y8 is given.  eps >= 0; a row of zeros with eps = 0 gives zeros.  Any finite x whose
- * sum with the residual is an fp32 number: squares beyond the fp32 range are taken care of.
+ * sum with the residual is an fp32 number: squares beyond the fp32 range are taken care of.  A row whose h has a NaN gives NaN in
+ * all of y and in all codes (scales 0); one with infinities, NaN in their places and zeros elsewhere; other rows are not touched.
  * x_type, h_type and w_type are LILY_BF16 or LILY_F32.  d a multiple of 8 (with y8 of 64) in [8, 16384]; N * H < 2^31.
  */
 typedef struct lily_norm_shape {
