@@ -15,7 +15,7 @@
 //
 // Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
 // cost 11.6 us for 1 token (6.5 TB/s), 12.0 for 8, 19.1 for 16, 30.7 for 32; launch, x and the last tiles 3 to 5 us (7 for 32
-// tokens).  130,001 rows and 4 tokens: 27.8 us; 5,120 rows and 1 token: 3.6.  The order of the
+// tokens).  130,001 rows and 4 tokens: 28.3 us; 5,120 rows and 1 token: 4.0.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and
@@ -46,6 +46,8 @@ __device__ __forceinline__ void copy(uint32_t to, const void *from, int n = BYTE
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(BYTES), "r"(n) : "memory");
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
@@ -313,8 +315,26 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         }
         copy_commit();
     };
-    for (int i = 0; i < kS - 1; ++i) load();  // the matrix is never written by a kernel of the library: ahead of the wait
+    // The matrix may come from a kernel before, so the copies stand behind the wait.  Ahead of it the first tiles are called to L2, which
+    // every store goes through: no value is taken.  (1 token on 5,120 rows of 2,048: 3.95 us, 4.44 without; 16 tokens on 65,536
+    // 23.4 against 24.2; 32 tokens on 65,536, where registers are short, 38.7 against 38.1.)
+    if (NT <= 3 && my_chunks > 0) {
+#pragma unroll
+        for (int i = 0; i < kS - 1; ++i) {
+            const int row = load_row + i * step_rows + lane % 16;
+            if (row < load_end) {
+                if (lane < 16) {
+                    prefetch_l2(a.w + row * half + k_warp * 128);
+                } else {
+                    const long long at = static_cast<long long>(row) * groups + k_warp * 4;
+                    prefetch_l2(a.s + at);
+                    prefetch_l2(a.b + at);
+                }
+            }
+        }
+    }
     pdl_wait();
+    for (int i = 0; i < kS - 1; ++i) load();
     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const unsigned char *tile = ring;
     const unsigned char *const ring_end = ring + kS * kTileBytes;

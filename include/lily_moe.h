@@ -519,6 +519,7 @@ int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride,
  * Weights and e4m3 x enter the products unrounded, bf16 x too, but for values below 2^-27 of the largest of the 256 channels
  * [256 i, 256 i + 256) of their token, which are off by at most 2^-35 of that largest; sums are fp32.  A token with values that
  * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 may lose bits.
+ * Like x, the matrix may be the output of an earlier kernel of the stream, the one just before among them.
  * Supported: 0 <= T <= 32 (in whole groups of 8: five tokens cost what eight do); K a multiple of 64 in [64, 16384];
  * 1 <= rows < 2^30.
  */
