@@ -89,7 +89,7 @@ struct Row {
 // the rest, times 2^22 and then 2^40, 22 and 18 more.  (Half as many cycles as the shifts: fp32 additions have twice the rate
 // of integer shifts.)
 struct Pieces {
-    int a, b, c;
+    uint32_t a, b, c;
 };
 
 __device__ __forceinline__ Pieces pieces(float p)  // p in [0, 1]
@@ -97,8 +97,11 @@ __device__ __forceinline__ Pieces pieces(float p)  // p in [0, 1]
     const float a = __fadd_rz(p, 2.0f), r = p - (a - 2.0f);
     const float b = __fmaf_rz(r, 0x1p22f, 2.0f), s = fmaf(b - 2.0f, -0x1p-22f, r);
     const float c = __fmaf_rz(s, 0x1p40f, 2.0f);
-    return {static_cast<int>(__float_as_uint(a)), static_cast<int>(__float_as_uint(b)), static_cast<int>(__float_as_uint(c))};
+    return {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c)};
 }
+
+// A 32-bit number, negative ones as they are modulo 2^64.
+__device__ __forceinline__ u64 signed64(uint32_t v) { return static_cast<u64>(static_cast<long long>(static_cast<int>(v))); }
 
 // A lane's part of the weights of [v0, v1): every 32nd, UNROLL loads of each row in flight.  (`gone` is taken off elsewhere.)
 template <int UNROLL, bool Q>
@@ -115,7 +118,7 @@ __device__ __forceinline__ u64 lane_sum(const Row &row, int v0, int v1, int lane
             pv[j] = on ? row.p[v + 32 * j] : 0.0f;
             if (Q) qv[j] = on ? row.q[v + 32 * j] : 0.0f;
         }
-        int a = 0, b = 0, c = 0;  // UNROLL differences of at most 2^22
+        uint32_t a = 0, b = 0, c = 0;  // modulo 2^32: UNROLL numbers of at most 2^22, or differences of them
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) {
             const float ps = __saturatef(pv[j]);  // 0 for NaN
@@ -134,7 +137,7 @@ __device__ __forceinline__ u64 lane_sum(const Row &row, int v0, int v1, int lane
                 c += p.c;
             }
         }
-        sum += static_cast<u64>(static_cast<long long>(a) << 40) + static_cast<u64>(static_cast<long long>(b) << 18) + static_cast<u64>(static_cast<long long>(c));
+        sum += (signed64(a) << 40) + (signed64(b) << 18) + signed64(c);
     }
     return sum;
 }
