@@ -1125,6 +1125,8 @@ int lily_rope(const lily_rope_shape *shape, const uint16_t *q, int64_t q_stride,
             return rc;
         if (k_out == k && k_out_stride != k_stride) return LILY_ERR_INVALID;
     }
+    const int sms = num_sms_current();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "device query");
     RopeArgs a{};
     a.N = s.N; a.H_q = s.H_q; a.H_k = s.H_k; a.D = s.D; a.rot = s.rot;
     a.next = s.interleaved != 0;
@@ -1134,7 +1136,7 @@ int lily_rope(const lily_rope_shape *shape, const uint16_t *q, int64_t q_stride,
     a.q_stride = q_stride; a.k_stride = k_stride; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
     a.positions = positions;
     a.table = reinterpret_cast<const unsigned long long *>(table);
-    return to_status(launch_rope(a, stream), "rotary positions launch");
+    return to_status(launch_rope(a, sms, stream), "rotary positions launch");
 }
 
 int lily_rope_frequencies(const lily_rope_scaling *scaling, int32_t rot, double *freq)
@@ -1191,13 +1193,15 @@ int lily_draft_verify(const lily_draft_shape *shape, const float *p, int64_t p_s
     if (s.N > 0 && ((rc = check_ptr(drafts)) || (rc = check_ptr(u)))) return rc;
     if (q && !aligned16(q)) return LILY_ERR_MISALIGNED;
     if ((rc = check_stride(p_stride, s.V, 1)) || (q && (rc = check_stride(q_stride, s.V, 1)))) return rc;
+    const int sms = num_sms_current();
+    if (sms <= 0) return cuda_fail(cudaGetLastError(), "device query");
     VerifyArgs a{};
     a.B = s.B; a.N = s.N; a.V = s.V;
     a.p = p; a.q = q; a.p_stride = p_stride; a.q_stride = q_stride;
     a.drafts = drafts; a.cu = cu; a.u = u; a.r = r;
     a.accepted = accepted; a.tokens = tokens;
     a.ctrl = at<Ctrl>(ws, 0);
-    return to_status(launch_verify(a, stream), "draft verification launch");
+    return to_status(launch_verify(a, sms, stream), "draft verification launch");
 }
 
 int lily_moe_route_noalloc(const lily_moe_shape *shape, const lily_moe_weights *w, const uint16_t *x,

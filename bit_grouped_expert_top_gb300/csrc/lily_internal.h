@@ -268,7 +268,7 @@ struct RopeArgs {
     int heads_each, slices;    // heads of a thread, threads that share a token's heads
     unsigned turn_blocks;      // CTAs that turn
 };
-cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs &a, int num_sms, cudaStream_t stream);
 
 // A few tokens times a 4-bit matrix (q4_matvec.cu).
 struct MatvecArgs {
@@ -303,7 +303,7 @@ struct VerifyArgs {
     Ctrl *ctrl;
     int ranks;                 // CTAs of a sequence (set by launch_verify)
 };
-cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyArgs &a, int num_sms, cudaStream_t stream);
 
 // Gated DeltaNet scan (gdn.cu): CTA (16-row slice of the state, value head).
 struct GdnArgs {

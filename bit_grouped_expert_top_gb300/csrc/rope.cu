@@ -100,13 +100,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs &args, cudaStream_t stream)
+cudaError_t launch_rope(const RopeArgs &args, int num_sms, cudaStream_t stream)
 {
     RopeArgs a = args;
     const int heads = a.H_q + a.H_k;
     // As many heads a thread as leave 512 threads an SM that turn.  8,192 tokens of 18 heads of 256, a quarter of which turns: 24.9 us
     // (6.1 TB/s); 33.6 with 2,048 threads an SM, 25.6 with 1,024, 28.1 with 128.
-    const long long wave = 152 * 512, turning = static_cast<long long>(a.N) * (a.rot / 16);
+    const long long wave = num_sms * 512ll, turning = static_cast<long long>(a.N) * (a.rot / 16);
     const long long most = turning * heads / wave;
     a.heads_each = static_cast<int>(most < 1 ? 1 : most < heads ? most : heads);
     a.slices = (heads + a.heads_each - 1) / a.heads_each;

@@ -251,12 +251,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs &args, cudaStream_t stream)
+cudaError_t launch_verify(const VerifyArgs &args, int num_sms, cudaStream_t stream)
 {
     VerifyArgs a = args;
     // One wave of CTAs (a CTA's time is a chain of loads and barriers, and clusters leave gaps between waves: 200 sequences of 20,000
     // tokens take 14.6 us with one CTA each, 20.4 with two, 69 with eight), in as many as that allows.
-    for (a.ranks = kMaxRanks; a.ranks > 1 && a.B * a.ranks > 152;) a.ranks /= 2;
+    for (a.ranks = kMaxRanks; a.ranks > 1 && a.B * a.ranks > num_sms;) a.ranks /= 2;
     // twice the threads for a CTA's part of a long row (64 rows of 131,072 in two parts 12.9 us against 15.2, eight of 100,003 in
     // eight parts 9.2 against 8.4)
     const bool wide = a.V / a.ranks >= 32768;

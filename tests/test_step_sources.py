@@ -1,5 +1,5 @@
 """What the kernels between the layers promise each other that no run can show, read from their sources: no value of global memory is
-taken before the wait for the kernels before."""
+taken before the wait for the kernels before, and no rule knows the GPU's size."""
 import os
 import re
 
@@ -57,3 +57,9 @@ def test_nothing_is_read_ahead_of_the_wait(name):
             if READS.search(does):
                 assert not re.search(rf"\b{called}\(", ahead), f"{kernel}: {called}() ahead of the wait"
     assert found == 1
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_rule_has_the_number_of_sms_written_in(name):
+    """It is the device's: a part of a GPU, or another one, has fewer."""
+    assert not re.search(r"\b152\b", text(name))
