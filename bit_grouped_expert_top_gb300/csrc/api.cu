@@ -1108,7 +1108,7 @@ int lily_rope(const lily_rope_shape *shape, const uint16_t *q, int64_t q_stride,
     if (s.interleaved != 0 && s.interleaved != 1) return LILY_ERR_INVALID;
     if (s.D % 16 != 0 || s.D > 512 || s.rot % 16 != 0) return LILY_ERR_UNSUPPORTED;
     const int64_t heads = static_cast<int64_t>(s.H_q) + s.H_k;
-    if (heads >= (1 << 20) || s.N * heads >= (int64_t(1) << 34) / s.D) return LILY_ERR_UNSUPPORTED;
+    if (heads >= (1 << 20) || s.N * heads > ((int64_t(1) << 34) - 1) / s.D) return LILY_ERR_UNSUPPORTED;
     if (s.N == 0) return LILY_OK;
     int rc;
     for (const void *p : {static_cast<const void *>(q), static_cast<const void *>(positions),

@@ -541,7 +541,7 @@ int lily_q4_matvec(const lily_q4_shape *shape, const lily_q4 *w, const void *x, 
  *   table      device, uint64 [rot/2]: round(f_i / (2 pi) * 2^64) of each pair, as lily_rope_table makes it (on the host)
  *   q_out, k_out  as q and k, with their own strides; either may be its input itself (with the same stride)
  * The angle is exact to 2^-31 half-turns at every position.  fp32 arithmetic, each output rounded once.
- * Supported: D a multiple of 16 in [16, 512], rot a multiple of 16 in [16, D]; N * (H_q + H_k) * D < 2^34.
+ * Supported: D a multiple of 16 in [16, 512], rot a multiple of 16 in [16, D]; H_q + H_k < 2^20, N * (H_q + H_k) * D < 2^34.
  */
 typedef struct lily_rope_shape {
     int32_t N, H_q, H_k, D, rot;
