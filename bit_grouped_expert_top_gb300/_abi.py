@@ -623,6 +623,11 @@ def _need_array(name: str, t, dtype, shape, dev: int) -> None:
           f"strides {t.stride()} on {t.device}")
 
 
+def _need_int32(*sizes) -> None:
+    """ctypes would pass the low 32 bits of larger ones."""
+    _need(max(sizes) < 1 << 31, f"sizes of more than 32 bits: {list(sizes)}")
+
+
 def lily_rms_norm(x, weight=None, y=None, y8=None, y8_scale=None, residual=None, h=None, eps: float = 1e-6,
                   weight_offset: float = 0.0, stream=None, *, check: bool = True) -> int:
     """Root-mean-square norm with the residual's addition (see include/lily_moe.h): x [N][d], or [N][H][d] for the heads
@@ -668,6 +673,8 @@ def lily_rms_norm(x, weight=None, y=None, y8=None, y8_scale=None, residual=None,
             _need_array("h", h, residual.dtype, size, dev)
         raise ValueError("tensors on different devices")
     N = size[0]
+    if (N | H | d) >> 31:
+        _need_int32(N, H, d)
     rc = (_lib or load()).lily_rms_norm(
         lily_norm_shape(N, H, d, xt is _F32, rt is _F32, wt is _F32), x.data_ptr(), st[0] if N > 1 else H * d, None if residual is None else residual.data_ptr(),
         None if h is None else h.data_ptr(), None if weight is None else weight.data_ptr(), weight_offset, eps,
@@ -686,6 +693,7 @@ def make_q4(q, scale, bias) -> lily_q4:
     _need(dev >= 0 and q.is_contiguous(), f"q: expected a contiguous CUDA tensor, got strides {q.stride()} on {q.device}")
     _need_array("scale", scale, _BF16, (rows, half // 32), dev)
     _need_array("bias", bias, _BF16, (rows, half // 32), dev)
+    _need_int32(rows, 2 * half)
     w = lily_q4(q.data_ptr(), scale.data_ptr(), bias.data_ptr())
     w.rows, w.K, w.device = rows, 2 * half, dev
     return w
@@ -713,6 +721,8 @@ def lily_q4_matvec(w: lily_q4, x, out, x_scale=None, stream=None, *, check: bool
         _need_array("out", out, ot, (size[0], rows), dev)
         raise ValueError("tensors on different devices")
     T = size[0]
+    if T >> 31:
+        _need_int32(T)
     rc = (_lib or load()).lily_q4_matvec(
         lily_q4_shape(T, rows, K, 2 if xt is _E4M3 else 0, ot is _F32), w, x.data_ptr(), st[0] if T > 1 else K,
         None if x_scale is None else x_scale.data_ptr(), out.data_ptr(), _launch_stream(stream, dev))
@@ -727,6 +737,7 @@ def rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none", fa
     """Angle of each of the rot / 2 pairs a position (fp64, on the host), scaled for contexts longer than the trained
     one: "none", "linear", "base" or "parts" (see lily_rope_frequencies in include/lily_moe.h)."""
     _need(scaling in ROPE_SCALING, f"scaling: expected one of {sorted(ROPE_SCALING)}, got {scaling!r}")
+    _need_int32(rot)
     out = torch.empty(max(rot // 2, 1), dtype=torch.float64)
     c = lily_rope_scaling(ROPE_SCALING[scaling], theta, factor, original, low, high)
     _check("lily_rope_frequencies", load().lily_rope_frequencies(c, rot, out.data_ptr()))
@@ -785,9 +796,12 @@ def lily_rope(q, k, positions, table, q_out=None, k_out=None, interleaved: bool 
         raise ValueError("tensors on different devices")
     N, H_q = qs[0], qs[1]
     H_k = 0 if k is None else ks[1]
+    rot = 2 * table.shape[0]
+    if (N | H_q | H_k | D | rot) >> 31:
+        _need_int32(N, H_q, H_k, D, rot)
     dense_q, dense_k = H_q * D, H_k * D
     rc = (_lib or load()).lily_rope(
-        lily_rope_shape(N, H_q, H_k, D, 2 * table.shape[0], 1 if interleaved else 0), q.data_ptr(), st[0] if N > 1 else dense_q,
+        lily_rope_shape(N, H_q, H_k, D, rot, 1 if interleaved else 0), q.data_ptr(), st[0] if N > 1 else dense_q,
         None if k is None else k.data_ptr(), 0 if k is None else kst[0] if N > 1 else dense_k, positions.data_ptr(),
         table.data_ptr(), amplitude, q_out.data_ptr(), so[0] if N > 1 else dense_q, None if k is None else k_out.data_ptr(),
         0 if k is None else kso[0] if N > 1 else dense_k, _launch_stream(stream, dev))
@@ -834,6 +848,8 @@ def lily_draft_verify(p, q, drafts, cu, u, r, accepted, tokens, ws, stream=None,
         _need_dense("ws", ws, _U8, 1, dev)
         raise ValueError("tensors on different devices")
     V = ps[1]
+    if (B | N | V) >> 31:
+        _need_int32(B, N, V)
     rc = (_lib or load()).lily_draft_verify(
         lily_draft_shape(B, N, V), p.data_ptr(), st[0] if N + B > 1 else V, None if q is None or N == 0 else q.data_ptr(),
         V if q is None or N <= 1 else q.stride(0), drafts.data_ptr() if N else None, cu.data_ptr(), u.data_ptr() if N else None,
