@@ -3,10 +3,10 @@
 // Pair i of a head is turned by the angle pos * f_i:
 //   (a, b) -> amplitude * (a cos - b sin, a sin + b cos)
 // with the pair's channels (i, i + rot/2) or (2i, 2i + 1) of the first `rot`.
-// f_i / 2 pi is held as a 64-bit fraction of a turn, so the turns of a position modulo one are an
-// integer product modulo 2^64: exact but for the fraction's own 2^-65, at any position.  Its top 32 bits, an
-// angle off by at most 2^-32 half-turns, go to sincospif.  In fp32, pos * f_i alone would be
-// off by 2^-5 at position 2^20.
+// f_i / 2 pi is held as a 64-bit fraction of a turn (53 bits of it, as it comes from fp64), so the turns of a position
+// modulo one are an integer product modulo 2^64: exact for that fraction, at any position.  Its top 32 bits, cut by up to
+// 2^-31 half-turns and rounded to fp32 by up to 2^-25 (as much as sincospif's own error), go to sincospif.  In
+// fp32, pos * f_i alone would be off by 2^-5 at position 2^20.
 //
 // Bound: HBM (4 bytes a channel) for a prompt, latency for a step.  A thread has the 16 channels of a pair of
 // 16-byte vectors (eight pairs to turn, or a piece of the tail to copy), and takes `heads_each` heads with the sines and

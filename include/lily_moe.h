@@ -538,9 +538,11 @@ int lily_q4_matvec(const lily_q4_shape *shape, const lily_q4 *w, const void *x, 
  * with (a, b) the channels (i, i + rot/2), or (2i, 2i + 1) where `interleaved` is not 0.
  *   q, k       bf16 [N][H_q][D], [N][H_k][D], token strides at least H * D, multiples of 8; k and k_out may be NULL with H_k = 0
  *   positions  int32 [N], any values
- *   table      device, uint64 [rot/2]: round(f_i / (2 pi) * 2^64) of each pair, as lily_rope_table makes it (on the host)
+ *   table      device, uint64 [rot/2]: f_i / (2 pi) * 2^64 of each pair, as lily_rope_table makes it (on the host)
  *   q_out, k_out  as q and k, with their own strides; either may be its input itself (with the same stride)
- * The angle is exact to 2^-31 half-turns at every position.  fp32 arithmetic, each output rounded once.
+ * The table's entry times the position is exact modulo a turn, at every position, and its sine and cosine are taken in fp32: the
+ * angle is off by at most 2^-24 half-turns + |positions[n]| * f_i * 2^-52 radians (the latter is the table's, whose entries are
+ * worked out in fp64).  fp32 arithmetic, each output rounded once.
  * Supported: D a multiple of 16 in [16, 512], rot a multiple of 16 in [16, D]; H_q + H_k < 2^20, N * (H_q + H_k) * D < 2^34.
  */
 typedef struct lily_rope_shape {
@@ -571,7 +573,8 @@ typedef struct lily_rope_scaling {
 
 int lily_rope_frequencies(const lily_rope_scaling *scaling, int32_t rot, double *freq);
 
-/* table[i] = round(freq[i] / (2 pi) * 2^64), for n frequencies in [0, 2 pi) (HOST arrays). */
+/* table[i] = round(t * 2^64) of t = freq[i] / (2 pi) in fp64 (off by less than 2^-52 of it), for n frequencies in
+ * [0, 2 pi) (HOST arrays). */
 int lily_rope_table(const double *freq, int32_t n, uint64_t *table);
 
 /*
