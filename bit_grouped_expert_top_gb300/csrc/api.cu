@@ -778,6 +778,8 @@ int lily_moe_decode(const lily_moe_shape *shape, int32_t n_layers, const lily_mo
 
     auto enqueue_all = [&](cudaStream_t st) -> cudaError_t {
         Ctrl *ctrl = at<Ctrl>(ws, L.ctrl);
+        // No kernel, so it starts after all that the stream held before, and the kernels behind it, whose first weight loads stand
+        // ahead of their waits, find weights that an earlier kernel of the stream wrote.
         cudaError_t e = cudaMemsetAsync(&ctrl->ticket2, 0, sizeof(unsigned int), st);
         if (e != cudaSuccess) return e;
         for (int l = 0; l < n_layers; ++l) {

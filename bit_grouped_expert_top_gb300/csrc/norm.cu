@@ -257,6 +257,8 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream)
     // of 256 heads' channels: 8.3 us with 16 threads a row, 10.3 with 32; 16,384 rows of 512: 16.5 with 16, 17.6 with 64, 41.8 with
     // 256; 8,192 rows of 1,024: 14.1 with 128, 20.9 with 32; 4,096 of 4,096: 29.5 with 512, 31.3 with 256; 1,024 of 16,384: 34.4 with
     // 512, 38.3 with 1,024, 46.0 with 256).  Few rows: as many threads as a row has vectors (8 rows of 512: 1.6 us with 128, 3.3 with 16).
+    // One border for three lengths: 2,047 rows of 128 take 3.6 us with 32 threads and 2.8 with 8, of 256 3.4 with 32 and 3.9 with 16, of
+    // 512 4.1 with 128 and 6.8 with 16; 8,192 rows 5.3 and 4.3, 5.4 and 5.3, 11.4 and 9.4.
     const bool few = a.rows < 2048;
     if (vecs <= 8) return launch<8, 1>(a, stream);
     if (few && vecs <= 32) return launch<32, 1>(a, stream);

@@ -14,8 +14,9 @@
 // bf16 numbers that add up to it exactly.
 //
 // Bound: HBM (0.5625 bytes a weight) up to 8 tokens, then the tensor cores' and the warps' instructions: 65,536 more rows of 2,048
-// cost 11.6 us for 1 token (6.5 TB/s), 12.0 for 8, 19.1 for 16, 30.7 for 32; launch, x and the last tiles 3 to 5 us (7 for 32
-// tokens).  130,001 rows and 4 tokens: 28.3 us; 5,120 rows and 1 token: 4.0.  The order of the
+// cost 11.4 us for 1 token (6.6 TB/s), 12.1 for 8, 19.1 for 16, 30.9 for 32; launch, x and the last tiles 4 to 5 us (7 for 32
+// tokens).  130,001 rows and 4 tokens: 28.1 us; 5,120 rows and 1 token: 4.0.  Warps along K are a power of two, and what K
+// does not fill of them waits: 20,001 rows of 2,112 take 10.1 us for 1 token and 27.7 for 32, of 2,048 half as much a weight.  The order of the
 // channels within an mma is free as long as both sides agree: a thread takes 16 consecutive channels of a group.  A warp keeps the
 // fragments of its four groups (a quad: 256 channels) of x in registers and takes the rows' pieces of that quad past them, one
 // tile of 16 rows after another, through a ring of asynchronous copies of its own; the warps of a CTA share a row's K and
@@ -126,8 +127,9 @@ template <int NT, bool VEC, bool CODES>
 __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecArgs &a, int g_first, int g_last, int lane, float *factors)
 {
     const int t = lane % 4;
-    // All loads first, to where their fp16 form goes: as asm, or the compiler puts some off until others are converted, which costs another
-    // round trip (2,048 rows of 4,096, 24 tokens: 8.9 us against 10.3).  Tokens past T are the last one again: their columns are not stored.
+    // All loads first, to where their fp16 form goes: as asm, so that the compiler puts none off until others are converted (it did, for
+    // another round trip; as the code stands it need not: 32 tokens on 65,536 rows of 2,048 38.1 us, 38.4 with plain loads, 24 on 2,048 of
+    // 4,096 9.3 both ways).  Tokens past T are the last one again: their columns are not stored.
     float scale[CODES ? NT : 1];  // of group t
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -209,8 +211,8 @@ __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecA
     }
 }
 
-// Stages of a warp's ring: what its memory time needs, and no more (65,536 rows of 2,048: 1 token 16.0 us with three, 16.5 with four; 16
-// tokens 23.5 with four, 24.0 with six; 32 tokens 37.8 with five, 38.3 with four).
+// Stages of a warp's ring: what its memory time needs, and no more (65,536 rows of 2,048: 16 tokens 23.4 us with four, 24.3 with six; 24
+// tokens 31.0 with four, 31.8 with five; 32 tokens 38.1 with five, 39.1 with four; a fourth for 16 warps has no room beside four steps a join).
 template <int NT, int WARPS>
 constexpr int kStages = WARPS == 16 ? 3 : NT <= 3 ? 4 : 5;
 
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
         copy_commit();
     };
     // The matrix may come from a kernel before, so the copies stand behind the wait.  Ahead of it the first tiles are called to L2, which
-    // every store goes through: no value is taken.  (1 token on 5,120 rows of 2,048: 3.95 us, 4.44 without; 16 tokens on 65,536
+    // every store goes through: no value is taken.  (1 token on 5,120 rows of 2,048: 4.0 us, 4.4 without; 16 tokens on 65,536
     // 23.4 against 24.2; 32 tokens on 65,536, where registers are short, 38.7 against 38.1.)
     if (NT <= 3 && my_chunks > 0) {
 #pragma unroll
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                                     mul2(acc[n][0], acc[n][1], f.x, f.y);
                                     mul2(acc[n][2], acc[n][3], f.x, f.y);
                                 }
-                                // two at once where registers are left for the pairs (16 tokens 24.0 us against 24.3, 32 tokens 38.7 against 37.8)
+                                // two at once where registers are left for the pairs (16 tokens 23.4 us against 24.0, 32 tokens 39.4 against 38.1)
                                 if (NT <= 2) {
                                     fma2(part[n][0], part[n][1], acc[n][0], acc[n][1], by[0]);
                                     fma2(part[n][2], part[n][3], acc[n][2], acc[n][3], by[1]);
@@ -525,9 +527,10 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
     const int quads = (a.K / 64 + 3) / 4, chunks = (quads + WARPS - 1) / WARPS;
     a.per_chunk = (quads + chunks - 1) / chunks;
     a.wk_log = log2_at_least(a.per_chunk);
-    // A unit is as many steps as some CTA has, up to four, which leaves a quarter of the barriers (8,192 rows of 2,048 and 1 token: 4.4 us
-    // against 4.7 with two; 130,001 of 2,048 and 4 tokens 27.8 against 28.8; 4,096 of 16,384 15.0 against 16.2 with one); above 8 tokens
-    // shared memory has room for two, and above 16 they pay where each CTA has two (32 tokens on 4,096 of 16,384: 62.0 us against 58.9).
+    // A unit is as many steps as some CTA has, up to four, which leaves a quarter of the barriers (8,192 rows of 2,048 and 1 token: 4.6 us
+    // against 4.9 with two; 130,001 of 2,048 and 4 tokens 28.0 against 29.1; 4,096 of 16,384 14.8 against 16.1 with one); above 8 tokens
+    // shared memory has room for two, and above 16 they pay where each CTA has two (32 tokens on 65,536 of 2,048 38.1 us against 39.4
+    // with one, but on 4,096 of 16,384, where some CTAs have one step, 48.5 against 47.3).
     const int step_rows = (WARPS >> a.wk_log) * 16;
     const long long wave = static_cast<long long>(step_rows) * num_sms;
     a.tiles_log = NT == 1 && a.rows > 2 * wave ? 2 : a.rows > (NT <= 2 ? 1 : 2) * wave ? 1 : 0;
@@ -547,7 +550,7 @@ cudaError_t launch(const MatvecArgs &args, int num_sms, cudaStream_t stream)
 cudaError_t launch_matvec(const MatvecArgs &a, int num_sms, cudaStream_t stream)
 {
     // Up to 8 tokens half the warps start sooner and join less, where they hold all of K and a CTA has up to eight steps (1,024 rows
-    // of 1,024: 2.3 us against 3.1; 10,240 of 2,048 4.8 against 5.3; 16,384 6.2 against 6.3; 65,536 19.5 against 16.7).
+    // of 1,024: 2.5 us against 3.3; 10,240 of 2,048 5.5 against 5.7; 19,456 6.9 against 7.0; 65,536 17.2 against 15.8).
     const int quads = (a.K + 255) / 256;
     if (a.T <= 8 && quads <= 8 && a.rows <= 8ll * (8 >> log2_at_least(quads)) * 16 * num_sms) return launch<1, 8>(a, num_sms, stream);
     if (a.T <= 8) return launch<1, 16>(a, num_sms, stream);

@@ -105,7 +105,8 @@ cudaError_t launch_rope(const RopeArgs &args, int num_sms, cudaStream_t stream)
     RopeArgs a = args;
     const int heads = a.H_q + a.H_k;
     // As many heads a thread as leave 512 threads an SM that turn.  8,192 tokens of 18 heads of 256, a quarter of which turns: 24.9 us
-    // (6.1 TB/s); 33.6 with 2,048 threads an SM, 25.6 with 1,024, 28.1 with 128.
+    // (6.1 TB/s); 33.4 with 2,048 threads an SM, 25.6 with 1,024, 28.0 with 128.  1,001 tokens of 16 heads of 128, all of which turns, have
+    // one head a thread: 4.3 us; 6.1 with 128 threads an SM.
     const long long wave = num_sms * 512ll, turning = static_cast<long long>(a.N) * (a.rot / 16);
     const long long most = turning * heads / wave;
     a.heads_each = static_cast<int>(most < 1 ? 1 : most < heads ? most : heads);

@@ -255,10 +255,10 @@ cudaError_t launch_verify(const VerifyArgs &args, int num_sms, cudaStream_t stre
 {
     VerifyArgs a = args;
     // One wave of CTAs (a CTA's time is a chain of loads and barriers, and clusters leave gaps between waves: 200 sequences of 20,000
-    // tokens take 14.6 us with one CTA each, 20.4 with two, 69 with eight), in as many as that allows.
+    // tokens take 18.4 us with one CTA each, 25.1 with two, 75.4 with eight), in as many as that allows (64 of 131,072 13.7 with two, 16.7 with one).
     for (a.ranks = kMaxRanks; a.ranks > 1 && a.B * a.ranks > num_sms;) a.ranks /= 2;
-    // twice the threads for a CTA's part of a long row (64 rows of 131,072 in two parts 12.9 us against 15.2, eight of 100,003 in
-    // eight parts 9.2 against 8.4)
+    // twice the threads for a CTA's part of a long row (64 rows of 131,072 in two parts 13.7 us against 14.7; 200 of 20,000 in one
+    // 19.2 against 18.4; eight of 100,003 in eight parts 10.1 against 10.3)
     const bool wide = a.V / a.ranks >= 32768;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.B * a.ranks);

@@ -518,9 +518,12 @@ int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride,
  *   out       out_type (LILY_BF16, LILY_F32) [T][rows] dense
  * Weights and e4m3 x enter the products unrounded, bf16 x too, but for values below 2^-27 of the largest of the 256 channels
  * [256 i, 256 i + 256) of their token, which are off by at most 2^-35 of that largest; sums are fp32.  A token with values that
- * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 may lose bits.
+ * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 may lose bits.  Codes and
+ * biases are summed apart: an output is off by less than (224 + K / 32) 2^-24 of sum_k |x| (q |scale| + |bias|), which may be far
+ * larger than the output itself where the two nearly cancel, and by its own rounding.
  * Like x, the matrix may be the output of an earlier kernel of the stream, the one just before among them.
- * Supported: 0 <= T <= 32 (in whole groups of 8: five tokens cost what eight do); K a multiple of 64 in [64, 16384];
+ * Supported: 0 <= T <= 32 (in whole groups of 8: five tokens cost what eight do; K in power-of-two numbers of 256 channels,
+ * where instructions and not the memory set the pace: 2,560 columns cost up to what 4,096 do); K a multiple of 64 in [64, 16384];
  * 1 <= rows < 2^30.
  */
 typedef struct lily_q4_shape {
