@@ -192,9 +192,11 @@ __device__ __forceinline__ void load_tokens(Tokens<NT, CODES> &to, const MatvecA
         const float keep0 = (t & 1 ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[0] : sum[1], 1);
         const float keep1 = (t & 1 ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, t & 1 ? sum[2] : sum[3], 1);
         float rest = (t & 2 ? keep1 : keep0) + __shfl_xor_sync(0xffffffffu, t & 2 ? keep0 : keep1, 2);
-        rest *= CODES ? scale[CODES ? n : 0] * 0.015625f : 0x1p-24f;
-        // products with codes are times 2^-24 and `by`
-        if (CODES) factors[((n * 4 + lane / 8) * 4 + t) * 2 + lane / 4 % 2] = scale[CODES ? n : 0] * 0x1p18f;
+        // Everything is 2^-10 of what it stands for until it is stored (kUnit), which leaves a factor of scale * 2^8 here: finite, and times a
+        // group's largest sum of products too, for every scale that the norm gives (fp32's largest number over 448).  Products with
+        // codes are times 2^-24 and `by`.
+        rest *= CODES ? scale[CODES ? n : 0] * 0x1p-16f : 0x1p-24f;
+        if (CODES) factors[((n * 4 + lane / 8) * 4 + t) * 2 + lane / 4 % 2] = scale[CODES ? n : 0] * 0x1p8f;
         // as three bf16 numbers: what is left of 24 bits after eight more
         const __nv_bfloat16 p0 = __float2bfloat16_rn(rest);
         rest -= __bfloat162float(p0);
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) matvec_kernel(const __grid_cons
                         so_far[i] = sum;
                         continue;
                     }
-                    constexpr float kUnit = CODES ? 1.0f : 1024.0f;  // bf16: codes times 2^-24, x times 2^14 over its factor
+                    constexpr float kUnit = 1024.0f;  // codes times 2^-24, bf16 x times 2^14 over its factor, e4m3 x times 2^6 and its factor 2^8
                     const float v[4] = {sum.x * kUnit, sum.y * kUnit, sum.z * kUnit, sum.w * kUnit};
                     const long long o = static_cast<long long>(token) * a.rows + row;
                     if (a.rows % 4 == 0) {

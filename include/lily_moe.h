@@ -518,7 +518,8 @@ int lily_rms_norm(const lily_norm_shape *shape, const void *x, int64_t x_stride,
  *   out       out_type (LILY_BF16, LILY_F32) [T][rows] dense
  * Weights and e4m3 x enter the products unrounded, bf16 x too, but for values below 2^-27 of the largest of the 256 channels
  * [256 i, 256 i + 256) of their token, which are off by at most 2^-35 of that largest; sums are fp32.  A token with values that
- * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 may lose bits.  Codes and
+ * are not finite leaves only its own outputs unspecified, a weight row only its own row.  Inputs below 2^-100 and outputs below
+ * 2^-100 may lose bits; x_scale is at most fp32's largest number over 448 (as the norm's are).  Codes and
  * biases are summed apart: an output is off by less than (224 + K / 32) 2^-24 of sum_k |x| (q |scale| + |bias|), which may be far
  * larger than the output itself where the two nearly cancel, and by its own rounding.
  * Like x, the matrix may be the output of an earlier kernel of the stream, the one just before among them.
