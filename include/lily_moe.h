@@ -476,7 +476,7 @@ int lily_gdn_scan(const lily_gdn_shape *shape, const uint16_t *q, const uint16_t
  * attention and the scan, and leaves these to the model; the 4-bit format is the page's
  * (section "Prefill e decode: onde estao os ganhos").
  *
- * All of them: row-major device arrays, 16-byte aligned, strides in elements; asynchronous on
+ * All of them: row-major device arrays, 16-byte aligned, strides in elements, at most 2^31; asynchronous on
  * `stream`, one kernel each, bit-reproducible; no tokens enqueue nothing.  Outputs may overlap neither
  * inputs nor other outputs, except where a call says so.
  */
